@@ -273,6 +273,166 @@ size_t gqaw_step_args_size(void);
  * other errors are those of gqa_windowed_step. */
 gqaw_status gqa_windowed_step_noalloc(const gqaw_step_args *args, void *stream);
 
+/* ---------------------------------------------------------------------------------
+ * Paged caches and per-head norms.  The pages do not define these operators; they are
+ * what a server built around gqa_windowed_step needs for layers that keep every key:
+ * a cache in fixed-size pages handed out by the caller, ragged batches of new tokens,
+ * and the RMS norm of queries and keys that many models apply before the rotation.
+ * ------------------------------------------------------------------------------- */
+
+/* Further bit of the device status word. */
+#define GQAW_DEV_BAD_PAGE 32u /* a page table entry that the call needs lies outside [0, num_pages) */
+
+/* Arguments of gqaw_qk_norm_rotary.  Every pointer is a DEVICE pointer.  Row (n, h) of
+ * query is the D elements at query[n * query_stride + h * D].  16-byte alignment:
+ * query, key, query_out, key_out, the weights, and the strides in bytes; cos_cache and
+ * sin_cache element-aligned, position_ids 8-byte. */
+typedef struct gqaw_qk_args {
+  int32_t num_tokens;         /* N >= 0 */
+  int32_t num_heads;          /* Nq >= 0: query heads */
+  int32_t kv_num_heads;       /* Nkv >= 0: key heads; a count of 0 leaves that tensor out */
+  int32_t head_size;          /* D: one of 8, 16, 32, 64, 128, 256 */
+  int32_t dtype;              /* GQAW_F32 or GQAW_BF16: rows, weights, cos_cache and sin_cache */
+  float norm_eps;             /* finite, >= 0; added to the mean square of a row */
+  const void *query;          /* (N, Nq, D) */
+  const void *key;            /* (N, Nkv, D) */
+  void *query_out;            /* == query with the same stride (in place), or disjoint from the inputs */
+  void *key_out;
+  int64_t query_stride;       /* elements between tokens: 0 for Nq * D, else >= Nq * D */
+  int64_t key_stride;         /* 0 for Nkv * D, else >= Nkv * D */
+  int64_t query_out_stride;   /* as query_stride */
+  int64_t key_out_stride;     /* as key_stride */
+  const void *query_weight;   /* (D,), or NULL: query rows are not normed */
+  const void *key_weight;     /* (D,), or NULL: key rows are not normed */
+  const void *cos_cache;      /* (rotary_cache_len, rd/2), or NULL (with sin_cache): no rotation */
+  const void *sin_cache;
+  const int64_t *position_ids; /* (N,): the row of the tables; needed with a rotation */
+  int32_t rotary_interleaved; /* as in gqaw_step_args */
+  int32_t rotary_dim;         /* rd: even, 2 <= rd <= D; 0 means D */
+  int32_t rotary_cache_len;   /* >= 1 with a rotation */
+  int32_t reserved;           /* 0 */
+  void *workspace;            /* >= 256 bytes, 256-byte aligned, zeroed once with
+                                 gqaw_workspace_init(): holds the device status word.  Needed
+                                 with a rotation (a position may lie outside the tables), else
+                                 may be NULL */
+  size_t workspace_bytes;
+} gqaw_qk_args;
+
+/* Per-head RMS norm of queries and keys with the rotary embedding in the same pass: for
+ * each row x (D elements of one head of one token)
+ *     y = x / sqrt(mean(x^2) + norm_eps) * weight      (without a weight: y = x)
+ * then the first rd dimensions of y are turned by the token's position as in a step with
+ * do_rotary.  Computed in fp32 and rounded once to dtype.  Its outputs are the query and
+ * key of a gqa_windowed_step with do_rotary = 0.  A position outside the tables sets
+ * GQAW_DEV_BAD_POSITION and leaves that row unturned (normed, if it has a weight). */
+gqaw_status gqaw_qk_norm_rotary(const gqaw_qk_args *args, void *stream);
+
+/* Arguments of the paged operators.  Every pointer is a DEVICE pointer.
+ *
+ * The cache.  key_pages and value_pages hold num_pages pages of page_size rows for each
+ * kv head: row r of head h in page p is the D elements at
+ *     p * page_stride + h * head_stride + r * row_stride
+ * so (pages, heads, rows, D) and (pages, rows, heads, D) are both expressible.  Position
+ * j of sequence b lives in row j % page_size of page page_table[b][j / page_size].
+ * Several sequences may share a page; the rows that one call writes must be distinct.
+ *
+ * The batch.  Sequence b brings S_b = query_start[b + 1] - query_start[b] new tokens (0
+ * is fine), rows query_start[b] .. of query, key, value and output, which end at length
+ * T_b = seqlens_k[b] + 1 (the length including them; seqlens_k[b] = -1 is an empty
+ * sequence).  Their positions are T_b - S_b .. T_b - 1.  Rows before query_start[0] and
+ * from query_start[B] on belong to nobody: they are not read and not written.
+ *
+ * Table entries.  An append reads those of the new positions, an attention those of the
+ * positions that some new token of the sequence attends; no other entry is looked at, so
+ * pages that have left every window may be given back.  An entry outside [0, num_pages)
+ * sets GQAW_DEV_BAD_PAGE: an append drops the row, an attention leaves the outputs of that
+ * sequence unspecified.  A sequence with S_b < 0, S_b > max_new_tokens, T_b < S_b,
+ * T_b > max_sequence_length or rows outside [0, total_new_tokens) sets
+ * GQAW_DEV_BAD_SEQLEN and is skipped.  Neither touches any other sequence.
+ *
+ * Alignment: query, key, value, the pages, output and the weights 16-byte, all strides
+ * multiples of 16 bytes; page_table, query_start, seqlens_k and head_sink 4-byte; cos_cache
+ * and sin_cache element-aligned; position_ids 8-byte; workspace 256-byte. */
+typedef struct gqaw_paged_args {
+  int32_t batch_size;          /* B >= 0 sequences */
+  int32_t total_new_tokens;    /* N >= 0: rows of query, key, value and output */
+  int32_t max_new_tokens;      /* >= every S_b; 0 <= max_new_tokens <= N */
+  int32_t max_sequence_length; /* >= every T_b; <= page_table_width * page_size */
+  int32_t num_heads;           /* Nq >= 1 */
+  int32_t kv_num_heads;        /* Nkv >= 1, Nq % Nkv == 0 */
+  int32_t head_size;           /* D: one of 8, 16, 32, 64, 128, 256 */
+  int32_t page_size;           /* rows of a page, >= 1 */
+  int32_t num_pages;           /* >= 0 */
+  int32_t page_table_width;    /* entries of a page table row, >= 0 */
+  int32_t local_window_size;   /* W: a token attends itself and the W - 1 keys before it;
+                                  0 for every key before it */
+  int32_t dtype;               /* GQAW_F32 or GQAW_BF16: all rows, pages, weights and tables */
+  float scale;                 /* > 0, or 0 for the default 1/sqrt(D) */
+  float softcap;               /* >= 0; 0 disables soft-capping */
+  float norm_eps;              /* finite, >= 0 */
+  int32_t smooth_softmax;      /* as in gqaw_step_args */
+  const void *query;           /* (N, Nq, D); attend and step */
+  const void *key;             /* (N, Nkv, D); append and step */
+  const void *value;           /* (N, Nkv, D); append and step */
+  void *output;                /* (N, Nq, D); attend and step */
+  int64_t query_stride;        /* elements between tokens: 0 for Nq * D, else >= Nq * D */
+  int64_t key_stride;          /* 0 for Nkv * D, else >= Nkv * D */
+  int64_t value_stride;
+  int64_t output_stride;
+  void *key_pages;
+  void *value_pages;
+  int64_t page_stride;         /* elements; all three 0: contiguous (num_pages, Nkv, page_size, D) */
+  int64_t head_stride;
+  int64_t row_stride;
+  const int32_t *page_table;   /* (B, page_table_width) int32, contiguous */
+  const int32_t *query_start;  /* (B + 1,) int32, ascending */
+  const int32_t *seqlens_k;    /* (B,) int32: T_b - 1 */
+  const float *head_sink;      /* NULL, or (Nq,) fp32, as in gqaw_step_args */
+  const void *query_weight;    /* (D,), or NULL: no norm of the query (step) */
+  const void *key_weight;      /* (D,), or NULL: no norm of the key (append and step) */
+  const void *cos_cache;       /* (rotary_cache_len, rd/2), or NULL (with sin_cache): no rotation */
+  const void *sin_cache;
+  const int64_t *position_ids; /* NULL (row n's position), or (N,) int64: the row of the tables */
+  int32_t rotary_interleaved;
+  int32_t rotary_dim;          /* rd: even, 2 <= rd <= D; 0 means D */
+  int32_t rotary_cache_len;    /* >= 1 with a rotation */
+  int32_t reserved;            /* 0 */
+  void *workspace;             /* gqaw_paged_workspace_bytes() bytes, zeroed once with
+                                  gqaw_workspace_init() before first use (and again after a
+                                  device error).  Every completed call leaves its tickets at
+                                  zero at a place that no size moves, so one workspace serves
+                                  paged calls of any shape in stream order, captured or not;
+                                  windowed steps on the same workspace follow the rule given
+                                  for gqaw_step_args.  Calls that share a workspace must not
+                                  overlap on the GPU */
+  size_t workspace_bytes;
+} gqaw_paged_args;
+
+/* Workspace bytes of any of the three calls below for these sizes (pointers may be NULL;
+ * split results grow with the GPU, not with the batch; gqaw_paged_step also keeps its
+ * turned queries there).  0 if the sizes are invalid. */
+size_t gqaw_paged_workspace_bytes(const gqaw_paged_args *args);
+
+/* Append: key rows, normed with key_weight and turned by their positions (each if given),
+ * rounded once to dtype, and value rows, copied, go to their places in the pages. */
+gqaw_status gqaw_paged_append(const gqaw_paged_args *args, void *stream);
+
+/* Attention of the new tokens over the paged cache, which holds their own keys and values
+ * already.  The token at position i attends the keys j <= i (and j > i - W with a window)
+ * of its sequence; logits, softcap, sinks and head grouping as in gqa_windowed_step.  The
+ * query is taken as it is given: query_weight and the tables are not applied.  Cache rows
+ * that a token does not attend never reach its output, whatever they hold. */
+gqaw_status gqaw_paged_attend(const gqaw_paged_args *args, void *stream);
+
+/* The whole step: append, and attention of the normed and turned queries (rounded to dtype
+ * in the workspace).  Two kernels; the same results as gqaw_qk_norm_rotary of the query,
+ * gqaw_paged_append and gqaw_paged_attend in turn. */
+gqaw_status gqaw_paged_step(const gqaw_paged_args *args, void *stream);
+
+/* sizeof(gqaw_qk_args) and sizeof(gqaw_paged_args) as compiled into the library. */
+size_t gqaw_qk_args_size(void);
+size_t gqaw_paged_args_size(void);
+
 #ifdef __cplusplus
 }
 #endif

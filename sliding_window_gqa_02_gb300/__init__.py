@@ -4,4 +4,5 @@ The computation lives in ``libgqaw.so`` (CUDA kernels behind the C ABI of
 include/gqaw.h); :mod:`.gqaw` is its ctypes binding.
 """
 from .gqaw import *  # noqa: F401,F403
-from .gqaw import load, make_args, new_workspace, check, GqawError  # noqa: F401
+from .gqaw import (load, make_args, make_paged_args, make_qk_args, new_paged_workspace,  # noqa: F401
+                   new_workspace, check, GqawError)

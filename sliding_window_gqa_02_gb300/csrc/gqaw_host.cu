@@ -531,7 +531,7 @@ bool encode_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *di
                 const cuuint32_t *box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (!fn) return false;
-  const cuuint32_t es[3] = {1, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -645,6 +645,14 @@ gqaw_status run_finish(const gqaw_step_args *a, const Launch &L, const gqaw::Par
 namespace gqaw {
 // Lets other translation units of the library report an error through gqaw_last_error().
 void set_error(const char *msg) { t_error = msg; }
+
+// ... and count a kernel launch, and share the record of the workspaces' ticket regions.
+void count_launch() { g_launches.fetch_add(1); }
+bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                     const cuuint32_t *box) {
+  return encode_map(m, base, rank, dims, strides, box);
+}
+bool workspace_tickets_need_clear(const void *ws, size_t t0, size_t t1) { return tickets_need_clear(ws, t0, t1); }
 
 // Bytes at the start of a step's workspace that must be zero when the step starts (the
 // status word, the cache-update counters and list, the tickets); 0 if the sizes are
