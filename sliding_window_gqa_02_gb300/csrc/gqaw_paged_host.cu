@@ -8,13 +8,17 @@
 #include <cstdio>
 #include <cstring>
 
-#include "gqaw_paged.cuh"
+#include "gqaw_paged_tc.cuh"
 
 namespace gqaw {
 void set_error(const char *msg);
 void count_launch();
 bool workspace_tickets_need_clear(const void *ws, size_t t0, size_t t1);
 cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool paged, bool bf16, cudaStream_t stream);
+bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                     const cuuint32_t *box);
+cudaError_t launch_paged_decode(const PagedParams &p, const PagedMaps &maps, int rows, int grid, cudaStream_t stream);
+cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, int grid, cudaStream_t stream);
 cudaError_t launch_paged_rows_attend_f32(const PagedParams &p, int bm, int grid, cudaStream_t stream);
 cudaError_t launch_paged_rows_attend_bf16(const PagedParams &p, int bm, int grid, cudaStream_t stream);
 }  // namespace gqaw
@@ -202,7 +206,7 @@ gqaw_status check_qk_pointers(const gqaw_qk_args *a, const QkPlan &L) {
 
 // ------------------------------------------------------------------------------ paged
 
-enum Path { kRows = 0 };
+enum Path { kRows = 0, kDecode = 1, kPrefill = 2 };
 
 struct Plan {
   int es, rot_dim, group, path, bm, rows, hblocks, gb, tpt, grid;
@@ -273,8 +277,31 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
   // when they are more than the tile has rows).
   L->group = a->num_heads / a->kv_num_heads;
   const long long rows = (long long)std::max(1, a->max_new_tokens) * L->group;
+  // The tensor cores take bf16 with head sizes from 64 on, and pages that tile 128 keys in
+  // whole 8-row groups of the swizzled layout.
+  const bool tc = a->dtype == GQAW_BF16 && D >= 64 && a->page_size % 8 == 0 &&
+                  (128 % a->page_size == 0 || a->page_size % 128 == 0) && a->num_pages > 0 &&
+                  std::max(L->sp, std::max(L->sh, L->sr)) * 2 < (1ll << 40) && std::max(L->qs, qrow) * 2 < (1ll << 40);
   size_t part_rows;  // rows of partial results per CTA
-  {
+  if (tc && rows <= 32) {
+    L->path = kDecode;
+    L->gb = L->group;
+    L->hblocks = 1;
+    L->tpt = std::max(1, a->max_new_tokens);
+    part_rows = rows <= 16 ? 16 : 32;
+    // no more CTAs than key tiles there can be
+    const long long span = a->local_window_size > 0 ? std::min<long long>(a->max_sequence_length, (long long)a->local_window_size + a->max_new_tokens)
+                                                     : a->max_sequence_length;
+    L->grid = (int)std::max(1ll, std::min<long long>(kSms, (long long)std::min(a->batch_size, gqaw::kPagedItems) *
+                                                               a->kv_num_heads * (ceil_div(span, 128) + 1)));
+  } else if (tc && L->group <= 128) {
+    L->path = kPrefill;
+    L->gb = L->group;
+    L->hblocks = 1;
+    L->tpt = 128 / L->group;
+    part_rows = 128;
+    L->grid = kSms;
+  } else {
     L->path = kRows;
     L->bm = rows <= 16 ? 16 : D == 256 ? 32 : 64;
     L->grid = L->bm == 16 ? kSms * 4 : kSms * 2;
@@ -414,18 +441,39 @@ gqaw_status run_rows(const PagedParams &p, int nq, int nk, int nv, bool paged, b
   return GQAW_OK;
 }
 
+gqaw_status make_maps(const gqaw_paged_args *a, const Plan &L, const PagedParams &p, gqaw::PagedMaps *m) {
+  const cuuint64_t D = (cuuint64_t)a->head_size;
+  const cuuint64_t qd[3] = {D, (cuuint64_t)a->num_heads, (cuuint64_t)a->total_new_tokens};
+  const cuuint64_t qst[2] = {D * 2, (cuuint64_t)p.qs * 2};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)L.group, (cuuint32_t)L.tpt};
+  const cuuint64_t cd[4] = {D, (cuuint64_t)a->page_size, (cuuint64_t)a->kv_num_heads, (cuuint64_t)a->num_pages};
+  const cuuint64_t cst[3] = {(cuuint64_t)L.sr * 2, (cuuint64_t)L.sh * 2, (cuuint64_t)L.sp * 2};
+  const cuuint32_t cb[4] = {64, (cuuint32_t)std::min(a->page_size, 128), 1, 1};
+  if (!gqaw::encode_bf16_map(&m->q, p.q, 3, qd, qst, qb) || !gqaw::encode_bf16_map(&m->k, a->key_pages, 4, cd, cst, cb) ||
+      !gqaw::encode_bf16_map(&m->v, a->value_pages, 4, cd, cst, cb))
+    return fail(GQAW_ECUDA, "cuTensorMapEncodeTiled failed for the paged attention");
+  return GQAW_OK;
+}
+
 // The attention, a launch for every kPagedItems sequences.
 gqaw_status run_paged_attend(const gqaw_paged_args *a, const Plan &L, PagedParams p, cudaStream_t st) {
   if (gqaw::workspace_tickets_need_clear(a->workspace, gqaw::kPagedTicketOffset, gqaw::kPagedPartialOffset)) {
     const cudaError_t e = cudaMemsetAsync(p.tickets, 0, gqaw::kPagedTickets * 4, st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync (tickets)");
   }
+  gqaw::PagedMaps maps;
+  if (L.path != kRows) {
+    const gqaw_status s = make_maps(a, L, p, &maps);
+    if (s != GQAW_OK) return s;
+  }
   for (int b0 = 0; b0 < a->batch_size; b0 += gqaw::kPagedItems) {
     p.B = std::min(gqaw::kPagedItems, a->batch_size - b0);
     p.table = a->page_table + (long long)b0 * a->page_table_width;
     p.qstart = a->query_start + b0;
     p.seqlens = a->seqlens_k + b0;
-    const cudaError_t e = a->dtype == GQAW_F32 ? gqaw::launch_paged_rows_attend_f32(p, L.bm, L.grid, st)
+    const cudaError_t e = L.path == kDecode    ? gqaw::launch_paged_decode(p, maps, L.rows, L.grid, st)
+                          : L.path == kPrefill ? gqaw::launch_paged_prefill(p, maps, L.grid, st)
+                          : a->dtype == GQAW_F32 ? gqaw::launch_paged_rows_attend_f32(p, L.bm, L.grid, st)
                                                  : gqaw::launch_paged_rows_attend_bf16(p, L.bm, L.grid, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel launch");
     gqaw::count_launch();
