@@ -22,7 +22,7 @@ cudaError_t launch_paged_rows_attend_one(const PagedParams &p, int grid, cudaStr
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(prow::kThreads);
+  cfg.blockDim = dim3(prow::Lay<T, D, BM>::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -48,12 +48,12 @@ cudaError_t launch_paged_rows_attend(const PagedParams &p, int bm, int grid, cud
     }
   }
   switch (p.D) {
-    case 8: return launch_paged_rows_attend_one<T, 8, 64>(p, grid, stream);
-    case 16: return launch_paged_rows_attend_one<T, 16, 64>(p, grid, stream);
-    case 32: return launch_paged_rows_attend_one<T, 32, 64>(p, grid, stream);
-    case 64: return launch_paged_rows_attend_one<T, 64, 64>(p, grid, stream);
-    case 128: return launch_paged_rows_attend_one<T, 128, 64>(p, grid, stream);
-    default: return launch_paged_rows_attend_one<T, 256, 32>(p, grid, stream);
+    case 8: return launch_paged_rows_attend_one<T, 8, 128>(p, grid, stream);
+    case 16: return launch_paged_rows_attend_one<T, 16, 128>(p, grid, stream);
+    case 32: return launch_paged_rows_attend_one<T, 32, 128>(p, grid, stream);
+    case 64: return launch_paged_rows_attend_one<T, 64, 128>(p, grid, stream);
+    case 128: return launch_paged_rows_attend_one<T, 128, 128>(p, grid, stream);
+    default: return launch_paged_rows_attend_one<T, 256, 64>(p, grid, stream);
   }
 }
 

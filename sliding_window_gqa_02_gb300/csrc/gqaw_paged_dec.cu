@@ -1,12 +1,12 @@
-// gqaw_paged_dec.cu -- paged attention of few query rows per kv head (decode and short
-// verify: at most 32 rows, tokens x query heads of a kv head) on the 5th-generation tensor
-// cores, bf16, head sizes 64, 128 and 256.
+// gqaw_paged_dec.cu -- paged attention of few query rows per kv head (decode: at most 8 rows,
+// tokens x query heads of a kv head) on the 5th-generation tensor cores, bf16, head sizes 64,
+// 128 and 256.
 //
-// Bound: HBM.  Every attended key and value row is read once; the arithmetic is 2 x 16 or
-// 2 x 32 padded rows wide.  So the products run transposed, the 128 keys of a tile as the
+// Bound: HBM.  Every attended key and value row is read once; the arithmetic is 2 x 16 padded
+// rows wide.  So the products run transposed, the 128 keys of a tile as the
 // MMA's M dimension, and little work is left per key:
-//   S^T = K Q^T        M = 128 keys, N = NPAD query rows, K = D dimensions
-//   O^T += V^T P^T     M = 128 dimensions (two blocks for 256), N = NPAD rows, K = 128 keys
+//   S^T = K Q^T        M = 128 keys, N = 16 query rows, K = D dimensions
+//   O^T += V^T P^T     M = 128 dimensions (two blocks for 256), N = 16 rows, K = 128 keys
 // With head size 64 the second 64 of V^T's M rows repeat the first (a leading offset of 0);
 // their results are not read.
 // A softmax thread owns one key (a TMEM lane) and NC of the query rows.  The rows keep a
@@ -16,8 +16,8 @@
 // in fp32.  P is rounded to bf16 for the product (relative 2^-9 of each weight, the size of
 // the output's own rounding); the sum is of the unrounded weights.
 //
-// Warps: 4 CG softmax warps, a TMA warp (one lane per box of a tile), one warp issuing S^T
-// and one issuing P.V.  K and V tiles alternate through one ring of kSlots tiles, so the
+// Warps: 4 CG softmax warps, a TMA warp for Q and K and one for V (a lane looks up each box of
+// a tile), one warp issuing S^T and one issuing P.V.  K and V tiles alternate through one ring of kSlots tiles, so the
 // loads run up to kSlots tiles ahead of the products, over the ends of units.  The schedule
 // is that of gqaw_paged.cuh.
 //
@@ -40,14 +40,22 @@ using ptc::kKeys;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr int kBar = 1;           // named barrier of the softmax warps
 
-template <int D, int NPAD>
+constexpr int NPAD = 16;   // rows of the MMA
+constexpr int CG = 2;      // column groups of softmax warps: more warps to overlap than the rows need
+constexpr int kThreads = 32 * (4 * CG + 4);
+
+template <int D>
 struct Lay {
   static constexpr int HALVES = D / 64;
   static constexpr int DM = D > 128 ? D / 128 : 1;  // 128-dimension blocks of O^T
   static constexpr int kTile = HALVES * kHalf;
   // as many tiles in flight as fit beside Q and P: at 44 bytes per ns and SM, a load that
   // takes 2 us needs 90 KB under way
-  static constexpr int kSlots = D == 64 ? 10 : D == 128 ? (NPAD == 16 ? 6 : 5) : 2;
+  static constexpr int kSlots = D == 64 ? 10 : D == 128 ? 6 : 2;
+  // Even, so that a slot holds keys only or values only: the one thread that consumes them
+  // has waited for the slot's last tile before it waits for the next.  (An odd count puts K
+  // where V was; the S^T thread could then take V's pending phase for K's completed one.)
+  static_assert(kSlots % 2 == 0, "slots alternate between K and V");
   static constexpr int kQHalf = NPAD * 128;           // 64 columns of Q or P^T
   static constexpr int kQBuf = HALVES * kQHalf;
   static constexpr int kQ = kSlots * kTile;           // two Q buffers
@@ -59,7 +67,8 @@ struct Lay {
   static constexpr int kNumBars = 2 * kSlots + 14;
   static constexpr int kMisc = kBars + kNumBars * 8;  // TMEM address, flags
   static constexpr int kAlloc = kMisc + 64 + 1024;    // and room to align the base
-  static constexpr uint32_t kCols = (2 + DM) * NPAD <= 64 ? 64 : 128;
+  static constexpr uint32_t kCols = 64;  // S^T twice, O^T
+  static_assert((2 + DM) * NPAD <= (int)kCols, "tensor memory columns");
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
@@ -81,15 +90,6 @@ __device__ __forceinline__ void tmem_ld<4>(uint32_t taddr, float (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <>
-__device__ __forceinline__ void tmem_ld<8>(uint32_t taddr, float (&v)[8]) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\ntcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[N]);
 template <>
@@ -104,17 +104,6 @@ __device__ __forceinline__ void tmem_st<4>(uint32_t taddr, const float (&v)[4]) 
                "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])) : "memory");
   tc::tmem_wait_st();
 }
-template <>
-__device__ __forceinline__ void tmem_st<8>(uint32_t taddr, const float (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])) : "memory");
-  tc::tmem_wait_st();
-}
-
-__host__ __device__ constexpr int threads(int cg) { return 32 * (4 * cg + 3); }
-
 // Does a pair of bf16 in a word hold an infinity or a NaN?
 __device__ __forceinline__ bool odd_pair(uint32_t w) {
   return (w & 0x7f800000u) == 0x7f800000u || (w & 0x00007f80u) == 0x00007f80u;
@@ -122,16 +111,15 @@ __device__ __forceinline__ bool odd_pair(uint32_t w) {
 
 }  // namespace pdec
 
-// NPAD: rows of the MMA (16 or 32); NVT: rows the softmax warps work on (4, 8, 16 or 32); CG:
-// column groups of softmax warps, NC = NVT / CG rows a thread.
-template <int D, int NPAD, int NVT, int CG>
-__global__ void __launch_bounds__(pdec::threads(CG), 1)
+// NVT: rows the softmax warps work on (4 or 8), NC = NVT / CG of them a thread.
+template <int D, int NVT>
+__global__ void __launch_bounds__(pdec::kThreads, 1)
     paged_decode_kernel(const PagedParams p, const __grid_constant__ PagedMaps maps) {
   using namespace pdec;
   using ptc::fast_exp2;
-  using L = Lay<D, NPAD>;
+  using L = Lay<D>;
   constexpr int NC = NVT / CG, kSoft = 128 * CG, DM = L::DM, kSlots = L::kSlots;
-  constexpr int kLoadWarp = 4 * CG, kSWarp = kLoadWarp + 1, kPVWarp = kLoadWarp + 2;
+  constexpr int kSoftWarps = 4 * CG, kKWarp = kSoftWarps, kVWarp = kKWarp + 1, kSWarp = kKWarp + 2, kPVWarp = kKWarp + 3;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   PSched *sched = reinterpret_cast<PSched *>(smem + L::kSched);
@@ -155,13 +143,13 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], kSoft);
-      mbar_init(&p_full[i], kSoft);
+      mbar_init(&s_free[i], kSoftWarps);
+      mbar_init(&p_full[i], kSoftWarps);
       mbar_init(&o_done[i], 1);
       mbar_init(&q_full[i], 1);
       mbar_init(&q_free[i], 1);
     }
-    mbar_init(o_free, kSoft);
+    mbar_init(o_free, kSoftWarps);
     mbar_init(mma_done, 2);
     mbar_fence_init();
     *s_abort = 0;
@@ -172,12 +160,13 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
   if (warp == 0) tc::tmem_alloc(tmem_slot, L::kCols);
   tc::fence_proxy_async_smem();
   pdl_wait();
-  sched_build<kKeys>(p, sched, threads(CG));
+  sched_build<kKeys>(p, sched, kThreads);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot, tmem_s = tmem, tmem_o = tmem + 2 * NPAD;
   const int g = p.group;
+  const PShape shp = shape_of(p);
   volatile int *abort_flag = s_abort;
 
   // K of tile kc (counted over the CTA's units) is load 2 kc, V load 2 kc + 1; load n sits in
@@ -187,49 +176,50 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
   auto qbuf = [&](int ui) { return smem + L::kQ + (ui & 1) * L::kQBuf; };
   auto pbuf = [&](int kc) { return smem + L::kP + (kc & 1) * 2 * L::kQHalf; };
 
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------------------ TMA loads (whole warp)
+  if (warp == kKWarp || warp == kVWarp) {
+    // ------------------------------------------------------------ loads: Q and K | V (whole warps)
+    const bool value = warp == kVWarp;
     const uint64_t pol = policy_evict_first(), qpol = tc::policy_evict_last();
-    PWalk<kKeys> w(p, sched);
+    PWalk<kKeys> w(shp, sched);
     PUnit u;
     ptc::Boxes bx;
-    int n = 0, ui = 0;
+    int n = value ? 1 : 0, ui = 0;  // this warp's loads are n, n + 2, ...
     bool alive = true;
-    while (alive && w.next(p, u)) {
+    while (alive && w.next(shp, u)) {
       bx.unit(p, u);
       bx.look_up(p, u.kt + u.k0, lane);
-      if (ui >= 2) alive = __all_sync(0xffffffffu, mbar_wait(&q_free[ui & 1], ((ui - 2) >> 1) & 1));
-      if (!alive) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[ui & 1], (uint32_t)(L::HALVES * g * p.tpt * 128));
-        for (int h = 0; h < L::HALVES; ++h)
-          tc::tma_load_3d(qbuf(ui) + h * L::kQHalf, &maps.q, h * 64, u.hu * g, u.row0, &q_full[ui & 1], qpol);
+      if (!value) {
+        if (ui >= 2) alive = __all_sync(0xffffffffu, mbar_wait(&q_free[ui & 1], ((ui - 2) >> 1) & 1));
+        if (!alive) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[ui & 1], (uint32_t)(L::HALVES * g * p.tpt * 128));
+          for (int h = 0; h < L::HALVES; ++h)
+            tc::tma_load_3d(qbuf(ui) + h * L::kQHalf, &maps.q, h * 64, u.hu * g, u.row0, &q_full[ui & 1], qpol);
+        }
+        ++ui;
       }
-      ++ui;
       for (int k = u.k0; k < u.k1 && alive; ++k) {
         const uint32_t mask = bx.valid(p, u.kt + k, lane);
         const uint32_t bytes = (uint32_t)(__popc(mask) * bx.rows * 128 * L::HALVES);
-        ptc::Boxes cur = bx;
-        if (k + 1 < u.k1) bx.look_up(p, u.kt + k + 1, lane);  // in flight while the slots are waited for
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int s = n % kSlots;
-          if (n >= kSlots) alive = __all_sync(0xffffffffu, mbar_wait(&empty[s], phase(n) ^ 1u));
-          alive = alive && !*abort_flag;
-          alive = __all_sync(0xffffffffu, alive);
-          if (!alive) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
-          __syncwarp();
-          cur.load<L::HALVES>(kv ? &maps.v : &maps.k, slot(n), &full[s], pol, mask, lane);
-        }
+        const ptc::Boxes cur = bx;
+        if (k + 1 < u.k1) bx.look_up(p, u.kt + k + 1, lane);  // in flight while the slot is waited for
+        const int s = n % kSlots;
+        if (n >= kSlots) alive = mbar_wait(&empty[s], phase(n) ^ 1u);
+        alive = __all_sync(0xffffffffu, alive && !*abort_flag);
+        if (!alive) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
+        cur.load<L::HALVES>(value ? &maps.v : &maps.k, slot(n), &full[s], pol, mask, lane);
+        n += 2;
       }
     }
-    if (!alive && lane == 0) {
-      pflag(p, GQAW_DEV_TIMEOUT);
-      *abort_flag = 1;
-    }
-    // no copy may still be landing in shared memory when the CTA exits
     if (lane == 0) {
-      for (int i = n > kSlots ? n - kSlots : 0; i < n; ++i)
+      if (!alive) {
+        pflag(p, GQAW_DEV_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // no copy may still be landing in shared memory when the CTA exits
+      const int first = value ? 1 : 0;
+      for (int i = n - kSlots > first ? n - kSlots : first; i < n; i += 2)
         if (!mbar_wait(&full[i % kSlots], phase(i))) pflag(p, GQAW_DEV_TIMEOUT);
       for (int i = ui > 2 ? ui - 2 : 0; i < ui; ++i)
         if (!mbar_wait(&q_full[i & 1], (i >> 1) & 1)) pflag(p, GQAW_DEV_TIMEOUT);
@@ -238,11 +228,11 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
     // ------------------------------------------------------------ S^T = K Q^T
     if (lane == 0) {
       constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kKeys, NPAD, 0, 0);
-      PWalk<kKeys> w(p, sched);
+      PWalk<kKeys> w(shp, sched);
       PUnit u;
       int kc = 0, ui = 0;
       bool fine = true;
-      while (fine && !*abort_flag && w.next(p, u)) {
+      while (fine && !*abort_flag && w.next(shp, u)) {
         fine = mbar_wait(&q_full[ui & 1], (ui >> 1) & 1);
         const uint64_t qd = tc::smem_desc_sw128(qbuf(ui), 16, 1024);
         for (int k = u.k0; k < u.k1 && fine; ++k, ++kc) {
@@ -271,11 +261,11 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
     // ------------------------------------------------------------ O^T += V^T P^T
     if (lane == 0) {
       constexpr uint32_t kIdesc = tc::idesc_bf16_f32(128, NPAD, 1, 0);
-      PWalk<kKeys> w(p, sched);
+      PWalk<kKeys> w(shp, sched);
       PUnit u;
       int kc = 0, ui = 0;
       bool fine = true;
-      while (fine && !*abort_flag && w.next(p, u)) {
+      while (fine && !*abort_flag && w.next(shp, u)) {
         for (int k = u.k0; k < u.k1 && fine; ++k, ++kc) {
           fine = mbar_wait(&full[(2 * kc + 1) % kSlots], phase(2 * kc + 1)) && mbar_wait(&p_full[kc & 1], (kc >> 1) & 1) &&
                  (k > u.k0 || ui == 0 || mbar_wait(o_free, (ui - 1) & 1));
@@ -311,11 +301,11 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
     const int wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-    PWalk<kKeys> w(p, sched);
+    PWalk<kKeys> w(shp, sched);
     PUnit u;
     int kc = 0;
     bool stop = false;
-    while (!stop && w.next(p, u)) {
+    while (!stop && w.next(shp, u)) {
       const int NV = u.ntok * g;
       const long long jlo = p.W > 0 && u.qpos - p.W + 1 > 0 ? u.qpos - p.W + 1 : 0, jhi = u.qpos + u.ntok;
       float m_ref[NC], lsum[NC], ext[DM][NC];
@@ -327,13 +317,20 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
         for (int m = 0; m < DM; ++m) ext[m][i] = 0.f;
       }
       bool any_ext = false;
+      // tiles [ka, kb) hold only keys that every token attends
+      const int ka = (int)(((p.W > 0 ? max(0LL, jhi - p.W) : 0LL) + kKeys - 1) / kKeys) - u.kt;
+      const int kb = (int)((u.qpos + 1) / kKeys) - u.kt;
       for (int k = u.k0; k < u.k1; ++k, ++kc) {
+        const bool inner = k >= ka && k < kb;
         const long long j0 = (long long)(u.kt + k) * kKeys, j = j0 + t;
         // tokens [ta, tz) of the unit attend key j; their rows are [ta g, tz g)
-        int ta = 0, tz = 0;
-        if (j >= jlo && j < jhi) {
-          ta = j > u.qpos ? (int)(j - u.qpos) : 0;
-          tz = p.W > 0 ? (int)min((long long)u.ntok, j - u.qpos + p.W) : u.ntok;
+        int ta = 0, tz = u.ntok;
+        if (!inner) {
+          tz = 0;
+          if (j >= jlo && j < jhi) {
+            ta = j > u.qpos ? (int)(j - u.qpos) : 0;
+            tz = p.W > 0 ? (int)min((long long)u.ntok, j - u.qpos + p.W) : u.ntok;
+          }
         }
         const int nlo = ta * g - col0, nhi = tz * g - col0;
         bool ok = mbar_wait(&s_full[kc & 1], (kc >> 1) & 1);
@@ -342,7 +339,8 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
         float z[NC];
         tmem_ld<NC>(tmem_s + (kc & 1) * NPAD + col0 + lane_off, z);
         tc::fence_before_sync();
-        mbar_arrive(&s_free[kc & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[kc & 1]);
         bool exceed = false;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -414,11 +412,10 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
           }
         }
         // value rows outside [jlo, jhi) were not loaded, or may hold anything: zero them
-        const int z0 = (int)max(0LL, jlo - j0), z1 = (int)min((long long)kKeys, jhi - j0);
-        const bool ends = z0 > 0 || z1 < kKeys;
-        // some key of the tile is attended by some tokens only
-        const bool part = u.ntok > 1 && (j0 + kKeys - 1 > u.qpos || (p.W > 0 && j0 < jhi - p.W));
-        if (ends || part) {
+        if (!inner) {
+          const int z0 = (int)max(0LL, jlo - j0), z1 = (int)min((long long)kKeys, jhi - j0);
+          // some key of the tile is attended by some tokens only
+          const bool part = u.ntok > 1 && (j0 + kKeys - 1 > u.qpos || (p.W > 0 && j0 < jhi - p.W));
           // With two slots, V(kc - 1) may not have landed yet, and a parity wait cannot tell two
           // phases apart: its product first.  (With more, the slot's last tile is behind the
           // o_done waited for above.)
@@ -479,7 +476,8 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
         }
         tc::fence_proxy_async_smem();
         tc::fence_before_sync();
-        mbar_arrive(&p_full[kc & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[kc & 1]);
       }
       if (stop) break;
 
@@ -500,7 +498,8 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
 #pragma unroll
       for (int m = 0; m < DM; ++m) tmem_ld<NC>(tmem_o + m * NPAD + col0 + lane_off, o[m]);
       tc::fence_before_sync();
-      mbar_arrive(o_free);  // the next unit may overwrite O^T
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);  // the next unit may overwrite O^T
       if (named_barrier_or(kBar, kSoft, !okd)) {
         pflag(p, GQAW_DEV_TIMEOUT);
         *abort_flag = 1;
@@ -597,21 +596,21 @@ __global__ void __launch_bounds__(pdec::threads(CG), 1)
   }
 }
 
-template <int D, int NPAD, int NVT, int CG>
+template <int D, int NVT>
 cudaError_t launch_paged_decode_one(const PagedParams &p, const PagedMaps &maps, int grid, cudaStream_t stream) {
-  constexpr int kMaxDevices = 64, kSmem = pdec::Lay<D, NPAD>::kAlloc;
+  constexpr int kMaxDevices = 64, kSmem = pdec::Lay<D>::kAlloc;
   static std::atomic<bool> ready[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(paged_decode_kernel<D, NPAD, NVT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(paged_decode_kernel<D, NVT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(pdec::threads(CG));
+  cfg.blockDim = dim3(pdec::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -619,20 +618,16 @@ cudaError_t launch_paged_decode_one(const PagedParams &p, const PagedMaps &maps,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, NPAD, NVT, CG>, p, maps);
+  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, NVT>, p, maps);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
-// rows: tokens of a query tile times group, at most 32.  NPAD is 16 up to 16 rows, else 32.
-// Eight softmax warps from the start: more warps to overlap than the rows need; sixteen for
-// 32 rows, where the exponentials are the longer part.
+// rows: tokens of a query tile times group, at most 8.
 template <int D>
 cudaError_t launch_paged_decode_d(const PagedParams &p, const PagedMaps &maps, int rows, int grid, cudaStream_t stream) {
-  if (rows <= 4) return launch_paged_decode_one<D, 16, 4, 2>(p, maps, grid, stream);
-  if (rows <= 8) return launch_paged_decode_one<D, 16, 8, 2>(p, maps, grid, stream);
-  if (rows <= 16) return launch_paged_decode_one<D, 16, 16, 2>(p, maps, grid, stream);
-  return launch_paged_decode_one<D, 32, 32, 4>(p, maps, grid, stream);
+  return rows <= 4 ? launch_paged_decode_one<D, 4>(p, maps, grid, stream)
+                   : launch_paged_decode_one<D, 8>(p, maps, grid, stream);
 }
 
 cudaError_t launch_paged_decode(const PagedParams &p, const PagedMaps &maps, int rows, int grid, cudaStream_t stream) {

@@ -283,12 +283,12 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
                   (128 % a->page_size == 0 || a->page_size % 128 == 0) && a->num_pages > 0 &&
                   std::max(L->sp, std::max(L->sh, L->sr)) * 2 < (1ll << 40) && std::max(L->qs, qrow) * 2 < (1ll << 40);
   size_t part_rows;  // rows of partial results per CTA
-  if (tc && rows <= 32) {
+  if (tc && rows <= 8) {
     L->path = kDecode;
     L->gb = L->group;
     L->hblocks = 1;
     L->tpt = std::max(1, a->max_new_tokens);
-    part_rows = rows <= 16 ? 16 : 32;
+    part_rows = 16;
     // no more CTAs than key tiles there can be
     const long long span = a->local_window_size > 0 ? std::min<long long>(a->max_sequence_length, (long long)a->local_window_size + a->max_new_tokens)
                                                      : a->max_sequence_length;
@@ -303,8 +303,8 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
     L->grid = kSms;
   } else {
     L->path = kRows;
-    L->bm = rows <= 16 ? 16 : D == 256 ? 32 : 64;
-    L->grid = L->bm == 16 ? kSms * 4 : kSms * 2;
+    L->bm = rows <= 16 ? 16 : D == 256 ? 64 : 128;
+    L->grid = L->bm == 16 ? kSms * 4 : kSms;
     L->gb = std::min(L->group, L->bm);
     L->hblocks = (int)ceil_div(L->group, L->gb);
     L->tpt = std::max(1, L->bm / L->gb);

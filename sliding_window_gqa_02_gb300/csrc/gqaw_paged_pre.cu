@@ -176,6 +176,34 @@ __device__ __forceinline__ float tile_p(uint32_t ts, uint32_t tp, int c_lo, int 
   return (l0 + l1) + (l2 + l3);
 }
 
+// Capped logits against a fixed reference of 0: P = 2^(cap tanh(z zs)), |cap| <= 64, of this
+// thread's 64 logits, as bf16 pairs into 32 columns at tp; returns their sum.
+template <bool kMasked>
+__device__ __forceinline__ float tile_p_cap(uint32_t ts, uint32_t tp, int c_lo, int c_hi, float zs, float cap) {
+  // tanh(x) = 1 - 2 / (e^(2x) + 1), which saturates to the right limits and keeps a NaN
+  const float z2 = 2.8853900817779268f * zs, c2 = -2.f * cap;
+  float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c32 = 0; c32 < kHalfKeys / 32; ++c32) {
+    float v[32];
+    tc::tmem_ld32(ts + c32 * 32, v);
+    const uint32_t m = kMasked ? chunk_mask(c32, c_lo, c_hi) : 0xffffffffu;
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(v[c] * z2)));
+      v[c] = fast_exp2(fmaf(c2, r, cap));
+      if (kMasked && !((m >> c) & 1u)) v[c] = 0.f;
+      ls[c & 3] += v[c];
+    }
+#pragma unroll
+    for (int c = 0; c < 16; ++c) pk[c] = tc::pack_bf16x2(v[2 * c], v[2 * c + 1]);
+    tc::tmem_st16_async(tp + c32 * 16, pk);
+  }
+  return (ls[0] + ls[1]) + (ls[2] + ls[3]);
+}
+
 __device__ __forceinline__ bool odd_pair(uint32_t w) {
   return (w & 0x7f800000u) == 0x7f800000u || (w & 0x00007f80u) == 0x00007f80u;
 }
@@ -237,6 +265,7 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int g = p.group;
+  const PShape shp = shape_of(p);
   // Key tiles are numbered across the CTA's units (gk), query tiles too (qi), so every ring
   // and barrier phase runs on from unit to unit.
 
@@ -248,12 +277,12 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
     uint64_t *full = value ? v_full : k_full, *empty = value ? v_free : k_free;
     unsigned char *ring = smem + (value ? L::kV : L::kK);
     const CUtensorMap *map = value ? &maps.v : &maps.k;
-    PWalk<kKeys> w(p, sched);
+    PWalk<kKeys> w(shp, sched);
     PUnit u;
     ptc::Boxes bx;
     int gk = 0, qi = 0;
     bool fine = true;
-    while (fine && w.next(p, u)) {
+    while (fine && w.next(shp, u)) {
       bx.unit(p, u);
       bx.look_up(p, u.kt + u.k0, lane);
       for (int k = u.k0; k < u.k1; ++k, ++gk) {
@@ -332,11 +361,11 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
         tc::mma_commit(&v_free[st]);
         return true;
       };
-      PWalk<kKeys> w(p, sched);
+      PWalk<kKeys> w(shp, sched);
       PUnit u;
       int gk = 0, qi = 0;
       bool fine = true;
-      while (fine && !*abort_flag && w.next(p, u)) {
+      while (fine && !*abort_flag && w.next(shp, u)) {
         const int n = u.k1 - u.k0;
         fine = mbar_wait(q_full, qi & 1) && s_product(gk);
         if (!fine) break;
@@ -377,13 +406,16 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t to = tmem + L::kTmemO + hf * OC + lane_off, tp = tmem + L::kTmemP + hf * 32 + lane_off;
     const bool plain = p.capmul == 0.f;
+    // A cap of at most 64 (log2 units) bounds every logit: P against the reference 0 stays
+    // within 2^64 both ways, so no maximum is taken and the two halves of a row never meet.
+    const bool fixed = p.capmul != 0.f && p.capmul <= 64.f;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-    PWalk<kKeys> w(p, sched);
+    PWalk<kKeys> w(shp, sched);
     PUnit u;
     int gk = 0, odd_par = 0;
     // A warp that gives up a tile (an expired wait, an abort elsewhere) still runs every unit's
     // epilogue: the 8 warps meet at its barriers.
-    while (w.next(p, u)) {
+    while (w.next(shp, u)) {
       const int rows = u.ntok * g, n = u.k1 - u.k0;
       const bool idle = wq * 32 >= rows;      // no row of this warp exists
       const bool row_ok = r < rows;
@@ -397,7 +429,7 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
       // 128 from tile to tile and are kept at -128 once below it
       int lo = (int)min(max(rlo - tile0 - hf * kHalfKeys, -128LL), 1LL << 30);
       int hi = (int)min(max(at + 1 - tile0 - hf * kHalfKeys, -128LL), 1LL << 30);
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = fixed ? 0.f : -INFINITY, l_run = 0.f;
       float pend = 1.f;  // the factor O in tensor memory still owes
       // some key of this CTA's tiles is attended by some of the unit's tokens only
       const bool has_part =
@@ -413,7 +445,13 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
         const bool okw = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&s_full[gt & 1], (gt >> 1) & 1));
         tc::fence_after_sync();
         bool okp = true;
-        if (!idle) {
+        if (idle || (fixed && !okw)) {
+          okp = okw;
+        } else if (fixed) {
+          const bool whole = __all_sync(0xffffffffu, c_lo == 0 && c_hi == kHalfKeys);
+          l_run += whole ? tile_p_cap<false>(ts, tpk, 0, kHalfKeys, p.qscale, p.capmul)
+                         : tile_p_cap<true>(ts, tpk, c_lo, c_hi, p.qscale, p.capmul);
+        } else {
           const bool whole = __all_sync(0xffffffffu, c_lo == 0 && c_hi == kHalfKeys);
           // Fast: a plain, wholly visible tile of rows that have a reference already: P against
           // it in the same pass as the maximum.  Else the maximum first (capped logits are
@@ -482,8 +520,6 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
               pend = alpha;
             }
           }
-        } else {
-          okp = okw;
         }
         if (!okp) {
           if (lane == 0) pflag(p, GQAW_DEV_TIMEOUT);

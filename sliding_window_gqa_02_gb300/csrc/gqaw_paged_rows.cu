@@ -6,15 +6,20 @@
 //     y = x * rsqrt(mean(x^2) + eps) * w,  then pairs (y1, y2) -> (y1 c - y2 s, y2 c + y1 s)
 // with c, s from row `pos` of the tables; everything in fp32, one rounding at the end.
 //
-// Bound: HBM.  Each row is read once and written once; the tables' row is shared by all heads
-// of a token.  So a lane owns 8 consecutive elements of a head (16 or 32 bytes: one or two
-// wide loads), D / 8 lanes make a row, and a warp keeps its token's cos and sin (and the
-// weights) in registers while it goes over kBatch groups of heads whose loads are all issued
-// before the first is used.  The mean is a butterfly over the row's lanes; the partner of a
-// split pair (i, i + rd/2) sits at the same place of another lane when rd/2 is a multiple of
-// 8, one shuffle per element; other widths pick it out of 8 shuffles.  A lane stores only what
-// it loaded, so the norm may work in place.
-// Measured on a GB300 (with what bounds each): see the table of figures at the end.
+// Bound: HBM for many tokens, latency for few.  Each row is read once and written once; the
+// tables' row and the weights are shared by all heads of a token.  So a lane owns 8 consecutive
+// elements of a head (16 or 32 bytes), D / 8 lanes make a row, and what a token's heads share is
+// folded once into two coefficients per element: with p the partner of element i in its pair,
+//     out_i = r (x_i (w_i c_i) + x_p (w_p s_i)),   s_i = -sin for the first of a pair, sin for the
+// second, and r the row's reciprocal root mean square, left for the last multiplication.  Per
+// element that is one product, one multiply-add and one product, on packed pairs of fp32.
+// The mean is a butterfly over the row's lanes.  The partner of a split pair (i, i + rd/2) sits
+// at the same place of another lane when rd/2 is a multiple of 8: its words are exchanged as
+// stored (4 shuffles for 8 bf16); other widths pick it out of the neighbours' elements.
+// A warp goes over BATCH groups of heads whose loads are all issued before the first is used:
+// 8 where there are tokens enough to fill the GPU, 2 where the chain of dependent look-ups
+// (sequence, position, tables) is the time.  A lane stores only what it loaded, so the norm may
+// work in place.
 #include <atomic>
 
 #include "gqaw_paged.cuh"
@@ -24,7 +29,7 @@ namespace gqaw {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;
+constexpr long long kManyWarps = 152 * 16;  // 16 warps a SM
 
 template <typename T> struct Oct;  // 8 elements as stored
 template <> struct Oct<float> {
@@ -41,6 +46,13 @@ template <> struct Oct<float> {
     Elem<float>::unpack(a, f);
     Elem<float>::unpack(b, f + 4);
   }
+  __device__ __forceinline__ Oct from(int src) const {  // the octet of another lane
+    Oct o;
+    o.a = make_uint4(__shfl_sync(~0u, a.x, src), __shfl_sync(~0u, a.y, src), __shfl_sync(~0u, a.z, src), __shfl_sync(~0u, a.w, src));
+    o.b = make_uint4(__shfl_sync(~0u, b.x, src), __shfl_sync(~0u, b.y, src), __shfl_sync(~0u, b.z, src), __shfl_sync(~0u, b.w, src));
+    return o;
+  }
+  __device__ __forceinline__ void clear() { a = b = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void set(const float (&f)[8]) {
     a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
@@ -51,6 +63,12 @@ template <> struct Oct<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16 *s) { a = *reinterpret_cast<const uint4 *>(s); }
   __device__ __forceinline__ void store(__nv_bfloat16 *d) const { *reinterpret_cast<uint4 *>(d) = a; }
   __device__ __forceinline__ void get(float (&f)[8]) const { Elem<__nv_bfloat16>::unpack(a, f); }
+  __device__ __forceinline__ Oct from(int src) const {
+    Oct o;
+    o.a = make_uint4(__shfl_sync(~0u, a.x, src), __shfl_sync(~0u, a.y, src), __shfl_sync(~0u, a.z, src), __shfl_sync(~0u, a.w, src));
+    return o;
+  }
+  __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ static uint32_t pair(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -91,33 +109,92 @@ __device__ __forceinline__ int find_sequence(const PagedParams &p, int n, int la
 
 }  // namespace
 
-template <typename T, int LPR>
+// Packed pairs of fp32: one instruction computes both lanes.
+__device__ __forceinline__ uint64_t pk(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpk(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The coefficients of a lane's 8 elements: x_i takes own[i], its partner takes other[i].
+struct Coef {
+  uint64_t own[4], other[4];
+};
+
+// wt: the weights, or NULL (1); cs, sn: the signed turn; pe: first element of the partner octet
+// (split pairs in whole octets) or -1 (pairs inside the octet, or no turn)
+template <typename T>
+__device__ __forceinline__ Coef make_coef(const T *wt, int e, int pe, const float (&cs)[8], const float (&sn)[8],
+                                          const PagedParams &p, bool turn, int half) {
+  float w[8], wp[8];
+#pragma unroll
+  for (int m = 0; m < 8; ++m) w[m] = wp[m] = 1.f;
+  if (wt) {
+    Oct<T> u;
+    u.load(wt + e);
+    u.get(w);
+    if (turn && p.rot_inter) {
+#pragma unroll
+      for (int m = 0; m < 8; ++m) wp[m] = w[m ^ 1];
+    } else if (turn && pe >= 0) {
+      u.load(wt + pe);
+      u.get(wp);
+    } else if (turn) {
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const int i = e + m, o = i < half ? i + half : i < p.rot_dim ? i - half : i;
+        wp[m] = Elem<T>::load(wt[o]);
+      }
+    }
+  }
+  Coef c;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    c.own[m] = turn ? pk(w[2 * m] * cs[2 * m], w[2 * m + 1] * cs[2 * m + 1]) : pk(w[2 * m], w[2 * m + 1]);
+    c.other[m] = turn ? pk(wp[2 * m] * sn[2 * m], wp[2 * m + 1] * sn[2 * m + 1]) : 0ull;
+  }
+  return c;
+}
+
+template <typename T, int LPR, int BATCH>
 __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const PagedParams p, const RowsJob j) {
   constexpr int RPW = 32 / LPR, D = LPR * 8;
   const int lane = threadIdx.x & 31, lr = lane % LPR, sub = lane / LPR;
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   pdl_wait();
   if (w < j.warps) {
-    const int n = (int)(w / j.chunks), c0 = (int)(w - (long long)n * j.chunks) * (kBatch * RPW);
-    const int heads = j.nq + j.nk + j.nv, e = lr * 8;
+    const int n = (int)(w / j.chunks), c0 = (int)(w - (long long)n * j.chunks) * (BATCH * RPW);
+    const int heads = j.nq + j.nk + j.nv, turned = j.nq + j.nk, e = lr * 8;
 
     // the rows themselves, ahead of the dependent look-ups
-    Oct<T> x[kBatch];
+    Oct<T> x[BATCH];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       const int h = c0 + i * RPW + sub;
       if (h < heads) {
-        const T *src = h < j.nq          ? static_cast<const T *>(p.q) + n * p.qs + h * D
-                       : h < j.nq + j.nk ? static_cast<const T *>(p.k) + n * p.ks + (h - j.nq) * D
-                                         : static_cast<const T *>(p.v) + n * p.vs + (h - j.nq - j.nk) * D;
+        const T *src = h < j.nq    ? static_cast<const T *>(p.q) + n * p.qs + h * D
+                       : h < turned ? static_cast<const T *>(p.k) + n * p.ks + (h - j.nq) * D
+                                    : static_cast<const T *>(p.v) + n * p.vs + (h - turned) * D;
         x[i].load(src + e);
+      } else {
+        x[i].clear();
       }
     }
-    int b = 0;
     long long pos = 0, page_at = -1;
     bool owned = true;
     if (j.paged) {
-      b = find_sequence(p, n, lane);
+      const int b = find_sequence(p, n, lane);
       owned = b >= 0;
       if (owned) {
         const int q0 = p.qstart[b], q1 = p.qstart[b + 1];
@@ -129,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const PagedParams 
           if (lane == 0) pflag(p, GQAW_DEV_BAD_SEQLEN);
         } else {
           pos = TT - (q1 - n);
-          if (c0 + kBatch * RPW > j.nq) {  // this warp has keys or values
+          if (c0 + BATCH * RPW > j.nq) {  // this warp has keys or values
             const int pg = (int)pos / p.page;
             const int id = p.table[(long long)b * p.width + pg];
             if ((unsigned)id < (unsigned)p.npages)
@@ -142,8 +219,10 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const PagedParams 
     }
     if (owned) {
       float cs[8], sn[8];
-      bool turn = p.rot_dim > 0 && c0 < j.nq + j.nk;
+      bool turn = p.rot_dim > 0 && c0 < turned;
       const int half = p.rot_dim / 2;
+      const bool octets = half % 8 == 0;  // split pairs lie in whole octets
+      const bool in = e < p.rot_dim;      // some element of this lane turns
       if (turn) {
         if (p.pos_ids) pos = p.pos_ids[n];
         if (pos < 0 || pos >= p.rot_len) {
@@ -151,123 +230,134 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const PagedParams 
           if (lane == 0) pflag(p, GQAW_DEV_BAD_POSITION);
         }
       }
-      if (turn) {
+#pragma unroll
+      for (int m = 0; m < 8; ++m) cs[m] = 1.f, sn[m] = 0.f;
+      if (turn && in) {
         const T *tc = static_cast<const T *>(p.rcos) + pos * half, *ts = static_cast<const T *>(p.rsin) + pos * half;
         if (p.rot_inter) {  // pair m of this lane: elements e + 2m, e + 2m + 1, column e/2 + m
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const bool in = e + 2 * m < p.rot_dim;
-            cs[2 * m] = cs[2 * m + 1] = in ? Elem<T>::load(tc[e / 2 + m]) : 1.f;
-            sn[2 * m] = sn[2 * m + 1] = in ? Elem<T>::load(ts[e / 2 + m]) : 0.f;
-          }
+          for (int m = 0; m < 4; ++m)
+            if (e + 2 * m < p.rot_dim) {
+              cs[2 * m] = cs[2 * m + 1] = Elem<T>::load(tc[e / 2 + m]);
+              sn[2 * m + 1] = Elem<T>::load(ts[e / 2 + m]);
+              sn[2 * m] = -sn[2 * m + 1];
+            }
         } else if (j.vec) {
-          if (e < p.rot_dim) {
-            const int col = e < half ? e : e - half;
-            Oct<T> u;
-            u.load(tc + col);
-            u.get(cs);
-            u.load(ts + col);
-            u.get(sn);
-          }
+          const int col = e < half ? e : e - half;
+          Oct<T> u;
+          u.load(tc + col);
+          u.get(cs);
+          u.load(ts + col);
+          u.get(sn);
+          if (e < half)
+#pragma unroll
+            for (int m = 0; m < 8; ++m) sn[m] = -sn[m];
         } else {
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
             const int i = e + m, col = i < half ? i : i - half;
-            cs[m] = i < p.rot_dim ? Elem<T>::load(tc[col]) : 1.f;
-            sn[m] = i < p.rot_dim ? Elem<T>::load(ts[col]) : 0.f;
+            if (i < p.rot_dim) {
+              cs[m] = Elem<T>::load(tc[col]);
+              sn[m] = Elem<T>::load(ts[col]);
+              if (i < half) sn[m] = -sn[m];
+            }
           }
         }
       }
+      const int pe = p.rot_inter || !octets ? -1 : e < half ? e + half : in ? e - half : e;
+      const int src = lane - lr + (pe < 0 ? e : pe) / 8;
+      const bool has_q = c0 < j.nq, has_k = c0 + BATCH * RPW > j.nq && c0 < turned;
+      Coef cq, ck;
+      if (has_q) cq = make_coef(static_cast<const T *>(p.qw), e, pe, cs, sn, p, turn, half);
+      if (has_k) ck = make_coef(static_cast<const T *>(p.kw), e, pe, cs, sn, p, turn, half);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = c0 + i * RPW + sub;  // lanes past the heads run along: they take part in the shuffles
-        const bool isq = h < j.nq, isk = !isq && h < j.nq + j.nk, on = h < heads;
-        if (c0 + i * RPW >= heads) break;  // uniform over the warp
-        if (c0 + i * RPW < j.nq + j.nk) {  // some row of the group is a query or a key
+      for (int i = 0; i < BATCH; ++i) {
+        const int h0 = c0 + i * RPW, h = h0 + sub;
+        if (h0 >= heads) break;  // uniform over the warp
+        const bool isq = h < j.nq, isk = !isq && h < turned;
+        const bool norm = isq ? p.qw != nullptr : p.kw != nullptr;
+        // some row of the group changes (uniform); lanes of other rows run along, as they take
+        // part in the shuffles
+        if (h0 < turned && (turn || p.qw || p.kw)) {
           float y[8];
-          if (on) {
-            x[i].get(y);
-          } else {
+          x[i].get(y);
+          uint64_t v[4], o[4];
 #pragma unroll
-            for (int m = 0; m < 8; ++m) y[m] = 0.f;
+          for (int m = 0; m < 4; ++m) v[m] = pk(y[2 * m], y[2 * m + 1]);
+          float r = 1.f;
+          if (p.qw || p.kw) {
+            uint64_t s2 = mul2(v[0], v[0]);
+#pragma unroll
+            for (int m = 1; m < 4; ++m) s2 = fma2(v[m], v[m], s2);
+            float s0, s1;
+            unpk(s2, s0, s1);
+            float ss = s0 + s1;
+#pragma unroll
+            for (int k = LPR / 2; k > 0; k >>= 1) ss += __shfl_xor_sync(~0u, ss, k);
+            if (norm) r = __frsqrt_rn(ss * (1.f / D) + p.eps);
           }
-          const T *wt = static_cast<const T *>(isq ? p.qw : p.kw);
-          float ss = 0.f;
 #pragma unroll
-          for (int m = 0; m < 8; ++m) ss = fmaf(y[m], y[m], ss);
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          if (wt) {
-            const float inv = __frsqrt_rn(ss * (1.f / D) + p.eps);
-            Oct<T> u;
-            float wf[8];
-            u.load(wt + e);
-            u.get(wf);
-#pragma unroll
-            for (int m = 0; m < 8; ++m) y[m] = y[m] * inv * wf[m];
-          }
+          for (int m = 0; m < 4; ++m) o[m] = 0ull;
           if (turn) {
             if (p.rot_inter) {
 #pragma unroll
-              for (int m = 0; m < 8; m += 2) {
-                if (e + m < p.rot_dim) {
-                  const float y1 = y[m], y2 = y[m + 1];
-                  y[m] = fmaf(y1, cs[m], -y2 * sn[m]);
-                  y[m + 1] = fmaf(y2, cs[m], y1 * sn[m]);
-                }
-              }
-            } else if (half % 8 == 0) {
-              const int src = e < half ? lane + half / 8 : e < p.rot_dim ? lane - half / 8 : lane;
+              for (int m = 0; m < 4; ++m)
+                if (e + 2 * m < p.rot_dim) o[m] = pk(y[2 * m + 1], y[2 * m]);
+            } else if (octets) {
+              Oct<T> other = x[i].from(src);
+              if (!in) other.clear();
+              float z[8];
+              other.get(z);
 #pragma unroll
-              for (int m = 0; m < 8; ++m) {
-                const float o = __shfl_sync(0xffffffffu, y[m], src);
-                if (e < half)
-                  y[m] = fmaf(y[m], cs[m], -o * sn[m]);
-                else if (e < p.rot_dim)
-                  y[m] = fmaf(y[m], cs[m], o * sn[m]);
-              }
+              for (int m = 0; m < 4; ++m) o[m] = pk(z[2 * m], z[2 * m + 1]);
             } else {
-              float o[8];
+              float z[8];
 #pragma unroll
               for (int m = 0; m < 8; ++m) {
-                const int el = e + m, other = el < half ? el + half : el < p.rot_dim ? el - half : el;
-                const int src = lane - lr + other / 8;
-                o[m] = 0.f;
+                const int el = e + m, at = el < half ? el + half : el < p.rot_dim ? el - half : el;
+                z[m] = 0.f;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                  const float t = __shfl_sync(0xffffffffu, y[k], src);
-                  if (other % 8 == k) o[m] = t;
+                  const float t = __shfl_sync(~0u, y[k], lane - lr + at / 8);
+                  if (at % 8 == k && el < p.rot_dim) z[m] = t;
                 }
               }
 #pragma unroll
-              for (int m = 0; m < 8; ++m)
-                if (e + m < p.rot_dim) y[m] = fmaf(y[m], cs[m], e + m < half ? -o[m] * sn[m] : o[m] * sn[m]);
+              for (int m = 0; m < 4; ++m) o[m] = pk(z[2 * m], z[2 * m + 1]);
             }
           }
-          if ((isq || isk) && (wt || turn)) x[i].set(y);  // otherwise the bits as they came
+          const uint64_t r2 = pk(r, r);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint64_t own = isq ? cq.own[m] : ck.own[m], oth = isq ? cq.other[m] : ck.other[m];
+            uint64_t t = mul2(v[m], own);
+            if (turn) t = fma2(o[m], oth, t);
+            unpk(mul2(t, r2), y[2 * m], y[2 * m + 1]);
+          }
+          if ((isq || isk) && (norm || turn)) x[i].set(y);  // otherwise the bits as they came
         }
-        if (!on) continue;
+        if (h >= heads) continue;
         if (isq)
           x[i].store(static_cast<T *>(p.qout) + n * p.qos + h * D + e);
         else if (!j.paged)
           x[i].store(static_cast<T *>(p.kout) + n * p.kos + (h - j.nq) * D + e);
         else if (page_at >= 0)
-          x[i].store(static_cast<T *>(isk ? p.kp : p.vp) + page_at + (isk ? h - j.nq : h - j.nq - j.nk) * p.sh + e);
+          x[i].store(static_cast<T *>(isk ? p.kp : p.vp) + page_at + (isk ? h - j.nq : h - turned) * p.sh + e);
       }
     }
   }
   pdl_launch_dependents();
 }
 
-template <typename T>
+template <typename T, int BATCH>
 cudaError_t launch_rows_t(const PagedParams &p, const RowsJob &j, const cudaLaunchConfig_t &cfg) {
   switch (p.D) {
-    case 8: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 1>, p, j);
-    case 16: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 2>, p, j);
-    case 32: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 4>, p, j);
-    case 64: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 8>, p, j);
-    case 128: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 16>, p, j);
-    default: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 32>, p, j);
+    case 8: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 1, BATCH>, p, j);
+    case 16: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 2, BATCH>, p, j);
+    case 32: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 4, BATCH>, p, j);
+    case 64: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 8, BATCH>, p, j);
+    case 128: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 16, BATCH>, p, j);
+    default: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 32, BATCH>, p, j);
   }
 }
 
@@ -281,7 +371,9 @@ cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool
   const int half = p.rot_dim / 2;
   j.vec = half % 8 == 0 && reinterpret_cast<uintptr_t>(p.rcos) % 16 == 0 && reinterpret_cast<uintptr_t>(p.rsin) % 16 == 0;
   const int rpw = 32 / (p.D / 8);
-  j.chunks = (nq + nk + nv + kBatch * rpw - 1) / (kBatch * rpw);
+  auto chunks = [&](int batch) { return (nq + nk + nv + batch * rpw - 1) / (batch * rpw); };
+  const bool many = (long long)p.N * chunks(8) >= kManyWarps;
+  j.chunks = chunks(many ? 8 : 2);
   j.warps = (long long)p.N * j.chunks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((j.warps + kThreads / 32 - 1) / (kThreads / 32)));
@@ -292,7 +384,8 @@ cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = bf16 ? launch_rows_t<__nv_bfloat16>(p, j, cfg) : launch_rows_t<float>(p, j, cfg);
+  const cudaError_t e = bf16 ? (many ? launch_rows_t<__nv_bfloat16, 8>(p, j, cfg) : launch_rows_t<__nv_bfloat16, 2>(p, j, cfg))
+                             : (many ? launch_rows_t<float, 8>(p, j, cfg) : launch_rows_t<float, 2>(p, j, cfg));
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -1,0 +1,233 @@
+// gqaw_paged_sched.cuh -- the schedule of the paged attention kernels: which key tiles of
+// which units each CTA takes.  No CUDA in here, so that the host can compile it too and check it
+// for any batch.
+//
+// Schedule.  A unit is (sequence, head block, query tile): `tpt` consecutive new tokens of
+// one sequence times the query heads of one kv head, against the key tiles (KEYS positions,
+// aligned to KEYS) that any of them attends.  Sequences differ wildly in length, so the unit
+// list is made on the device: every CTA scans the batch's lengths (a few KB from L2, about
+// a microsecond) into a list of the sequences with work and the running count of their key
+// tiles, which closed forms give without visiting the query tiles.  Then either
+//   - split: CTA c takes tiles [c V / G, (c + 1) V / G) of the flattened sequence of all
+//     units' tiles: equal work whatever the lengths.  A unit cut by a boundary is finished by
+//     the last of its contributors, through partial results and a ticket; or
+//   - whole: CTA c takes unit c alone, when the units fit in the grid and the longest costs
+//     no more than an equal share plus the second unit epilogue that a cut brings
+//     (kEpilogueTiles tiles each: a merge is a chain of dependent memory round trips).
+// The ticket of a cut unit is indexed by the CTA it starts in (at most one unit leaves a CTA
+// at its end), so the tickets have a fixed place whatever the shapes.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define GQAW_HD __host__ __device__ inline
+#else
+#define GQAW_HD inline
+#endif
+
+namespace gqaw {
+
+constexpr int kPagedItems = 256;  // sequences of one launch; larger batches take several
+
+// What the schedule needs to know of a call.
+struct PShape {
+  int tpt, W, heads;  // tokens per query tile; window (0: none); kv heads x head blocks
+};
+
+// A sequence with new tokens, as the schedule keeps it in shared memory.
+struct PItem {
+  long long tiles;  // key tiles of all sequences before this one
+  long long units;  // units before it (64 bits: malformed row ranges may repeat rows)
+  int b, T, qs, S;
+};
+
+// Where a CTA starts: found once, by one thread, and copied by every role's walker.
+struct PStart {
+  long long tb, te;  // this CTA's flattened tiles (split), or units (whole)
+  long long pos;     // split: flattened index of the first tile of the unit it starts in
+  int it, hu, r;     // that unit
+  int G;             // CTAs that share the tiles
+  bool whole;
+};
+
+struct PSched {
+  PItem items[kPagedItems];
+  long long V, U;   // key tiles and units in all
+  int n;            // sequences with work
+  int longest;      // key tiles of the longest unit
+  long long wsum[32], wunits[32];
+  int wcnt[32], wmax[32];
+  PStart start;
+};
+
+// sum over i in [0, n) of floor((a i + b) / m); a, b >= 0, m > 0.
+GQAW_HD long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+template <int KEYS>
+struct PTiles {
+  long long P;
+  int S, tpt, W, rt;
+  GQAW_HD PTiles(const PShape &p, int T, int S_)
+      : P((long long)T - S_), S(S_), tpt(p.tpt), W(p.W), rt((S_ + p.tpt - 1) / p.tpt) {}
+  // first and one past the last key tile of query tile r
+  GQAW_HD int lo(int r) const {
+    const long long j = W > 0 ? P + (long long)r * tpt - W + 1 : 0;
+    return (int)((j > 0 ? j : 0) / KEYS);
+  }
+  GQAW_HD int hi(int r) const {
+    const long long s1 = (long long)(r + 1) * tpt < S ? (long long)(r + 1) * tpt : S;
+    return (int)((P + s1 - 1) / KEYS) + 1;
+  }
+  // key tiles of query tiles [0, r)
+  GQAW_HD long long before(int r) const {
+    if (r <= 0) return 0;
+    if (r == 1) return hi(0) - lo(0);
+    const int full = r == rt ? r - 1 : r;  // the last query tile may be short
+    long long s = full + floor_sum(full, KEYS, tpt, P + tpt - 1) + (r == rt ? hi(r - 1) : 0);
+    if (W > 0) {
+      const long long need = (long long)W - 1 - P;
+      const long long i0 = need > 0 ? (need + tpt - 1) / tpt : 0;
+      if (i0 < r) s -= floor_sum(r - i0, KEYS, tpt, P + i0 * tpt - W + 1);
+    }
+    return s;
+  }
+  // most key tiles of any query tile (an upper bound, exact for one)
+  GQAW_HD int most() const {
+    if (rt == 1) return hi(0) - lo(0);
+    const int all = hi(rt - 1), span = W > 0 ? (int)(((long long)W - 2 + tpt) / KEYS) + 2 : all;
+    return all < span ? all : span;
+  }
+};
+
+constexpr int kEpilogueTiles = 6;
+
+template <int KEYS>
+GQAW_HD void sched_start(const PShape &p, PSched *s, int cta, int grid) {
+  PStart w;
+  const long long V = s->V;
+  const int heads = p.heads;
+  // at least a few tiles a CTA: a cut costs more than it saves below that
+  const long long want = s->U > (V + 3) / 4 ? s->U : (V + 3) / 4;
+  w.G = (int)(want < 1 ? 1 : want < grid ? want : grid);
+  w.whole = s->U <= grid && s->longest + kEpilogueTiles <= (V + w.G - 1) / w.G + 2 * kEpilogueTiles;
+  w.it = w.hu = w.r = 0;
+  w.pos = 0;
+  if (w.whole) {
+    w.tb = cta;
+    w.te = cta < s->U ? cta + 1 : cta;
+  } else {
+    w.tb = cta < w.G ? cta * V / w.G : 0;
+    w.te = cta < w.G ? (cta + 1) * V / w.G : 0;
+  }
+  if (w.tb < w.te) {
+    int a = 0, b = s->n - 1;  // the last item that starts at or before tb
+    while (a < b) {
+      const int m = (a + b + 1) / 2;
+      if ((w.whole ? s->items[m].units : s->items[m].tiles) <= w.tb)
+        a = m;
+      else
+        b = m - 1;
+    }
+    w.it = a;
+    const PItem &x = s->items[a];
+    const PTiles<KEYS> t(p, x.T, x.S);
+    if (w.whole) {
+      const int off = (int)(w.tb - x.units);
+      w.hu = off / t.rt;
+      w.r = off - w.hu * t.rt;
+    } else {
+      const long long per = t.before(t.rt), off = w.tb - x.tiles;
+      w.hu = (int)(off / per);
+      const long long rem = off - w.hu * per;
+      int c = 0, d = t.rt - 1;
+      while (c < d) {
+        const int m = (c + d + 1) / 2;
+        if (t.before(m) <= rem)
+          c = m;
+        else
+          d = m - 1;
+      }
+      w.r = c;
+      w.pos = x.tiles + w.hu * per + t.before(c);
+    }
+    if (w.hu >= heads) w.te = w.tb;  // cannot happen: the counts above are of these units
+  }
+  s->start = w;
+}
+
+// The unit a walker stands on, and the part of its key tiles that this CTA does.
+struct PUnit {
+  int b, hu;           // sequence, head unit (kv head * hblocks + block)
+  int row0, ntok;      // first row of query / output, tokens
+  long long qpos;      // position of the first token
+  int kt, nt;          // first key tile, key tiles of the unit
+  int k0, k1;          // this CTA's tiles [k0, k1) of the nt
+  long long g0;        // flattened index of its first tile (split)
+};
+
+// Walks the units of this CTA.
+template <int KEYS>
+struct PWalk {
+  const PSched *s;
+  PStart w;
+  int heads;
+  bool started;
+
+  GQAW_HD PWalk(const PShape &p, const PSched *s_)
+      : s(s_), w(s_->start), heads(p.heads), started(false) {}
+  // the CTA whose range holds flattened tile x
+  GQAW_HD int owner(long long x) const { return (int)(((x + 1) * w.G - 1) / s->V); }
+
+  GQAW_HD bool next(const PShape &p, PUnit &u) {
+    if (w.tb >= w.te) return false;
+    if (started) {
+      if (w.whole || w.pos >= w.te) return false;
+      const int rt = (s->items[w.it].S + p.tpt - 1) / p.tpt;
+      if (++w.r == rt) {
+        w.r = 0;
+        if (++w.hu == heads) {
+          w.hu = 0;
+          if (++w.it >= s->n) return false;
+        }
+      }
+    }
+    started = true;
+    const PItem &x = s->items[w.it];
+    const PTiles<KEYS> t(p, x.T, x.S);
+    u.b = x.b;
+    u.hu = w.hu;
+    u.row0 = x.qs + w.r * p.tpt;
+    u.ntok = x.S - w.r * p.tpt < p.tpt ? x.S - w.r * p.tpt : p.tpt;
+    u.qpos = t.P + (long long)w.r * p.tpt;
+    u.kt = t.lo(w.r);
+    u.nt = t.hi(w.r) - u.kt;
+    u.g0 = w.pos;
+    if (w.whole) {
+      u.k0 = 0;
+      u.k1 = u.nt;
+    } else {
+      u.k0 = (int)(w.tb > w.pos ? w.tb - w.pos : 0);
+      u.k1 = (int)(w.te - w.pos < u.nt ? w.te - w.pos : u.nt);
+      w.pos += u.nt;
+    }
+    return true;
+  }
+};
+
+}  // namespace gqaw

@@ -40,9 +40,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// tanh(x) = 1 - 2 / (e^(2x) + 1), absolute error about 1e-7.
+// tanh(x) = 1 - 2 / (e^(2x) + 1), absolute error about 1e-7; saturates to the right limits and
+// keeps a NaN.
 __device__ __forceinline__ float fast_tanh(float x) {
-  const float e = fast_exp2(2.8853900817779268f * fminf(fmaxf(x, -15.f), 15.f));
+  const float e = fast_exp2(2.8853900817779268f * x);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return fmaf(-2.f, r, 1.f);
@@ -80,15 +81,19 @@ struct Boxes {
     if (want && !ok) pflag(p, GQAW_DEV_BAD_PAGE);
     return __ballot_sync(0xffffffffu, ok);
   }
-  // issues the loads of one operand tile (all lanes; `mask` from valid())
+  // issues the loads of one operand tile (all lanes; `mask` from valid()).  One lane issues
+  // them all: the instruction takes its operands from uniform registers, and lanes that each
+  // issue their own box are serialised at a higher cost.
   template <int HALVES>
   __device__ __forceinline__ void load(const CUtensorMap *map, unsigned char *dst, uint64_t *bar, uint64_t pol,
                                        uint32_t mask, int lane) const {
-    for (int e = lane; e < ((n * HALVES + 31) & ~31); e += 32) {
-      const int i = e % n, hf = e / n;
+    for (int i = 0; i < n; ++i) {
       const int bid = __shfl_sync(0xffffffffu, id, i), brow = __shfl_sync(0xffffffffu, row, i);
-      if (hf < HALVES && ((mask >> i) & 1u))
-        tma_load_4d(dst + hf * kHalf + i * rows * 128, map, hf * 64, brow, kvh, bid, bar, pol);
+      if (lane == 0 && ((mask >> i) & 1u)) {
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf)
+          tma_load_4d(dst + hf * kHalf + i * rows * 128, map, hf * 64, brow, kvh, bid, bar, pol);
+      }
     }
   }
 };

@@ -76,10 +76,12 @@ def test_layouts_and_strides(dtype, lens, D):
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
-@pytest.mark.parametrize("lens", [[(1, 9000), (1, 40), (1, 20000)], [(16, 9000), (300, 6000)]], ids=["decode", "chunks"])
-def test_long_split(dtype, lens):
-    """Few sequences, long axes: units cut over many CTAs and merged."""
-    b = Batch(lens, 4, 1, 128, 64, dtype, seed=5)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[(1, 9000), (1, 40), (1, 20000)], [(8, 9000), (3, 16000)], [(4, 9000), (1, 9999)],
+                                  [(16, 9000), (300, 6000)]], ids=["decode", "verify8", "verify4", "chunks"])
+def test_long_split(dtype, lens, D):
+    """Few sequences, long axes: units cut over many CTAs and merged, rings that go round often."""
+    b = Batch(lens, 4, 1, D, 64, dtype, seed=5)
     b.call(gqaw.gqaw_paged_attend)
     b.check_output()
     again = b.out.clone()
