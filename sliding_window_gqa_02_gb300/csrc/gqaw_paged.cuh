@@ -35,14 +35,16 @@ struct PagedParams {
   long long qos, kos;
 };
 
-__device__ __forceinline__ PShape shape_of(const PagedParams &p) { return PShape{p.tpt, p.W, p.Nkv * p.hblocks}; }
+__device__ __forceinline__ PShape shape_of(const PagedParams &p, int unit_cost) {
+  return PShape{p.tpt, p.W, p.Nkv * p.hblocks, unit_cost};
+}
 
 __device__ __forceinline__ void pflag(const PagedParams &p, uint32_t bits) { atomicOr(p.status, bits); }
 
 // Builds the list and this CTA's start; all `nt` threads of the CTA (a multiple of 32) call
 // it, and it ends with a barrier.  CTA 0 flags the malformed sequences.
 template <int KEYS>
-__device__ inline void sched_build(const PagedParams &p, PSched *s, int nt) {
+__device__ inline void sched_build(const PagedParams &p, const PShape &shp, PSched *s, int nt) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
   const int heads = p.Nkv * p.hblocks;
   long long base = 0, units = 0;
@@ -60,7 +62,7 @@ __device__ inline void sched_build(const PagedParams &p, PSched *s, int nt) {
         if (blockIdx.x == 0) pflag(p, GQAW_DEV_BAD_SEQLEN);
       } else if (S > 0) {
         T = (int)TT;
-        const PTiles<KEYS> t(shape_of(p), T, S);
+        const PTiles<KEYS> t(shp, T, S);
         has = 1;
         n = t.before(t.rt) * heads;
         u = (long long)t.rt * heads;
@@ -100,7 +102,7 @@ __device__ inline void sched_build(const PagedParams &p, PSched *s, int nt) {
     s->n = count;
     s->U = units;
     s->longest = longest;
-    sched_start<KEYS>(shape_of(p), s, blockIdx.x, gridDim.x);
+    sched_start<KEYS>(shp, s, blockIdx.x, gridDim.x);
   }
   __syncthreads();
 }

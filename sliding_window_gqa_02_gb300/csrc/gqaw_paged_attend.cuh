@@ -27,6 +27,7 @@ namespace gqaw {
 
 namespace prow {
 constexpr int kKeys = 32;
+constexpr int kUnitCost = 4;  // see gqaw_paged_sched.cuh
 
 template <typename T, int D, int BM>
 struct Lay {
@@ -110,8 +111,8 @@ __global__ void __launch_bounds__(prow::Lay<T, D, BM>::kThreads) paged_rows_atte
   float *sq = reinterpret_cast<float *>(smem + L::kQ);
   float *sp = reinterpret_cast<float *>(smem + L::kP);
   pdl_wait();
-  sched_build<kKeys>(p, &sched, kThreads);
-  const PShape shp = shape_of(p);
+  const PShape shp = shape_of(p, kUnitCost);
+  sched_build<kKeys>(p, shp, &sched, kThreads);
   PWalk<kKeys> walk(shp, &sched);
   PUnit u;
   while (walk.next(shp, u)) {

@@ -39,6 +39,7 @@ using ptc::kHalf;
 using ptc::kKeys;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr int kBar = 1;           // named barrier of the softmax warps
+constexpr int kUnitCost = 2;      // see gqaw_paged_sched.cuh
 
 constexpr int NPAD = 16;   // rows of the MMA
 constexpr int CG = 2;      // column groups of softmax warps: more warps to overlap than the rows need
@@ -160,13 +161,13 @@ __global__ void __launch_bounds__(pdec::kThreads, 1)
   if (warp == 0) tc::tmem_alloc(tmem_slot, L::kCols);
   tc::fence_proxy_async_smem();
   pdl_wait();
-  sched_build<kKeys>(p, sched, kThreads);
+  const PShape shp = shape_of(p, kUnitCost);
+  sched_build<kKeys>(p, shp, sched, kThreads);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot, tmem_s = tmem, tmem_o = tmem + 2 * NPAD;
   const int g = p.group;
-  const PShape shp = shape_of(p);
   volatile int *abort_flag = s_abort;
 
   // K of tile kc (counted over the CTA's units) is load 2 kc, V load 2 kc + 1; load n sits in

@@ -21,6 +21,8 @@ cudaError_t launch_paged_decode(const PagedParams &p, const PagedMaps &maps, int
 cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, int grid, cudaStream_t stream);
 cudaError_t launch_paged_rows_attend_f32(const PagedParams &p, int bm, int grid, cudaStream_t stream);
 cudaError_t launch_paged_rows_attend_bf16(const PagedParams &p, int bm, int grid, cudaStream_t stream);
+cudaError_t launch_paged_warp_attend_f32(const PagedParams &p, int rows, int sms, cudaStream_t stream);
+cudaError_t launch_paged_warp_attend_bf16(const PagedParams &p, int rows, int sms, cudaStream_t stream);
 }  // namespace gqaw
 
 namespace {
@@ -206,7 +208,7 @@ gqaw_status check_qk_pointers(const gqaw_qk_args *a, const QkPlan &L) {
 
 // ------------------------------------------------------------------------------ paged
 
-enum Path { kRows = 0, kDecode = 1, kPrefill = 2 };
+enum Path { kRows = 0, kDecode = 1, kPrefill = 2, kWarp = 3 };
 
 struct Plan {
   int es, rot_dim, group, path, bm, rows, hblocks, gb, tpt, grid;
@@ -301,6 +303,13 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
     L->tpt = 128 / L->group;
     part_rows = 128;
     L->grid = kSms;
+  } else if (rows <= 8 && D * L->es <= 512) {
+    L->path = kWarp;
+    L->gb = L->group;
+    L->hblocks = 1;
+    L->tpt = std::max(1, a->max_new_tokens);
+    part_rows = 16;
+    L->grid = kSms * 2;  // at most two CTAs a SM
   } else {
     L->path = kRows;
     L->bm = rows <= 16 ? 16 : D == 256 ? 64 : 128;
@@ -462,7 +471,7 @@ gqaw_status run_paged_attend(const gqaw_paged_args *a, const Plan &L, PagedParam
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync (tickets)");
   }
   gqaw::PagedMaps maps;
-  if (L.path != kRows) {
+  if (L.path == kDecode || L.path == kPrefill) {
     const gqaw_status s = make_maps(a, L, p, &maps);
     if (s != GQAW_OK) return s;
   }
@@ -471,10 +480,19 @@ gqaw_status run_paged_attend(const gqaw_paged_args *a, const Plan &L, PagedParam
     p.table = a->page_table + (long long)b0 * a->page_table_width;
     p.qstart = a->query_start + b0;
     p.seqlens = a->seqlens_k + b0;
-    const cudaError_t e = L.path == kDecode    ? gqaw::launch_paged_decode(p, maps, L.rows, L.grid, st)
-                          : L.path == kPrefill ? gqaw::launch_paged_prefill(p, maps, L.grid, st)
-                          : a->dtype == GQAW_F32 ? gqaw::launch_paged_rows_attend_f32(p, L.bm, L.grid, st)
-                                                 : gqaw::launch_paged_rows_attend_bf16(p, L.bm, L.grid, st);
+    const bool f32 = a->dtype == GQAW_F32;
+    cudaError_t e;
+    switch (L.path) {
+      case kDecode: e = gqaw::launch_paged_decode(p, maps, L.rows, L.grid, st); break;
+      case kPrefill: e = gqaw::launch_paged_prefill(p, maps, L.grid, st); break;
+      case kWarp:
+        e = f32 ? gqaw::launch_paged_warp_attend_f32(p, L.rows, kSms, st)
+                : gqaw::launch_paged_warp_attend_bf16(p, L.rows, kSms, st);
+        break;
+      default:
+        e = f32 ? gqaw::launch_paged_rows_attend_f32(p, L.bm, L.grid, st)
+                : gqaw::launch_paged_rows_attend_bf16(p, L.bm, L.grid, st);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel launch");
     gqaw::count_launch();
   }

@@ -48,6 +48,7 @@ constexpr int kHalfKeys = 64;
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10;
 constexpr int kThreads = 352;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kUnitCost = 3;   // see gqaw_paged_sched.cuh
 constexpr float kRescaleLog2 = 8.0f, kDangerLog2 = 16.0f;  // log2 units
 constexpr int kSoftBar = 5;    // named barrier of the 8 softmax warps (1-4: pairs of warps)
 
@@ -68,7 +69,8 @@ struct Lay {
   // [unit & 1][column half][0: after the first token, 1: before the last token's window][4]
   static constexpr int kOdd = kXch + 3 * 2 * kRows * 4;
   static constexpr int kMisc = kOdd + 2 * 16 * 4;  // flags
-  static constexpr int kBars = kMisc + 128;
+  static constexpr int kStage = (kMisc + 128 + 255) / 256 * 256;  // 32 rows x 32 columns of output per softmax warp
+  static constexpr int kBars = kStage + 8 * 2048;
   static constexpr int kAlloc = kBars + 32 * 8 + 1024;  // and room to align the base
   static_assert(kAlloc <= 232448, "shared memory");
 };
@@ -259,13 +261,13 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
   if (warp == 0) tc::tmem_alloc(tmem_slot, kTmemCols);
   tc::fence_proxy_async_smem();
   pdl_wait();
-  sched_build<kKeys>(p, sched, kThreads);
+  const PShape shp = shape_of(p, kUnitCost);
+  sched_build<kKeys>(p, shp, sched, kThreads);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int g = p.group;
-  const PShape shp = shape_of(p);
   // Key tiles are numbered across the CTA's units (gk), query tiles too (qi), so every ring
   // and barrier phase runs on from unit to unit.
 
@@ -590,8 +592,31 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
       auto part_at = [&](int c, int c4) {
         return parts + (((long long)c * 2 + (c == cf ? 1 : 0)) * (D / 4 + 1) + c4) * kRows + r;
       };
-      __nv_bfloat16 *orow = out + (u.row0 + tok) * p.os + (long long)h * D;
       const float inv = cut ? 1.f : sink_reciprocal(l_run, m_run, paged_sink_log2(p, h));
+      // 32 columns of the warp's 32 rows to memory, by way of shared memory: 4 lanes write the 64
+      // bytes of a row (a lane writing its own row would touch 32 lines with every store)
+      const long long orow = (u.row0 + tok) * p.os + (long long)h * D;  // of this lane's row
+      auto put_rows = [&](const float (&v)[32], float f, int d0) {
+        unsigned char *st = smem + L::kStage + warp * 2048;
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint4 x;
+          x.x = tc::pack_bf16x2(v[8 * c] * f, v[8 * c + 1] * f);
+          x.y = tc::pack_bf16x2(v[8 * c + 2] * f, v[8 * c + 3] * f);
+          x.z = tc::pack_bf16x2(v[8 * c + 4] * f, v[8 * c + 5] * f);
+          x.w = tc::pack_bf16x2(v[8 * c + 6] * f, v[8 * c + 7] * f);
+          *reinterpret_cast<uint4 *>(st + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = x;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = i * 8 + (lane >> 2), c = lane & 3;
+          const long long at_ = __shfl_sync(0xffffffffu, orow, row);
+          const uint4 x = *reinterpret_cast<const uint4 *>(st + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+          if (wq * 32 + row < rows) *reinterpret_cast<uint4 *>(out + at_ + d0 + c * 8) = x;
+        }
+      };
 #pragma unroll
       for (int c32 = 0; c32 < OC / 32; ++c32) {
         float v[32];
@@ -602,8 +627,8 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(o_free);
         }
-        if (!row_ok) continue;
         const int d0 = hf * OC + c32 * 32;
+        if (row_ok) {
 #pragma unroll
         for (int c = 0; c < 32; ++c) v[c] *= pend;
         if (any_odd) {  // their weights anew, from the cache, for the rows that attend them
@@ -625,19 +650,13 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
               for (int c = 0; c < 32; ++c) v[c] = fmaf(pr, __bfloat162float(vr[c]), v[c]);
             }
         }
-        if (!cut) {
+        }
+        if (cut) {
+          if (row_ok)
 #pragma unroll
-          for (int c = 0; c < 32; c += 8) {
-            uint4 x;
-            x.x = tc::pack_bf16x2(v[c] * inv, v[c + 1] * inv);
-            x.y = tc::pack_bf16x2(v[c + 2] * inv, v[c + 3] * inv);
-            x.z = tc::pack_bf16x2(v[c + 4] * inv, v[c + 5] * inv);
-            x.w = tc::pack_bf16x2(v[c + 6] * inv, v[c + 7] * inv);
-            *reinterpret_cast<uint4 *>(orow + d0 + c) = x;
-          }
+            for (int c = 0; c < 32; c += 4) *part_at(cta, (d0 + c) / 4) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         } else {
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) *part_at(cta, (d0 + c) / 4) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+          put_rows(v, inv, d0);
         }
       }
       if (has_part) odd_par ^= 1;
@@ -651,23 +670,23 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
         named_barrier(kSoftBar, 256);
         if (*s_last) {
           __threadfence();
-          if (row_ok) {
-            float M = -INFINITY, S = 0.f;
+          float M = -INFINITY, S = 0.f;
 #pragma unroll 4
-            for (int c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(part_at(c, D / 4)).x);
-            const float ref = M == -INFINITY ? 0.f : M;
+          for (int c = cf; c <= cl; ++c) M = fmaxf(M, row_ok ? __ldcg(part_at(c, D / 4)).x : 0.f);
+          const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
-            for (int c = cf; c <= cl; ++c) {
-              const float4 ml = __ldcg(part_at(c, D / 4));
-              S = fmaf(fast_exp2(ml.x - ref), ml.y, S);
-            }
-            const float winv = sink_reciprocal(S, M, paged_sink_log2(p, h));
+          for (int c = cf; c <= cl; ++c) {
+            const float4 ml = row_ok ? __ldcg(part_at(c, D / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            S = fmaf(fast_exp2(ml.x - ref), ml.y, S);
+          }
+          const float winv = sink_reciprocal(S, M, paged_sink_log2(p, h));
 #pragma unroll 1
-            for (int c32 = 0; c32 < OC / 32; ++c32) {
-              const int d0 = hf * OC + c32 * 32;
-              float acc[32];
+          for (int c32 = 0; c32 < OC / 32; ++c32) {
+            const int d0 = hf * OC + c32 * 32;
+            float acc[32];
 #pragma unroll
-              for (int c = 0; c < 32; ++c) acc[c] = 0.f;
+            for (int c = 0; c < 32; ++c) acc[c] = 0.f;
+            if (row_ok)
               for (int c = cf; c <= cl; ++c) {
                 const float f = fast_exp2(__ldcg(part_at(c, D / 4)).x - ref);
                 float4 x[8];
@@ -681,16 +700,7 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
                   acc[4 * i + 3] = fmaf(f, x[i].w, acc[4 * i + 3]);
                 }
               }
-#pragma unroll
-              for (int c = 0; c < 32; c += 8) {
-                uint4 x;
-                x.x = tc::pack_bf16x2(acc[c] * winv, acc[c + 1] * winv);
-                x.y = tc::pack_bf16x2(acc[c + 2] * winv, acc[c + 3] * winv);
-                x.z = tc::pack_bf16x2(acc[c + 4] * winv, acc[c + 5] * winv);
-                x.w = tc::pack_bf16x2(acc[c + 6] * winv, acc[c + 7] * winv);
-                *reinterpret_cast<uint4 *>(orow + d0 + c) = x;
-              }
-            }
+            put_rows(acc, winv, d0);
           }
           if (tid == 0) p.tickets[cf] = 0u;
         }

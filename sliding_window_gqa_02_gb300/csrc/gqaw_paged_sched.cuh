@@ -7,13 +7,17 @@
 // aligned to KEYS) that any of them attends.  Sequences differ wildly in length, so the unit
 // list is made on the device: every CTA scans the batch's lengths (a few KB from L2, about
 // a microsecond) into a list of the sequences with work and the running count of their key
-// tiles, which closed forms give without visiting the query tiles.  Then either
-//   - split: CTA c takes tiles [c V / G, (c + 1) V / G) of the flattened sequence of all
-//     units' tiles: equal work whatever the lengths.  A unit cut by a boundary is finished by
-//     the last of its contributors, through partial results and a ticket; or
-//   - whole: CTA c takes unit c alone, when the units fit in the grid and the longest costs
-//     no more than an equal share plus the second unit epilogue that a cut brings
-//     (kEpilogueTiles tiles each: a merge is a chain of dependent memory round trips).
+// tiles, which closed forms give without visiting the query tiles.  A unit costs its key tiles
+// and, whatever their number, `unit_cost` tiles more (the pipeline drains and fills, rows go
+// out: 4 us of a 128-row unit against 1.1 us a tile; a batch of short prompts counted without it
+// left some CTAs twice the time of others).  Then either
+//   - split: CTA c takes [c V / G, (c + 1) V / G) of the flattened sequence of all units' cost,
+//     each unit's fixed part first: equal work whatever the lengths.  A unit whose tiles a
+//     boundary cuts is finished by the last of its contributors, through partial results and a
+//     ticket; or
+//   - whole: CTA c takes unit c alone, when the units fit in the grid and the longest costs no
+//     more than an equal share plus kMergeTiles, what a cut costs (a merge is a chain of
+//     dependent memory round trips).
 // The ticket of a cut unit is indexed by the CTA it starts in (at most one unit leaves a CTA
 // at its end), so the tickets have a fixed place whatever the shapes.
 #pragma once
@@ -33,19 +37,20 @@ constexpr int kPagedItems = 256;  // sequences of one launch; larger batches tak
 // What the schedule needs to know of a call.
 struct PShape {
   int tpt, W, heads;  // tokens per query tile; window (0: none); kv heads x head blocks
+  int unit_cost;      // key tiles that a unit costs beside its own
 };
 
 // A sequence with new tokens, as the schedule keeps it in shared memory.
 struct PItem {
-  long long tiles;  // key tiles of all sequences before this one
+  long long tiles;  // cost of all sequences before this one, in key tiles
   long long units;  // units before it (64 bits: malformed row ranges may repeat rows)
   int b, T, qs, S;
 };
 
 // Where a CTA starts: found once, by one thread, and copied by every role's walker.
 struct PStart {
-  long long tb, te;  // this CTA's flattened tiles (split), or units (whole)
-  long long pos;     // split: flattened index of the first tile of the unit it starts in
+  long long tb, te;  // this CTA's part of the flattened cost (split), or units (whole)
+  long long pos;     // split: where the unit it starts in begins
   int it, hu, r;     // that unit
   int G;             // CTAs that share the tiles
   bool whole;
@@ -53,9 +58,9 @@ struct PStart {
 
 struct PSched {
   PItem items[kPagedItems];
-  long long V, U;   // key tiles and units in all
+  long long V, U;   // cost and units in all
   int n;            // sequences with work
-  int longest;      // key tiles of the longest unit
+  int longest;      // cost of the longest unit
   long long wsum[32], wunits[32];
   int wcnt[32], wmax[32];
   PStart start;
@@ -82,9 +87,9 @@ GQAW_HD long long floor_sum(long long n, long long m, long long a, long long b) 
 template <int KEYS>
 struct PTiles {
   long long P;
-  int S, tpt, W, rt;
+  int S, tpt, W, rt, c0;
   GQAW_HD PTiles(const PShape &p, int T, int S_)
-      : P((long long)T - S_), S(S_), tpt(p.tpt), W(p.W), rt((S_ + p.tpt - 1) / p.tpt) {}
+      : P((long long)T - S_), S(S_), tpt(p.tpt), W(p.W), rt((S_ + p.tpt - 1) / p.tpt), c0(p.unit_cost) {}
   // first and one past the last key tile of query tile r
   GQAW_HD int lo(int r) const {
     const long long j = W > 0 ? P + (long long)r * tpt - W + 1 : 0;
@@ -94,12 +99,12 @@ struct PTiles {
     const long long s1 = (long long)(r + 1) * tpt < S ? (long long)(r + 1) * tpt : S;
     return (int)((P + s1 - 1) / KEYS) + 1;
   }
-  // key tiles of query tiles [0, r)
+  // cost of query tiles [0, r) for one head
   GQAW_HD long long before(int r) const {
     if (r <= 0) return 0;
-    if (r == 1) return hi(0) - lo(0);
+    if (r == 1) return hi(0) - lo(0) + c0;
     const int full = r == rt ? r - 1 : r;  // the last query tile may be short
-    long long s = full + floor_sum(full, KEYS, tpt, P + tpt - 1) + (r == rt ? hi(r - 1) : 0);
+    long long s = (long long)r * c0 + full + floor_sum(full, KEYS, tpt, P + tpt - 1) + (r == rt ? hi(r - 1) : 0);
     if (W > 0) {
       const long long need = (long long)W - 1 - P;
       const long long i0 = need > 0 ? (need + tpt - 1) / tpt : 0;
@@ -107,15 +112,15 @@ struct PTiles {
     }
     return s;
   }
-  // most key tiles of any query tile (an upper bound, exact for one)
+  // most that any query tile costs (an upper bound, exact for one)
   GQAW_HD int most() const {
-    if (rt == 1) return hi(0) - lo(0);
+    if (rt == 1) return hi(0) - lo(0) + c0;
     const int all = hi(rt - 1), span = W > 0 ? (int)(((long long)W - 2 + tpt) / KEYS) + 2 : all;
-    return all < span ? all : span;
+    return (all < span ? all : span) + c0;
   }
 };
 
-constexpr int kEpilogueTiles = 6;
+constexpr int kMergeTiles = 6;
 
 template <int KEYS>
 GQAW_HD void sched_start(const PShape &p, PSched *s, int cta, int grid) {
@@ -125,7 +130,7 @@ GQAW_HD void sched_start(const PShape &p, PSched *s, int cta, int grid) {
   // at least a few tiles a CTA: a cut costs more than it saves below that
   const long long want = s->U > (V + 3) / 4 ? s->U : (V + 3) / 4;
   w.G = (int)(want < 1 ? 1 : want < grid ? want : grid);
-  w.whole = s->U <= grid && s->longest + kEpilogueTiles <= (V + w.G - 1) / w.G + 2 * kEpilogueTiles;
+  w.whole = s->U <= grid && s->longest <= (V + w.G - 1) / w.G + kMergeTiles;
   w.it = w.hu = w.r = 0;
   w.pos = 0;
   if (w.whole) {
@@ -178,7 +183,7 @@ struct PUnit {
   long long qpos;      // position of the first token
   int kt, nt;          // first key tile, key tiles of the unit
   int k0, k1;          // this CTA's tiles [k0, k1) of the nt
-  long long g0;        // flattened index of its first tile (split)
+  long long g0;        // its first tile in the flattened cost (split)
 };
 
 // Walks the units of this CTA.
@@ -191,42 +196,43 @@ struct PWalk {
 
   GQAW_HD PWalk(const PShape &p, const PSched *s_)
       : s(s_), w(s_->start), heads(p.heads), started(false) {}
-  // the CTA whose range holds flattened tile x
+  // the CTA whose part holds x of the flattened cost
   GQAW_HD int owner(long long x) const { return (int)(((x + 1) * w.G - 1) / s->V); }
 
+  // The next unit with tiles for this CTA (a boundary may fall into a unit's fixed part).
   GQAW_HD bool next(const PShape &p, PUnit &u) {
-    if (w.tb >= w.te) return false;
-    if (started) {
-      if (w.whole || w.pos >= w.te) return false;
-      const int rt = (s->items[w.it].S + p.tpt - 1) / p.tpt;
-      if (++w.r == rt) {
-        w.r = 0;
-        if (++w.hu == heads) {
-          w.hu = 0;
-          if (++w.it >= s->n) return false;
+    for (;;) {
+      if (w.tb >= w.te) return false;
+      if (started) {
+        if (w.whole || w.pos >= w.te) return false;
+        const int rt = (s->items[w.it].S + p.tpt - 1) / p.tpt;
+        if (++w.r == rt) {
+          w.r = 0;
+          if (++w.hu == heads) {
+            w.hu = 0;
+            if (++w.it >= s->n) return false;
+          }
         }
       }
-    }
-    started = true;
-    const PItem &x = s->items[w.it];
-    const PTiles<KEYS> t(p, x.T, x.S);
-    u.b = x.b;
-    u.hu = w.hu;
-    u.row0 = x.qs + w.r * p.tpt;
-    u.ntok = x.S - w.r * p.tpt < p.tpt ? x.S - w.r * p.tpt : p.tpt;
-    u.qpos = t.P + (long long)w.r * p.tpt;
-    u.kt = t.lo(w.r);
-    u.nt = t.hi(w.r) - u.kt;
-    u.g0 = w.pos;
-    if (w.whole) {
+      started = true;
+      const PItem &x = s->items[w.it];
+      const PTiles<KEYS> t(p, x.T, x.S);
+      u.b = x.b;
+      u.hu = w.hu;
+      u.row0 = x.qs + w.r * p.tpt;
+      u.ntok = x.S - w.r * p.tpt < p.tpt ? x.S - w.r * p.tpt : p.tpt;
+      u.qpos = t.P + (long long)w.r * p.tpt;
+      u.kt = t.lo(w.r);
+      u.nt = t.hi(w.r) - u.kt;
       u.k0 = 0;
       u.k1 = u.nt;
-    } else {
-      u.k0 = (int)(w.tb > w.pos ? w.tb - w.pos : 0);
-      u.k1 = (int)(w.te - w.pos < u.nt ? w.te - w.pos : u.nt);
-      w.pos += u.nt;
+      u.g0 = w.pos + p.unit_cost;
+      if (w.whole) return true;
+      if (w.tb > u.g0) u.k0 = (int)(w.tb - u.g0);
+      if (w.te < u.g0 + u.nt) u.k1 = (int)(w.te - u.g0 > 0 ? w.te - u.g0 : 0);
+      w.pos = u.g0 + u.nt;
+      if (u.k0 < u.k1) return true;
     }
-    return true;
   }
 };
 

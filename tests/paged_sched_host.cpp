@@ -10,10 +10,10 @@ extern "C" {
 // lens: (S, T) per sequence.  out: 12 numbers per (CTA, unit): cta, b, hu, row0, ntok, qpos, kt,
 // nt, k0, k1, first owner, last owner.  Returns the count of rows (or -1 if `cap` is too small);
 // totals: V, U, whole.
-long long paged_schedule(const int *lens, int n, int tpt, int window, int heads, int grid, int keys32, long long *out,
+long long paged_schedule(const int *lens, int n, int tpt, int window, int heads, int grid, int keys32, int unit_cost, long long *out,
                          long long cap, long long *totals) {
   using namespace gqaw;
-  const PShape p{tpt, window, heads};
+  const PShape p{tpt, window, heads, unit_cost};
   std::vector<char> mem(sizeof(PSched));
   PSched *s = reinterpret_cast<PSched *>(mem.data());
   long long rows = 0;

@@ -22,11 +22,11 @@ def sched(tmp_path_factory):
     lib = ctypes.CDLL(so)
     lib.paged_schedule.restype = ctypes.c_longlong
 
-    def run(lens, tpt, window, heads, grid, keys):
+    def run(lens, tpt, window, heads, grid, keys, cost):
         flat = np.array([x for st in lens for x in st], np.int32)
         cap = 200000
         out, tot = np.zeros((cap, 12), np.int64), np.zeros(3, np.int64)
-        n = lib.paged_schedule(flat.ctypes.data_as(ctypes.c_void_p), len(lens), tpt, window, heads, grid, int(keys == 32),
+        n = lib.paged_schedule(flat.ctypes.data_as(ctypes.c_void_p), len(lens), tpt, window, heads, grid, int(keys == 32), cost,
                                out.ctypes.data_as(ctypes.c_void_p), ctypes.c_longlong(cap),
                                tot.ctypes.data_as(ctypes.c_void_p))
         assert n >= 0
@@ -35,8 +35,8 @@ def sched(tmp_path_factory):
     return run
 
 
-def check(run, lens, tpt, window, heads, grid, keys):
-    rows, tot = run(lens, tpt, window, heads, grid, keys)
+def check(run, lens, tpt, window, heads, grid, keys, cost):
+    rows, tot = run(lens, tpt, window, heads, grid, keys, cost)
     want = {}
     row = 0
     for b, (S, T) in enumerate(lens):
@@ -48,14 +48,14 @@ def check(run, lens, tpt, window, heads, grid, keys):
             for h in range(heads):
                 want[(b, h, row + s0)] = (s1 - s0, P + s0, lo, hi - lo)
         row += S
-    assert tot[1] == len(want) and tot[0] == sum(w[3] for w in want.values())
+    assert tot[1] == len(want) and tot[0] == sum(w[3] + cost for w in want.values())
     got, load = {}, {}
     for cta, b, hu, row0, ntok, qpos, kt, nt, k0, k1, cf, cl in rows.tolist():
         key = (b, hu, row0)
         assert want[key] == (ntok, qpos, kt, nt), (key, want[key], (ntok, qpos, kt, nt))
         assert 0 <= k0 < k1 <= nt
         got.setdefault(key, []).append((k0, k1, cta, cf, cl))
-        load[cta] = load.get(cta, 0) + k1 - k0
+        load[cta] = load.get(cta, 0) + k1 - k0 + (cost if k0 == 0 else 0)
     assert set(got) == set(want)
     tickets = {}
     slots = set()
@@ -90,7 +90,8 @@ CASES = [
 
 @pytest.mark.parametrize("case", CASES, ids=range(len(CASES)))
 def test_listed(sched, case):
-    check(sched, *case)
+    for cost in (0, 3):
+        check(sched, *case, cost)
 
 
 def test_random(sched):
@@ -105,7 +106,8 @@ def test_random(sched):
             lens.append((min(T, rng.choice([0, 1, rng.randint(0, most)])), T))
         tpt = rng.choice([1, 2, 4, 8, 16, 18, 32, 42, 128])
         window = rng.choice([0, 0, 1, 5, 100, 128, 129, 3000, 4096])
+        cost = rng.choice([0, 2, 3])
         load, tot = check(sched, lens, tpt, window, rng.choice([1, 2, 3, 8]), rng.choice([1, 2, 16, 152, 608]),
-                          rng.choice([32, 128]))
-        if load and not tot[2]:
-            assert max(load.values()) - min(load.values()) <= 1  # equal shares
+                          rng.choice([32, 128]), cost)
+        if load and not tot[2]:  # equal shares, but for a boundary inside a unit's fixed part
+            assert max(load.values()) - min(load.values()) <= 1 + 2 * cost
