@@ -18,7 +18,7 @@ cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool
 bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                      const cuuint32_t *box);
 cudaError_t launch_paged_decode(const PagedParams &p, const PagedMaps &maps, int rows, int grid, cudaStream_t stream);
-cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, int grid, cudaStream_t stream);
+cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, int halves, int grid, cudaStream_t stream);
 cudaError_t launch_paged_rows_attend_f32(const PagedParams &p, int bm, int grid, cudaStream_t stream);
 cudaError_t launch_paged_rows_attend_bf16(const PagedParams &p, int bm, int grid, cudaStream_t stream);
 cudaError_t launch_paged_warp_attend_f32(const PagedParams &p, int rows, int sms, cudaStream_t stream);
@@ -211,7 +211,7 @@ gqaw_status check_qk_pointers(const gqaw_qk_args *a, const QkPlan &L) {
 enum Path { kRows = 0, kDecode = 1, kPrefill = 2, kWarp = 3 };
 
 struct Plan {
-  int es, rot_dim, group, path, bm, rows, hblocks, gb, tpt, grid;
+  int es, rot_dim, group, path, bm, rows, halves, hblocks, gb, tpt, grid;
   long long qs, ks, vs, os, sp, sh, sr;
   size_t off_q, ws_bytes;
 };
@@ -300,8 +300,10 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
     L->path = kPrefill;
     L->gb = L->group;
     L->hblocks = 1;
-    L->tpt = 128 / L->group;
-    part_rows = 128;
+    // two query tiles of 128 rows at once when a sequence may fill more than one
+    L->halves = rows > 128 && D <= 128 ? 2 : 1;
+    L->tpt = L->halves * (128 / L->group);
+    part_rows = 128 * L->halves;
     L->grid = kSms;
   } else if (rows <= 8 && D * L->es <= 512) {
     L->path = kWarp;
@@ -454,7 +456,7 @@ gqaw_status make_maps(const gqaw_paged_args *a, const Plan &L, const PagedParams
   const cuuint64_t D = (cuuint64_t)a->head_size;
   const cuuint64_t qd[3] = {D, (cuuint64_t)a->num_heads, (cuuint64_t)a->total_new_tokens};
   const cuuint64_t qst[2] = {D * 2, (cuuint64_t)p.qs * 2};
-  const cuuint32_t qb[3] = {64, (cuuint32_t)L.group, (cuuint32_t)L.tpt};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)L.group, (cuuint32_t)(L.path == kPrefill ? L.tpt / L.halves : L.tpt)};
   const cuuint64_t cd[4] = {D, (cuuint64_t)a->page_size, (cuuint64_t)a->kv_num_heads, (cuuint64_t)a->num_pages};
   const cuuint64_t cst[3] = {(cuuint64_t)L.sr * 2, (cuuint64_t)L.sh * 2, (cuuint64_t)L.sp * 2};
   const cuuint32_t cb[4] = {64, (cuuint32_t)std::min(a->page_size, 128), 1, 1};
@@ -484,7 +486,7 @@ gqaw_status run_paged_attend(const gqaw_paged_args *a, const Plan &L, PagedParam
     cudaError_t e;
     switch (L.path) {
       case kDecode: e = gqaw::launch_paged_decode(p, maps, L.rows, L.grid, st); break;
-      case kPrefill: e = gqaw::launch_paged_prefill(p, maps, L.grid, st); break;
+      case kPrefill: e = gqaw::launch_paged_prefill(p, maps, L.halves, L.grid, st); break;
       case kWarp:
         e = f32 ? gqaw::launch_paged_warp_attend_f32(p, L.rows, kSms, st)
                 : gqaw::launch_paged_warp_attend_bf16(p, L.rows, kSms, st);
