@@ -648,9 +648,10 @@ void set_error(const char *msg) { t_error = msg; }
 
 // ... and count a kernel launch, and share the record of the workspaces' ticket regions.
 void count_launch() { g_launches.fetch_add(1); }
-bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                     const cuuint32_t *box) {
-  return encode_map(m, base, rank, dims, strides, box);
+bool encode_tensor_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                       const cuuint32_t *box, bool bf16) {
+  return encode_map(m, base, rank, dims, strides, box,
+                    bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
 }
 bool workspace_tickets_need_clear(const void *ws, size_t t0, size_t t1) { return tickets_need_clear(ws, t0, t1); }
 

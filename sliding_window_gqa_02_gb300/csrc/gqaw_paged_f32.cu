@@ -1,0 +1,359 @@
+// gqaw_paged_f32.cu -- paged attention of at most 8 query rows per kv head over an fp32 cache
+// (decode), head sizes 32, 64 and 128, with pages that tile 16 keys in whole 8-row groups.
+//
+// The same work as gqaw_paged_warp.cuh (its comment has the formulas and the reasons: a warp on
+// its own, a reference maximum that rarely moves), which measured 2000 instructions per 32 keys
+// on four warps a SM, many of them address arithmetic of the loads, and ran at a quarter of the
+// memory's rate.  Here the tiles come by tensor TMA through the page table, a few instructions
+// each, and are half as tall, so that twice the warps fit:
+//   - a tile is 16 keys; K and V in blocks of 32 dimensions, rows of 128 bytes in the 128-byte
+//     swizzle, whose exclusive-or of the 16-byte part with the row is what lets neighbouring
+//     lanes read neighbouring keys without a bank conflict;
+//   - z: lane (key, half) has half of the dimensions of one key against all rows; one exchange;
+//   - o: a lane has D / 32 dimensions of all rows, the weights of a key come as one broadcast.
+#include <atomic>
+
+#include "gqaw_paged_attend.cuh"
+#include "gqaw_paged_tc.cuh"
+
+namespace gqaw {
+
+namespace pf32 {
+
+using prow::fma2;
+using prow::pk;
+using prow::unpk;
+constexpr int kKeys = 16;
+constexpr int kUnitCost = 6;  // see gqaw_paged_sched.cuh
+
+template <int D>
+struct Lay {
+  static constexpr int B = D / 32;                     // blocks of 32 dimensions
+  static constexpr int kBlock = kKeys * 128;           // bytes of a block
+  static constexpr int kStage = 2 * B * kBlock;        // K and V
+  static constexpr int W = D == 128 ? 6 : 8, S = D == 32 ? 4 : D == 64 ? 3 : 2;
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kQ = W * S * kStage;            // [8][D] fp32, scaled
+  static constexpr int kP = kQ + 8 * D * 4;            // [W][16 keys][8 rows]
+  static constexpr int kBars = kP + W * kKeys * 8 * 4;
+  static constexpr int kTotal = kBars + W * S * 8 + 1024;  // and room to align the base
+  static_assert(8 * (D + 2) * 4 <= S * kStage, "a warp's state fits in its ring");
+  static_assert(kTotal + 12 * 1024 <= 232448, "shared memory");
+};
+
+}  // namespace pf32
+
+// RM: 4 or 8 rows.
+template <int D, int RM>
+__global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
+    paged_f32_decode_kernel(const PagedParams p, const __grid_constant__ PagedMaps maps) {
+  using namespace pf32;
+  using L = Lay<D>;
+  constexpr int W = L::W, S = L::S, VW = D / 32;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ PSched sched;
+  __shared__ int s_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float *sq = reinterpret_cast<float *>(smem + L::kQ);
+  float *sp = reinterpret_cast<float *>(smem + L::kP) + warp * kKeys * 8;
+  unsigned char *ring = smem + warp * S * L::kStage;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars) + warp * S;  // this warp's stages
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(&full[i], 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
+  pdl_wait();
+  const PShape shp = shape_of(p, kUnitCost);
+  sched_build<kKeys>(p, shp, &sched, L::kThreads);
+  PWalk<kKeys> walk(shp, &sched);
+  PUnit u;
+  const uint64_t pol = policy_evict_first();
+  const int box = p.page < kKeys ? p.page : kKeys, nbox = kKeys / box;  // rows of a box, boxes of a tile
+  int used = 0;      // tiles this warp has loaded, over its units: stage used % S, phase used / S
+  bool fine = true;  // no wait of this warp has expired
+  while (walk.next(shp, u)) {
+    const int g = p.group, rows = u.ntok * g;
+    const long long jlo = p.W > 0 && u.qpos - p.W + 1 > 0 ? u.qpos - p.W + 1 : 0, jhi = u.qpos + u.ntok;
+    const int n = (u.k1 - u.k0 - warp + W - 1) / W;  // tiles of this warp: k0 + warp, k0 + warp + W, ...
+    const int first = used;                          // the number of the unit's first tile
+    auto key0 = [&](int i) { return (long long)(u.kt + u.k0 + warp + i * W) * kKeys; };
+    // lane b < nbox looks up box b of the warp's tile i: -2 when no row attends any of its keys
+    auto look_up = [&](int i) {
+      const long long j = key0(i) + lane * box;
+      return i < n && lane < nbox && j < jhi && j + box > jlo ? p.table[(long long)u.b * p.width + (int)j / p.page] : -2;
+    };
+    auto load = [&](int i, int id) {
+      if (i >= n) return;  // uniform over the warp
+      const int st = (first + i) % S;
+      const int j = (int)key0(i) + lane * box, row = j - j / p.page * p.page;
+      const bool ok = id != -2 && (unsigned)id < (unsigned)p.npages;
+      if (id != -2 && !ok) pflag(p, GQAW_DEV_BAD_PAGE);
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * 2 * L::B * box * 128));
+      for (int b = 0; b < nbox; ++b) {
+        const int pid = __shfl_sync(0xffffffffu, id, b), prow_ = __shfl_sync(0xffffffffu, row, b);
+        if (lane == 0 && ((mask >> b) & 1u)) {
+          unsigned char *dst = ring + st * L::kStage + b * box * 128;
+#pragma unroll
+          for (int c = 0; c < L::B; ++c) {
+            ptc::tma_load_4d(dst + c * L::kBlock, &maps.k, c * 32, prow_, u.hu, pid, &full[st], pol);
+            ptc::tma_load_4d(dst + (L::B + c) * L::kBlock, &maps.v, c * 32, prow_, u.hu, pid, &full[st], pol);
+          }
+        }
+      }
+    };
+    int id = look_up(0);
+    for (int i = 0; i < S - 1; ++i) {
+      const int next = look_up(i + 1);
+      load(i, id);
+      id = next;
+    }
+    for (int e = tid; e < RM * D; e += L::kThreads) {
+      const int r = e / D, d = e - r * D, tok = r / g, hh = r - tok * g;
+      sq[e] = r < rows ? static_cast<const float *>(p.q)[(u.row0 + tok) * p.qs + (long long)(u.hu * g + hh) * D + d] * p.qscale : 0.f;
+    }
+    __syncthreads();
+
+    float m[RM], l[RM];
+    uint64_t o[RM / 2][VW];  // pairs of rows
+#pragma unroll
+    for (int r = 0; r < RM; ++r) m[r] = -INFINITY, l[r] = 0.f;
+#pragma unroll
+    for (int r = 0; r < RM / 2; ++r)
+#pragma unroll
+      for (int d = 0; d < VW; ++d) o[r][d] = 0ull;
+    const int key = lane & 15, hf = lane >> 4;
+    for (int i = 0; i < n; ++i) {
+      const int next = look_up(i + S);
+      load(i + S - 1, id);
+      id = next;
+      const int st = (first + i) % S;
+      if (!__all_sync(0xffffffffu, fine && mbar_wait(&full[st], ((first + i) / S) & 1))) fine = false;
+      const unsigned char *kb = ring + st * L::kStage, *vb = kb + L::B * L::kBlock;
+      uint64_t z2[RM];
+#pragma unroll
+      for (int r = 0; r < RM; ++r) z2[r] = 0ull;
+#pragma unroll
+      for (int c0 = 0; c0 < D / 8; ++c0) {  // 16-byte parts of this lane's half row
+        const int c = hf * (D / 8) + c0;
+        const ulonglong2 kv = *reinterpret_cast<const ulonglong2 *>(kb + (c >> 3) * L::kBlock + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+          const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(sq + r * D + c * 4);
+          z2[r] = fma2(q.x, kv.x, z2[r]);
+          z2[r] = fma2(q.y, kv.y, z2[r]);
+        }
+      }
+      const long long j0 = key0(i), j = j0 + key;
+      const bool inner = j0 >= jlo && j0 + kKeys - 1 <= u.qpos && (p.W == 0 || j0 >= jhi - p.W);
+      float z[RM];
+      bool up = false;
+#pragma unroll
+      for (int r = 0; r < RM; ++r) {
+        const float2 f = unpk(z2[r]);
+        z[r] = f.x + f.y;
+        z[r] += __shfl_xor_sync(0xffffffffu, z[r], 16);
+        if (p.capmul != 0.f) z[r] = cap_logit(p, z[r]);
+        if (!inner) {
+          const long long at = u.qpos + r / g;
+          if (r >= rows || j > at || j < jlo || (p.W > 0 && j <= at - p.W)) z[r] = -INFINITY;
+        }
+        up |= z[r] > m[r] + 8.f;
+      }
+      if (__any_sync(0xffffffffu, up)) {
+        float f[RM];
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+          float mx = z[r];
+#pragma unroll
+          for (int s = 8; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+          f[r] = 1.f;
+          if (mx > m[r] + 8.f) {
+            f[r] = exp2f(m[r] - mx);  // 0 while nothing was seen
+            m[r] = mx;
+            l[r] *= f[r];
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RM / 2; ++r)
+#pragma unroll
+          for (int d = 0; d < VW; ++d) o[r][d] = fma2(o[r][d], pk(f[2 * r], f[2 * r + 1]), 0ull);
+      }
+#pragma unroll
+      for (int r = 0; r < RM; ++r) {
+        const bool hid = !inner && z[r] == -INFINITY;
+        const float pr = exp2f(z[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+        l[r] += pr;  // both lanes of a key count it: halved at the end
+        z[r] = hid ? -1.f : pr;  // hidden: its value row is not touched
+      }
+      if (hf == 0) {
+#pragma unroll
+        for (int r = 0; r < RM; r += 4)
+          *reinterpret_cast<float4 *>(sp + key * 8 + r) = make_float4(z[r], z[r + 1], z[r + 2], z[r + 3]);
+      }
+      __syncwarp();
+      // this lane's dimensions: VW from lane * VW
+      const int blk = lane * VW / 32, part = lane * VW % 32 / 4, byte = lane * VW % 4 * 4;
+#pragma unroll
+      for (int k = 0; k < kKeys; ++k) {
+        float v[VW];
+        prow::lds<VW>(reinterpret_cast<const float *>(vb + blk * L::kBlock + k * 128 + ((part ^ (k & 7)) << 4) + byte), v);
+        uint64_t w[RM / 2];
+#pragma unroll
+        for (int r = 0; r < RM / 2; r += 2) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(sp + k * 8 + 2 * r);
+          w[r] = x.x, w[r + 1] = x.y;
+        }
+        if (inner) {
+#pragma unroll
+          for (int r = 0; r < RM / 2; ++r)
+#pragma unroll
+            for (int d = 0; d < VW; ++d) o[r][d] = fma2(w[r], pk(v[d], v[d]), o[r][d]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < RM / 2; ++r) {
+            const float2 x = unpk(w[r]);
+#pragma unroll
+            for (int d = 0; d < VW; ++d) {
+              float2 a = unpk(o[r][d]);
+              if (x.x != -1.f) a.x = fmaf(x.x, v[d], a.x);
+              if (x.y != -1.f) a.y = fmaf(x.y, v[d], a.y);
+              o[r][d] = pk(a.x, a.y);
+            }
+          }
+        }
+      }
+      __syncwarp();  // the stage and sp are free
+    }
+    used = first + (n > 0 ? n : 0);
+
+    // ---- the warp's state into its ring: [RM][D + 2]
+    constexpr int PS = D + 2;
+    float *mine = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int r = 0; r < RM; ++r) {
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], s);
+      if (lane == 0) {
+        mine[r * PS + D] = m[r];
+        mine[r * PS + D + 1] = 0.5f * l[r];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RM / 2; ++r)
+#pragma unroll
+      for (int d = 0; d < VW; ++d) {
+        const float2 a = unpk(o[r][d]);
+        mine[2 * r * PS + lane * VW + d] = a.x;
+        mine[(2 * r + 1) * PS + lane * VW + d] = a.y;
+      }
+    __syncthreads();
+    // ---- the warps' states joined
+    const bool cut = u.k0 > 0 || u.k1 < u.nt;
+    const int cta = blockIdx.x, cf = cut ? walk.owner(u.g0) : cta, cl = cut ? walk.owner(u.g0 + u.nt - 1) : cta;
+    float *out = static_cast<float *>(p.out);
+    float *part = p.partials + ((long long)cta * 2 + (cta == cf ? 1 : 0)) * 16 * PS;
+    for (int e = tid; e < rows * D; e += L::kThreads) {
+      const int r = e / D, d = e - r * D, tok = r / g, h = u.hu * g + r - tok * g;
+      float M = -INFINITY, A = 0.f, Z = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) M = fmaxf(M, reinterpret_cast<const float *>(smem + w * S * L::kStage)[r * PS + D]);
+      const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float *x = reinterpret_cast<const float *>(smem + w * S * L::kStage) + r * PS;
+        const float f = exp2f(x[D] - ref);
+        Z = fmaf(f, x[D + 1], Z);
+        A = fmaf(f, x[d], A);
+      }
+      if (cut) {
+        part[r * PS + d] = A;
+        if (d == 0) {
+          part[r * PS + D] = M;
+          part[r * PS + D + 1] = Z;
+        }
+      } else {
+        out[(u.row0 + tok) * p.os + (long long)h * D + d] = A * sink_reciprocal(Z, M, paged_sink_log2(p, h));
+      }
+    }
+    if (cut) {
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        s_last = atomicAdd(&p.tickets[cf], 1u) == (unsigned)(cl - cf);
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int e = tid; e < rows * D; e += L::kThreads) {
+          const int r = e / D, d = e - r * D, tok = r / g, h = u.hu * g + r - tok * g;
+          float M = -INFINITY, A = 0.f, Z = 0.f;
+#pragma unroll 4
+          for (int c = cf; c <= cl; ++c)
+            M = fmaxf(M, __ldcg(p.partials + ((long long)c * 2 + (c == cf)) * 16 * PS + r * PS + D));
+          const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+          for (int c = cf; c <= cl; ++c) {
+            const float *x = p.partials + ((long long)c * 2 + (c == cf)) * 16 * PS + r * PS;
+            const float f = exp2f(__ldcg(x + D) - ref);
+            Z = fmaf(f, __ldcg(x + D + 1), Z);
+            A = fmaf(f, __ldcg(x + d), A);
+          }
+          out[(u.row0 + tok) * p.os + (long long)h * D + d] = A * sink_reciprocal(Z, M, paged_sink_log2(p, h));
+        }
+        if (tid == 0) p.tickets[cf] = 0u;
+      }
+    }
+    // the state was written by ordinary stores where the next unit's tiles land by TMA
+    tc::fence_proxy_async_smem();
+    __syncthreads();  // sq and the rings are reused by the next unit
+  }
+  // every load that was issued has been waited for, unless a wait expired
+  if (!fine) {
+    if (lane == 0) {
+      pflag(p, GQAW_DEV_TIMEOUT);
+      for (int i = used > S ? used - S : 0; i < used; ++i) mbar_wait(&full[i % S], (i / S) & 1);
+    }
+  }
+  pdl_launch_dependents();
+}
+
+template <int D, int RM>
+cudaError_t launch_paged_f32_one(const PagedParams &p, const PagedMaps &maps, int sms, cudaStream_t stream) {
+  using L = pf32::Lay<D>;
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> ready[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(paged_f32_decode_kernel<D, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kTotal;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait()
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, paged_f32_decode_kernel<D, RM>, p, maps);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_f32_decode(const PagedParams &p, const PagedMaps &maps, int rows, int sms, cudaStream_t stream) {
+  switch (p.D) {
+    case 32: return rows <= 4 ? launch_paged_f32_one<32, 4>(p, maps, sms, stream) : launch_paged_f32_one<32, 8>(p, maps, sms, stream);
+    case 64: return rows <= 4 ? launch_paged_f32_one<64, 4>(p, maps, sms, stream) : launch_paged_f32_one<64, 8>(p, maps, sms, stream);
+    default: return rows <= 4 ? launch_paged_f32_one<128, 4>(p, maps, sms, stream) : launch_paged_f32_one<128, 8>(p, maps, sms, stream);
+  }
+}
+
+}  // namespace gqaw

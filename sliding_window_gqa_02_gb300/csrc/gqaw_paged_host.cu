@@ -15,8 +15,9 @@ void set_error(const char *msg);
 void count_launch();
 bool workspace_tickets_need_clear(const void *ws, size_t t0, size_t t1);
 cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool paged, bool bf16, cudaStream_t stream);
-bool encode_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                     const cuuint32_t *box);
+bool encode_tensor_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                       const cuuint32_t *box, bool bf16);
+cudaError_t launch_paged_f32_decode(const PagedParams &p, const PagedMaps &maps, int rows, int sms, cudaStream_t stream);
 cudaError_t launch_paged_decode(const PagedParams &p, const PagedMaps &maps, int rows, int grid, cudaStream_t stream);
 cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, int halves, int grid, cudaStream_t stream);
 cudaError_t launch_paged_rows_attend_f32(const PagedParams &p, int bm, int grid, cudaStream_t stream);
@@ -208,7 +209,7 @@ gqaw_status check_qk_pointers(const gqaw_qk_args *a, const QkPlan &L) {
 
 // ------------------------------------------------------------------------------ paged
 
-enum Path { kRows = 0, kDecode = 1, kPrefill = 2, kWarp = 3 };
+enum Path { kRows = 0, kDecode = 1, kPrefill = 2, kWarp = 3, kF32 = 4 };
 
 struct Plan {
   int es, rot_dim, group, path, bm, rows, halves, hblocks, gb, tpt, grid;
@@ -281,9 +282,11 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
   const long long rows = (long long)std::max(1, a->max_new_tokens) * L->group;
   // The tensor cores take bf16 with head sizes from 64 on, and pages that tile 128 keys in
   // whole 8-row groups of the swizzled layout.
-  const bool tc = a->dtype == GQAW_BF16 && D >= 64 && a->page_size % 8 == 0 &&
-                  (128 % a->page_size == 0 || a->page_size % 128 == 0) && a->num_pages > 0 &&
-                  std::max(L->sp, std::max(L->sh, L->sr)) * 2 < (1ll << 40) && std::max(L->qs, qrow) * 2 < (1ll << 40);
+  auto tiled = [&](int keys) {  // may a tile of `keys` keys come by tensor TMA?
+    return a->page_size % 8 == 0 && (keys % a->page_size == 0 || a->page_size % keys == 0) && a->num_pages > 0 &&
+           std::max(L->sp, std::max(L->sh, L->sr)) * L->es < (1ll << 40) && std::max(L->qs, qrow) * L->es < (1ll << 40);
+  };
+  const bool tc = a->dtype == GQAW_BF16 && D >= 64 && tiled(128);
   size_t part_rows;  // rows of partial results per CTA
   if (tc && rows <= 8) {
     L->path = kDecode;
@@ -306,7 +309,7 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
     part_rows = 128 * L->halves;
     L->grid = kSms;
   } else if (rows <= 8 && D * L->es <= 512) {
-    L->path = kWarp;
+    L->path = a->dtype == GQAW_F32 && D >= 32 && tiled(16) ? kF32 : kWarp;
     L->gb = L->group;
     L->hblocks = 1;
     L->tpt = std::max(1, a->max_new_tokens);
@@ -452,18 +455,27 @@ gqaw_status run_rows(const PagedParams &p, int nq, int nk, int nv, bool paged, b
   return GQAW_OK;
 }
 
+// Tensor maps: 128-byte rows of the swizzle (64 bf16 or 32 fp32 dimensions), boxes of whole
+// pages or of a tile's rows.
 gqaw_status make_maps(const gqaw_paged_args *a, const Plan &L, const PagedParams &p, gqaw::PagedMaps *m) {
-  const cuuint64_t D = (cuuint64_t)a->head_size;
-  const cuuint64_t qd[3] = {D, (cuuint64_t)a->num_heads, (cuuint64_t)a->total_new_tokens};
-  const cuuint64_t qst[2] = {D * 2, (cuuint64_t)p.qs * 2};
-  const cuuint32_t qb[3] = {64, (cuuint32_t)L.group, (cuuint32_t)(L.path == kPrefill ? L.tpt / L.halves : L.tpt)};
+  const bool bf16 = a->dtype == GQAW_BF16;
+  const cuuint64_t D = (cuuint64_t)a->head_size, es = (cuuint64_t)L.es;
+  const cuuint32_t inner = (cuuint32_t)(128 / L.es);
+  const int keys = L.path == kF32 ? 16 : 128;
   const cuuint64_t cd[4] = {D, (cuuint64_t)a->page_size, (cuuint64_t)a->kv_num_heads, (cuuint64_t)a->num_pages};
-  const cuuint64_t cst[3] = {(cuuint64_t)L.sr * 2, (cuuint64_t)L.sh * 2, (cuuint64_t)L.sp * 2};
-  const cuuint32_t cb[4] = {64, (cuuint32_t)std::min(a->page_size, 128), 1, 1};
-  if (!gqaw::encode_bf16_map(&m->q, p.q, 3, qd, qst, qb) || !gqaw::encode_bf16_map(&m->k, a->key_pages, 4, cd, cst, cb) ||
-      !gqaw::encode_bf16_map(&m->v, a->value_pages, 4, cd, cst, cb))
-    return fail(GQAW_ECUDA, "cuTensorMapEncodeTiled failed for the paged attention");
-  return GQAW_OK;
+  const cuuint64_t cst[3] = {(cuuint64_t)L.sr * es, (cuuint64_t)L.sh * es, (cuuint64_t)L.sp * es};
+  const cuuint32_t cb[4] = {inner, (cuuint32_t)std::min(a->page_size, keys), 1, 1};
+  bool ok = gqaw::encode_tensor_map(&m->k, a->key_pages, 4, cd, cst, cb, bf16) &&
+            gqaw::encode_tensor_map(&m->v, a->value_pages, 4, cd, cst, cb, bf16);
+  if (L.path == kF32) {
+    m->q = m->k;  // not used: queries come by ordinary loads
+  } else {
+    const cuuint64_t qd[3] = {D, (cuuint64_t)a->num_heads, (cuuint64_t)a->total_new_tokens};
+    const cuuint64_t qst[2] = {D * es, (cuuint64_t)p.qs * es};
+    const cuuint32_t qb[3] = {inner, (cuuint32_t)L.group, (cuuint32_t)(L.path == kPrefill ? L.tpt / L.halves : L.tpt)};
+    ok = ok && gqaw::encode_tensor_map(&m->q, p.q, 3, qd, qst, qb, bf16);
+  }
+  return ok ? GQAW_OK : fail(GQAW_ECUDA, "cuTensorMapEncodeTiled failed for the paged attention");
 }
 
 // The attention, a launch for every kPagedItems sequences.
@@ -473,7 +485,7 @@ gqaw_status run_paged_attend(const gqaw_paged_args *a, const Plan &L, PagedParam
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync (tickets)");
   }
   gqaw::PagedMaps maps;
-  if (L.path == kDecode || L.path == kPrefill) {
+  if (L.path == kDecode || L.path == kPrefill || L.path == kF32) {
     const gqaw_status s = make_maps(a, L, p, &maps);
     if (s != GQAW_OK) return s;
   }
@@ -487,6 +499,7 @@ gqaw_status run_paged_attend(const gqaw_paged_args *a, const Plan &L, PagedParam
     switch (L.path) {
       case kDecode: e = gqaw::launch_paged_decode(p, maps, L.rows, L.grid, st); break;
       case kPrefill: e = gqaw::launch_paged_prefill(p, maps, L.halves, L.grid, st); break;
+      case kF32: e = gqaw::launch_paged_f32_decode(p, maps, L.rows, kSms, st); break;
       case kWarp:
         e = f32 ? gqaw::launch_paged_warp_attend_f32(p, L.rows, kSms, st)
                 : gqaw::launch_paged_warp_attend_bf16(p, L.rows, kSms, st);

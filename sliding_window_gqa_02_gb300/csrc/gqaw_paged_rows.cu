@@ -16,8 +16,8 @@
 // The mean is a butterfly over the row's lanes.  The partner of a split pair (i, i + rd/2) sits
 // at the same place of another lane when rd/2 is a multiple of 8: its words are exchanged as
 // stored (4 shuffles for 8 bf16); other widths pick it out of the neighbours' elements.
-// A warp goes over BATCH groups of heads whose loads are all issued before the first is used:
-// 8 where there are tokens enough to fill the GPU, 2 where the chain of dependent look-ups
+// A warp goes over BATCH groups of heads of one tensor, whose loads are all issued before the
+// first is used: 128 bytes a lane where there are tokens enough to fill the GPU, 2 groups where the chain of dependent look-ups
 // (sequence, position, tables) is the time.  A lane stores only what it loaded, so the norm may
 // work in place.
 #include <atomic>
@@ -80,14 +80,16 @@ template <> struct Oct<__nv_bfloat16> {
 };
 
 // What one launch does with a token's heads: nq query heads (to qout), nk key heads (to kout,
-// or the pages), nv value heads (to the pages).
+// or the pages), nv value heads (to the pages); cq, ck, cv warps a token for each.
 struct RowsJob {
-  int nq, nk, nv;
+  int nq, nk, nv, cq, ck, cv;
   bool paged;    // rows belong to sequences; keys go to the pages
   bool vec;      // the tables' rows split into whole vectors for a lane
-  int chunks;    // warps per token
   long long warps;
 };
+
+// How a row's pairs lie for its lanes.
+enum Turn { kNoTurn = 0, kOctets = 1, kInside = 2, kAnywhere = 3 };
 
 // The sequence that row n belongs to: the last b with query_start[b] <= n, searched 32 ways
 // at a time by the warp; -1 when there is none.
@@ -132,39 +134,73 @@ struct Coef {
   uint64_t own[4], other[4];
 };
 
-// wt: the weights, or NULL (1); cs, sn: the signed turn; pe: first element of the partner octet
-// (split pairs in whole octets) or -1 (pairs inside the octet, or no turn)
-template <typename T>
-__device__ __forceinline__ Coef make_coef(const T *wt, int e, int pe, const float (&cs)[8], const float (&sn)[8],
-                                          const PagedParams &p, bool turn, int half) {
-  float w[8], wp[8];
+// BATCH groups of RPW heads of one tensor, in `x`: norm (wt), turn, store.  Heads [h, nh), D
+// elements (in) and `step` elements (out) apart.
+template <int MODE, typename T, int LPR, int BATCH>
+__device__ __forceinline__ void rows_out(const PagedParams &p, Oct<T> (&x)[BATCH], const Coef &c, bool norm, T *dst,
+                                         long long step, int h, int nh, int e, int src) {
+  constexpr int RPW = 32 / LPR, D = LPR * 8;
+  const int lane = threadIdx.x & 31, lr = lane % LPR, half = p.rot_dim / 2;
+  const int h0 = h - lane / LPR;  // the warp's first head
 #pragma unroll
-  for (int m = 0; m < 8; ++m) w[m] = wp[m] = 1.f;
-  if (wt) {
-    Oct<T> u;
-    u.load(wt + e);
-    u.get(w);
-    if (turn && p.rot_inter) {
+  for (int i = 0; i < BATCH; ++i) {
+    if (h0 + i * RPW >= nh) break;  // uniform over the warp; lanes past the heads run along
+    if (MODE != kNoTurn || norm) {
+      float y[8];
+      x[i].get(y);
+      uint64_t v[4];
 #pragma unroll
-      for (int m = 0; m < 8; ++m) wp[m] = w[m ^ 1];
-    } else if (turn && pe >= 0) {
-      u.load(wt + pe);
-      u.get(wp);
-    } else if (turn) {
+      for (int m = 0; m < 4; ++m) v[m] = pk(y[2 * m], y[2 * m + 1]);
+      float r = 1.f;
+      if (norm) {
+        uint64_t s2 = mul2(v[0], v[0]);
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const int i = e + m, o = i < half ? i + half : i < p.rot_dim ? i - half : i;
-        wp[m] = Elem<T>::load(wt[o]);
+        for (int m = 1; m < 4; ++m) s2 = fma2(v[m], v[m], s2);
+        float s0, s1;
+        unpk(s2, s0, s1);
+        float ss = s0 + s1;
+#pragma unroll
+        for (int k = LPR / 2; k > 0; k >>= 1) ss += __shfl_xor_sync(~0u, ss, k);
+        r = __frsqrt_rn(ss * (1.f / D) + p.eps);
       }
-    }
-  }
-  Coef c;
+      uint64_t o[4] = {0ull, 0ull, 0ull, 0ull};
+      if (MODE == kInside) {
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    c.own[m] = turn ? pk(w[2 * m] * cs[2 * m], w[2 * m + 1] * cs[2 * m + 1]) : pk(w[2 * m], w[2 * m + 1]);
-    c.other[m] = turn ? pk(wp[2 * m] * sn[2 * m], wp[2 * m + 1] * sn[2 * m + 1]) : 0ull;
+        for (int m = 0; m < 4; ++m)
+          if (e + 2 * m < p.rot_dim) o[m] = pk(y[2 * m + 1], y[2 * m]);
+      } else if (MODE == kOctets) {
+        Oct<T> other = x[i].from(src);
+        if (e >= p.rot_dim) other.clear();  // what does not turn takes nothing, not 0 times infinity
+        float z[8];
+        other.get(z);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) o[m] = pk(z[2 * m], z[2 * m + 1]);
+      } else if (MODE == kAnywhere) {
+        float z[8];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          const int el = e + m, at = el < half ? el + half : el < p.rot_dim ? el - half : el;
+          z[m] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float t = __shfl_sync(~0u, y[k], lane - lr + at / 8);
+            if (at % 8 == k && el < p.rot_dim) z[m] = t;
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) o[m] = pk(z[2 * m], z[2 * m + 1]);
+      }
+      const uint64_t r2 = pk(r, r);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        uint64_t t = mul2(v[m], c.own[m]);
+        if (MODE != kNoTurn) t = fma2(o[m], c.other[m], t);
+        unpk(mul2(t, r2), y[2 * m], y[2 * m + 1]);
+      }
+      x[i].set(y);
+    }
+    if (h + i * RPW < nh) x[i].store(dst + (long long)i * RPW * step);
   }
-  return c;
 }
 
 template <typename T, int LPR, int BATCH>
@@ -174,22 +210,23 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const PagedParams 
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   pdl_wait();
   if (w < j.warps) {
-    const int n = (int)(w / j.chunks), c0 = (int)(w - (long long)n * j.chunks) * (BATCH * RPW);
-    const int heads = j.nq + j.nk + j.nv, turned = j.nq + j.nk, e = lr * 8;
+    const int chunks = j.cq + j.ck + j.cv, n = (int)(w / chunks);
+    int c = (int)(w - (long long)n * chunks);
+    const int kind = c < j.cq ? 0 : c < j.cq + j.ck ? 1 : 2;  // queries, keys, values
+    c -= kind == 0 ? 0 : kind == 1 ? j.cq : j.cq + j.ck;
+    const int nh = kind == 0 ? j.nq : kind == 1 ? j.nk : j.nv, h = c * (BATCH * RPW) + sub, e = lr * 8;
 
     // the rows themselves, ahead of the dependent look-ups
     Oct<T> x[BATCH];
+    const T *in = (kind == 0   ? static_cast<const T *>(p.q) + n * p.qs
+                   : kind == 1 ? static_cast<const T *>(p.k) + n * p.ks
+                               : static_cast<const T *>(p.v) + n * p.vs) + (long long)h * D + e;
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      const int h = c0 + i * RPW + sub;
-      if (h < heads) {
-        const T *src = h < j.nq    ? static_cast<const T *>(p.q) + n * p.qs + h * D
-                       : h < turned ? static_cast<const T *>(p.k) + n * p.ks + (h - j.nq) * D
-                                    : static_cast<const T *>(p.v) + n * p.vs + (h - turned) * D;
-        x[i].load(src + e);
-      } else {
+      if (h + i * RPW < nh)
+        x[i].load(in + i * RPW * D);
+      else
         x[i].clear();
-      }
     }
     long long pos = 0, page_at = -1;
     bool owned = true;
@@ -206,23 +243,33 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const PagedParams 
           if (lane == 0) pflag(p, GQAW_DEV_BAD_SEQLEN);
         } else {
           pos = TT - (q1 - n);
-          if (c0 + BATCH * RPW > j.nq) {  // this warp has keys or values
+          if (kind > 0) {
             const int pg = (int)pos / p.page;
             const int id = p.table[(long long)b * p.width + pg];
             if ((unsigned)id < (unsigned)p.npages)
               page_at = id * p.sp + (pos - (long long)pg * p.page) * p.sr;
             else if (lane == 0)
               pflag(p, GQAW_DEV_BAD_PAGE);
+            owned = page_at >= 0;
           }
         }
       }
     }
     if (owned) {
-      float cs[8], sn[8];
-      bool turn = p.rot_dim > 0 && c0 < turned;
+      T *dst;
+      long long step = D;
+      if (kind == 0) {
+        dst = static_cast<T *>(p.qout) + n * p.qos;
+      } else if (!j.paged) {
+        dst = static_cast<T *>(p.kout) + n * p.kos;
+      } else {
+        dst = static_cast<T *>(kind == 1 ? p.kp : p.vp) + page_at;
+        step = p.sh;
+      }
+      dst += h * step + e;
+      const T *wt = static_cast<const T *>(kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr);
       const int half = p.rot_dim / 2;
-      const bool octets = half % 8 == 0;  // split pairs lie in whole octets
-      const bool in = e < p.rot_dim;      // some element of this lane turns
+      bool turn = p.rot_dim > 0 && kind < 2;
       if (turn) {
         if (p.pos_ids) pos = p.pos_ids[n];
         if (pos < 0 || pos >= p.rot_len) {
@@ -230,11 +277,13 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const PagedParams 
           if (lane == 0) pflag(p, GQAW_DEV_BAD_POSITION);
         }
       }
+      const int mode = !turn ? kNoTurn : p.rot_inter ? kInside : half % 8 == 0 ? kOctets : kAnywhere;
+      float cs[8], sn[8], wo[8], wp[8];
 #pragma unroll
-      for (int m = 0; m < 8; ++m) cs[m] = 1.f, sn[m] = 0.f;
-      if (turn && in) {
+      for (int m = 0; m < 8; ++m) cs[m] = 1.f, sn[m] = 0.f, wo[m] = wp[m] = 1.f;
+      if (turn && e < p.rot_dim) {
         const T *tc = static_cast<const T *>(p.rcos) + pos * half, *ts = static_cast<const T *>(p.rsin) + pos * half;
-        if (p.rot_inter) {  // pair m of this lane: elements e + 2m, e + 2m + 1, column e/2 + m
+        if (mode == kInside) {  // pair m of this lane: elements e + 2m, e + 2m + 1, column e/2 + m
 #pragma unroll
           for (int m = 0; m < 4; ++m)
             if (e + 2 * m < p.rot_dim) {
@@ -264,85 +313,38 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const PagedParams 
           }
         }
       }
-      const int pe = p.rot_inter || !octets ? -1 : e < half ? e + half : in ? e - half : e;
-      const int src = lane - lr + (pe < 0 ? e : pe) / 8;
-      const bool has_q = c0 < j.nq, has_k = c0 + BATCH * RPW > j.nq && c0 < turned;
-      Coef cq, ck;
-      if (has_q) cq = make_coef(static_cast<const T *>(p.qw), e, pe, cs, sn, p, turn, half);
-      if (has_k) ck = make_coef(static_cast<const T *>(p.kw), e, pe, cs, sn, p, turn, half);
+      // first element of the partner octet, and the lane that holds it
+      const int pe = mode != kOctets || e >= p.rot_dim ? e : e < half ? e + half : e - half, src = lane - lr + pe / 8;
+      if (wt) {
+        Oct<T> u;
+        u.load(wt + e);
+        u.get(wo);
+        if (mode == kInside) {
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const int h0 = c0 + i * RPW, h = h0 + sub;
-        if (h0 >= heads) break;  // uniform over the warp
-        const bool isq = h < j.nq, isk = !isq && h < turned;
-        const bool norm = isq ? p.qw != nullptr : p.kw != nullptr;
-        // some row of the group changes (uniform); lanes of other rows run along, as they take
-        // part in the shuffles
-        if (h0 < turned && (turn || p.qw || p.kw)) {
-          float y[8];
-          x[i].get(y);
-          uint64_t v[4], o[4];
+          for (int m = 0; m < 8; ++m) wp[m] = wo[m ^ 1];
+        } else if (mode == kOctets) {
+          u.load(wt + pe);
+          u.get(wp);
+        } else if (mode == kAnywhere) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) v[m] = pk(y[2 * m], y[2 * m + 1]);
-          float r = 1.f;
-          if (p.qw || p.kw) {
-            uint64_t s2 = mul2(v[0], v[0]);
-#pragma unroll
-            for (int m = 1; m < 4; ++m) s2 = fma2(v[m], v[m], s2);
-            float s0, s1;
-            unpk(s2, s0, s1);
-            float ss = s0 + s1;
-#pragma unroll
-            for (int k = LPR / 2; k > 0; k >>= 1) ss += __shfl_xor_sync(~0u, ss, k);
-            if (norm) r = __frsqrt_rn(ss * (1.f / D) + p.eps);
+          for (int m = 0; m < 8; ++m) {
+            const int i = e + m;
+            wp[m] = Elem<T>::load(wt[i < half ? i + half : i < p.rot_dim ? i - half : i]);
           }
-#pragma unroll
-          for (int m = 0; m < 4; ++m) o[m] = 0ull;
-          if (turn) {
-            if (p.rot_inter) {
-#pragma unroll
-              for (int m = 0; m < 4; ++m)
-                if (e + 2 * m < p.rot_dim) o[m] = pk(y[2 * m + 1], y[2 * m]);
-            } else if (octets) {
-              Oct<T> other = x[i].from(src);
-              if (!in) other.clear();
-              float z[8];
-              other.get(z);
-#pragma unroll
-              for (int m = 0; m < 4; ++m) o[m] = pk(z[2 * m], z[2 * m + 1]);
-            } else {
-              float z[8];
-#pragma unroll
-              for (int m = 0; m < 8; ++m) {
-                const int el = e + m, at = el < half ? el + half : el < p.rot_dim ? el - half : el;
-                z[m] = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float t = __shfl_sync(~0u, y[k], lane - lr + at / 8);
-                  if (at % 8 == k && el < p.rot_dim) z[m] = t;
-                }
-              }
-#pragma unroll
-              for (int m = 0; m < 4; ++m) o[m] = pk(z[2 * m], z[2 * m + 1]);
-            }
-          }
-          const uint64_t r2 = pk(r, r);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const uint64_t own = isq ? cq.own[m] : ck.own[m], oth = isq ? cq.other[m] : ck.other[m];
-            uint64_t t = mul2(v[m], own);
-            if (turn) t = fma2(o[m], oth, t);
-            unpk(mul2(t, r2), y[2 * m], y[2 * m + 1]);
-          }
-          if ((isq || isk) && (norm || turn)) x[i].set(y);  // otherwise the bits as they came
         }
-        if (h >= heads) continue;
-        if (isq)
-          x[i].store(static_cast<T *>(p.qout) + n * p.qos + h * D + e);
-        else if (!j.paged)
-          x[i].store(static_cast<T *>(p.kout) + n * p.kos + (h - j.nq) * D + e);
-        else if (page_at >= 0)
-          x[i].store(static_cast<T *>(isk ? p.kp : p.vp) + page_at + (isk ? h - j.nq : h - turned) * p.sh + e);
+      }
+      Coef c;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        c.own[m] = pk(wo[2 * m] * cs[2 * m], wo[2 * m + 1] * cs[2 * m + 1]);
+        c.other[m] = pk(wp[2 * m] * sn[2 * m], wp[2 * m + 1] * sn[2 * m + 1]);
+      }
+      // one loop for each way, so that the one taken is short
+      switch (mode) {
+        case kNoTurn: rows_out<kNoTurn, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, h, nh, e, src); break;
+        case kOctets: rows_out<kOctets, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, h, nh, e, src); break;
+        case kInside: rows_out<kInside, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, h, nh, e, src); break;
+        default: rows_out<kAnywhere, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, h, nh, e, src);
       }
     }
   }
@@ -371,10 +373,14 @@ cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool
   const int half = p.rot_dim / 2;
   j.vec = half % 8 == 0 && reinterpret_cast<uintptr_t>(p.rcos) % 16 == 0 && reinterpret_cast<uintptr_t>(p.rsin) % 16 == 0;
   const int rpw = 32 / (p.D / 8);
-  auto chunks = [&](int batch) { return (nq + nk + nv + batch * rpw - 1) / (batch * rpw); };
-  const bool many = (long long)p.N * chunks(8) >= kManyWarps;
-  j.chunks = chunks(many ? 8 : 2);
-  j.warps = (long long)p.N * j.chunks;
+  auto chunks = [&](int heads, int batch) { return (heads + batch * rpw - 1) / (batch * rpw); };
+  const int deep = bf16 ? 8 : 4;  // 128 bytes of loads a lane
+  const bool many = (long long)p.N * (chunks(nq, deep) + chunks(nk, deep) + chunks(nv, deep)) >= kManyWarps;
+  const int batch = many ? deep : 2;
+  j.cq = chunks(nq, batch);
+  j.ck = chunks(nk, batch);
+  j.cv = chunks(nv, batch);
+  j.warps = (long long)p.N * (j.cq + j.ck + j.cv);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((j.warps + kThreads / 32 - 1) / (kThreads / 32)));
   cfg.blockDim = dim3(kThreads);
@@ -385,7 +391,7 @@ cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t e = bf16 ? (many ? launch_rows_t<__nv_bfloat16, 8>(p, j, cfg) : launch_rows_t<__nv_bfloat16, 2>(p, j, cfg))
-                             : (many ? launch_rows_t<float, 8>(p, j, cfg) : launch_rows_t<float, 2>(p, j, cfg));
+                             : (many ? launch_rows_t<float, 4>(p, j, cfg) : launch_rows_t<float, 2>(p, j, cfg));
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
