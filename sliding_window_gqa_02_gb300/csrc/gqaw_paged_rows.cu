@@ -204,7 +204,7 @@ __device__ __forceinline__ void rows_out(const PagedParams &p, Oct<T> (&x)[BATCH
 }
 
 template <typename T, int LPR, int BATCH>
-__global__ void __launch_bounds__(kThreads) paged_rows_kernel(const PagedParams p, const RowsJob j) {
+__global__ void __launch_bounds__(kThreads, 3) paged_rows_kernel(const PagedParams p, const RowsJob j) {
   constexpr int RPW = 32 / LPR, D = LPR * 8;
   const int lane = threadIdx.x & 31, lr = lane % LPR, sub = lane / LPR;
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
