@@ -13,6 +13,7 @@ constexpr size_t kPagedPartialOffset = kPagedTicketOffset + kPagedTickets * 4;
 
 struct PagedParams {
   const void *q, *k, *v;
+  const void *qlo;                  // bf16: what rounding left of turned queries, laid out as q; NULL: q is all
   void *out;
   void *kp, *vp;
   long long qs, ks, vs, os;         // elements between tokens

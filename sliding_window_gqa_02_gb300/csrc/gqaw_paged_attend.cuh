@@ -163,8 +163,13 @@ __global__ void __launch_bounds__(prow::Lay<T, D, BM>::kThreads) paged_rows_atte
     // the query rows, scaled
     for (int e = tid; e < BM * D; e += kThreads) {
       const int r = e / D, d = e - r * D, tok = r / g, hh = r - tok * g;
-      sq[e] = r < rows ? Elem<T>::load(static_cast<const T *>(p.q)[(u.row0 + tok) * p.qs + (long long)(h0 + hh) * D + d]) * p.qscale
-                       : 0.f;
+      float x = 0.f;
+      if (r < rows) {
+        const long long at = (u.row0 + tok) * p.qs + (long long)(h0 + hh) * D + d;
+        x = Elem<T>::load(static_cast<const T *>(p.q)[at]);
+        if (p.qlo) x += Elem<T>::load(static_cast<const T *>(p.qlo)[at]);
+      }
+      sq[e] = x * p.qscale;
     }
     __syncthreads();
     for (int k = 0; k < kStages - 1; ++k) load(u.k0 + k);

@@ -195,9 +195,11 @@ __global__ void __launch_bounds__(pdec::kThreads, 1)
         if (ui >= 2) alive = __all_sync(0xffffffffu, mbar_wait(&q_free[ui & 1], ((ui - 2) >> 1) & 1));
         if (!alive) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[ui & 1], (uint32_t)(L::HALVES * g * p.tpt * 128));
-          for (int h = 0; h < L::HALVES; ++h)
+          mbar_arrive_expect_tx(&q_full[ui & 1], (uint32_t)((p.qlo ? 2 : 1) * L::HALVES * g * p.tpt * 128));
+          for (int h = 0; h < L::HALVES; ++h) {
             tc::tma_load_3d(qbuf(ui) + h * L::kQHalf, &maps.q, h * 64, u.hu * g, u.row0, &q_full[ui & 1], qpol);
+            if (p.qlo) tc::tma_load_3d(qbuf(ui) + h * L::kQHalf + 1024, &maps.ql, h * 64, u.hu * g, u.row0, &q_full[ui & 1], qpol);
+          }
         }
         ++ui;
       }
@@ -341,6 +343,12 @@ __global__ void __launch_bounds__(pdec::kThreads, 1)
         tc::fence_after_sync();
         float z[NC];
         tmem_ld<NC>(tmem_s + (kc & 1) * NPAD + col0 + lane_off, z);
+        if (p.qlo) {  // an infinite logit stays what it is
+          float rest[NC];
+          tmem_ld<NC>(tmem_s + (kc & 1) * NPAD + 8 + col0 + lane_off, rest);
+#pragma unroll
+          for (int i = 0; i < NC; ++i) z[i] = fabsf(z[i]) < INFINITY ? z[i] + rest[i] : z[i];
+        }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[kc & 1]);
@@ -465,8 +473,9 @@ __global__ void __launch_bounds__(pdec::kThreads, 1)
 #pragma unroll
                       for (int i = 0; i < NC; ++i) {
                         const int n = col0 + i;
-                        const float pr = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(
-                            pbuf(kc) + (jj >> 6) * L::kQHalf + n * 128 + ((((jj & 63) >> 3) ^ (n & 7)) << 4) + (jj & 7) * 2));
+                        const __nv_bfloat16 *pp = reinterpret_cast<const __nv_bfloat16 *>(
+                            pbuf(kc) + (jj >> 6) * L::kQHalf + n * 128 + ((((jj & 63) >> 3) ^ (n & 7)) << 4) + (jj & 7) * 2);
+                        const float pr = __bfloat162float(pp[0]) + __bfloat162float(pp[512]);
                         if (n >= ra && n < rz) ext[m][i] = fmaf(pr, v, ext[m][i]);
                       }
                     }

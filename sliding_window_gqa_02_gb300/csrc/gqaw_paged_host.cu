@@ -214,7 +214,8 @@ enum Path { kRows = 0, kDecode = 1, kPrefill = 2, kWarp = 3, kF32 = 4 };
 struct Plan {
   int es, rot_dim, group, path, bm, rows, halves, hblocks, gb, tpt, grid;
   long long qs, ks, vs, os, sp, sh, sr;
-  size_t off_q, ws_bytes;
+  size_t off_q, off_qlo, ws_bytes;
+  bool split_q;         // turned queries in two parts
 };
 
 gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
@@ -328,6 +329,12 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
   L->ws_bytes = gqaw::kPagedPartialOffset + align256((size_t)L->grid * 2 * part_rows * (D + 4) * 4);
   L->off_q = L->ws_bytes;
   L->ws_bytes += align256((size_t)a->total_new_tokens * qrow * L->es);
+  // What bf16 leaves of a turned query is kept beside it, and both parts multiply the keys: the
+  // rounding of the queries alone otherwise adds 0.0014 to the outputs' error of 0.0016.  (Head
+  // size 256 on the 128-row kernel has no shared memory for a second part.)
+  L->split_q = a->dtype == GQAW_BF16 && !(L->path == kPrefill && D == 256);
+  L->off_qlo = L->ws_bytes;
+  if (L->split_q) L->ws_bytes += align256((size_t)a->total_new_tokens * qrow * L->es);
   return GQAW_OK;
 }
 
@@ -468,12 +475,14 @@ gqaw_status make_maps(const gqaw_paged_args *a, const Plan &L, const PagedParams
   bool ok = gqaw::encode_tensor_map(&m->k, a->key_pages, 4, cd, cst, cb, bf16) &&
             gqaw::encode_tensor_map(&m->v, a->value_pages, 4, cd, cst, cb, bf16);
   if (L.path == kF32) {
-    m->q = m->k;  // not used: queries come by ordinary loads
+    m->q = m->ql = m->k;  // not used: queries come by ordinary loads
   } else {
     const cuuint64_t qd[3] = {D, (cuuint64_t)a->num_heads, (cuuint64_t)a->total_new_tokens};
     const cuuint64_t qst[2] = {D * es, (cuuint64_t)p.qs * es};
     const cuuint32_t qb[3] = {inner, (cuuint32_t)L.group, (cuuint32_t)(L.path == kPrefill ? L.tpt / L.halves : L.tpt)};
     ok = ok && gqaw::encode_tensor_map(&m->q, p.q, 3, qd, qst, qb, bf16);
+    m->ql = m->q;
+    if (p.qlo) ok = ok && gqaw::encode_tensor_map(&m->ql, p.qlo, 3, qd, qst, qb, bf16);
   }
   return ok ? GQAW_OK : fail(GQAW_ECUDA, "cuTensorMapEncodeTiled failed for the paged attention");
 }
@@ -529,6 +538,7 @@ gqaw_status run_paged(const gqaw_paged_args *a, void *stream, bool append, bool 
     const bool turn_q = attend && (L.rot_dim > 0 || a->query_weight);
     p.qout = static_cast<char *>(a->workspace) + L.off_q;
     p.qos = (long long)a->num_heads * a->head_size;
+    if (turn_q && L.split_q) p.qlo = static_cast<char *>(a->workspace) + L.off_qlo;
     s = run_rows(p, turn_q ? a->num_heads : 0, a->kv_num_heads, a->kv_num_heads, true, a->dtype == GQAW_BF16, st);
     if (s != GQAW_OK) return s;
     if (turn_q) {

@@ -34,6 +34,7 @@
 //
 // Every wait is bounded; one that expires flags GQAW_DEV_TIMEOUT and the CTA winds down.
 #include <atomic>
+#include <type_traits>
 
 #include "gqaw_paged_tc.cuh"
 
@@ -57,16 +58,16 @@ constexpr int kUnitCost = 3;   // see gqaw_paged_sched.cuh
 constexpr float kRescaleLog2 = 8.0f;  // log2 units
 constexpr int kSoftBar = 5;    // named barrier of the softmax warps (1-4: those of a lane quarter)
 
-template <int D>
+template <int D, bool SPLIT>
 struct Lay {
   static constexpr int HALVES = D / 64;
   static constexpr int kTile = HALVES * kHalf;
-  static constexpr int kKSt = D == 64 ? 4 : D == 128 ? 3 : 1;
+  static constexpr int kKSt = D == 64 ? 4 : D == 128 ? (SPLIT ? 2 : 3) : 1;
   static constexpr int kVSt = D == 64 ? 4 : D == 128 ? 2 : 1;
   static constexpr int kSBuf = D == 256 ? 1 : 2;
   static constexpr uint32_t kTmemP = D == 256 ? 128 : 384, kTmemO = 256;
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + kTile;
+  static constexpr int kK = kQ + (SPLIT ? 2 : 1) * kTile;  // Q, and what bf16 left of it
   static constexpr int kV = kK + kKSt * kTile;
   static constexpr int kSched = kV + kVSt * kTile;
   static constexpr int kXch = kSched + (int)((sizeof(PSched) + 15) / 16 * 16);  // float [3][kParts][128]
@@ -183,11 +184,12 @@ __device__ __forceinline__ bool odd_pair(uint32_t w) {
 
 }  // namespace ppre
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(ppre::kThreads, 1)
     paged_prefill_kernel(const PagedParams p, const __grid_constant__ PagedMaps maps) {
   using namespace ppre;
-  using L = Lay<D>;
+  using L = Lay<D, SPLIT>;
+  constexpr int QP = SPLIT ? 2 : 1;  // parts of the queries
   constexpr int OC = D / kParts;  // output columns of a softmax thread
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
     for (int i = 0; i < 2 * kParts * 8; ++i) odd[i] = 0u;
   }
   // query rows past tpt * group stay zero
-  for (int e = tid; e < L::kTile / 16; e += kThreads) reinterpret_cast<uint4 *>(smem + L::kQ)[e] = make_uint4(0, 0, 0, 0);
+  for (int e = tid; e < QP * L::kTile / 16; e += kThreads) reinterpret_cast<uint4 *>(smem + L::kQ)[e] = make_uint4(0, 0, 0, 0);
   if (warp == 0) tc::tmem_alloc(tmem_slot, kTmemCols);
   tc::fence_proxy_async_smem();
   pdl_wait();
@@ -278,9 +280,9 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
             break;
           }
           if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, (uint32_t)(L::HALVES * g * p.tpt * 128));
-            for (int h = 0; h < L::HALVES; ++h)
-              tc::tma_load_3d(smem + L::kQ + h * kHalf, &maps.q, h * 64, u.hu * g, u.row0, q_full, qpol);
+            mbar_arrive_expect_tx(q_full, (uint32_t)(QP * L::HALVES * g * p.tpt * 128));
+            for (int h = 0; h < QP * L::HALVES; ++h)
+              tc::tma_load_3d(smem + L::kQ + h * kHalf, h < L::HALVES ? &maps.q : &maps.ql, h % L::HALVES * 64, u.hu * g, u.row0, q_full, qpol);
           }
           ++qi;
         }
@@ -313,10 +315,14 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
         const uint64_t b0 = dk + (uint64_t)((st * L::kTile) >> 4);
         const uint32_t ds = tmem + (gt % L::kSBuf) * kKeys;
         if (elect_one()) {
+#pragma unroll 1
+          for (int q = 0; q < QP; ++q) {  // not unrolled: the descriptors of 16 products would spill
+            const uint64_t aq = dq + (uint64_t)((q * L::kTile) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (uint64_t)(((kk / 4) * kHalf + (kk % 4) * 32) >> 4);
-            tc::mma_bf16_ss(ds, dq + off, b0 + off, kIdescQK, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (uint64_t)(((kk / 4) * kHalf + (kk % 4) * 32) >> 4);
+              tc::mma_bf16_ss(ds, aq + off, b0 + off, kIdescQK, q + kk > 0);
+            }
           }
           tc::mma_commit(&s_full[gt & 1]);
           tc::mma_commit(&k_free[st]);
@@ -598,9 +604,16 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
               if (off < 0) continue;
               const __nv_bfloat16 *kr = static_cast<const __nv_bfloat16 *>(p.kp) + off;
               const __nv_bfloat16 *vr = static_cast<const __nv_bfloat16 *>(p.vp) + off + d0;
-              const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(p.q) + (u.row0 + tok) * p.qs + (long long)h * D;
+              const long long q_at = (u.row0 + tok) * p.qs + (long long)h * D;
+              const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(p.q) + q_at;
+              const __nv_bfloat16 *ql = static_cast<const __nv_bfloat16 *>(p.qlo) + q_at;
               float z = 0.f;
-              for (int d = 0; d < D; ++d) z = fmaf(__bfloat162float(qr[d]), __bfloat162float(kr[d]), z);
+#pragma unroll 4
+              for (int d = 0; d < D; ++d) {
+                float x = __bfloat162float(qr[d]);
+                if (SPLIT) x += __bfloat162float(ql[d]);
+                z = fmaf(x, __bfloat162float(kr[d]), z);
+              }
               z *= p.qscale;
               if (!plain) z = p.capmul * ptc::fast_tanh(z);
               const float pr = fast_exp2(z - m_run);
@@ -696,13 +709,13 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
 
 namespace ppre {
 
-template <int D>
+template <int D, bool SPLIT>
 struct Lay2 {
   static constexpr int HALVES = D / 64;
   static constexpr int kTile = HALVES * kHalf;
-  static constexpr int kSt = D == 64 ? 4 : 2;  // K tiles, and V tiles
+  static constexpr int kSt = D == 64 ? 4 : SPLIT ? 1 : 2;  // K tiles, and V tiles
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + 2 * kTile;
+  static constexpr int kK = kQ + (SPLIT ? 4 : 2) * kTile;  // Q of both halves, and what bf16 left of them
   static constexpr int kV = kK + kSt * kTile;
   static constexpr int kStage = kV + kSt * kTile;  // 32 rows x 32 columns of output per softmax warp
   static constexpr int kSched = kStage + 8 * 2048;
@@ -736,11 +749,12 @@ __device__ __forceinline__ Halves halves_of(const PagedParams &p, const PUnit &u
 
 // 384 threads launched with 168 registers; the two softmax warpgroups take 208 and the third gives
 // back to 88: 256 x 208 + 128 x 88 = 384 x 168.
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(ppre::kThreads2, 1)
     paged_prefill2_kernel(const PagedParams p, const __grid_constant__ PagedMaps maps) {
   using namespace ppre;
-  using L = Lay2<D>;
+  using L = Lay2<D, SPLIT>;
+  constexpr int QP = SPLIT ? 2 : 1;  // parts of the queries
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   PSched *sched = reinterpret_cast<PSched *>(smem + L::kSched);
@@ -774,7 +788,7 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
     for (int i = 0; i < 32; ++i) odd[i] = 0u;
   }
   // query rows past a half's tokens stay zero
-  for (int e = tid; e < 2 * L::kTile / 16; e += kThreads2) reinterpret_cast<uint4 *>(smem + L::kQ)[e] = make_uint4(0, 0, 0, 0);
+  for (int e = tid; e < 2 * QP * L::kTile / 16; e += kThreads2) reinterpret_cast<uint4 *>(smem + L::kQ)[e] = make_uint4(0, 0, 0, 0);
   if (warp == 0) tc::tmem_alloc(tmem_slot, kTmemCols);
   tc::fence_proxy_async_smem();
   pdl_wait();
@@ -825,10 +839,11 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
           }
           if (lane == 0) {
             const int parts = u.ntok > t1 ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, (uint32_t)(parts * L::HALVES * g * t1 * 128));
+            mbar_arrive_expect_tx(q_full, (uint32_t)(parts * QP * L::HALVES * g * t1 * 128));
             for (int x = 0; x < parts; ++x)
-              for (int h = 0; h < L::HALVES; ++h)
-                tc::tma_load_3d(smem + L::kQ + x * L::kTile + h * kHalf, &maps.q, h * 64, u.hu * g, u.row0 + x * t1, q_full, qpol);
+              for (int h = 0; h < QP * L::HALVES; ++h)
+                tc::tma_load_3d(smem + L::kQ + x * QP * L::kTile + h * kHalf, h < L::HALVES ? &maps.q : &maps.ql,
+                                h % L::HALVES * 64, u.hu * g, u.row0 + x * t1, q_full, qpol);
           }
           ++qi;
         }
@@ -864,13 +879,17 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
         if (!warp_wait(&k_full[st], (kt / L::kSt) & 1)) return false;
         if (pvs[x] > 0 && !warp_wait(&pv_done[x], (pvs[x] - 1) & 1)) return false;
         tc::fence_after_sync();
-        const uint64_t a0 = dq + (uint64_t)((x * L::kTile) >> 4), b0 = dk + (uint64_t)((st * L::kTile) >> 4);
+        const uint64_t a0 = dq + (uint64_t)((x * QP * L::kTile) >> 4), b0 = dk + (uint64_t)((st * L::kTile) >> 4);
         const bool second = hv.a[1] <= k && k < hv.b[1];
         if (elect_one()) {
+#pragma unroll 1
+          for (int q = 0; q < QP; ++q) {  // not unrolled: the descriptors of 16 products would spill
+            const uint64_t aq = a0 + (uint64_t)((q * L::kTile) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (uint64_t)(((kk / 4) * kHalf + (kk % 4) * 32) >> 4);
-            tc::mma_bf16_ss(tmem + x * kKeys, a0 + off, b0 + off, kIdescQK, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (uint64_t)(((kk / 4) * kHalf + (kk % 4) * 32) >> 4);
+              tc::mma_bf16_ss(tmem + x * kKeys, aq + off, b0 + off, kIdescQK, q + kk > 0);
+            }
           }
           tc::mma_commit(&s_full[x]);
           if (x == 1 || !second) tc::mma_commit(&k_free[st]);
@@ -1130,9 +1149,16 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
                 if (off < 0) continue;
                 const __nv_bfloat16 *kr = static_cast<const __nv_bfloat16 *>(p.kp) + off;
                 const __nv_bfloat16 *vr = static_cast<const __nv_bfloat16 *>(p.vp) + off + d0;
-                const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(p.q) + (u.row0 + tok) * p.qs + (long long)h * D;
+                const long long q_at = (u.row0 + tok) * p.qs + (long long)h * D;
+                const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(p.q) + q_at;
+                const __nv_bfloat16 *ql = static_cast<const __nv_bfloat16 *>(p.qlo) + q_at;
                 float z = 0.f;
-                for (int d = 0; d < D; ++d) z = fmaf(__bfloat162float(qr[d]), __bfloat162float(kr[d]), z);
+#pragma unroll 4
+                for (int d = 0; d < D; ++d) {
+                  float x = __bfloat162float(qr[d]);
+                  if (SPLIT) x += __bfloat162float(ql[d]);
+                  z = fmaf(x, __bfloat162float(kr[d]), z);
+                }
                 z *= p.qscale;
                 if (!plain) z = p.capmul * ptc::fast_tanh(z);
                 const float pr = fast_exp2(z - m_run);
@@ -1234,17 +1260,32 @@ cudaError_t launch_prefill(K kernel, std::atomic<bool> *ready, int threads, int 
   return cudaGetLastError();
 }
 
-// halves: query tiles of 128 rows per unit, 1 or 2 (2: head sizes 64 and 128).
+// halves: query tiles of 128 rows per unit, 1 or 2 (2: head sizes 64 and 128).  The queries come
+// in two parts where p.qlo is set (head sizes 64 and 128).
 cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, int halves, int grid, cudaStream_t stream) {
-  static std::atomic<bool> ready[5][kPrefillDevices];
-  if (halves == 2)
-    return p.D == 64 ? launch_prefill(paged_prefill2_kernel<64>, ready[0], ppre::kThreads2, ppre::Lay2<64>::kAlloc, p, maps, grid, stream)
-                     : launch_prefill(paged_prefill2_kernel<128>, ready[1], ppre::kThreads2, ppre::Lay2<128>::kAlloc, p, maps, grid, stream);
-  switch (p.D) {
-    case 64: return launch_prefill(paged_prefill_kernel<64>, ready[2], ppre::kThreads, ppre::Lay<64>::kAlloc, p, maps, grid, stream);
-    case 128: return launch_prefill(paged_prefill_kernel<128>, ready[3], ppre::kThreads, ppre::Lay<128>::kAlloc, p, maps, grid, stream);
-    default: return launch_prefill(paged_prefill_kernel<256>, ready[4], ppre::kThreads, ppre::Lay<256>::kAlloc, p, maps, grid, stream);
+  static std::atomic<bool> ready[9][kPrefillDevices];
+  auto one = [&](auto d, auto split, int i) {
+    return launch_prefill(paged_prefill_kernel<d.value, split.value>, ready[i], ppre::kThreads,
+                          ppre::Lay<d.value, split.value>::kAlloc, p, maps, grid, stream);
+  };
+  auto two = [&](auto d, auto split, int i) {
+    return launch_prefill(paged_prefill2_kernel<d.value, split.value>, ready[i], ppre::kThreads2,
+                          ppre::Lay2<d.value, split.value>::kAlloc, p, maps, grid, stream);
+  };
+  constexpr std::integral_constant<int, 64> d64{};
+  constexpr std::integral_constant<int, 128> d128{};
+  constexpr std::integral_constant<int, 256> d256{};
+  constexpr std::true_type split{};
+  constexpr std::false_type whole{};
+  if (p.D == 64) {
+    if (halves == 2) return p.qlo ? two(d64, split, 0) : two(d64, whole, 1);
+    return p.qlo ? one(d64, split, 2) : one(d64, whole, 3);
   }
+  if (p.D == 128) {
+    if (halves == 2) return p.qlo ? two(d128, split, 4) : two(d128, whole, 5);
+    return p.qlo ? one(d128, split, 6) : one(d128, whole, 7);
+  }
+  return one(d256, whole, 8);
 }
 
 }  // namespace gqaw

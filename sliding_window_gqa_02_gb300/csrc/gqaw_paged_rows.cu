@@ -135,10 +135,11 @@ struct Coef {
 };
 
 // BATCH groups of RPW heads of one tensor, in `x`: norm (wt), turn, store.  Heads [h, nh), D
-// elements (in) and `step` elements (out) apart.
-template <int MODE, typename T, int LPR, int BATCH>
+// elements (in) and `step` elements (out) apart.  SPLIT: with `lo` not 0, what the rounding to
+// bf16 leaves is stored too, that many elements on.
+template <int MODE, bool SPLIT, typename T, int LPR, int BATCH>
 __device__ __forceinline__ void rows_out(const PagedParams &p, Oct<T> (&x)[BATCH], const Coef &c, bool norm, T *dst,
-                                         long long step, int h, int nh, int e, int src) {
+                                         long long step, long long lo, int h, int nh, int e, int src) {
   constexpr int RPW = 32 / LPR, D = LPR * 8;
   const int lane = threadIdx.x & 31, lr = lane % LPR, half = p.rot_dim / 2;
   const int h0 = h - lane / LPR;  // the warp's first head
@@ -198,12 +199,25 @@ __device__ __forceinline__ void rows_out(const PagedParams &p, Oct<T> (&x)[BATCH
         unpk(mul2(t, r2), y[2 * m], y[2 * m + 1]);
       }
       x[i].set(y);
+      if (SPLIT && lo) {
+        float z[8];
+        x[i].get(z);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) z[m] = fabsf(z[m]) < INFINITY ? y[m] - z[m] : 0.f;
+        Oct<T> rest;
+        rest.set(z);
+        if (h + i * RPW < nh) rest.store(dst + lo + (long long)i * RPW * step);
+      }
+    } else if (SPLIT && lo) {
+      Oct<T> rest;
+      rest.clear();
+      if (h + i * RPW < nh) rest.store(dst + lo + (long long)i * RPW * step);
     }
     if (h + i * RPW < nh) x[i].store(dst + (long long)i * RPW * step);
   }
 }
 
-template <typename T, int LPR, int BATCH>
+template <bool SPLIT, typename T, int LPR, int BATCH>
 __global__ void __launch_bounds__(kThreads, 3) paged_rows_kernel(const PagedParams p, const RowsJob j) {
   constexpr int RPW = 32 / LPR, D = LPR * 8;
   const int lane = threadIdx.x & 31, lr = lane % LPR, sub = lane / LPR;
@@ -257,9 +271,10 @@ __global__ void __launch_bounds__(kThreads, 3) paged_rows_kernel(const PagedPara
     }
     if (owned) {
       T *dst;
-      long long step = D;
+      long long step = D, lo = 0;
       if (kind == 0) {
         dst = static_cast<T *>(p.qout) + n * p.qos;
+        if (SPLIT) lo = static_cast<const T *>(p.qlo) - static_cast<const T *>(p.qout);
       } else if (!j.paged) {
         dst = static_cast<T *>(p.kout) + n * p.kos;
       } else {
@@ -341,25 +356,25 @@ __global__ void __launch_bounds__(kThreads, 3) paged_rows_kernel(const PagedPara
       }
       // one loop for each way, so that the one taken is short
       switch (mode) {
-        case kNoTurn: rows_out<kNoTurn, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, h, nh, e, src); break;
-        case kOctets: rows_out<kOctets, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, h, nh, e, src); break;
-        case kInside: rows_out<kInside, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, h, nh, e, src); break;
-        default: rows_out<kAnywhere, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, h, nh, e, src);
+        case kNoTurn: rows_out<kNoTurn, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src); break;
+        case kOctets: rows_out<kOctets, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src); break;
+        case kInside: rows_out<kInside, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src); break;
+        default: rows_out<kAnywhere, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src);
       }
     }
   }
   pdl_launch_dependents();
 }
 
-template <typename T, int BATCH>
+template <bool SPLIT, typename T, int BATCH>
 cudaError_t launch_rows_t(const PagedParams &p, const RowsJob &j, const cudaLaunchConfig_t &cfg) {
   switch (p.D) {
-    case 8: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 1, BATCH>, p, j);
-    case 16: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 2, BATCH>, p, j);
-    case 32: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 4, BATCH>, p, j);
-    case 64: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 8, BATCH>, p, j);
-    case 128: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 16, BATCH>, p, j);
-    default: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, 32, BATCH>, p, j);
+    case 8: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 1, BATCH>, p, j);
+    case 16: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 2, BATCH>, p, j);
+    case 32: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 4, BATCH>, p, j);
+    case 64: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 8, BATCH>, p, j);
+    case 128: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 16, BATCH>, p, j);
+    default: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 32, BATCH>, p, j);
   }
 }
 
@@ -390,8 +405,14 @@ cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = bf16 ? (many ? launch_rows_t<__nv_bfloat16, 8>(p, j, cfg) : launch_rows_t<__nv_bfloat16, 2>(p, j, cfg))
-                             : (many ? launch_rows_t<float, 4>(p, j, cfg) : launch_rows_t<float, 2>(p, j, cfg));
+  // p.qlo: a variant of its own, for the rows that need no second part are 6% slower with the choice inside
+  cudaError_t e;
+  if (!bf16)
+    e = many ? launch_rows_t<false, float, 4>(p, j, cfg) : launch_rows_t<false, float, 2>(p, j, cfg);
+  else if (p.qlo)
+    e = many ? launch_rows_t<true, __nv_bfloat16, 8>(p, j, cfg) : launch_rows_t<true, __nv_bfloat16, 2>(p, j, cfg);
+  else
+    e = many ? launch_rows_t<false, __nv_bfloat16, 8>(p, j, cfg) : launch_rows_t<false, __nv_bfloat16, 2>(p, j, cfg);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -16,6 +16,7 @@ namespace gqaw {
 
 struct PagedMaps {
   CUtensorMap q;   // query (N, Nq, D): box (64, group, tokens of a query tile)
+  CUtensorMap ql;  // the same of what bf16 left of the queries (PagedParams::qlo); encoded where that is set
   CUtensorMap k;   // key pages (pages, kv heads, rows, D): box (64, box rows, 1, 1)
   CUtensorMap v;   // value pages
 };

@@ -102,8 +102,13 @@ __global__ void __launch_bounds__(pwarp::Lay<T, D>::kThreads, pwarp::Lay<T, D>::
     }
     for (int e = tid; e < RM * D; e += L::kThreads) {
       const int r = e / D, d = e - r * D, tok = r / g, hh = r - tok * g;
-      sq[e] = r < rows ? Elem<T>::load(static_cast<const T *>(p.q)[(u.row0 + tok) * p.qs + (long long)(h0 + hh) * D + d]) * p.qscale
-                       : 0.f;
+      float x = 0.f;
+      if (r < rows) {
+        const long long at = (u.row0 + tok) * p.qs + (long long)(h0 + hh) * D + d;
+        x = Elem<T>::load(static_cast<const T *>(p.q)[at]);
+        if (p.qlo) x += Elem<T>::load(static_cast<const T *>(p.qlo)[at]);
+      }
+      sq[e] = x * p.qscale;
     }
     __syncthreads();
 

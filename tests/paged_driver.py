@@ -112,8 +112,10 @@ class Batch:
         return ref.norm_turn(self.q.reshape(-1, self.Nq, self.D), self.qw, 1e-5, self.cos, self.sin, self.table_pos(),
                              self.interleaved)
 
-    def check_output(self, turned=False, skip=()):
-        """Every output row against the definition over the cache as it is now."""
+    def check_output(self, turned=False, skip=(), parts=1):
+        """Every output row against the definition over the cache as it is now.  ``turned``: with
+        queries that the call norms and turns, kept in ``parts`` numbers of the type: what each
+        leaves is within u of it, so two are within u * u."""
         worst = 0.0
         qv = None
         if turned:
@@ -125,7 +127,7 @@ class Batch:
             k = ref.gather(self.kp, self.table[i], t, self.hir)
             v = ref.gather(self.vp, self.table[i], t, self.hir)
             q = (qv if turned else self.q.reshape(-1, self.Nq, self.D).double())[self.rows(i)]
-            rounded = ref.u(self.dtype) + 64 * ref.F32 if turned else 0.0
+            rounded = ref.u(self.dtype) ** parts + 64 * ref.F32 if turned else 0.0
             if turned:  # the turn's own error, relative to the row (a bound for every element)
                 rounded += float((qb[self.rows(i)] / q.abs().amax(-1, keepdim=True).clamp_min(1e-30)).max()) * 4
             want, bound = ref.attend(q, k, v, t - s, self.window, self.scale or 1 / math.sqrt(self.D), self.softcap, sink,

@@ -131,12 +131,12 @@ def test_nothing_to_do_needs_no_pointers(lib):
 
 
 def test_paged_workspace(lib):
-    """The split results follow the grid, the turned queries the tokens; sizes alone matter."""
+    """The split results follow the grid, the turned queries (two parts of bf16) the tokens; sizes alone matter."""
     a = _paged(lib, query=None, workspace=None)
     n = lib.gqaw_paged_workspace_bytes(a)
     assert n > 4096 and n % 256 == 0
     more = lib.gqaw_paged_workspace_bytes(_paged(lib, total_new_tokens=1010))
-    assert more - n == (1010 * 8 * 64 * 2 + 255) // 256 * 256 - 10 * 8 * 64 * 2 // 256 * 256
+    assert more - n == 2 * ((1010 * 8 * 64 * 2 + 255) // 256 * 256 - 10 * 8 * 64 * 2 // 256 * 256)
     assert lib.gqaw_paged_workspace_bytes(_paged(lib, batch_size=3000)) < n + 64 * MB
     assert lib.gqaw_paged_workspace_bytes(_paged(lib, head_size=96)) == 0
 
