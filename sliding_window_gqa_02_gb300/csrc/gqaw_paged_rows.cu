@@ -17,9 +17,13 @@
 // at the same place of another lane when rd/2 is a multiple of 8: its words are exchanged as
 // stored (4 shuffles for 8 bf16); other widths pick it out of the neighbours' elements.
 // A warp goes over BATCH groups of heads of one tensor, whose loads are all issued before the
-// first is used: 128 bytes a lane where there are tokens enough to fill the GPU, 2 groups where the chain of dependent look-ups
-// (sequence, position, tables) is the time.  A lane stores only what it loaded, so the norm may
-// work in place.
+// first is used: 4 where there are tokens enough to fill the GPU, 2 where the chain of dependent
+// look-ups (sequence, position, tables) is the time.  What hides that chain is many warps, so
+// registers are the price: the usual pairing has a kernel of its own that fits 64 of them (32
+// warps a SM; 4099 tokens of 40 heads of 128 in bf16: 22.6 us, 3.8 TB/s; with 8 groups and 80
+// registers 23.2 us, with every pairing in one kernel 24.0, in CTAs of 256 threads 25.4; 48
+// registers spill: 29).  fp32 takes 80: 33.4 us, 5.1 TB/s, against 41.8 with 64.
+// A lane stores only what it loaded, so the norm may work in place.
 #include <atomic>
 
 #include "gqaw_paged.cuh"
@@ -28,7 +32,7 @@ namespace gqaw {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr long long kManyWarps = 152 * 16;  // 16 warps a SM
 
 template <typename T> struct Oct;  // 8 elements as stored
@@ -217,8 +221,10 @@ __device__ __forceinline__ void rows_out(const PagedParams &p, Oct<T> (&x)[BATCH
   }
 }
 
-template <bool SPLIT, typename T, int LPR, int BATCH>
-__global__ void __launch_bounds__(kThreads, 3) paged_rows_kernel(const PagedParams p, const RowsJob j) {
+// OCTETS: pairs lie in octets of other lanes, or nothing turns (the common case, in fewer registers).
+template <bool OCTETS, bool SPLIT, typename T, int LPR, int BATCH>
+__global__ void __launch_bounds__(kThreads, OCTETS && sizeof(T) == 2 ? 8 : 6)
+    paged_rows_kernel(const PagedParams p, const RowsJob j) {
   constexpr int RPW = 32 / LPR, D = LPR * 8;
   const int lane = threadIdx.x & 31, lr = lane % LPR, sub = lane / LPR;
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_rows_kernel(const PagedPara
           if (lane == 0) pflag(p, GQAW_DEV_BAD_POSITION);
         }
       }
-      const int mode = !turn ? kNoTurn : p.rot_inter ? kInside : half % 8 == 0 ? kOctets : kAnywhere;
+      const int mode = !turn ? kNoTurn : OCTETS ? kOctets : p.rot_inter ? kInside : half % 8 == 0 ? kOctets : kAnywhere;
       float cs[8], sn[8], wo[8], wp[8];
 #pragma unroll
       for (int m = 0; m < 8; ++m) cs[m] = 1.f, sn[m] = 0.f, wo[m] = wp[m] = 1.f;
@@ -358,23 +364,23 @@ __global__ void __launch_bounds__(kThreads, 3) paged_rows_kernel(const PagedPara
       switch (mode) {
         case kNoTurn: rows_out<kNoTurn, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src); break;
         case kOctets: rows_out<kOctets, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src); break;
-        case kInside: rows_out<kInside, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src); break;
-        default: rows_out<kAnywhere, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src);
+        case kInside: if (!OCTETS) rows_out<kInside, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src); break;
+        default: if (!OCTETS) rows_out<kAnywhere, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src);
       }
     }
   }
   pdl_launch_dependents();
 }
 
-template <bool SPLIT, typename T, int BATCH>
+template <bool OCTETS, bool SPLIT, typename T, int BATCH>
 cudaError_t launch_rows_t(const PagedParams &p, const RowsJob &j, const cudaLaunchConfig_t &cfg) {
   switch (p.D) {
-    case 8: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 1, BATCH>, p, j);
-    case 16: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 2, BATCH>, p, j);
-    case 32: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 4, BATCH>, p, j);
-    case 64: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 8, BATCH>, p, j);
-    case 128: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 16, BATCH>, p, j);
-    default: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<SPLIT, T, 32, BATCH>, p, j);
+    case 8: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<OCTETS, SPLIT, T, 1, BATCH>, p, j);
+    case 16: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<OCTETS, SPLIT, T, 2, BATCH>, p, j);
+    case 32: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<OCTETS, SPLIT, T, 4, BATCH>, p, j);
+    case 64: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<OCTETS, SPLIT, T, 8, BATCH>, p, j);
+    case 128: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<OCTETS, SPLIT, T, 16, BATCH>, p, j);
+    default: return cudaLaunchKernelEx(&cfg, paged_rows_kernel<OCTETS, SPLIT, T, 32, BATCH>, p, j);
   }
 }
 
@@ -389,7 +395,7 @@ cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool
   j.vec = half % 8 == 0 && reinterpret_cast<uintptr_t>(p.rcos) % 16 == 0 && reinterpret_cast<uintptr_t>(p.rsin) % 16 == 0;
   const int rpw = 32 / (p.D / 8);
   auto chunks = [&](int heads, int batch) { return (heads + batch * rpw - 1) / (batch * rpw); };
-  const int deep = bf16 ? 8 : 4;  // 128 bytes of loads a lane
+  const int deep = 4;  // 64 bytes of loads a lane, or 128 of fp32
   const bool many = (long long)p.N * (chunks(nq, deep) + chunks(nk, deep) + chunks(nv, deep)) >= kManyWarps;
   const int batch = many ? deep : 2;
   j.cq = chunks(nq, batch);
@@ -406,13 +412,17 @@ cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // p.qlo: a variant of its own, for the rows that need no second part are 6% slower with the choice inside
+  const bool octets = !p.rot_inter && half % 8 == 0;
   cudaError_t e;
   if (!bf16)
-    e = many ? launch_rows_t<false, float, 4>(p, j, cfg) : launch_rows_t<false, float, 2>(p, j, cfg);
+    e = !many ? launch_rows_t<false, false, float, 2>(p, j, cfg)
+        : octets ? launch_rows_t<true, false, float, 4>(p, j, cfg) : launch_rows_t<false, false, float, 4>(p, j, cfg);
   else if (p.qlo)
-    e = many ? launch_rows_t<true, __nv_bfloat16, 8>(p, j, cfg) : launch_rows_t<true, __nv_bfloat16, 2>(p, j, cfg);
+    e = !many ? launch_rows_t<false, true, __nv_bfloat16, 2>(p, j, cfg)
+        : octets ? launch_rows_t<true, true, __nv_bfloat16, 4>(p, j, cfg) : launch_rows_t<false, true, __nv_bfloat16, 4>(p, j, cfg);
   else
-    e = many ? launch_rows_t<false, __nv_bfloat16, 8>(p, j, cfg) : launch_rows_t<false, __nv_bfloat16, 2>(p, j, cfg);
+    e = !many ? launch_rows_t<false, false, __nv_bfloat16, 2>(p, j, cfg)
+        : octets ? launch_rows_t<true, false, __nv_bfloat16, 4>(p, j, cfg) : launch_rows_t<false, false, __nv_bfloat16, 4>(p, j, cfg);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
