@@ -24,6 +24,7 @@ struct PagedParams {
   int B, N, max_new, max_len, Nq, Nkv, D, page, npages, width, W;  // W: 0 without a window
   int group, hblocks, gb;           // query heads per kv head; head blocks of gb heads per kv head
   int tpt;                          // tokens per query tile
+  int s_lo, s_hi;                   // only sequences of [s_lo, s_hi] new tokens are this launch's
   float qscale, capmul;             // as in Params
   uint32_t *status, *tickets;
   float *partials;
@@ -61,7 +62,7 @@ __device__ inline void sched_build(const PagedParams &p, const PShape &shp, PSch
       S = q1 - q0;
       if (q0 < 0 || q1 < q0 || q1 > p.N || S > p.max_new || TT < S || TT > p.max_len) {
         if (blockIdx.x == 0) pflag(p, GQAW_DEV_BAD_SEQLEN);
-      } else if (S > 0) {
+      } else if (S >= p.s_lo && S <= p.s_hi) {
         T = (int)TT;
         const PTiles<KEYS> t(shp, T, S);
         has = 1;

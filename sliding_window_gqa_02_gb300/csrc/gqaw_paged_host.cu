@@ -216,6 +216,7 @@ struct Plan {
   long long qs, ks, vs, os, sp, sh, sr;
   size_t off_q, off_qlo, ws_bytes;
   bool split_q;         // turned queries in two parts
+  int few;              // kPrefill: sequences of at most this many tokens go to the decode kernel (0: none)
 };
 
 gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
@@ -309,6 +310,17 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
     L->tpt = L->halves * (128 / L->group);
     part_rows = 128 * L->halves;
     L->grid = kSms;
+    // A sequence of a token or two fills at most 8 of the 256 rows, yet its key tiles cost half of
+    // a full one's and more.  Where the batch may hold many (the others hold at most
+    // max_new_tokens, which bounds their number), they go to the decode kernel, in a launch of
+    // its own: 32 contexts of 4096 to 32768 beside a chunk of 512, 491 -> 379 us.  The launch
+    // costs 4 to 8 us when there are none, what kShort sequence heads of 2000 keys win; at 20
+    // sequences of 128 to 8192 keys and two chunks both ways take 119 us.  Head size 256, one
+    // tile of 128 rows, loses (160 -> 195 us).
+    constexpr int kShort = 64;
+    const long long tok = L->halves == 2 && L->group <= 8 ? 8 / L->group : 0;
+    const long long spare = (long long)a->total_new_tokens - a->batch_size * tok;
+    if (tok && (a->batch_size - (spare > 0 ? ceil_div(spare, a->max_new_tokens) : 0)) * a->kv_num_heads >= kShort) L->few = (int)tok;
   } else if (rows <= 8 && D * L->es <= 512) {
     L->path = a->dtype == GQAW_F32 && D >= 32 && tiled(16) ? kF32 : kWarp;
     L->gb = L->group;
@@ -464,7 +476,8 @@ gqaw_status run_rows(const PagedParams &p, int nq, int nk, int nv, bool paged, b
 
 // Tensor maps: 128-byte rows of the swizzle (64 bf16 or 32 fp32 dimensions), boxes of whole
 // pages or of a tile's rows.
-gqaw_status make_maps(const gqaw_paged_args *a, const Plan &L, const PagedParams &p, gqaw::PagedMaps *m) {
+// tokens: those of a query box.
+gqaw_status make_maps(const gqaw_paged_args *a, const Plan &L, const PagedParams &p, int tokens, gqaw::PagedMaps *m) {
   const bool bf16 = a->dtype == GQAW_BF16;
   const cuuint64_t D = (cuuint64_t)a->head_size, es = (cuuint64_t)L.es;
   const cuuint32_t inner = (cuuint32_t)(128 / L.es);
@@ -479,7 +492,7 @@ gqaw_status make_maps(const gqaw_paged_args *a, const Plan &L, const PagedParams
   } else {
     const cuuint64_t qd[3] = {D, (cuuint64_t)a->num_heads, (cuuint64_t)a->total_new_tokens};
     const cuuint64_t qst[2] = {D * es, (cuuint64_t)p.qs * es};
-    const cuuint32_t qb[3] = {inner, (cuuint32_t)L.group, (cuuint32_t)(L.path == kPrefill ? L.tpt / L.halves : L.tpt)};
+    const cuuint32_t qb[3] = {inner, (cuuint32_t)L.group, (cuuint32_t)tokens};
     ok = ok && gqaw::encode_tensor_map(&m->q, p.q, 3, qd, qst, qb, bf16);
     m->ql = m->q;
     if (p.qlo) ok = ok && gqaw::encode_tensor_map(&m->ql, p.qlo, 3, qd, qst, qb, bf16);
@@ -493,11 +506,14 @@ gqaw_status run_paged_attend(const gqaw_paged_args *a, const Plan &L, PagedParam
     const cudaError_t e = cudaMemsetAsync(p.tickets, 0, gqaw::kPagedTickets * 4, st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync (tickets)");
   }
-  gqaw::PagedMaps maps;
-  if (L.path == kDecode || L.path == kPrefill || L.path == kF32) {
-    const gqaw_status s = make_maps(a, L, p, &maps);
-    if (s != GQAW_OK) return s;
-  }
+  gqaw::PagedMaps maps, few_maps;
+  gqaw_status s = GQAW_OK;
+  if (L.path == kDecode || L.path == kPrefill || L.path == kF32)
+    s = make_maps(a, L, p, L.path == kPrefill ? L.tpt / L.halves : L.tpt, &maps);
+  if (s == GQAW_OK && L.few) s = make_maps(a, L, p, L.few, &few_maps);
+  if (s != GQAW_OK) return s;
+  p.s_lo = L.few + 1;
+  p.s_hi = a->max_new_tokens;
   for (int b0 = 0; b0 < a->batch_size; b0 += gqaw::kPagedItems) {
     p.B = std::min(gqaw::kPagedItems, a->batch_size - b0);
     p.table = a->page_table + (long long)b0 * a->page_table_width;
@@ -507,7 +523,16 @@ gqaw_status run_paged_attend(const gqaw_paged_args *a, const Plan &L, PagedParam
     cudaError_t e;
     switch (L.path) {
       case kDecode: e = gqaw::launch_paged_decode(p, maps, L.rows, L.grid, st); break;
-      case kPrefill: e = gqaw::launch_paged_prefill(p, maps, L.halves, L.grid, st); break;
+      case kPrefill:
+        e = gqaw::launch_paged_prefill(p, maps, L.halves, L.grid, st);
+        if (e == cudaSuccess && L.few) {
+          gqaw::count_launch();
+          PagedParams few = p;
+          few.s_lo = 1;
+          few.s_hi = few.tpt = L.few;
+          e = gqaw::launch_paged_decode(few, few_maps, L.few * L.group, kSms, st);
+        }
+        break;
       case kF32: e = gqaw::launch_paged_f32_decode(p, maps, L.rows, kSms, st); break;
       case kWarp:
         e = f32 ? gqaw::launch_paged_warp_attend_f32(p, L.rows, kSms, st)
@@ -524,7 +549,7 @@ gqaw_status run_paged_attend(const gqaw_paged_args *a, const Plan &L, PagedParam
 }
 
 gqaw_status run_paged(const gqaw_paged_args *a, void *stream, bool append, bool attend) {
-  Plan L;
+  Plan L{};
   gqaw_status s = plan_paged(a, &L);
   if (s != GQAW_OK) return s;
   if (a->batch_size == 0 || a->total_new_tokens == 0 || a->max_new_tokens == 0) return GQAW_OK;  // no token, nothing to do
@@ -584,7 +609,7 @@ gqaw_status gqaw_qk_norm_rotary(const gqaw_qk_args *a, void *stream) {
 }
 
 size_t gqaw_paged_workspace_bytes(const gqaw_paged_args *args) {
-  Plan L;
+  Plan L{};
   return plan_paged(args, &L) == GQAW_OK ? L.ws_bytes : 0;
 }
 

@@ -49,6 +49,34 @@ def test_window(dtype, lens, window):
     b.check_output()
 
 
+MIXED = [(1, 500), (2, 300), (1, 1), (70, 200), (0, 9), (3, 4), (1, 129), (8, 2000), (9, 9), (2, 2), (140, 141)]
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(window=100, sink=True), dict(softcap=20.0)], ids=str)
+@pytest.mark.parametrize("D,Nq,Nkv,page,launches", [(64, 16, 16, 16, 2), (64, 64, 8, 64, 2), (128, 32, 8, 32, 2), (128, 24, 8, 16, 2),
+                                                    (128, 8, 2, 32, 1), (256, 32, 8, 16, 1), (128, 72, 8, 16, 1)])
+def test_short_sequences_among_chunks(D, Nq, Nkv, page, launches, kw):
+    """Many sequences of a few rows take the kernel for few rows, in a launch of their own: every
+    sequence is one launch's, on either side of the border of 8 rows."""
+    b = Batch(MIXED, Nq, Nkv, D, page, BF, seed=21, extra_rows=2, **kw)
+    n0 = gqaw.gqaw_launch_count()
+    b.call(gqaw.gqaw_paged_attend)
+    assert gqaw.gqaw_launch_count() - n0 == launches
+    b.check_output()
+    b.check_untouched()
+    first = b.out.clone()
+    b.call(gqaw.gqaw_paged_attend)  # the workspace as the launches left it
+    assert torch.equal(first, b.out)
+
+
+def test_equal_chunks_are_one_launch():
+    b = Batch([(9, 300)] * 4, 8, 2, 64, 16, BF, seed=22)
+    n0 = gqaw.gqaw_launch_count()
+    b.call(gqaw.gqaw_paged_attend)
+    assert gqaw.gqaw_launch_count() - n0 == 1
+    b.check_output()
+
+
 @pytest.mark.parametrize("dtype", [BF, F])
 @pytest.mark.parametrize("kw", [dict(softcap=20.0), dict(sink=True), dict(smooth=True), dict(scale=0.31),
                                 dict(softcap=5.0, sink=True, window=50)], ids=str)
