@@ -43,68 +43,61 @@ __device__ __forceinline__ PShape shape_of(const PagedParams &p, int unit_cost) 
 
 __device__ __forceinline__ void pflag(const PagedParams &p, uint32_t bits) { atomicOr(p.status, bits); }
 
-// Builds the list and this CTA's start; all `nt` threads of the CTA (a multiple of 32) call
-// it, and it ends with a barrier.  CTA 0 flags the malformed sequences.
+// Builds the list and this CTA's start; all threads of the CTA call it, and it ends with a
+// barrier.  One warp does it all, since what it takes is a chain of latencies: spread over the
+// CTA, barriers and the sums over warps made it longer (2.7 us for one sequence).  CTA 0
+// flags the malformed sequences.
 template <int KEYS>
-__device__ inline void sched_build(const PagedParams &p, const PShape &shp, PSched *s, int nt) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-  const int heads = p.Nkv * p.hblocks;
-  long long base = 0, units = 0;
-  int count = 0, longest = 0;
-  for (int b0 = 0; b0 < p.B; b0 += nt) {
-    const int b = b0 + tid;
-    long long n = 0, u = 0;
-    int mx = 0, has = 0, T = 0, q0 = 0, S = 0;
-    if (b < p.B) {
-      q0 = p.qstart[b];
-      const int q1 = p.qstart[b + 1];
-      const long long TT = (long long)p.seqlens[b] + 1;
-      S = q1 - q0;
-      if (q0 < 0 || q1 < q0 || q1 > p.N || S > p.max_new || TT < S || TT > p.max_len) {
-        if (blockIdx.x == 0) pflag(p, GQAW_DEV_BAD_SEQLEN);
-      } else if (S >= p.s_lo && S <= p.s_hi) {
-        T = (int)TT;
-        const PTiles<KEYS> t(shp, T, S);
-        has = 1;
+__device__ inline void sched_build(const PagedParams &p, const PShape &shp, PSched *s) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, heads = shp.heads;
+    long long base = 0, units = 0;
+    int count = 0, longest = 0;
+    auto at = [&](const int32_t *x, int b, int end) { return b < end ? x[b] : 0; };
+    int q0 = at(p.qstart, lane, p.B + 1), q1 = at(p.qstart, lane + 1, p.B + 1), len = at(p.seqlens, lane, p.B);
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane, S = q1 - q0, qs = q0;
+      const long long TT = (long long)len + 1;
+      const bool bad = b < p.B && (q0 < 0 || q1 < q0 || q1 > p.N || S > p.max_new || TT < S || TT > p.max_len);
+      if (b0 + 32 < p.B) {  // the next ones, ahead of the arithmetic
+        q0 = at(p.qstart, b + 32, p.B + 1);
+        q1 = at(p.qstart, b + 33, p.B + 1);
+        len = at(p.seqlens, b + 32, p.B);
+      }
+      long long n = 0, u = 0;
+      int mx = 0;
+      const bool has = b < p.B && !bad && S >= p.s_lo && S <= p.s_hi;
+      if (bad && blockIdx.x == 0) pflag(p, GQAW_DEV_BAD_SEQLEN);
+      if (has) {
+        const PTiles<KEYS> t(shp, (int)TT, S);
         n = t.before(t.rt) * heads;
         u = (long long)t.rt * heads;
         mx = t.most();
       }
-    }
-    long long in = n, iu = u;  // inclusive scans over the warp, then over the warps
+      const uint32_t vote = __ballot_sync(0xffffffffu, has);
+      if (!vote) continue;
+      long long in = n, iu = u;  // inclusive scans
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, in, o);
-      const long long y = __shfl_up_sync(0xffffffffu, iu, o);
-      if (lane >= o) in += x, iu += y;
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, in, o);
+        const long long y = __shfl_up_sync(0xffffffffu, iu, o);
+        if (lane >= o) in += x, iu += y;
+      }
+      if (has) s->items[count + __popc(vote & ((1u << lane) - 1u))] = PItem{base + in - n, units + iu - u, b, (int)TT, qs, S};
+      count += __popc(vote);
+      longest = max(longest, __reduce_max_sync(0xffffffffu, mx));
+      base += __shfl_sync(0xffffffffu, in, 31);
+      units += __shfl_sync(0xffffffffu, iu, 31);
     }
-    const uint32_t vote = __ballot_sync(0xffffffffu, has);
-    if (lane == 31) {
-      s->wsum[warp] = in;
-      s->wunits[warp] = iu;
-      s->wcnt[warp] = __popc(vote);
-      s->wmax[warp] = mx;
+    if (lane == 0) {
+      s->V = base;
+      s->n = count;
+      s->U = units;
+      s->longest = longest;
     }
-    __syncthreads();
-    long long at = base + in - n, au = units + iu - u;
-    int ac = count + __popc(vote & ((1u << lane) - 1u));
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) at += s->wsum[w], au += s->wunits[w], ac += s->wcnt[w];
-      base += s->wsum[w];
-      units += s->wunits[w];
-      count += s->wcnt[w];
-      longest = max(longest, s->wmax[w]);
-    }
-    if (has) s->items[ac] = PItem{at, au, b, T, q0, S};
-    __syncthreads();
-  }
-  if (tid == 0) {
-    s->V = base;
-    s->n = count;
-    s->U = units;
-    s->longest = longest;
-    sched_start<KEYS>(shp, s, blockIdx.x, gridDim.x);
+    __syncwarp();
+    const PStart w = sched_start<KEYS>(shp, s, blockIdx.x, gridDim.x);
+    if (lane == 0) s->start = w;
   }
   __syncthreads();
 }

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(prow::Lay<T, D, BM>::kThreads) paged_rows_atte
   float *sp = reinterpret_cast<float *>(smem + L::kP);
   pdl_wait();
   const PShape shp = shape_of(p, kUnitCost);
-  sched_build<kKeys>(p, shp, &sched, kThreads);
+  sched_build<kKeys>(p, shp, &sched);
   PWalk<kKeys> walk(shp, &sched);
   PUnit u;
   while (walk.next(shp, u)) {

@@ -140,6 +140,9 @@ __global__ void __launch_bounds__(pdec::kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
+    ptc::prefetch_map(&maps.q);
+    ptc::prefetch_map(&maps.k);
+    ptc::prefetch_map(&maps.v);
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(pdec::kThreads, 1)
   tc::fence_proxy_async_smem();
   pdl_wait();
   const PShape shp = shape_of(p, kUnitCost);
-  sched_build<kKeys>(p, shp, sched, kThreads);
+  sched_build<kKeys>(p, shp, sched);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();

@@ -59,6 +59,10 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
   float *sp = reinterpret_cast<float *>(smem + L::kP) + warp * kKeys * 8;
   unsigned char *ring = smem + warp * S * L::kStage;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars) + warp * S;  // this warp's stages
+  if (tid == 0) {
+    ptc::prefetch_map(&maps.k);
+    ptc::prefetch_map(&maps.v);
+  }
   if (lane == 0) {
     for (int i = 0; i < S; ++i) mbar_init(&full[i], 1);
     mbar_fence_init();
@@ -66,7 +70,7 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
   __syncwarp();
   pdl_wait();
   const PShape shp = shape_of(p, kUnitCost);
-  sched_build<kKeys>(p, shp, &sched, L::kThreads);
+  sched_build<kKeys>(p, shp, &sched);
   PWalk<kKeys> walk(shp, &sched);
   PUnit u;
   const uint64_t pol = policy_evict_first();

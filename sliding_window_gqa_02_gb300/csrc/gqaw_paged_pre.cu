@@ -207,6 +207,9 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
+    ptc::prefetch_map(&maps.q);
+    ptc::prefetch_map(&maps.k);
+    ptc::prefetch_map(&maps.v);
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
     mbar_init(o_free, kSoft / 32);
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
   tc::fence_proxy_async_smem();
   pdl_wait();
   const PShape shp = shape_of(p, kUnitCost);
-  sched_build<kKeys>(p, shp, sched, kThreads);
+  sched_build<kKeys>(p, shp, sched);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -768,6 +771,9 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
+    ptc::prefetch_map(&maps.q);
+    ptc::prefetch_map(&maps.k);
+    ptc::prefetch_map(&maps.v);
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
     mbar_init(mma_done, 1);
@@ -793,7 +799,7 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
   tc::fence_proxy_async_smem();
   pdl_wait();
   const PShape shp = shape_of(p, kUnitCost);
-  sched_build<kKeys>(p, shp, sched, kThreads2);
+  sched_build<kKeys>(p, shp, sched);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();

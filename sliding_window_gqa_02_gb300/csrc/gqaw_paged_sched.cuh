@@ -61,8 +61,6 @@ struct PSched {
   long long V, U;   // cost and units in all
   int n;            // sequences with work
   int longest;      // cost of the longest unit
-  long long wsum[32], wunits[32];
-  int wcnt[32], wmax[32];
   PStart start;
 };
 
@@ -122,8 +120,35 @@ struct PTiles {
 
 constexpr int kMergeTiles = 6;
 
+// The last i in [0, n) with le(i), for le that holds at 0 and, once false, stays false.  On the
+// device a whole warp calls it: 32 places at a time, for le may be a chain of divisions.
+template <typename F>
+GQAW_HD int last_where(int n, F le) {
+  int lo = 0;
+#ifdef __CUDA_ARCH__
+  const int lane = threadIdx.x & 31;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, i < n && le(lo + i)));
+    lo += (c - 1) * step;
+    n = step < n - (c - 1) * step ? step : n - (c - 1) * step;
+  }
+#else
+  int hi = n - 1;
+  while (lo < hi) {
+    const int m = (lo + hi + 1) / 2;
+    if (le(m))
+      lo = m;
+    else
+      hi = m - 1;
+  }
+#endif
+  return lo;
+}
+
+// Where CTA `cta` starts; on the device a whole warp computes it.
 template <int KEYS>
-GQAW_HD void sched_start(const PShape &p, PSched *s, int cta, int grid) {
+GQAW_HD PStart sched_start(const PShape &p, const PSched *s, int cta, int grid) {
   PStart w;
   const long long V = s->V;
   const int heads = p.heads;
@@ -141,14 +166,7 @@ GQAW_HD void sched_start(const PShape &p, PSched *s, int cta, int grid) {
     w.te = cta < w.G ? (cta + 1) * V / w.G : 0;
   }
   if (w.tb < w.te) {
-    int a = 0, b = s->n - 1;  // the last item that starts at or before tb
-    while (a < b) {
-      const int m = (a + b + 1) / 2;
-      if ((w.whole ? s->items[m].units : s->items[m].tiles) <= w.tb)
-        a = m;
-      else
-        b = m - 1;
-    }
+    const int a = last_where(s->n, [&](int m) { return (w.whole ? s->items[m].units : s->items[m].tiles) <= w.tb; });
     w.it = a;
     const PItem &x = s->items[a];
     const PTiles<KEYS> t(p, x.T, x.S);
@@ -160,20 +178,13 @@ GQAW_HD void sched_start(const PShape &p, PSched *s, int cta, int grid) {
       const long long per = t.before(t.rt), off = w.tb - x.tiles;
       w.hu = (int)(off / per);
       const long long rem = off - w.hu * per;
-      int c = 0, d = t.rt - 1;
-      while (c < d) {
-        const int m = (c + d + 1) / 2;
-        if (t.before(m) <= rem)
-          c = m;
-        else
-          d = m - 1;
-      }
+      const int c = last_where(t.rt, [&](int m) { return t.before(m) <= rem; });
       w.r = c;
       w.pos = x.tiles + w.hu * per + t.before(c);
     }
     if (w.hu >= heads) w.te = w.tb;  // cannot happen: the counts above are of these units
   }
-  s->start = w;
+  return w;
 }
 
 // The unit a walker stands on, and the part of its key tiles that this CTA does.

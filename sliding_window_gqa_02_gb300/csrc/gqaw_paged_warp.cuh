@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(pwarp::Lay<T, D>::kThreads, pwarp::Lay<T, D>::
   unsigned char *ring = smem + warp * S * L::kStage;
   pdl_wait();
   const PShape shp = shape_of(p, kUnitCost);
-  sched_build<kKeys>(p, shp, &sched, L::kThreads);
+  sched_build<kKeys>(p, shp, &sched);
   PWalk<kKeys> walk(shp, &sched);
   PUnit u;
   while (walk.next(shp, u)) {

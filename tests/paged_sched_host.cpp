@@ -34,7 +34,7 @@ long long paged_schedule(const int *lens, int n, int tpt, int window, int heads,
       row += S;
     }
     for (int cta = 0; cta < grid; ++cta) {
-      sched_start<KEYS>(p, s, cta, grid);
+      s->start = sched_start<KEYS>(p, s, cta, grid);
       PWalk<KEYS> w(p, s);
       PUnit u;
       while (w.next(p, u)) {
