@@ -115,6 +115,45 @@ __device__ __forceinline__ float paged_sink_log2(const PagedParams &p, int h) {
   return p.sink_mode == 2 ? 0.f : -INFINITY;
 }
 
+// A row of a cut unit from the partial results of CTAs [cf, cl], for this thread's elements d, d +
+// 128, ...: at(c) is the row in CTA c's block, D weighted sums and behind them the row's maximum
+// (log2) and sum of weights.  Eight parts are loaded before the first is used, since each is a
+// round trip to L2 (19 parts one after the other took 20 us); their order is fixed.
+template <int D, int ND, typename At>
+__device__ __forceinline__ void merge_row(int cf, int cl, int d, At at, float &M, float &S, float (&A)[ND]) {
+  M = -INFINITY;
+  S = 0.f;
+#pragma unroll
+  for (int k = 0; k < ND; ++k) A[k] = 0.f;
+  for (int c0 = cf; c0 <= cl; c0 += 8) {
+    float m[8], s[8], a[8][ND];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = c0 + i <= cl;
+      const float *q = at(in ? c0 + i : cl);
+      m[i] = in ? __ldcg(q + D) : -INFINITY;
+      s[i] = in ? __ldcg(q + D + 1) : 0.f;
+#pragma unroll
+      for (int k = 0; k < ND; ++k) a[i][k] = in && d + k * 128 < D ? __ldcg(q + d + k * 128) : 0.f;
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, m[i]);
+    const float ref = top == -INFINITY ? 0.f : top, f0 = exp2f(M - ref);
+    S *= f0;
+#pragma unroll
+    for (int k = 0; k < ND; ++k) A[k] *= f0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = exp2f(m[i] - ref);
+      S = fmaf(f, s[i], S);
+#pragma unroll
+      for (int k = 0; k < ND; ++k) A[k] = fmaf(f, a[i][k], A[k]);
+    }
+    M = top;
+  }
+}
+
 // softcap: tanh with its own saturation; an absolute error of about 1e-7
 __device__ __forceinline__ float cap_logit(const PagedParams &p, float x) { return p.capmul * tanhf(x); }
 

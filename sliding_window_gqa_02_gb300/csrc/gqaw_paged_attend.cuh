@@ -370,18 +370,10 @@ __global__ void __launch_bounds__(prow::Lay<T, D, BM>::kThreads) paged_rows_atte
         __threadfence();
         for (int e = tid; e < rows * D; e += kThreads) {
           const int r = e / D, d = e - r * D, tok = r / g, h = h0 + r - tok * g;
-          float M = -INFINITY, A = 0.f, S = 0.f;
-          for (int c = cf; c <= cl; ++c)
-            M = fmaxf(M, __ldcg(p.partials + ((long long)c * 2 + (c == cf)) * BM * PS + r * PS + D));
-          const float ref = M == -INFINITY ? 0.f : M;
-          for (int c = cf; c <= cl; ++c) {
-            const float *q = p.partials + ((long long)c * 2 + (c == cf)) * BM * PS + r * PS;
-            const float f = exp2f(__ldcg(q + D) - ref);
-            S = fmaf(f, __ldcg(q + D + 1), S);
-            A = fmaf(f, __ldcg(q + d), A);
-          }
+          float M, S, A[1];
+          merge_row<D, 1>(cf, cl, d, [&](int c) { return p.partials + ((long long)c * 2 + (c == cf)) * BM * PS + r * PS; }, M, S, A);
           out[(u.row0 + tok) * p.os + (long long)h * D + d] =
-              Elem<T>::store(A * sink_reciprocal(S, M, paged_sink_log2(p, h)));
+              Elem<T>::store(A[0] * sink_reciprocal(S, M, paged_sink_log2(p, h)));
         }
         if (tid == 0) p.tickets[cf] = 0u;
       }

@@ -583,21 +583,8 @@ __global__ void __launch_bounds__(pdec::kThreads, 1)
           for (int i = 0; i < NC; ++i) {
             const int n = col0 + i;
             if (n < NV) {
-              float M = -INFINITY, S = 0.f, A[DM];
-#pragma unroll
-              for (int m = 0; m < DM; ++m) A[m] = 0.f;
-#pragma unroll 4
-              for (int c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(at(c) + n * PS + D));
-              const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-              for (int c = cf; c <= cl; ++c) {
-                const float *q = at(c) + n * PS;
-                const float f = fast_exp2(__ldcg(q + D) - ref);
-                S = fmaf(f, __ldcg(q + D + 1), S);
-#pragma unroll
-                for (int m = 0; m < DM; ++m)
-                  if (m * 128 + t < D) A[m] = fmaf(f, __ldcg(q + m * 128 + t), A[m]);
-              }
+              float M, S, A[DM];
+              merge_row<D, DM>(cf, cl, t, [&](int c) { return at(c) + n * PS; }, M, S, A);
               const int tok = n / g, h = u.hu * g + n - tok * g;
               const float inv = sink_reciprocal(S, M, paged_sink_log2(p, h));
               __nv_bfloat16 *row = out + (u.row0 + tok) * p.os + (long long)h * D;

@@ -5,7 +5,8 @@
 // its own, a reference maximum that rarely moves), which measured 2000 instructions per 32 keys
 // on four warps a SM, many of them address arithmetic of the loads, and ran at a quarter of the
 // memory's rate.  Here the tiles come by tensor TMA through the page table, a few instructions
-// each, and are half as tall, so that twice the warps fit:
+// each, and are half as tall, so that more warps fit (head size 64: 12 warps with two stages each,
+// 8 contexts of 8192 with 4 rows 57 us, against 71 with 8 warps of three; 8 rows 94 against 103):
 //   - a tile is 16 keys; K and V in blocks of 32 dimensions, rows of 128 bytes in the 128-byte
 //     swizzle, whose exclusive-or of the 16-byte part with the row is what lets neighbouring
 //     lanes read neighbouring keys without a bank conflict;
@@ -24,14 +25,14 @@ using prow::fma2;
 using prow::pk;
 using prow::unpk;
 constexpr int kKeys = 16;
-constexpr int kUnitCost = 6;  // see gqaw_paged_sched.cuh
+constexpr int kUnitCost = 24;  // see gqaw_paged_sched.cuh; 6 to 64 differ by 8% here
 
 template <int D>
 struct Lay {
   static constexpr int B = D / 32;                     // blocks of 32 dimensions
   static constexpr int kBlock = kKeys * 128;           // bytes of a block
   static constexpr int kStage = 2 * B * kBlock;        // K and V
-  static constexpr int W = D == 128 ? 6 : 8, S = D == 32 ? 4 : D == 64 ? 3 : 2;
+  static constexpr int W = D == 128 ? 6 : D == 64 ? 12 : 8, S = D == 32 ? 4 : 2;
   static constexpr int kThreads = 32 * W;
   static constexpr int kQ = W * S * kStage;            // [8][D] fp32, scaled
   static constexpr int kP = kQ + 8 * D * 4;            // [W][16 keys][8 rows]
@@ -293,19 +294,9 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
         __threadfence();
         for (int e = tid; e < rows * D; e += L::kThreads) {
           const int r = e / D, d = e - r * D, tok = r / g, h = u.hu * g + r - tok * g;
-          float M = -INFINITY, A = 0.f, Z = 0.f;
-#pragma unroll 4
-          for (int c = cf; c <= cl; ++c)
-            M = fmaxf(M, __ldcg(p.partials + ((long long)c * 2 + (c == cf)) * 16 * PS + r * PS + D));
-          const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-          for (int c = cf; c <= cl; ++c) {
-            const float *x = p.partials + ((long long)c * 2 + (c == cf)) * 16 * PS + r * PS;
-            const float f = exp2f(__ldcg(x + D) - ref);
-            Z = fmaf(f, __ldcg(x + D + 1), Z);
-            A = fmaf(f, __ldcg(x + d), A);
-          }
-          out[(u.row0 + tok) * p.os + (long long)h * D + d] = A * sink_reciprocal(Z, M, paged_sink_log2(p, h));
+          float M, Z, A[1];
+          merge_row<D, 1>(cf, cl, d, [&](int c) { return p.partials + ((long long)c * 2 + (c == cf)) * 16 * PS + r * PS; }, M, Z, A);
+          out[(u.row0 + tok) * p.os + (long long)h * D + d] = A[0] * sink_reciprocal(Z, M, paged_sink_log2(p, h));
         }
         if (tid == 0) p.tickets[cf] = 0u;
       }

@@ -301,19 +301,9 @@ __global__ void __launch_bounds__(pwarp::Lay<T, D>::kThreads, pwarp::Lay<T, D>::
         __threadfence();
         for (int e = tid; e < rows * D; e += L::kThreads) {
           const int r = e / D, d = e - r * D, tok = r / g, h = h0 + r - tok * g;
-          float M = -INFINITY, A = 0.f, Z = 0.f;
-#pragma unroll 4
-          for (int c = cf; c <= cl; ++c)
-            M = fmaxf(M, __ldcg(p.partials + ((long long)c * 2 + (c == cf)) * 16 * PS + r * PS + D));
-          const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-          for (int c = cf; c <= cl; ++c) {
-            const float *x = p.partials + ((long long)c * 2 + (c == cf)) * 16 * PS + r * PS;
-            const float f = exp2f(__ldcg(x + D) - ref);
-            Z = fmaf(f, __ldcg(x + D + 1), Z);
-            A = fmaf(f, __ldcg(x + d), A);
-          }
-          out[(u.row0 + tok) * p.os + (long long)h * D + d] = Elem<T>::store(A * sink_reciprocal(Z, M, paged_sink_log2(p, h)));
+          float M, Z, A[1];
+          merge_row<D, 1>(cf, cl, d, [&](int c) { return p.partials + ((long long)c * 2 + (c == cf)) * 16 * PS + r * PS; }, M, Z, A);
+          out[(u.row0 + tok) * p.os + (long long)h * D + d] = Elem<T>::store(A[0] * sink_reciprocal(Z, M, paged_sink_log2(p, h)));
         }
         if (tid == 0) p.tickets[cf] = 0u;
       }
