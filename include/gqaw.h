@@ -421,12 +421,20 @@ gqaw_status gqaw_paged_append(const gqaw_paged_args *args, void *stream);
  * already.  The token at position i attends the keys j <= i (and j > i - W with a window)
  * of its sequence; logits, softcap, sinks and head grouping as in gqa_windowed_step.  The
  * query is taken as it is given: query_weight and the tables are not applied.  Cache rows
- * that a token does not attend never reach its output, whatever they hold. */
+ * that a token does not attend never reach its output, whatever they hold; one that it does
+ * attend and that is not finite makes the elements of its output that depend on it not finite
+ * or, for a key, unspecified.  bf16 on the tensor cores (head sizes from 64, pages of a power of
+ * two rows, or a multiple of 128, from 8 on) rounds the softmax weights to bf16 where a kv head
+ * has more than 8 rows of queries in a tile; sums and statistics are fp32 throughout.  One
+ * kernel, or two where single tokens and long chunks come together; the same inputs give the
+ * same bits. */
 gqaw_status gqaw_paged_attend(const gqaw_paged_args *args, void *stream);
 
-/* The whole step: append, and attention of the normed and turned queries (rounded to dtype
- * in the workspace).  Two kernels; the same results as gqaw_qk_norm_rotary of the query,
- * gqaw_paged_append and gqaw_paged_attend in turn. */
+/* The whole step: append, and attention of the normed and turned queries.  The cache is the one
+ * that gqaw_paged_append leaves, and the output that of gqaw_qk_norm_rotary of the query and
+ * gqaw_paged_attend, but closer to the formula in bf16: what the queries lose in their rounding
+ * is kept beside them in the workspace and multiplies the keys too (not for head size 256 with
+ * more than 8 rows of queries per kv head). */
 gqaw_status gqaw_paged_step(const gqaw_paged_args *args, void *stream);
 
 /* sizeof(gqaw_qk_args) and sizeof(gqaw_paged_args) as compiled into the library. */

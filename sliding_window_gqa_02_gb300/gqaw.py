@@ -433,6 +433,8 @@ def _rows(name, t, heads: int, head_size: int, like=None):
                          % (name, heads * head_size, heads, head_size, tuple(t.shape)))
     if heads and t.shape[0] and (t.stride(-1) != 1 or (t.dim() == 3 and heads > 1 and t.stride(1) != head_size)):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
+    if t.shape[0] > 1 and t.stride(0) < heads * head_size:  # 0 (an expanded tensor) would mean contiguous rows
+        raise ValueError("%s: tokens must not overlap" % name)
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise ValueError("%s: must have the dtype and device of the other tensors" % name)
     return _ptr(t), int(t.stride(0)) if t.shape[0] > 1 else 0
@@ -469,6 +471,14 @@ def _tables(a, cos_cache, sin_cache, interleaved, like):
     a.rotary_interleaved = int(bool(interleaved))
 
 
+def _workspace(a, t, like):
+    if t is None:
+        return
+    if t.device != like.device or not t.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on the rows' device")
+    a.workspace, a.workspace_bytes = _ptr(t), int(t.numel() * t.element_size())
+
+
 def make_qk_args(query, key, query_out, key_out, num_heads: int, kv_num_heads: int, head_size: int,
                  query_weight=None, key_weight=None, norm_eps: float = 1e-6, cos_cache=None, sin_cache=None,
                  position_ids=None, rotary_interleaved: bool = False, workspace=None) -> gqaw_qk_args:
@@ -497,8 +507,7 @@ def make_qk_args(query, key, query_out, key_out, num_heads: int, kv_num_heads: i
     a.key_weight = _vector("key_weight", key_weight, head_size, like)
     _tables(a, cos_cache, sin_cache, rotary_interleaved, like)
     a.position_ids = _index("position_ids", position_ids, "int64", (a.num_tokens,), like)
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = _ptr(workspace), int(workspace.numel() * workspace.element_size())
+    _workspace(a, workspace, like)
     return a
 
 
@@ -524,6 +533,8 @@ def make_paged_args(query, key, value, key_pages, value_pages, page_table, query
         raise ValueError("key_pages and value_pages: equal 4-dimensional tensors")
     if tuple(key_pages.stride()) != tuple(value_pages.stride()) or key_pages.stride(-1) != 1:
         raise ValueError("key_pages and value_pages: equal strides, the last dimension contiguous")
+    if any(n > 1 and st < key_pages.shape[3] for n, st in zip(key_pages.shape[:3], key_pages.stride()[:3])):
+        raise ValueError("key_pages and value_pages: rows must not overlap")
     pages, d1, d2, D = (int(x) for x in key_pages.shape)
     heads, page = (d2, d1) if heads_inside_rows else (d1, d2)
     if heads != kv_num_heads:
@@ -563,8 +574,7 @@ def make_paged_args(query, key, value, key_pages, value_pages, page_table, query
     a.key_weight = _vector("key_weight", key_weight, D, like)
     _tables(a, cos_cache, sin_cache, rotary_interleaved, like)
     a.position_ids = _index("position_ids", position_ids, "int64", (a.total_new_tokens,), like)
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = _ptr(workspace), int(workspace.numel() * workspace.element_size())
+    _workspace(a, workspace, like)
     return a
 
 

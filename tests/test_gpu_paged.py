@@ -361,3 +361,57 @@ def test_offsets_past_32_bits(dtype):
         b.call(gqaw.gqaw_paged_step)
         b.check_output()
         assert used.numel()
+
+
+def test_host_memory_is_refused():
+    """A workspace or query that is not this device's memory is refused before any launch."""
+    b = Batch([(1, 40)], 4, 2, 64, 16, BF, seed=23, norm=True, rotary=64)
+    a = b.args()
+    n0, stream = gqaw.gqaw_launch_count(), torch.cuda.current_stream().cuda_stream
+    host = torch.zeros(a.workspace_bytes + 256, dtype=torch.uint8).pin_memory()
+    a.workspace = (host.data_ptr() + 255) // 256 * 256
+    for fn in (gqaw.gqaw_paged_append, gqaw.gqaw_paged_attend, gqaw.gqaw_paged_step):
+        assert fn(a, stream) == gqaw.GQAW_EINVAL
+    rows = torch.zeros(3, 4 * 64, dtype=BF).pin_memory()
+    q = gqaw.gqaw_qk_args(num_tokens=3, num_heads=4, head_size=64, dtype=gqaw.GQAW_BF16, query=rows.data_ptr(),
+                          query_out=rows.data_ptr())
+    assert gqaw.gqaw_qk_norm_rotary(q, stream) == gqaw.GQAW_EINVAL
+    assert gqaw.gqaw_launch_count() == n0
+
+
+def test_steps_one_after_the_other_without_waiting():
+    """Steps of several shapes enqueued together through one workspace, each reading what the
+    one before it appended: the bits of the same steps with a wait between them."""
+    outs = []
+    for wait in (True, False):
+        g = torch.Generator().manual_seed(24)
+        Nq, Nkv, D, page = 16, 4, 128, 16
+        steps = [300, 1, 7, 1, 90, 1, 1]
+        total = sum(steps)
+        kp, vp = (torch.zeros(total // page + 1, Nkv, page, D, dtype=BF, device="cuda") for _ in range(2))
+        table = torch.randperm(kp.shape[0], generator=g).to(torch.int32)[None].cuda()
+        w = (torch.rand(D, generator=g) + 0.5).to(BF).cuda()
+        calls, T = [], 0
+        for S in steps:
+            q, k, v = (torch.randn(S, n * D, generator=g).to(BF).cuda() for n in (Nq, Nkv, Nkv))
+            T += S
+            calls.append(gqaw.make_paged_args(q, k, v, kp, vp, table, torch.tensor([0, S], dtype=torch.int32, device="cuda"),
+                                              torch.tensor([T - 1], dtype=torch.int32, device="cuda"), S, total, Nq, Nkv,
+                                              torch.empty_like(q), query_weight=w, key_weight=w))
+            calls[-1].keep = (q, k, v)
+        size = max(gqaw.gqaw_paged_workspace_bytes(a) for a in calls)
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.current_stream().cuda_stream
+        gqaw.check(gqaw.gqaw_workspace_init(ws.data_ptr(), size, stream))
+        out = [torch.zeros(S, Nq * D, dtype=BF, device="cuda") for S in steps]
+        for a, o in zip(calls, out):
+            a.workspace, a.workspace_bytes, a.output = ws.data_ptr(), size, o.data_ptr()
+        torch.cuda.synchronize()
+        for a in calls:
+            gqaw.check(gqaw.gqaw_paged_step(a, stream))
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        outs.append(out + [kp])
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)

@@ -230,3 +230,25 @@ def test_binding_checks_shapes(lib):
                 dict(position_ids=torch.zeros(5)), dict(key=torch.zeros(5, Nkv * D, dtype=torch.bfloat16))):
         with pytest.raises((ValueError, TypeError)):
             lib.make_qk_args(**dict(q, **bad))
+
+
+def test_binding_refuses_overlapping_rows_and_foreign_workspaces(lib):
+    """A stride of 0 means contiguous rows to the library: an expanded tensor is refused before that."""
+    one = torch.zeros(1, 4 * 16)
+    rows, kv, pages = torch.zeros(5, 4 * 16), torch.zeros(5, 2 * 16), torch.zeros(3, 2, 8, 16)
+    table, start, lens = torch.zeros(1, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+
+    def paged(q=rows, k=kv, kp=pages, **kw):
+        return lib.make_paged_args(q, k, kv, kp, kp, table, start, lens, 5, 24, 4, 2, rows, **kw)
+
+    paged()
+    for kw in (dict(q=one.expand(5, -1)), dict(k=torch.zeros(5 * 32).as_strided((5, 32), (16, 1))),
+               dict(kp=torch.zeros(1, 1, 1, 16).expand(3, 2, 8, 16)), dict(kp=torch.zeros(1, 2, 8, 16).expand(3, 2, 8, 16)),
+               dict(workspace=torch.zeros(4096, dtype=torch.uint8, device="meta")),
+               dict(workspace=torch.zeros(8192, dtype=torch.uint8)[::2])):
+        with pytest.raises(ValueError):
+            paged(**kw)
+    lib.make_qk_args(rows, None, rows, None, 4, 0, 16)
+    for q, kw in ((one.expand(5, -1), {}), (rows, dict(workspace=torch.zeros(256, dtype=torch.uint8, device="meta")))):
+        with pytest.raises(ValueError):
+            lib.make_qk_args(q, None, rows, None, 4, 0, 16, **kw)
