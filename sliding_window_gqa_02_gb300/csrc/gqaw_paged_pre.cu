@@ -16,7 +16,10 @@
 // unit 18%).  The four share the row's maximum through shared memory; the reference moves only
 // when exceeded by more than 2^8, so O is rarely rescaled.  Sums are fp32 of the unrounded
 // weights; P is rounded to bf16 for its product (2^-9 relative, the size of the output's own
-// rounding).  Warps without rows (a decoding sequence among chunks has `group` rows of the 128)
+// rounding: what bf16 leaves of P would cost a second product).  Queries that the step has turned
+// come in two bf16 parts (SPLIT, head sizes 64 and 128) and S is the sum of two products: error
+// of a whole prompt step 0.0025 -> 0.0020 for 8% more time, where the outputs' own rounding is
+// 0.0016.  Warps without rows (a decoding sequence among chunks has `group` rows of the 128)
 // only keep the barriers turning.
 //
 // Tensor memory (512 columns), head sizes 64 and 128: S in two buffers [0, 256), O from 256,
@@ -707,8 +710,11 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
 // half's products run.  That also means O may be rescaled as soon as S(k + 1) is there.
 //
 // Warps: 0-3 softmax of the first half, 4-7 of the second, 8 MMA issue, 9 loads of Q and K,
-// 10 loads of V, 11 idle (whole warpgroups).  A half skips the key tiles that none of its rows attends.  The value rows of
-// a tile are checked (see above) by the first half that uses the tile.
+// 10 loads of V, 11 idle (whole warpgroups).  A half skips the key tiles that none of its rows
+// attends.  The value rows of a tile are checked (see above) by the first half that uses the tile.
+// Measured: 8 chunks of 512 tokens with a window of 4096 in 318 us (865 TFLOP/s), a prompt of 8192
+// in 0.54 ms (1015 TFLOP/s, 53% of the measured bf16 rate); tensor pipe 39% busy, issue slots
+// 31%, exponential unit 20%, DRAM 43%: the chain of a half is the limit, no unit.
 
 namespace ppre {
 
@@ -807,154 +813,154 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
   const int g = p.group, t1 = p.tpt / 2;
 
   if (warp >= kMmaWarp2) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == kKWarp2 || warp == kVWarp2) {
-    // ------------------------------------------------------------ loads (whole warp)
-    const bool value = warp == kVWarp2;
-    const uint64_t pol = tc::policy_evict_normal(), qpol = policy_evict_first();
-    uint64_t *full = value ? v_full : k_full, *empty = value ? v_free : k_free;
-    unsigned char *ring = smem + (value ? L::kV : L::kK);
-    const CUtensorMap *map = value ? &maps.v : &maps.k;
-    PWalk<kKeys> w(shp, sched);
-    PUnit u;
-    ptc::Boxes bx;
-    int gk = 0, qi = 0;
-    bool fine = true;
-    while (fine && w.next(shp, u)) {
-      bx.unit(p, u);
-      bx.look_up(p, u.kt + u.k0, lane);
-      for (int k = u.k0; k < u.k1; ++k, ++gk) {
-        const uint32_t mask = bx.valid(p, u.kt + k, lane);
-        const ptc::Boxes cur = bx;
-        if (k + 1 < u.k1) bx.look_up(p, u.kt + k + 1, lane);
-        const int st = gk % L::kSt;
-        if (gk >= L::kSt) fine = mbar_wait(&empty[st], ((gk / L::kSt) & 1) ^ 1);
-        fine = __all_sync(0xffffffffu, fine && !*abort_flag);
-        if (!fine) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * bx.rows * 128 * L::HALVES));
-        __syncwarp();
-        cur.load<L::HALVES>(map, ring + st * L::kTile, &full[st], pol, mask, lane);
-        // the queries after the unit's first K tile, once the last S product with the previous
-        // ones is done
-        if (k == u.k0 && !value) {
-          if (qi > 0) fine = mbar_wait(q_free, (qi - 1) & 1);
-          fine = __all_sync(0xffffffffu, fine);
-          if (!fine) {
-            ++gk;
-            break;
-          }
-          if (lane == 0) {
-            const int parts = u.ntok > t1 ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, (uint32_t)(parts * QP * L::HALVES * g * t1 * 128));
-            for (int x = 0; x < parts; ++x)
-              for (int h = 0; h < QP * L::HALVES; ++h)
-                tc::tma_load_3d(smem + L::kQ + x * QP * L::kTile + h * kHalf, h < L::HALVES ? &maps.q : &maps.ql,
-                                h % L::HALVES * 64, u.hu * g, u.row0 + x * t1, q_full, qpol);
-          }
-          ++qi;
-        }
-      }
-    }
-    if (lane == 0) {
-      if (!fine) {
-        pflag(p, GQAW_DEV_TIMEOUT);
-        *abort_flag = 1;
-      }
-      // no copy may still be landing in shared memory when the CTA exits
-      for (int j = gk > L::kSt ? gk - L::kSt : 0; j < gk; ++j)
-        if (!mbar_wait(&full[j % L::kSt], (j / L::kSt) & 1)) pflag(p, GQAW_DEV_TIMEOUT);
-      if (!value && qi > 0 && !mbar_wait(q_full, (qi - 1) & 1)) pflag(p, GQAW_DEV_TIMEOUT);
-    }
-  } else if (warp == kMmaWarp2) {
-    // ------------------------------------------------------------ MMA issue
-    // The whole warp runs the loop and one elected thread issues: descriptors and addresses are
-    // then uniform values, which is what the instruction takes.
-    {
-      constexpr uint32_t kIdescQK = tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
-      constexpr uint32_t kIdescPV = tc::idesc_bf16_f32(kRows, D, 0, 1);
-      const uint64_t dq = tc::smem_desc_sw128(smem + L::kQ, 16, 1024);
-      const uint64_t dk = tc::smem_desc_sw128(smem + L::kK, 16, 1024);
-      const uint64_t dv = tc::smem_desc_sw128(smem + L::kV, kHalf, 1024);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kKWarp2 || warp == kVWarp2) {
+      // ------------------------------------------------------------ loads (whole warp)
+      const bool value = warp == kVWarp2;
+      const uint64_t pol = tc::policy_evict_normal(), qpol = policy_evict_first();
+      uint64_t *full = value ? v_full : k_full, *empty = value ? v_free : k_free;
+      unsigned char *ring = smem + (value ? L::kV : L::kK);
+      const CUtensorMap *map = value ? &maps.v : &maps.k;
       PWalk<kKeys> w(shp, sched);
       PUnit u;
-      Halves hv{};
-      int gk = 0, qi = 0, pvs[2] = {0, 0}, outs[2] = {0, 0};  // products O += P V issued, units finished
-      // S of half x for tile k of the unit, once the half's last P V has completed
-      auto s_product = [&](int x, int k) -> bool {
-        const int kt = gk + k - u.k0, st = kt % L::kSt;
-        if (!warp_wait(&k_full[st], (kt / L::kSt) & 1)) return false;
-        if (pvs[x] > 0 && !warp_wait(&pv_done[x], (pvs[x] - 1) & 1)) return false;
-        tc::fence_after_sync();
-        const uint64_t a0 = dq + (uint64_t)((x * QP * L::kTile) >> 4), b0 = dk + (uint64_t)((st * L::kTile) >> 4);
-        const bool second = hv.a[1] <= k && k < hv.b[1];
-        if (elect_one()) {
-#pragma unroll 1
-          for (int q = 0; q < QP; ++q) {  // not unrolled: the descriptors of 16 products would spill
-            const uint64_t aq = a0 + (uint64_t)((q * L::kTile) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk / 4) * kHalf + (kk % 4) * 32) >> 4);
-              tc::mma_bf16_ss(tmem + x * kKeys, aq + off, b0 + off, kIdescQK, q + kk > 0);
-            }
-          }
-          tc::mma_commit(&s_full[x]);
-          if (x == 1 || !second) tc::mma_commit(&k_free[st]);
-          // the unit's last S product: the second half's, if it has any tile here
-          if (k + 1 == hv.b[x] && x == (hv.a[1] < hv.b[1] ? 1 : 0)) tc::mma_commit(q_free);
-        }
-        __syncwarp();
-        return true;
-      };
+      ptc::Boxes bx;
+      int gk = 0, qi = 0;
       bool fine = true;
-      while (fine && __all_sync(0xffffffffu, !*abort_flag) && w.next(shp, u)) {
-        hv = halves_of(p, u);
-        fine = warp_wait(q_full, qi & 1);
-        for (int x = 0; x < 2 && fine; ++x)
-          if (hv.a[x] == u.k0 && hv.a[x] < hv.b[x]) fine = s_product(x, u.k0);
-        for (int k = u.k0; k < u.k1 && fine; ++k) {
-          const int kt = gk + k - u.k0, st = kt % L::kSt;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!fine) break;
-            if (hv.a[x] <= k && k < hv.b[x]) {
-              const bool first = k == hv.a[x];
-              fine = warp_wait(&p_full[x], pvs[x] & 1) &&
-                     // the first P V of a unit overwrites O: the softmax has read the last unit's
-                     (!first || outs[x] == 0 || warp_wait(&o_free[x], (outs[x] - 1) & 1)) &&
-                     warp_wait(&v_full[st], (kt / L::kSt) & 1);
-              if (!fine) break;
-              tc::fence_after_sync();
-              const uint64_t b0 = dv + (uint64_t)((st * L::kTile) >> 4);
-              const bool second = hv.a[1] <= k && k < hv.b[1];
-              if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                  tc::mma_bf16_ts(tmem + 256 + x * D, tmem + x * kKeys + kk * 8, b0 + (uint64_t)((kk * 16 * 128) >> 4), kIdescPV,
-                                  !first || kk > 0);
-                tc::mma_commit(&pv_done[x]);
-                if (x == 1 || !second) tc::mma_commit(&v_free[st]);
-              }
-              __syncwarp();
-              ++pvs[x];
-              if (k + 1 < hv.b[x]) fine = s_product(x, k + 1);
-            } else if (k + 1 == hv.a[x] && hv.a[x] < hv.b[x]) {
-              fine = s_product(x, k + 1);
+      while (fine && w.next(shp, u)) {
+        bx.unit(p, u);
+        bx.look_up(p, u.kt + u.k0, lane);
+        for (int k = u.k0; k < u.k1; ++k, ++gk) {
+          const uint32_t mask = bx.valid(p, u.kt + k, lane);
+          const ptc::Boxes cur = bx;
+          if (k + 1 < u.k1) bx.look_up(p, u.kt + k + 1, lane);
+          const int st = gk % L::kSt;
+          if (gk >= L::kSt) fine = mbar_wait(&empty[st], ((gk / L::kSt) & 1) ^ 1);
+          fine = __all_sync(0xffffffffu, fine && !*abort_flag);
+          if (!fine) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * bx.rows * 128 * L::HALVES));
+          __syncwarp();
+          cur.load<L::HALVES>(map, ring + st * L::kTile, &full[st], pol, mask, lane);
+          // the queries after the unit's first K tile, once the last S product with the previous
+          // ones is done
+          if (k == u.k0 && !value) {
+            if (qi > 0) fine = mbar_wait(q_free, (qi - 1) & 1);
+            fine = __all_sync(0xffffffffu, fine);
+            if (!fine) {
+              ++gk;
+              break;
             }
+            if (lane == 0) {
+              const int parts = u.ntok > t1 ? 2 : 1;
+              mbar_arrive_expect_tx(q_full, (uint32_t)(parts * QP * L::HALVES * g * t1 * 128));
+              for (int x = 0; x < parts; ++x)
+                for (int h = 0; h < QP * L::HALVES; ++h)
+                  tc::tma_load_3d(smem + L::kQ + x * QP * L::kTile + h * kHalf, h < L::HALVES ? &maps.q : &maps.ql,
+                                  h % L::HALVES * 64, u.hu * g, u.row0 + x * t1, q_full, qpol);
+            }
+            ++qi;
           }
         }
+      }
+      if (lane == 0) {
+        if (!fine) {
+          pflag(p, GQAW_DEV_TIMEOUT);
+          *abort_flag = 1;
+        }
+        // no copy may still be landing in shared memory when the CTA exits
+        for (int j = gk > L::kSt ? gk - L::kSt : 0; j < gk; ++j)
+          if (!mbar_wait(&full[j % L::kSt], (j / L::kSt) & 1)) pflag(p, GQAW_DEV_TIMEOUT);
+        if (!value && qi > 0 && !mbar_wait(q_full, (qi - 1) & 1)) pflag(p, GQAW_DEV_TIMEOUT);
+      }
+    } else if (warp == kMmaWarp2) {
+      // ------------------------------------------------------------ MMA issue
+      // The whole warp runs the loop and one elected thread issues: descriptors and addresses are
+      // then uniform values, which is what the instruction takes.
+      {
+        constexpr uint32_t kIdescQK = tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
+        constexpr uint32_t kIdescPV = tc::idesc_bf16_f32(kRows, D, 0, 1);
+        const uint64_t dq = tc::smem_desc_sw128(smem + L::kQ, 16, 1024);
+        const uint64_t dk = tc::smem_desc_sw128(smem + L::kK, 16, 1024);
+        const uint64_t dv = tc::smem_desc_sw128(smem + L::kV, kHalf, 1024);
+        PWalk<kKeys> w(shp, sched);
+        PUnit u;
+        Halves hv{};
+        int gk = 0, qi = 0, pvs[2] = {0, 0}, outs[2] = {0, 0};  // products O += P V issued, units finished
+        // S of half x for tile k of the unit, once the half's last P V has completed
+        auto s_product = [&](int x, int k) -> bool {
+          const int kt = gk + k - u.k0, st = kt % L::kSt;
+          if (!warp_wait(&k_full[st], (kt / L::kSt) & 1)) return false;
+          if (pvs[x] > 0 && !warp_wait(&pv_done[x], (pvs[x] - 1) & 1)) return false;
+          tc::fence_after_sync();
+          const uint64_t a0 = dq + (uint64_t)((x * QP * L::kTile) >> 4), b0 = dk + (uint64_t)((st * L::kTile) >> 4);
+          const bool second = hv.a[1] <= k && k < hv.b[1];
+          if (elect_one()) {
+#pragma unroll 1
+            for (int q = 0; q < QP; ++q) {  // not unrolled: the descriptors of 16 products would spill
+              const uint64_t aq = a0 + (uint64_t)((q * L::kTile) >> 4);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) outs[x] += hv.a[x] < hv.b[x] ? 1 : 0;
-        gk += u.k1 - u.k0;
-        ++qi;
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (uint64_t)(((kk / 4) * kHalf + (kk % 4) * 32) >> 4);
+                tc::mma_bf16_ss(tmem + x * kKeys, aq + off, b0 + off, kIdescQK, q + kk > 0);
+              }
+            }
+            tc::mma_commit(&s_full[x]);
+            if (x == 1 || !second) tc::mma_commit(&k_free[st]);
+            // the unit's last S product: the second half's, if it has any tile here
+            if (k + 1 == hv.b[x] && x == (hv.a[1] < hv.b[1] ? 1 : 0)) tc::mma_commit(q_free);
+          }
+          __syncwarp();
+          return true;
+        };
+        bool fine = true;
+        while (fine && __all_sync(0xffffffffu, !*abort_flag) && w.next(shp, u)) {
+          hv = halves_of(p, u);
+          fine = warp_wait(q_full, qi & 1);
+          for (int x = 0; x < 2 && fine; ++x)
+            if (hv.a[x] == u.k0 && hv.a[x] < hv.b[x]) fine = s_product(x, u.k0);
+          for (int k = u.k0; k < u.k1 && fine; ++k) {
+            const int kt = gk + k - u.k0, st = kt % L::kSt;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (!fine) break;
+              if (hv.a[x] <= k && k < hv.b[x]) {
+                const bool first = k == hv.a[x];
+                fine = warp_wait(&p_full[x], pvs[x] & 1) &&
+                       // the first P V of a unit overwrites O: the softmax has read the last unit's
+                       (!first || outs[x] == 0 || warp_wait(&o_free[x], (outs[x] - 1) & 1)) &&
+                       warp_wait(&v_full[st], (kt / L::kSt) & 1);
+                if (!fine) break;
+                tc::fence_after_sync();
+                const uint64_t b0 = dv + (uint64_t)((st * L::kTile) >> 4);
+                const bool second = hv.a[1] <= k && k < hv.b[1];
+                if (elect_one()) {
+#pragma unroll
+                  for (int kk = 0; kk < kKeys / 16; ++kk)
+                    tc::mma_bf16_ts(tmem + 256 + x * D, tmem + x * kKeys + kk * 8, b0 + (uint64_t)((kk * 16 * 128) >> 4), kIdescPV,
+                                    !first || kk > 0);
+                  tc::mma_commit(&pv_done[x]);
+                  if (x == 1 || !second) tc::mma_commit(&v_free[st]);
+                }
+                __syncwarp();
+                ++pvs[x];
+                if (k + 1 < hv.b[x]) fine = s_product(x, k + 1);
+              } else if (k + 1 == hv.a[x] && hv.a[x] < hv.b[x]) {
+                fine = s_product(x, k + 1);
+              }
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) outs[x] += hv.a[x] < hv.b[x] ? 1 : 0;
+          gk += u.k1 - u.k0;
+          ++qi;
+        }
+        if (!fine) {
+          if (lane == 0) pflag(p, GQAW_DEV_TIMEOUT);
+          *abort_flag = 1;
+        }
+        if (elect_one()) tc::mma_commit(mma_done);  // every MMA issued has completed before TMEM is released
+        if (!warp_wait(mma_done, 0)) if (lane == 0) pflag(p, GQAW_DEV_TIMEOUT);
       }
-      if (!fine) {
-        if (lane == 0) pflag(p, GQAW_DEV_TIMEOUT);
-        *abort_flag = 1;
-      }
-      if (elect_one()) tc::mma_commit(mma_done);  // every MMA issued has completed before TMEM is released
-      if (!warp_wait(mma_done, 0)) if (lane == 0) pflag(p, GQAW_DEV_TIMEOUT);
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax (warps 0-7)
