@@ -152,7 +152,7 @@ def test_large_logits(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
-@pytest.mark.parametrize("S", [1, 3, 50])
+@pytest.mark.parametrize("S", [1, 3, 50, 90])
 def test_many_sequences(dtype, S):
     """More sequences than one launch takes, most of them idle."""
     lens = [(0, 0) if i % 3 else (min(S, 1 + i % 90), 1 + i % 90) for i in range(700)]
