@@ -50,7 +50,8 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
     paged_f32_decode_kernel(const PagedParams p, const __grid_constant__ PagedMaps maps) {
   using namespace pf32;
   using L = Lay<D>;
-  constexpr int W = L::W, S = L::S, VW = D / 32;
+  constexpr int W = L::W, S = L::S, VW = D / 32, J = D / 32, NZ = RM / 2;
+  constexpr bool QREG = RM * D / 8 <= 64;  // queries in registers
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PSched sched;
@@ -121,15 +122,25 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
     }
     __syncthreads();
 
-    float m[RM], l[RM];
-    uint64_t o[RM / 2][VW];  // pairs of rows
+    // z: a lane has four dimensions of every block (ds) of four keys (kg); its part of the queries
+    // stays in registers where they allow
+    const int ds = lane & 7, kg = lane >> 3;
+    ulonglong2 qr[QREG ? RM : 1][J];
+    if (QREG) {
 #pragma unroll
-    for (int r = 0; r < RM; ++r) m[r] = -INFINITY, l[r] = 0.f;
+      for (int r = 0; r < RM; ++r)
+#pragma unroll
+        for (int c = 0; c < J; ++c) qr[QREG ? r : 0][c] = *reinterpret_cast<const ulonglong2 *>(sq + r * D + c * 32 + ds * 4);
+    }
+    // after the sum over the lanes of a key: this lane's row, and its NZ keys
+    const int row = RM == 8 ? ds : ds >> 1;
+    auto key_of = [&](int i) { return ((RM == 8 ? 0 : 2 * (ds & 1)) + i) * 4 + kg; };
+    float m = -INFINITY, l = 0.f;  // of the row; l of this lane's keys
+    uint64_t o[RM / 2][VW];  // pairs of rows
 #pragma unroll
     for (int r = 0; r < RM / 2; ++r)
 #pragma unroll
       for (int d = 0; d < VW; ++d) o[r][d] = 0ull;
-    const int key = lane & 15, hf = lane >> 4;
     for (int i = 0; i < n; ++i) {
       const int next = look_up(i + S);
       load(i + S - 1, id);
@@ -137,66 +148,124 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
       const int st = (first + i) % S;
       if (!__all_sync(0xffffffffu, fine && mbar_wait(&full[st], ((first + i) / S) & 1))) fine = false;
       const unsigned char *kb = ring + st * L::kStage, *vb = kb + L::B * L::kBlock;
-      uint64_t z2[RM];
+      float z[4][RM];  // this lane's part of four keys' logits
+      auto part_of = [&](int c, int key) {
+        return *reinterpret_cast<const ulonglong2 *>(kb + c * L::kBlock + key * 128 + ((ds ^ (key & 7)) << 4));
+      };
+      if constexpr (QREG) {
 #pragma unroll
-      for (int r = 0; r < RM; ++r) z2[r] = 0ull;
+        for (int k = 0; k < 4; ++k) {
+          uint64_t z2[RM];
 #pragma unroll
-      for (int c0 = 0; c0 < D / 8; ++c0) {  // 16-byte parts of this lane's half row
-        const int c = hf * (D / 8) + c0;
-        const ulonglong2 kv = *reinterpret_cast<const ulonglong2 *>(kb + (c >> 3) * L::kBlock + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+          for (int c = 0; c < J; ++c) {
+            const ulonglong2 kv = part_of(c, k * 4 + kg);
 #pragma unroll
-        for (int r = 0; r < RM; ++r) {
-          const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(sq + r * D + c * 4);
-          z2[r] = fma2(q.x, kv.x, z2[r]);
-          z2[r] = fma2(q.y, kv.y, z2[r]);
+            for (int r = 0; r < RM; ++r) {
+              z2[r] = fma2(qr[r][c].x, kv.x, c ? z2[r] : 0ull);
+              z2[r] = fma2(qr[r][c].y, kv.y, z2[r]);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < RM; ++r) {
+            const float2 f = unpk(z2[r]);
+            z[k][r] = f.x + f.y;
+          }
         }
-      }
-      const long long j0 = key0(i), j = j0 + key;
-      const bool inner = j0 >= jlo && j0 + kKeys - 1 <= u.qpos && (p.W == 0 || j0 >= jhi - p.W);
-      float z[RM];
-      bool up = false;
+      } else {
+        uint64_t z2[4][RM];
 #pragma unroll
-      for (int r = 0; r < RM; ++r) {
-        const float2 f = unpk(z2[r]);
-        z[r] = f.x + f.y;
-        z[r] += __shfl_xor_sync(0xffffffffu, z[r], 16);
-        if (p.capmul != 0.f) z[r] = cap_logit(p, z[r]);
-        if (!inner) {
-          const long long at = u.qpos + r / g;
-          if (r >= rows || j > at || j < jlo || (p.W > 0 && j <= at - p.W)) z[r] = -INFINITY;
-        }
-        up |= z[r] > m[r] + 8.f;
-      }
-      if (__any_sync(0xffffffffu, up)) {
-        float f[RM];
+        for (int c = 0; c < J; ++c) {
+          ulonglong2 kv[4];
 #pragma unroll
-        for (int r = 0; r < RM; ++r) {
-          float mx = z[r];
+          for (int k = 0; k < 4; ++k) kv[k] = part_of(c, k * 4 + kg);
 #pragma unroll
-          for (int s = 8; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-          f[r] = 1.f;
-          if (mx > m[r] + 8.f) {
-            f[r] = exp2f(m[r] - mx);  // 0 while nothing was seen
-            m[r] = mx;
-            l[r] *= f[r];
+          for (int r = 0; r < RM; ++r) {
+            const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(sq + r * D + c * 32 + ds * 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              z2[k][r] = fma2(q.x, kv[k].x, c ? z2[k][r] : 0ull);
+              z2[k][r] = fma2(q.y, kv[k].y, z2[k][r]);
+            }
           }
         }
 #pragma unroll
-        for (int r = 0; r < RM / 2; ++r)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int d = 0; d < VW; ++d) o[r][d] = fma2(o[r][d], pk(f[2 * r], f[2 * r + 1]), 0ull);
+          for (int r = 0; r < RM; ++r) {
+            const float2 f = unpk(z2[k][r]);
+            z[k][r] = f.x + f.y;
+          }
+      }
+      // the sum over the eight lanes of a key: each step, a lane gives away the half that its
+      // partner keeps
+      float y[4];
+      {
+        float a[4][RM / 2], b[4][RM / 4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int r = 0; r < RM / 2; ++r) {
+            const float mine = ds & 4 ? z[k][r + RM / 2] : z[k][r], his = ds & 4 ? z[k][r] : z[k][r + RM / 2];
+            a[k][r] = mine + __shfl_xor_sync(0xffffffffu, his, 4);
+          }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int r = 0; r < RM / 4; ++r) {
+            const float mine = ds & 2 ? a[k][r + RM / 4] : a[k][r], his = ds & 2 ? a[k][r] : a[k][r + RM / 4];
+            b[k][r] = mine + __shfl_xor_sync(0xffffffffu, his, 2);
+          }
+#pragma unroll
+        for (int k = 0; k < NZ; ++k) {
+          float mine, his;
+          if constexpr (RM == 8) {
+            mine = ds & 1 ? b[k][RM / 4 - 1] : b[k][0];
+            his = ds & 1 ? b[k][0] : b[k][RM / 4 - 1];
+          } else {
+            mine = ds & 1 ? b[k + 2][0] : b[k][0];
+            his = ds & 1 ? b[k][0] : b[k + 2][0];
+          }
+          y[k] = mine + __shfl_xor_sync(0xffffffffu, his, 1);
+        }
+      }
+      const long long j0 = key0(i);
+      const bool inner = j0 >= jlo && j0 + kKeys - 1 <= u.qpos && (p.W == 0 || j0 >= jhi - p.W);
+      bool up = false;
+#pragma unroll
+      for (int k = 0; k < NZ; ++k) {
+        if (p.capmul != 0.f) y[k] = cap_logit(p, y[k]);
+        if (!inner) {
+          const long long at = u.qpos + row / g, j = j0 + key_of(k);
+          if (row >= rows || j > at || j < jlo || (p.W > 0 && j <= at - p.W)) y[k] = -INFINITY;
+        }
+        up |= y[k] > m + 8.f;
+      }
+      if (__any_sync(0xffffffffu, up)) {
+        float mx = y[0];
+#pragma unroll
+        for (int k = 1; k < NZ; ++k) mx = fmaxf(mx, y[k]);
+        if (RM == 4) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        float f = 1.f;
+        if (mx > m + 8.f) {
+          f = exp2f(m - mx);  // 0 while nothing was seen
+          m = mx;
+          l *= f;
+        }
+#pragma unroll
+        for (int r = 0; r < RM / 2; ++r) {  // rows 2r and 2r + 1: of lanes with kg = 0
+          const float f0 = __shfl_sync(0xffffffffu, f, 2 * r * (8 / RM)), f1 = __shfl_sync(0xffffffffu, f, (2 * r + 1) * (8 / RM));
+#pragma unroll
+          for (int d = 0; d < VW; ++d) o[r][d] = fma2(o[r][d], pk(f0, f1), 0ull);
+        }
       }
 #pragma unroll
-      for (int r = 0; r < RM; ++r) {
-        const bool hid = !inner && z[r] == -INFINITY;
-        const float pr = exp2f(z[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-        l[r] += pr;  // both lanes of a key count it: halved at the end
-        z[r] = hid ? -1.f : pr;  // hidden: its value row is not touched
-      }
-      if (hf == 0) {
-#pragma unroll
-        for (int r = 0; r < RM; r += 4)
-          *reinterpret_cast<float4 *>(sp + key * 8 + r) = make_float4(z[r], z[r + 1], z[r + 2], z[r + 3]);
+      for (int k = 0; k < NZ; ++k) {
+        const float pr = exp2f(y[k] - (m == -INFINITY ? 0.f : m));
+        l += pr;
+        // a hidden key: its value row is not touched
+        sp[key_of(k) * 8 + row] = !inner && y[k] == -INFINITY ? -1.f : pr;
       }
       __syncwarp();
       // this lane's dimensions: VW from lane * VW
@@ -237,14 +306,12 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
     // ---- the warp's state into its ring: [RM][D + 2]
     constexpr int PS = D + 2;
     float *mine = reinterpret_cast<float *>(ring);
-#pragma unroll
-    for (int r = 0; r < RM; ++r) {
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], s);
-      if (lane == 0) {
-        mine[r * PS + D] = m[r];
-        mine[r * PS + D + 1] = 0.5f * l[r];
-      }
+    if (RM == 4) l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    if (lane == row * (8 / RM)) {
+      mine[row * PS + D] = m;
+      mine[row * PS + D + 1] = l;
     }
 #pragma unroll
     for (int r = 0; r < RM / 2; ++r)
