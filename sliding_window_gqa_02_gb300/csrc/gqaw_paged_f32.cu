@@ -6,12 +6,20 @@
 // on four warps a SM, many of them address arithmetic of the loads, and ran at a quarter of the
 // memory's rate.  Here the tiles come by tensor TMA through the page table, a few instructions
 // each, and are half as tall, so that more warps fit (head size 64: 12 warps with two stages each,
-// 8 contexts of 8192 with 4 rows 57 us, against 71 with 8 warps of three; 8 rows 94 against 103):
+// 8 contexts of 8192 with 8 rows 62 us, 67 with 10 warps; three stages and 8 warps 77 before the
+// sums of o by halves, 68 then with 12):
 //   - a tile is 16 keys; K and V in blocks of 32 dimensions, rows of 128 bytes in the 128-byte
 //     swizzle, whose exclusive-or of the 16-byte part with the row is what lets neighbouring
 //     lanes read neighbouring keys without a bank conflict;
-//   - z: lane (key, half) has half of the dimensions of one key against all rows; one exchange;
-//   - o: a lane has D / 32 dimensions of all rows, the weights of a key come as one broadcast.
+//   - z: a lane has 4 dimensions of each block (ds) for four keys (kg) and all rows; its part of the
+//     queries stays in registers, and the sum over the eight lanes of a key is an exchange of
+//     halves that leaves a lane one row of its keys (28 exchanges instead of a reduction each);
+//   - o: half a warp has a key, 4 dimensions a lane (head size 128: the whole warp), the weights of a
+//     key come as one broadcast; the halves are added at the unit's end.
+// Bound: what shared memory returns to registers, 128 bytes a cycle.  With one key and half of the
+// dimensions a lane, the queries from shared memory and two dimensions of o, a tile took 448
+// cycles of it; now some 160 (8 contexts of 8192 keys, 8 rows: 89 -> 62 us, 4.3 TB/s; 4 rows 55
+// -> 48 us, 5.6 TB/s; head size 128, 4 rows 104 -> 92 us, 5.8 TB/s).
 #include <atomic>
 
 #include "gqaw_paged_attend.cuh"
@@ -50,7 +58,8 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
     paged_f32_decode_kernel(const PagedParams p, const __grid_constant__ PagedMaps maps) {
   using namespace pf32;
   using L = Lay<D>;
-  constexpr int W = L::W, S = L::S, VW = D / 32, J = D / 32, NZ = RM / 2;
+  constexpr int W = L::W, S = L::S, J = D / 32, NZ = RM / 2;
+  constexpr int KS = D <= 64 ? 2 : 1, LK = 32 / KS, VW = D / LK;  // o: keys at a time, lanes of a key, dimensions of a lane
   constexpr bool QREG = RM * D / 8 <= 64;  // queries in registers
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -268,10 +277,11 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
         sp[key_of(k) * 8 + row] = !inner && y[k] == -INFINITY ? -1.f : pr;
       }
       __syncwarp();
-      // this lane's dimensions: VW from lane * VW
-      const int blk = lane * VW / 32, part = lane * VW % 32 / 4, byte = lane * VW % 4 * 4;
+      // this lane's dimensions: VW from lane % LK * VW, of every KS-th key from lane / LK on
+      const int d0 = lane % LK * VW, blk = d0 / 32, part = d0 % 32 / 4, byte = d0 % 4 * 4;
 #pragma unroll
-      for (int k = 0; k < kKeys; ++k) {
+      for (int k0 = 0; k0 < kKeys; k0 += KS) {
+        const int k = k0 + lane / LK;
         float v[VW];
         prow::lds<VW>(reinterpret_cast<const float *>(vb + blk * L::kBlock + k * 128 + ((part ^ (k & 7)) << 4) + byte), v);
         uint64_t w[RM / 2];
@@ -317,9 +327,15 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
     for (int r = 0; r < RM / 2; ++r)
 #pragma unroll
       for (int d = 0; d < VW; ++d) {
-        const float2 a = unpk(o[r][d]);
-        mine[2 * r * PS + lane * VW + d] = a.x;
-        mine[(2 * r + 1) * PS + lane * VW + d] = a.y;
+        float2 a = unpk(o[r][d]);
+        if (KS == 2) {
+          a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+          a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+        }
+        if (lane / LK == r % KS) {
+          mine[2 * r * PS + lane % LK * VW + d] = a.x;
+          mine[(2 * r + 1) * PS + lane % LK * VW + d] = a.y;
+        }
       }
     __syncthreads();
     // ---- the warps' states joined
