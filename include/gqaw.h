@@ -433,8 +433,7 @@ gqaw_status gqaw_paged_attend(const gqaw_paged_args *args, void *stream);
 /* The whole step: append, and attention of the normed and turned queries.  The cache is the one
  * that gqaw_paged_append leaves, and the output that of gqaw_qk_norm_rotary of the query and
  * gqaw_paged_attend, but closer to the formula in bf16: what the queries lose in their rounding
- * is kept beside them in the workspace and multiplies the keys too (not for head size 256 with
- * more than 8 rows of queries per kv head). */
+ * is kept beside them in the workspace and multiplies the keys too. */
 gqaw_status gqaw_paged_step(const gqaw_paged_args *args, void *stream);
 
 /* sizeof(gqaw_qk_args) and sizeof(gqaw_paged_args) as compiled into the library. */

@@ -16,10 +16,11 @@
 //     halves that leaves a lane one row of its keys (28 exchanges instead of a reduction each);
 //   - o: half a warp has a key, 4 dimensions a lane (head size 128: the whole warp), the weights of a
 //     key come as one broadcast; the halves are added at the unit's end.
-// Bound: what shared memory returns to registers, 128 bytes a cycle.  With one key and half of the
-// dimensions a lane, the queries from shared memory and two dimensions of o, a tile took 448
-// cycles of it; now some 160 (8 contexts of 8192 keys, 8 rows: 89 -> 62 us, 4.3 TB/s; 4 rows 55
-// -> 48 us, 5.6 TB/s; head size 128, 4 rows 104 -> 92 us, 5.8 TB/s).
+// Bound: it was what shared memory returns to registers, 128 bytes a cycle: with one key and half
+// of the dimensions a lane, the queries from shared memory and two dimensions of o, a tile took 448
+// cycles of it, now some 160 (8 contexts of 8192 keys, 8 rows: 89 -> 62 us, 4.3 TB/s; 4 rows 55
+// -> 48 us, 5.6 TB/s; head size 128, 4 rows 104 -> 92 us, 5.8 TB/s).  Now it is instruction issue
+// and its latencies: 42% of the slots busy, memory 44%.
 #include <atomic>
 
 #include "gqaw_paged_attend.cuh"

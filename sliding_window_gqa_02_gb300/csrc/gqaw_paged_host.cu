@@ -342,9 +342,8 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
   L->off_q = L->ws_bytes;
   L->ws_bytes += align256((size_t)a->total_new_tokens * qrow * L->es);
   // What bf16 leaves of a turned query is kept beside it, and both parts multiply the keys: the
-  // rounding of the queries alone otherwise adds 0.0014 to the outputs' error of 0.0016.  (Head
-  // size 256 on the 128-row kernel has no shared memory for a second part.)
-  L->split_q = a->dtype == GQAW_BF16 && !(L->path == kPrefill && D == 256);
+  // rounding of the queries alone otherwise adds 0.0014 to the outputs' error of 0.0016.
+  L->split_q = a->dtype == GQAW_BF16;
   L->off_qlo = L->ws_bytes;
   if (L->split_q) L->ws_bytes += align256((size_t)a->total_new_tokens * qrow * L->es);
   return GQAW_OK;

@@ -17,7 +17,7 @@
 // when exceeded by more than 2^8, so O is rarely rescaled.  Sums are fp32 of the unrounded
 // weights; P is rounded to bf16 for its product (2^-9 relative, the size of the output's own
 // rounding: what bf16 leaves of P would cost a second product).  Queries that the step has turned
-// come in two bf16 parts (SPLIT, head sizes 64 and 128) and S is the sum of two products: error
+// come in two bf16 parts (SPLIT) and S is the sum of two products: error
 // of a whole prompt step 0.0025 -> 0.0020 for 8% more time, where the outputs' own rounding is
 // 0.0016.  Warps without rows (a decoding sequence among chunks has `group` rows of the 128)
 // only keep the barriers turning.
@@ -71,7 +71,9 @@ struct Lay {
   static constexpr uint32_t kTmemP = D == 256 ? 128 : 384, kTmemO = 256;
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + (SPLIT ? 2 : 1) * kTile;  // Q, and what bf16 left of it
-  static constexpr int kV = kK + kKSt * kTile;
+  // Two parts of Q leave head size 256 one slot, which a tile's keys and then its values take
+  static constexpr bool kOneSlot = D == 256 && SPLIT;
+  static constexpr int kV = kOneSlot ? kK : kK + kKSt * kTile;
   static constexpr int kSched = kV + kVSt * kTile;
   static constexpr int kXch = kSched + (int)((sizeof(PSched) + 15) / 16 * 16);  // float [3][kParts][128]
   // keys attended by some rows only whose values are not finite, as bits: uint32
@@ -271,6 +273,8 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
         if (k + 1 < u.k1) bx.look_up(p, u.kt + k + 1, lane);
         const int st = gk % nst;
         if (gk >= nst) fine = mbar_wait(&empty[st], ((gk / nst) & 1) ^ 1);
+        // one slot: keys after the last tile's values have been used, values after this tile's keys
+        if (L::kOneSlot && fine && (value || gk > 0)) fine = mbar_wait(value ? k_free : v_free, (value ? gk : gk - 1) & 1);
         fine = __all_sync(0xffffffffu, fine && !*abort_flag);
         if (!fine) break;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * bx.rows * 128 * L::HALVES));
@@ -365,6 +369,15 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
         for (int k = 0; k < n && fine; ++k) {
           const int gt = gk + k;
           bool have_p = false;
+          if (L::kOneSlot) {  // S(k + 1) has its keys only once P(k) V(k) is done
+            fine = warp_wait(&p_full[gt & 1], (gt >> 1) & 1) && (k > 0 || qi == 0 || warp_wait(o_free, (qi - 1) & 1)) &&
+                   pv_product(gt, k > 0);
+            if (fine && k + 1 < n) {
+              fine = s_product(gt + 1);
+              if (fine && k + 2 == n && elect_one()) tc::mma_commit(q_free);
+            }
+            continue;
+          }
           if (L::kSBuf == 1) {  // the one S buffer is free once P(k) is written
             fine = warp_wait(&p_full[gt & 1], (gt >> 1) & 1);
             have_p = true;
@@ -1273,9 +1286,9 @@ cudaError_t launch_prefill(K kernel, std::atomic<bool> *ready, int threads, int 
 }
 
 // halves: query tiles of 128 rows per unit, 1 or 2 (2: head sizes 64 and 128).  The queries come
-// in two parts where p.qlo is set (head sizes 64 and 128).
+// in two parts where p.qlo is set.
 cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, int halves, int grid, cudaStream_t stream) {
-  static std::atomic<bool> ready[9][kPrefillDevices];
+  static std::atomic<bool> ready[10][kPrefillDevices];
   auto one = [&](auto d, auto split, int i) {
     return launch_prefill(paged_prefill_kernel<d.value, split.value>, ready[i], ppre::kThreads,
                           ppre::Lay<d.value, split.value>::kAlloc, p, maps, grid, stream);
@@ -1297,7 +1310,7 @@ cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, in
     if (halves == 2) return p.qlo ? two(d128, split, 4) : two(d128, whole, 5);
     return p.qlo ? one(d128, split, 6) : one(d128, whole, 7);
   }
-  return one(d256, whole, 8);
+  return p.qlo ? one(d256, split, 8) : one(d256, whole, 9);
 }
 
 }  // namespace gqaw

@@ -191,7 +191,7 @@ def test_append_odd_rotary_widths(rd, interleaved):
 def test_step(dtype, lens, D, kw):
     """The step against the definition, and against its three parts one after the other: the same
     bits, but where bf16 queries turned by the step keep a second part that the parts' do not."""
-    two = dtype == BF and "rotary" in kw and (D < 256 or lens is RAGGED)
+    two = dtype == BF and "rotary" in kw
     mk = lambda: Batch(lens, 8, 2, D, 16, dtype, seed=11, filled=False, extra_rows=1, **kw)
     b = mk()
     k0, v0 = b.kp.clone(), b.vp.clone()
