@@ -41,6 +41,10 @@ __device__ __forceinline__ PShape shape_of(const PagedParams &p, int unit_cost) 
   return PShape{p.tpt, p.W, p.Nkv * p.hblocks, unit_cost};
 }
 
+__device__ __forceinline__ PBatch batch_of(const PagedParams &p) {
+  return PBatch{p.qstart, p.seqlens, p.B, p.N, p.max_new, p.max_len};
+}
+
 __device__ __forceinline__ void pflag(const PagedParams &p, uint32_t bits) { atomicOr(p.status, bits); }
 
 // Builds the list and this CTA's start; all threads of the CTA call it, and it ends with a
@@ -58,7 +62,7 @@ __device__ inline void sched_build(const PagedParams &p, const PShape &shp, PSch
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int b = b0 + lane, S = q1 - q0, qs = q0;
       const long long TT = (long long)len + 1;
-      const bool bad = b < p.B && (q0 < 0 || q1 < q0 || q1 > p.N || S > p.max_new || TT < S || TT > p.max_len);
+      const bool bad = b < p.B && malformed(batch_of(p), q0, q1, len);
       if (b0 + 32 < p.B) {  // the next ones, ahead of the arithmetic
         q0 = at(p.qstart, b + 32, p.B + 1);
         q1 = at(p.qstart, b + 33, p.B + 1);

@@ -90,6 +90,7 @@ struct RowsJob {
   bool paged;    // rows belong to sequences; keys go to the pages
   bool vec;      // the tables' rows split into whole vectors for a lane
   long long warps;
+  int checks;    // warps behind those, which flag malformed sequences, 32 each (no row need be theirs)
 };
 
 // How a row's pairs lie for its lanes.
@@ -368,6 +369,9 @@ __global__ void __launch_bounds__(kThreads, OCTETS && sizeof(T) == 2 ? 8 : 6)
         default: if (!OCTETS) rows_out<kAnywhere, SPLIT, T, LPR, BATCH>(p, x, c, wt != nullptr, dst, step, lo, h, nh, e, src);
       }
     }
+  } else if (w < j.warps + j.checks) {
+    const int b = (int)(w - j.warps) * 32 + lane;
+    if (b < p.B && malformed(batch_of(p), p.qstart[b], p.qstart[b + 1], p.seqlens[b])) pflag(p, GQAW_DEV_BAD_SEQLEN);
   }
   pdl_launch_dependents();
 }
@@ -403,7 +407,8 @@ cudaError_t launch_paged_rows(const PagedParams &p, int nq, int nk, int nv, bool
   j.cv = chunks(nv, batch);
   j.warps = (long long)p.N * (j.cq + j.ck + j.cv);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((j.warps + kThreads / 32 - 1) / (kThreads / 32)));
+  j.checks = paged ? (p.B + 31) / 32 : 0;
+  cfg.gridDim = dim3((unsigned)((j.warps + j.checks + kThreads / 32 - 1) / (kThreads / 32)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -34,6 +34,19 @@ namespace gqaw {
 
 constexpr int kPagedItems = 256;  // sequences of one launch; larger batches take several
 
+// The batch as the device sees it: sequence b has rows [qstart[b], qstart[b + 1]) and length
+// seqlens[b] + 1.
+struct PBatch {
+  const int32_t *qstart, *seqlens;
+  int B, N, max_new, max_len;
+};
+
+// Is a sequence with rows [q0, q1) and length len + 1 one that no call touches?
+GQAW_HD bool malformed(const PBatch &p, int q0, int q1, int len) {
+  const long long S = (long long)q1 - q0, T = (long long)len + 1;
+  return q0 < 0 || S < 0 || q1 > p.N || S > p.max_new || T < S || T > p.max_len;
+}
+
 // What the schedule needs to know of a call.
 struct PShape {
   int tpt, W, heads;  // tokens per query tile; window (0: none); kv heads x head blocks
