@@ -348,7 +348,10 @@ gqaw_status gqaw_qk_norm_rotary(const gqaw_qk_args *args, void *stream);
  * sets GQAW_DEV_BAD_PAGE: an append drops the row, an attention leaves the outputs of that
  * sequence unspecified.  A sequence with S_b < 0, S_b > max_new_tokens, T_b < S_b,
  * T_b > max_sequence_length or rows outside [0, total_new_tokens) sets
- * GQAW_DEV_BAD_SEQLEN and is skipped.  Neither touches any other sequence.
+ * GQAW_DEV_BAD_SEQLEN and is skipped.  Neither touches any other sequence.  Where query_start
+ * descends (which some S_b < 0 shows), several sequences may claim the same row: their outputs and
+ * their new rows of the cache are then unspecified, and nothing else is.  A call without any token
+ * (total_new_tokens or max_new_tokens 0) looks at no sequence.
  *
  * Alignment: query, key, value, the pages, output and the weights 16-byte, all strides
  * multiples of 16 bytes; page_table, query_start, seqlens_k and head_sink 4-byte; cos_cache

@@ -96,24 +96,6 @@ struct RowsJob {
 // How a row's pairs lie for its lanes.
 enum Turn { kNoTurn = 0, kOctets = 1, kInside = 2, kAnywhere = 3 };
 
-// The sequence that row n belongs to: the last b with query_start[b] <= n, searched 32 ways
-// at a time by the warp; -1 when there is none.
-__device__ __forceinline__ int find_sequence(const PagedParams &p, int n, int lane) {
-  int lo = 0, size = p.B;
-  bool first = true;
-  while (size > 1 || first) {
-    first = false;
-    const int step = (size + 31) / 32, i = lo + lane * step;
-    const bool le = lane * step < size && p.qstart[i] <= n;
-    const int c = __popc(__ballot_sync(0xffffffffu, le));
-    if (c == 0) return -1;
-    const int end = lo + size;
-    lo += (c - 1) * step;
-    size = min(step, end - lo);
-  }
-  return lo;
-}
-
 }  // namespace
 
 // Packed pairs of fp32: one instruction computes both lanes.
@@ -252,27 +234,18 @@ __global__ void __launch_bounds__(kThreads, OCTETS && sizeof(T) == 2 ? 8 : 6)
     long long pos = 0, page_at = -1;
     bool owned = true;
     if (j.paged) {
-      const int b = find_sequence(p, n, lane);
-      owned = b >= 0;
+      const int b = find_sequence(batch_of(p), n);
+      owned = b >= 0;  // else nobody's, or a malformed sequence's
       if (owned) {
-        const int q0 = p.qstart[b], q1 = p.qstart[b + 1];
-        const long long TT = (long long)p.seqlens[b] + 1;
-        if (n >= q1) {
-          owned = false;  // behind the last sequence
-        } else if (q0 < 0 || q1 > p.N || q1 - q0 > p.max_new || TT < q1 - q0 || TT > p.max_len) {
-          owned = false;
-          if (lane == 0) pflag(p, GQAW_DEV_BAD_SEQLEN);
-        } else {
-          pos = TT - (q1 - n);
-          if (kind > 0) {
-            const int pg = (int)pos / p.page;
-            const int id = p.table[(long long)b * p.width + pg];
-            if ((unsigned)id < (unsigned)p.npages)
-              page_at = id * p.sp + (pos - (long long)pg * p.page) * p.sr;
-            else if (lane == 0)
-              pflag(p, GQAW_DEV_BAD_PAGE);
-            owned = page_at >= 0;
-          }
+        pos = (long long)p.seqlens[b] + 1 - (p.qstart[b + 1] - n);
+        if (kind > 0) {
+          const int pg = (int)pos / p.page;
+          const int id = p.table[(long long)b * p.width + pg];
+          if ((unsigned)id < (unsigned)p.npages)
+            page_at = id * p.sp + (pos - (long long)pg * p.page) * p.sr;
+          else if (lane == 0)
+            pflag(p, GQAW_DEV_BAD_PAGE);
+          owned = page_at >= 0;
         }
       }
     }

@@ -34,6 +34,25 @@ namespace gqaw {
 
 constexpr int kPagedItems = 256;  // sequences of one launch; larger batches take several
 
+// A vote of a whole warp: bit i is pred(i).  The host goes over the 32 lanes.
+template <typename F>
+GQAW_HD uint32_t warp_vote(F pred) {
+#ifdef __CUDA_ARCH__
+  return __ballot_sync(0xffffffffu, pred((int)(threadIdx.x & 31)));
+#else
+  uint32_t m = 0;
+  for (int i = 0; i < 32; ++i) m |= pred(i) ? 1u << i : 0u;
+  return m;
+#endif
+}
+GQAW_HD int bits_set(uint32_t m) {
+#ifdef __CUDA_ARCH__
+  return __popc(m);
+#else
+  return __builtin_popcount(m);
+#endif
+}
+
 // The batch as the device sees it: sequence b has rows [qstart[b], qstart[b + 1]) and length
 // seqlens[b] + 1.
 struct PBatch {
@@ -45,6 +64,39 @@ struct PBatch {
 GQAW_HD bool malformed(const PBatch &p, int q0, int q1, int len) {
   const long long S = (long long)q1 - q0, T = (long long)len + 1;
   return q0 < 0 || S < 0 || q1 > p.N || S > p.max_new || T < S || T > p.max_len;
+}
+
+// The sequence that row n belongs to: qstart[b] <= n < qstart[b + 1], and not malformed; -1 when
+// there is none.  On the device a whole warp calls it.  The last b with qstart[b] <= n is
+// searched 32 ways at a time, which finds it where the starts ascend.  Where they do not it may be
+// any sequence: so what was found is checked, and if the row is not its own every sequence is asked,
+// but for a row behind all of them (the padding of a batch).
+GQAW_HD int find_sequence(const PBatch &p, int n) {
+  auto owns = [&](int b) {
+    const int q0 = p.qstart[b], q1 = p.qstart[b + 1];
+    return q0 <= n && n < q1 && !malformed(p, q0, q1, p.seqlens[b]);
+  };
+  int lo = 0, size = p.B;
+  for (bool first = true; size > 1 || first; first = false) {
+    const int step = (size + 31) / 32;
+    const int c = bits_set(warp_vote([&](int lane) { return lane * step < size && p.qstart[lo + lane * step] <= n; }));
+    if (c == 0) break;
+    const int rest = size - (c - 1) * step;
+    lo += (c - 1) * step;
+    size = step < rest ? step : rest;
+  }
+  if (owns(lo)) return lo;
+  const bool behind = !warp_vote([&](int lane) {
+    int top = 0;
+#pragma unroll 8
+    for (int b = lane; b <= p.B; b += 32) top = top > p.qstart[b] ? top : p.qstart[b];
+    return top > n;
+  });
+  for (int b0 = 0; b0 < p.B && !behind; b0 += 32) {
+    const uint32_t m = warp_vote([&](int lane) { return b0 + lane < p.B && owns(b0 + lane); });
+    if (m) return b0 + bits_set((m & (0u - m)) - 1u);
+  }
+  return -1;
 }
 
 // What the schedule needs to know of a call.
