@@ -60,6 +60,12 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kUnitCost = 3;   // see gqaw_paged_sched.cuh
 constexpr float kRescaleLog2 = 8.0f;  // log2 units
 constexpr int kSoftBar = 5;    // named barrier of the softmax warps (1-4: those of a lane quarter)
+// Buffers of the bits of values that are not finite.  Unit i (of those with keys that only some rows
+// attend) sets bits in buffer i % kOddBufs, its warps meet at a barrier and read them, and behind the
+// barrier buffer (i - 1) % kOddBufs is cleared, which every warp has read before it came there.  It is
+// next used by unit i + 2, whose bits are set behind the next barrier: with two buffers it would be
+// unit i + 1's, and a warp that is ahead could set bits before they are cleared.
+constexpr int kOddBufs = 3;
 
 template <int D, bool SPLIT>
 struct Lay {
@@ -77,9 +83,9 @@ struct Lay {
   static constexpr int kSched = kV + kVSt * kTile;
   static constexpr int kXch = kSched + (int)((sizeof(PSched) + 15) / 16 * 16);  // float [3][kParts][128]
   // keys attended by some rows only whose values are not finite, as bits: uint32
-  // [unit & 1][part of the dimensions][0: after the first token, 1: before the last token's window][4]
+  // [buffer][part of the dimensions][0: after the first token, 1: before the last token's window][4]
   static constexpr int kOdd = kXch + 3 * kParts * kRows * 4;
-  static constexpr int kMisc = kOdd + 2 * kParts * 8 * 4;  // flags
+  static constexpr int kMisc = kOdd + kOddBufs * kParts * 8 * 4;  // flags
   static constexpr int kStage = (kMisc + 16 + 255) / 256 * 256;  // 32 rows x 16 columns of output per softmax warp
   static constexpr int kBars = kStage + kSoft / 32 * 1024;
   static constexpr int kAlloc = kBars + 32 * 8 + 1024;  // and room to align the base
@@ -234,7 +240,7 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
     }
     mbar_fence_init();
     *abort_flag = 0;
-    for (int i = 0; i < 2 * kParts * 8; ++i) odd[i] = 0u;
+    for (int i = 0; i < kOddBufs * kParts * 8; ++i) odd[i] = 0u;
   }
   // query rows past tpt * group stay zero
   for (int e = tid; e < QP * L::kTile / 16; e += kThreads) reinterpret_cast<uint4 *>(smem + L::kQ)[e] = make_uint4(0, 0, 0, 0);
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
     PWalk<kKeys> w(shp, sched);
     PUnit u;
-    int gk = 0, odd_par = 0;
+    int gk = 0, odd_at = 0;  // ... and the unit's buffer of odd bits
     // A warp that gives up a tile (an expired wait, an abort elsewhere) still runs every unit's
     // epilogue: the softmax warps meet at its barriers.
     while (w.next(shp, u)) {
@@ -537,7 +543,7 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
             }
             if (zero) {
               const int kind = j > u.qpos ? 0 : 1, i = (int)(j - (kind ? jlo : u.qpos));
-              atomicOr(&odd[(odd_par * kParts + hf) * 8 + kind * 4 + i / 32], 1u << (i & 31));
+              atomicOr(&odd[(odd_at * kParts + hf) * 8 + kind * 4 + i / 32], 1u << (i & 31));
             }
           }
           if (zero)
@@ -564,11 +570,11 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
       l_run = (xs[0] + xs[kRows]) + (xs[2 * kRows] + xs[3 * kRows]);
       tc::fence_after_sync();
       bool any_odd = false;
-      const volatile uint32_t *mine = odd + (odd_par * kParts + hf) * 8;
-      if (has_part) {  // also orders the bits of units two apart
+      const volatile uint32_t *mine = odd + (odd_at * kParts + hf) * 8;
+      if (has_part) {
         named_barrier(kSoftBar, kSoft);
         for (int i = 0; i < 8; ++i) any_odd |= mine[i] != 0u;
-        if (tid < kParts * 8) odd[(odd_par ^ 1) * kParts * 8 + tid] = 0u;
+        if (tid < kParts * 8) odd[(odd_at + kOddBufs - 1) % kOddBufs * kParts * 8 + tid] = 0u;
       }
 
       // ---- this part's OC columns of (O, m, l), 16 at a time
@@ -647,7 +653,7 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
           put_rows(v, inv, d0);
         }
       }
-      if (has_part) odd_par ^= 1;
+      if (has_part) odd_at = (odd_at + 1) % kOddBufs;
       if (cut) {
         if (hf == 0 && row_ok) *part_at(cta, D / 4) = make_float4(m_run, l_run, 0.f, 0.f);
         named_barrier(kSoftBar, kSoft);
@@ -741,8 +747,8 @@ struct Lay2 {
   static constexpr int kV = kK + kSt * kTile;
   static constexpr int kStage = kV + kSt * kTile;  // 32 rows x 32 columns of output per softmax warp
   static constexpr int kSched = kStage + 8 * 2048;
-  static constexpr int kOdd = kSched + (int)((sizeof(PSched) + 15) / 16 * 16);  // uint32 [unit & 1][kind][8]
-  static constexpr int kMisc = kOdd + 2 * 16 * 4;
+  static constexpr int kOdd = kSched + (int)((sizeof(PSched) + 15) / 16 * 16);  // uint32 [buffer][kind][8]
+  static constexpr int kMisc = kOdd + kOddBufs * 16 * 4;
   static constexpr int kBars = kMisc + 16;
   static constexpr int kAlloc = kBars + 40 * 8 + 1024;  // and room to align the base
   static_assert(kAlloc <= 232448, "shared memory");
@@ -810,7 +816,7 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
     }
     mbar_fence_init();
     *abort_flag = 0;
-    for (int i = 0; i < 32; ++i) odd[i] = 0u;
+    for (int i = 0; i < kOddBufs * 16; ++i) odd[i] = 0u;
   }
   // query rows past a half's tokens stay zero
   for (int e = tid; e < 2 * QP * L::kTile / 16; e += kThreads2) reinterpret_cast<uint4 *>(smem + L::kQ)[e] = make_uint4(0, 0, 0, 0);
@@ -985,7 +991,7 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
     PWalk<kKeys> w(shp, sched);
     PUnit u;
-    int gk = 0, cnt = 0, odd_par = 0;  // key tiles of the CTA's units so far, and of this half
+    int gk = 0, cnt = 0, odd_at = 0;  // key tiles of the CTA's units so far, and of this half; buffer of odd bits
     // A warp that gives up a tile (an expired wait, an abort elsewhere) still runs every unit's
     // epilogue: the softmax warps meet at its barriers.
     while (w.next(shp, u)) {
@@ -1086,7 +1092,7 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
             // its last token's window
             if (zero) {
               const int kind = j > u.qpos ? 0 : 1, i = (int)(j - (kind ? jlo : u.qpos));
-              atomicOr(&odd[odd_par * 16 + kind * 8 + i / 32], 1u << (i & 31));
+              atomicOr(&odd[odd_at * 16 + kind * 8 + i / 32], 1u << (i & 31));
             }
           }
           if (zero)
@@ -1109,11 +1115,11 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
       }
       tc::fence_after_sync();
       bool any_odd = false;
-      const volatile uint32_t *mine = odd + odd_par * 16;
-      if (has_part) {  // both halves' checks are in; also orders the bits of units two apart
+      const volatile uint32_t *mine = odd + odd_at * 16;
+      if (has_part) {  // both halves' checks are in
         named_barrier(kSoftBar, kSoft2);
         for (int i = 0; i < 16; ++i) any_odd |= mine[i] != 0u;
-        if (tid < 16) odd[(odd_par ^ 1) * 16 + tid] = 0u;
+        if (tid < 16) odd[(odd_at + kOddBufs - 1) % kOddBufs * 16 + tid] = 0u;
       }
 
       // ---- the row's D columns of O, and (m, l), 32 at a time
@@ -1199,7 +1205,7 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
           }
         }
       }
-      if (has_part) odd_par ^= 1;
+      if (has_part) odd_at = (odd_at + 1) % kOddBufs;
       if (cut) {
         if (row_ok) *part_at(cta, D / 4) = make_float4(have ? m_run : -INFINITY, have ? l_run : 0.f, 0.f, 0.f);
         named_barrier(kSoftBar, kSoft2);
