@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 
 #include "gqaw_paged_tc.cuh"
@@ -356,6 +357,25 @@ unsigned long long pages_bytes(const gqaw_paged_args *a, const Plan &L) {
           (unsigned long long)(a->page_size - 1) * L.sr + a->head_size) * L.es;
 }
 
+// Do the rows of two caches of the same strides lie apart, though the bytes between their first and
+// last overlap?  With the strides ascending, a block of a level is what its inner dimensions reach
+// over, and the blocks lie a stride apart: two caches woven at that level have each other's blocks
+// between their own (a page's, a head's or a row's keys beside its values).
+bool woven_pages(const gqaw_paged_args *a, const Plan &L) {
+  struct {
+    long long stride, count;
+  } dim[3] = {{L.sr, a->page_size}, {L.sh, a->kv_num_heads}, {L.sp, a->num_pages}};
+  std::sort(dim, dim + 3, [](const auto &x, const auto &y) { return x.stride < y.stride; });
+  const long long gap = std::llabs(static_cast<const char *>(a->key_pages) - static_cast<const char *>(a->value_pages)) / L.es;
+  long long block = a->head_size;
+  for (const auto &d : dim) {
+    if (d.count < 2) continue;  // such a dimension may have any stride
+    if (gap >= block && gap + block <= d.stride) return true;
+    block += (d.count - 1) * d.stride;
+  }
+  return false;
+}
+
 gqaw_status check_paged_pointers(const gqaw_paged_args *a, const Plan &L, bool append, bool attend) {
   gqaw_status s;
   const long long N = a->total_new_tokens, D = a->head_size;
@@ -386,17 +406,11 @@ gqaw_status check_paged_pointers(const gqaw_paged_args *a, const Plan &L, bool a
     all[n++] = range_of(a->value, rows_bytes(N, L.vs, a->kv_num_heads * D, L.es), "value");
   }
   if (attend) all[n++] = range_of(a->query, rows_bytes(N, L.qs, a->num_heads * D, L.es), "query");
-  // key and value pages woven into one tensor (a page's keys beside its values) overlap as
-  // ranges without sharing a row: allowed when they lie a head, row or page apart
   for (int i = 0; i < nw; ++i)
     for (int k = i + 1; k < n; ++k) {
       if (!overlap(all[i], all[k])) continue;
       const bool kv = std::strcmp(all[i].name, "key_pages") == 0 && std::strcmp(all[k].name, "value_pages") == 0;
-      if (kv) {
-        const unsigned long long gap = (unsigned long long)std::llabs(all[k].lo - all[i].lo) / L.es;
-        const unsigned long long inner = (unsigned long long)(a->kv_num_heads - 1) * L.sh + (unsigned long long)(a->page_size - 1) * L.sr + D;
-        if (gap >= inner && gap + inner <= (unsigned long long)L.sp) continue;
-      }
+      if (kv && woven_pages(a, L)) continue;
       return fail(GQAW_EINVAL, "%s overlaps %s", all[i].name, all[k].name);
     }
   const struct {
