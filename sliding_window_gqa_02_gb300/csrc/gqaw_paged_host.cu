@@ -64,13 +64,22 @@ unsigned long long rows_bytes(long long n, long long stride, long long row, int 
   return n <= 0 ? 0ull : ((unsigned long long)(n - 1) * (unsigned long long)stride + (unsigned long long)row) * (unsigned)es;
 }
 
-constexpr long long kMaxStride = 1ll << 40;  // keeps every byte count far inside 64 bits
+// What a tensor's strides reach over, and its bytes, stay far inside 64 bits (and inside what an
+// address can hold).
+constexpr long long kMaxStride = 1ll << 40, kMaxElements = 1ll << 48;
 
-gqaw_status row_stride(const char *name, int64_t given, long long row, int es, long long *out) {
+// n blocks of `block` elements that lie `stride` elements apart; kMaxElements if that or more.
+long long reach(long long n, long long stride, long long block) {
+  const __int128 x = n <= 0 ? 0 : (__int128)(n - 1) * stride + block;
+  return x < kMaxElements ? (long long)x : kMaxElements;
+}
+
+gqaw_status row_stride(const char *name, int64_t given, long long row, int es, long long n, long long *out) {
   *out = given ? given : row;
   if (given < 0 || (given && given < row)) return fail(GQAW_EINVAL, "%s %lld: 0 or at least %lld", name, (long long)given, row);
   if (given > kMaxStride) return fail(GQAW_EUNSUPPORTED, "%s %lld is too large", name, (long long)given);
   if (*out * es % 16 != 0) return fail(GQAW_EINVAL, "%s %lld is not a multiple of 16 bytes", name, *out);
+  if (reach(n, *out, row) == kMaxElements) return fail(GQAW_EUNSUPPORTED, "%s %lld is too large for %lld tokens", name, *out, n);
   return GQAW_OK;
 }
 
@@ -149,11 +158,11 @@ gqaw_status plan_qk(const gqaw_qk_args *a, QkPlan *L) {
   gqaw_status s = check_rotary(a->cos_cache, a->sin_cache, a->rotary_dim, a->rotary_cache_len, a->head_size, &L->rot_dim);
   if (s != GQAW_OK) return s;
   const long long qrow = (long long)a->num_heads * a->head_size, krow = (long long)a->kv_num_heads * a->head_size;
-  if (a->num_heads && ((s = row_stride("query_stride", a->query_stride, qrow, L->es, &L->qs)) != GQAW_OK ||
-                       (s = row_stride("query_out_stride", a->query_out_stride, qrow, L->es, &L->qos)) != GQAW_OK))
+  if (a->num_heads && ((s = row_stride("query_stride", a->query_stride, qrow, L->es, a->num_tokens, &L->qs)) != GQAW_OK ||
+                       (s = row_stride("query_out_stride", a->query_out_stride, qrow, L->es, a->num_tokens, &L->qos)) != GQAW_OK))
     return s;
-  if (a->kv_num_heads && ((s = row_stride("key_stride", a->key_stride, krow, L->es, &L->ks)) != GQAW_OK ||
-                          (s = row_stride("key_out_stride", a->key_out_stride, krow, L->es, &L->kos)) != GQAW_OK))
+  if (a->kv_num_heads && ((s = row_stride("key_stride", a->key_stride, krow, L->es, a->num_tokens, &L->ks)) != GQAW_OK ||
+                          (s = row_stride("key_out_stride", a->key_out_stride, krow, L->es, a->num_tokens, &L->kos)) != GQAW_OK))
     return s;
   return GQAW_OK;
 }
@@ -254,10 +263,10 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
   gqaw_status s = check_rotary(a->cos_cache, a->sin_cache, a->rotary_dim, a->rotary_cache_len, a->head_size, &L->rot_dim);
   if (s != GQAW_OK) return s;
   const long long D = a->head_size, qrow = a->num_heads * D, krow = a->kv_num_heads * D;
-  if ((s = row_stride("query_stride", a->query_stride, qrow, L->es, &L->qs)) != GQAW_OK ||
-      (s = row_stride("key_stride", a->key_stride, krow, L->es, &L->ks)) != GQAW_OK ||
-      (s = row_stride("value_stride", a->value_stride, krow, L->es, &L->vs)) != GQAW_OK ||
-      (s = row_stride("output_stride", a->output_stride, qrow, L->es, &L->os)) != GQAW_OK)
+  if ((s = row_stride("query_stride", a->query_stride, qrow, L->es, a->total_new_tokens, &L->qs)) != GQAW_OK ||
+      (s = row_stride("key_stride", a->key_stride, krow, L->es, a->total_new_tokens, &L->ks)) != GQAW_OK ||
+      (s = row_stride("value_stride", a->value_stride, krow, L->es, a->total_new_tokens, &L->vs)) != GQAW_OK ||
+      (s = row_stride("output_stride", a->output_stride, qrow, L->es, a->total_new_tokens, &L->os)) != GQAW_OK)
     return s;
   if (!a->page_stride && !a->head_stride && !a->row_stride) {
     L->sr = D;
@@ -273,11 +282,13 @@ gqaw_status plan_paged(const gqaw_paged_args *a, Plan *L) {
       if (x * L->es % 16 != 0) return fail(GQAW_EINVAL, "a page stride of %lld is not a multiple of 16 bytes", x);
     }
     // no two rows share an element: heads within rows, or rows within heads, inside a page
-    const long long h = a->kv_num_heads, r = a->page_size;
-    const bool rows_inside = L->sh >= (r - 1) * L->sr + D && L->sp >= (h - 1) * L->sh + (r - 1) * L->sr + D;
-    const bool heads_inside = L->sr >= (h - 1) * L->sh + D && L->sp >= (r - 1) * L->sr + (h - 1) * L->sh + D;
+    const long long h = a->kv_num_heads, r = a->page_size, of_head = reach(r, L->sr, D), of_row = reach(h, L->sh, D);
+    const bool rows_inside = L->sh >= of_head && L->sp >= reach(h, L->sh, of_head);
+    const bool heads_inside = L->sr >= of_row && L->sp >= reach(r, L->sr, of_row);
     if (!rows_inside && !heads_inside) return fail(GQAW_EINVAL, "the page strides make rows of the cache overlap");
   }
+  if (reach(a->num_pages, L->sp, reach(a->kv_num_heads, L->sh, reach(a->page_size, L->sr, D))) == kMaxElements)
+    return fail(GQAW_EUNSUPPORTED, "the pages reach over 2^48 elements or more");
 
   // The kernel.  A query tile is tokens times the query heads of a kv head (a block of them
   // when they are more than the tile has rows).
