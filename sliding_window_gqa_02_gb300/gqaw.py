@@ -463,7 +463,8 @@ def _tables(a, cos_cache, sin_cache, interleaved, like):
     if cos_cache is None:
         return
     for t in (cos_cache, sin_cache):
-        if t.dim() != 2 or tuple(t.shape) != tuple(cos_cache.shape) or not t.is_contiguous() \
+        # an empty tensor has no address, which would mean no rotation
+        if t.dim() != 2 or t.numel() == 0 or tuple(t.shape) != tuple(cos_cache.shape) or not t.is_contiguous() \
                 or t.dtype != like.dtype or t.device != like.device:
             raise ValueError("cos_cache/sin_cache: equal contiguous (max_pos, rd/2) tensors of the rows' dtype and device")
     a.cos_cache, a.sin_cache = _ptr(cos_cache), _ptr(sin_cache)
