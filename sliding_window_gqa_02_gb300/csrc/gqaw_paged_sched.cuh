@@ -185,29 +185,17 @@ struct PTiles {
 
 constexpr int kMergeTiles = 7;
 
-// The last i in [0, n) with le(i), for le that holds at 0 and, once false, stays false.  On the
-// device a whole warp calls it: 32 places at a time, for le may be a chain of divisions.
+// The last i in [0, n) with le(i), for le that holds at 0 and, once false, stays false: 32 places
+// at a time, for le may be a chain of divisions.  On the device a whole warp calls it.
 template <typename F>
 GQAW_HD int last_where(int n, F le) {
   int lo = 0;
-#ifdef __CUDA_ARCH__
-  const int lane = threadIdx.x & 31;
   while (n > 1) {
-    const int step = (n + 31) / 32, i = lane * step;
-    const int c = __popc(__ballot_sync(0xffffffffu, i < n && le(lo + i)));
+    const int step = (n + 31) / 32;
+    const int c = bits_set(warp_vote([&](int lane) { return lane * step < n && le(lo + lane * step); }));
     lo += (c - 1) * step;
     n = step < n - (c - 1) * step ? step : n - (c - 1) * step;
   }
-#else
-  int hi = n - 1;
-  while (lo < hi) {
-    const int m = (lo + hi + 1) / 2;
-    if (le(m))
-      lo = m;
-    else
-      hi = m - 1;
-  }
-#endif
   return lo;
 }
 
