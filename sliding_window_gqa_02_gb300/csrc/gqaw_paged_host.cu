@@ -450,8 +450,9 @@ void fill(const gqaw_paged_args *a, const Plan &L, PagedParams *p) {
   p->k = a->key;
   p->v = a->value;
   p->out = a->output;
-  p->kp = a->key_pages;
-  p->vp = a->value_pages;
+  // without pages no row is read, but copies of no bytes still name a source: a valid address
+  p->kp = a->num_pages ? a->key_pages : a->workspace;
+  p->vp = a->num_pages ? a->value_pages : a->workspace;
   p->qs = L.qs, p->ks = L.ks, p->vs = L.vs, p->os = L.os;
   p->sp = L.sp, p->sh = L.sh, p->sr = L.sr;
   p->table = a->page_table;

@@ -91,3 +91,18 @@ def test_shared_rows_touch_only_their_sequences(call, dtype):
     b.check_pages(k0, v0)
     if call == "gqaw_paged_step":
         b.check_output()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("D,S", [(64, 1), (64, 40), (256, 1), (32, 3)])
+def test_a_cache_without_pages(D, S, dtype):
+    """No page exists: every table entry is out of range, and the tokens' outputs are unspecified."""
+    b = Batch([(S, 40), (0, 5), (1, 9)], 4, 2, D, 16, dtype, seed=34, norm=True, rotary=D, extra_rows=2)
+    b.kp, b.vp = b.kp[:0], b.vp[:0]
+    assert b.args().num_pages == 0
+    for call in (gqaw.gqaw_paged_append, gqaw.gqaw_paged_attend, gqaw.gqaw_paged_step):
+        b.call(call, flags=gqaw.GQAW_DEV_BAD_PAGE)
+    assert (b.out[S + 1:] == 7.0).all()
+    c = Batch([(S, 40), (1, 9)], 4, 2, D, 16, dtype, seed=35)
+    c.call(gqaw.gqaw_paged_attend)
+    c.check_output()
