@@ -336,6 +336,9 @@ gqaw_status gqaw_qk_norm_rotary(const gqaw_qk_args *args, void *stream);
  * j of sequence b lives in row j % page_size of page page_table[b][j / page_size].
  * Several sequences may share a page; the rows that one call writes must be distinct.
  *
+ * Every pointer has to be memory that the current device can use: the calls look at one (the
+ * workspace; the norms at their first rows), and refuse another device's or the host's there.
+ *
  * The batch.  Sequence b brings S_b = query_start[b + 1] - query_start[b] new tokens (0
  * is fine), rows query_start[b] .. of query, key, value and output, which end at length
  * T_b = seqlens_k[b] + 1 (the length including them; seqlens_k[b] = -1 is an empty
@@ -428,9 +431,9 @@ gqaw_status gqaw_paged_append(const gqaw_paged_args *args, void *stream);
  * attend and that is not finite makes the elements of its output that depend on it not finite
  * or, for a key, unspecified.  bf16 on the tensor cores (head sizes from 64, pages of a power of
  * two rows, or a multiple of 128, from 8 on) rounds the softmax weights to bf16 where a kv head
- * has more than 8 rows of queries in a tile; sums and statistics are fp32 throughout.  One
- * kernel, or two where single tokens and long chunks come together; the same inputs give the
- * same bits. */
+ * has more than 8 rows of queries in a tile; sums and statistics are fp32 throughout.  For
+ * every 256 sequences one kernel, or two where single tokens and long chunks come together; the
+ * same inputs give the same bits. */
 gqaw_status gqaw_paged_attend(const gqaw_paged_args *args, void *stream);
 
 /* The whole step: append, and attention of the normed and turned queries.  The cache is the one

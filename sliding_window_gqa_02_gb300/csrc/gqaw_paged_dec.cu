@@ -19,8 +19,9 @@
 // only rounding is its own (error against 64 bits 0.0023 -> 0.0017 relative).  Likewise rows 8 to 15
 // of Q hold what bf16 left of queries that the step has turned, and the two logits are added.
 //
-// Measured: 64 contexts of 4096 to 32768 keys (3.6 GB) in 506 us, 7.1 TB/s, 107% of the measured
-// copy rate; one sequence of 131 keys 8.0 us.
+// Measured: 64 contexts of 4096 to 32768 keys (3.6 GB) in 506 to 515 us on different machines, 7.0 to
+// 7.1 TB/s, 105 to 107% of the measured copy rate; one sequence of 131 keys 8.0 us.  Head sizes 64
+// and 256 reach 6.5 and 7.0 TB/s with pages of 64 rows, 4.7 and 5.0 with pages of 16 (copies of 2 KB).
 //
 // Warps: 4 CG softmax warps, a TMA warp for Q and K and one for V (a lane looks up each box of
 // a tile), one warp issuing S^T and one issuing P.V.  K and V tiles alternate through one ring of

@@ -35,6 +35,10 @@
 // for rows that are not finite among those that only some attend (0 x inf is NaN): these are
 // zeroed too, and added at the unit's end to the rows that attend them, from global memory.
 //
+// Up to 32 rows (a verify step) lie in one quarter of the lanes, whose warps share one scheduler and
+// its exponential unit: that bounds such a step (16 x 8 tokens, window 4096: 53.7 us, 59.7 with a cap,
+// whose logits take three of its operations each; 40.6 of memory).
+//
 // Every wait is bounded; one that expires flags GQAW_DEV_TIMEOUT and the CTA winds down.
 #include <atomic>
 #include <type_traits>
@@ -733,7 +737,9 @@ __global__ void __launch_bounds__(ppre::kThreads, 1)
 // attends.  The value rows of a tile are checked (see above) by the first half that uses the tile.
 // Measured: 8 chunks of 512 tokens with a window of 4096 in 318 us (865 TFLOP/s), a prompt of 8192
 // in 0.54 ms (1015 TFLOP/s, 53% of the measured bf16 rate); tensor pipe 39% busy, issue slots
-// 31%, exponential unit 20%, DRAM 43%: the chain of a half is the limit, no unit.
+// 31%, exponential unit 20%, DRAM 43%: the chain of a half is the limit, no unit.  The 128 logits do
+// not fit beside what else a thread holds: 320 bytes of spill stores and 424 of loads (queries in two
+// parts 196 and 272, head size 64 148 and 212, 100 and 140).
 
 namespace ppre {
 
@@ -741,7 +747,8 @@ template <int D, bool SPLIT>
 struct Lay2 {
   static constexpr int HALVES = D / 64;
   static constexpr int kTile = HALVES * kHalf;
-  static constexpr int kSt = D == 64 ? 4 : SPLIT ? 1 : 2;  // K tiles, and V tiles
+  // K tiles, and V tiles.  One of each: K(k + 1) is loaded only behind both halves' S(k)
+  static constexpr int kSt = D == 64 ? 4 : SPLIT ? 1 : 2;
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + (SPLIT ? 4 : 2) * kTile;  // Q of both halves, and what bf16 left of them
   static constexpr int kV = kK + kSt * kTile;

@@ -20,9 +20,9 @@
 // first is used: 4 where there are tokens enough to fill the GPU, 2 where the chain of dependent
 // look-ups (sequence, position, tables) is the time.  What hides that chain is many warps, so
 // registers are the price: the usual pairing has a kernel of its own that fits 64 of them (32
-// warps a SM; 4099 tokens of 40 heads of 128 in bf16: 22.6 us, 3.8 TB/s; with 8 groups and 80
+// warps a SM; 4099 tokens of 40 heads of 128 in bf16: 21.9 us, 3.9 TB/s; with 8 groups and 80
 // registers 23.2 us, with every pairing in one kernel 24.0, in CTAs of 256 threads 25.4; 48
-// registers spill: 29).  fp32 takes 80: 33.4 us, 5.1 TB/s, against 41.8 with 64.
+// registers spill: 29).  fp32 takes 80: 33.6 us, 5.1 TB/s, against 41.8 with 64.
 // A lane stores only what it loaded, so the norm may work in place.
 #include <atomic>
 
