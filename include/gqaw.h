@@ -446,6 +446,81 @@ gqaw_status gqaw_paged_step(const gqaw_paged_args *args, void *stream);
 size_t gqaw_qk_args_size(void);
 size_t gqaw_paged_args_size(void);
 
+/* ---------------------------------------------------------------------------------
+ * Paged caches held in 4 bits.  The pages name quantized caches with one scale per tensor
+ * and 8-bit codes only; these operators are the paged ones for a cache that takes 28% of a
+ * bf16 one's bytes, with scales found as the rows are written.
+ *
+ * A row of D elements is D / 2 bytes of codes, element 2 i in the low and 2 i + 1 in the high
+ * four bits of byte i, and D / 32 bf16 scales, one for every GQAW_I4_GROUP consecutive
+ * elements.  Code c stands for (c - 8) * scale.  Rows are written with
+ *     scale = max |x| / 7 over the group (in fp32), rounded up to five significant bits,
+ *     c = 8 + round(x / scale)       (in fp32, halves to even; so 1 <= c <= 15),
+ * a scale and codes of 0 and 8 for a group of zeros, and a scale that is not a number for a
+ * group with an element that is not finite.  Five bits times the three of c - 8 make every
+ * value a bf16 number: reading a row back as bf16 or fp32 loses nothing, and the tensor cores
+ * see the values that the cache holds.  Other writers may use any bf16 scale and any code; a
+ * product of more than eight bits is then rounded to bf16 where it is needed as bf16 (reading
+ * back as bf16, attention of more than 32 query rows per kv head in bf16).
+ * ------------------------------------------------------------------------------- */
+
+#define GQAW_I4_GROUP 32
+
+/* Arguments of the operators on 4-bit caches: those of the paged operators, with these
+ * differences.
+ *   - head_size is 32, 64, 128 or 256.
+ *   - key_pages and value_pages hold codes.  page_stride, head_stride and row_stride are in
+ *     BYTES, multiples of 16; all three 0 for contiguous (num_pages, Nkv, page_size, D / 2).
+ *   - dtype is that of the rows outside the cache: query, key, value, output, key_out,
+ *     value_out, the weights and the tables.
+ * Key and value codes and their scales may lie in one buffer, woven at any level that their
+ * strides agree on; no two bytes that a call may write are the same. */
+typedef struct gqaw_paged_i4_args {
+  gqaw_paged_args paged;
+  void *key_scales;           /* bf16: group e of row r of head h in page p at p * scale_page_stride
+                                 + h * scale_head_stride + r * scale_row_stride + e.  Every row of
+                                 scales is aligned to its D / 16 bytes */
+  void *value_scales;
+  int64_t scale_page_stride;  /* elements, multiples of D / 32; all three 0: contiguous
+                                 (num_pages, Nkv, page_size, D / 32) */
+  int64_t scale_head_stride;
+  int64_t scale_row_stride;
+  void *key_out;              /* read: (N, Nkv, D), 16-byte aligned, or NULL: no keys */
+  void *value_out;            /* read: the same for values; not both are NULL */
+  int64_t key_out_stride;     /* elements between tokens: 0 for Nkv * D, else >= Nkv * D */
+  int64_t value_out_stride;
+} gqaw_paged_i4_args;
+
+/* Workspace bytes of any of the four calls below, as gqaw_paged_workspace_bytes(); an append and a
+ * read need 256 bytes alone, for the device status word.  A workspace serves paged calls on 4-bit and
+ * on other caches alike, in stream order, if it is large enough for each. */
+size_t gqaw_paged_i4_workspace_bytes(const gqaw_paged_i4_args *args);
+
+/* Append: key rows, normed with key_weight and turned by their positions (each if given) in
+ * fp32, and value rows are quantized to their places in the pages.  With y = x r w, r = 1 /
+ * sqrt(mean(x^2) + norm_eps) rounded once to fp32 and every product and sum of the norm and
+ * the turn rounded by itself, so that codes do not depend on the order of a sum. */
+gqaw_status gqaw_paged_i4_append(const gqaw_paged_i4_args *args, void *stream);
+
+/* Attention over the cache as gqaw_paged_attend; logits and outputs are those of the values that
+ * the codes stand for.  Sums and statistics are fp32.  Up to 32 query rows per kv head in a
+ * sequence (and fp32 rows at any number) are multiplied as they are, in two parts of fp16 for
+ * fp32; the softmax weights, times the value scales, are rounded to fp16 (2^-12 relative), or
+ * two parts of it for fp32.  More rows in bf16: softmax weights are rounded to bf16. */
+gqaw_status gqaw_paged_i4_attend(const gqaw_paged_i4_args *args, void *stream);
+
+/* The whole step as gqaw_paged_step: append, and attention of the normed and turned queries. */
+gqaw_status gqaw_paged_i4_step(const gqaw_paged_i4_args *args, void *stream);
+
+/* Reading back, the inverse of an append's placing: the values of positions T_b - S_b .. T_b - 1 of
+ * every sequence go to rows query_start[b] .. of key_out and value_out, rounded once to dtype
+ * (exact for rows that the append wrote).  S_b = T_b reads a whole sequence.  A row whose table
+ * entry is out of range is left as it was, and GQAW_DEV_BAD_PAGE is set. */
+gqaw_status gqaw_paged_i4_read(const gqaw_paged_i4_args *args, void *stream);
+
+/* sizeof(gqaw_paged_i4_args) as compiled into the library. */
+size_t gqaw_paged_i4_args_size(void);
+
 #ifdef __cplusplus
 }
 #endif

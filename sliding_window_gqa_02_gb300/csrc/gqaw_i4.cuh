@@ -1,0 +1,31 @@
+// gqaw_i4.cuh -- parameters of the operators on paged caches held in 4 bits.
+//
+// A row of D elements: D / 2 bytes of codes (element 2 i low, 2 i + 1 high in byte i) and D / 32
+// bf16 scales; code c stands for (c - 8) scale.  In PagedParams kp and vp are the codes, and sp, sh,
+// sr their strides in bytes.
+#pragma once
+
+#include "gqaw_paged.cuh"
+
+namespace gqaw {
+
+constexpr int kI4Group = 32;
+
+struct I4Params : PagedParams {
+  uint16_t *kscale, *vscale;    // bf16 bits
+  long long tp, th, tr;         // elements between pages, heads, rows of scales
+  void *ko, *vo;                // read: rows out, either may be NULL
+  long long kos, vos;
+};
+
+// Where position j of sequence b lies: page and row in it; page -1 when its entry is bad.
+struct I4Place {
+  long long page;
+  int row;
+};
+__device__ __forceinline__ I4Place i4_place(const I4Params &p, int b, long long j) {
+  const int pg = (int)(j / p.page), id = p.table[(long long)b * p.width + pg];
+  return {(unsigned)id < (unsigned)p.npages ? id : -1, (int)(j - (long long)pg * p.page)};
+}
+
+}  // namespace gqaw

@@ -1,0 +1,248 @@
+// gqaw_i4_host.cu -- the C ABI of the operators on paged caches held in 4 bits (include/gqaw.h):
+// argument checks, the choice of kernel, launches.  No allocation and no synchronisation.
+#include "gqaw_i4.cuh"
+#include "gqaw_paged_check.cuh"
+
+namespace gqaw {
+cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read, bool bf16, cudaStream_t stream);
+cudaError_t launch_i4_attend(const I4Params &p, bool bf16, cudaStream_t stream);
+}  // namespace gqaw
+
+namespace {
+
+using gqaw::I4Params;
+using namespace gqaw::pcheck;
+
+struct I4Plan : PagedSizes {
+  long long sp, sh, sr;          // codes, bytes
+  long long tp, th, tr;          // scales, elements
+  long long kos, vos;
+  size_t off_q, off_qlo, ws_bytes;
+};
+
+// Strides of one part of the cache: rows of `row` units.  `unit`: what a stride is a multiple of.
+gqaw_status page_strides(const char *what, int64_t page, int64_t head, int64_t rows, long long row, long long unit,
+                         const gqaw_paged_args *a, long long *sp, long long *sh, long long *sr) {
+  if (!page && !head && !rows) {
+    *sr = row;
+    *sh = row * a->page_size;
+    *sp = *sh * a->kv_num_heads;
+  } else {
+    *sp = page;
+    *sh = head;
+    *sr = rows;
+    for (long long x : {*sp, *sh, *sr}) {
+      if (x < row) return fail(GQAW_EINVAL, "the page, head and row strides of the %s: all 0, or each at least %lld", what, row);
+      if (x > kMaxStride) return fail(GQAW_EUNSUPPORTED, "a stride of the %s of %lld is too large", what, x);
+      if (x % unit != 0) return fail(GQAW_EINVAL, "a stride of the %s of %lld is not a multiple of %lld", what, x, unit);
+    }
+    // no two rows share a byte: heads within rows, or rows within heads, inside a page
+    const long long h = a->kv_num_heads, r = a->page_size, of_head = reach(r, *sr, row), of_row = reach(h, *sh, row);
+    const bool rows_inside = *sh >= of_head && *sp >= reach(h, *sh, of_head);
+    const bool heads_inside = *sr >= of_row && *sp >= reach(r, *sr, of_row);
+    if (!rows_inside && !heads_inside) return fail(GQAW_EINVAL, "the strides make rows of the %s overlap", what);
+  }
+  if (reach(a->num_pages, *sp, reach(a->kv_num_heads, *sh, reach(a->page_size, *sr, row))) == kMaxElements)
+    return fail(GQAW_EUNSUPPORTED, "the %s reach over 2^48 elements or more", what);
+  return GQAW_OK;
+}
+
+gqaw_status plan_i4(const gqaw_paged_i4_args *x, I4Plan *L) {
+  if (!x) return fail(GQAW_EINVAL, "args is NULL");
+  const gqaw_paged_args *a = &x->paged;
+  gqaw_status s = check_paged_sizes(a, L);
+  if (s != GQAW_OK) return s;
+  const long long D = a->head_size, krow = a->kv_num_heads * D;
+  if (D < gqaw::kI4Group) return fail(GQAW_EUNSUPPORTED, "head_size %d: a 4-bit cache takes 32, 64, 128, 256", a->head_size);
+  if ((s = page_strides("codes", a->page_stride, a->head_stride, a->row_stride, D / 2, 16, a, &L->sp, &L->sh, &L->sr)) != GQAW_OK ||
+      (s = page_strides("scales", x->scale_page_stride, x->scale_head_stride, x->scale_row_stride, D / gqaw::kI4Group,
+                        D / gqaw::kI4Group, a, &L->tp, &L->th, &L->tr)) != GQAW_OK ||
+      (s = row_stride("key_out_stride", x->key_out_stride, krow, L->es, a->total_new_tokens, &L->kos)) != GQAW_OK ||
+      (s = row_stride("value_out_stride", x->value_out_stride, krow, L->es, a->total_new_tokens, &L->vos)) != GQAW_OK)
+    return s;
+  L->ws_bytes = gqaw::kPagedPartialOffset;
+  L->off_q = L->ws_bytes;
+  L->ws_bytes += align256((size_t)a->total_new_tokens * a->num_heads * D * L->es);
+  L->off_qlo = L->ws_bytes;  // what bf16 leaves of turned queries
+  if (a->dtype == GQAW_BF16) L->ws_bytes += align256((size_t)a->total_new_tokens * a->num_heads * D * L->es);
+  return GQAW_OK;
+}
+
+// A part of the cache as bytes: three strides, each with a count, and the row inside.
+struct Part {
+  Range all;
+  struct {
+    long long stride, count;
+  } dim[3];  // the largest stride first
+  long long row;
+  int n;     // dimensions of more than one element
+};
+
+Part part_of(const void *p, const char *name, const gqaw_paged_args *a, long long sp, long long sh, long long sr, long long row, int unit) {
+  Part x;
+  x.row = row * unit;
+  x.n = 0;
+  const struct {
+    long long stride, count;
+  } dims[3] = {{sp, a->num_pages}, {sh, a->kv_num_heads}, {sr, a->page_size}};
+  unsigned long long bytes = (unsigned long long)x.row;
+  for (const auto &d : dims) {
+    bytes += (unsigned long long)(d.count > 0 ? d.count - 1 : 0) * d.stride * unit;
+    if (d.count > 1) x.dim[x.n++] = {d.stride * unit, d.count};
+  }
+  std::sort(x.dim, x.dim + x.n, [](const auto &u, const auto &v) { return u.stride > v.stride; });
+  x.all = range_of(p, a->num_pages ? bytes : 0, name);
+  return x;
+}
+
+// Do two parts of the cache lie apart, though the bytes between their first and last overlap?  At a
+// level down to which their strides agree, what the inner dimensions of one reach over lies between two of
+// the other's.
+bool woven_parts(const Part &x, const Part &y) {
+  const Part &f = x.all.lo < y.all.lo ? x : y, &g = x.all.lo < y.all.lo ? y : x;
+  const long long gap = g.all.lo - f.all.lo;
+  auto inner = [](const Part &p, int from) {
+    long long b = p.row;
+    for (int i = from; i < p.n; ++i) b += (p.dim[i].count - 1) * p.dim[i].stride;
+    return b;
+  };
+  for (int k = 0; k < f.n && k < g.n && f.dim[k].stride == g.dim[k].stride && f.dim[k].count == g.dim[k].count; ++k)
+    if (gap >= inner(f, k + 1) && gap + inner(g, k + 1) <= f.dim[k].stride) return true;
+  return false;
+}
+
+enum What { kAppend = 1, kAttend = 2, kRead = 4 };
+
+gqaw_status check_i4_pointers(const gqaw_paged_i4_args *x, const I4Plan &L, int what) {
+  const gqaw_paged_args *a = &x->paged;
+  gqaw_status s;
+  const long long N = a->total_new_tokens, D = a->head_size;
+  const bool append = what & kAppend, attend = what & kAttend, read = what & kRead;
+  const size_t need = attend ? L.ws_bytes : 256;  // an append and a read only flag
+  if ((s = check_workspace(a->workspace, a->workspace_bytes, need)) != GQAW_OK) return s;
+  const size_t scale_row = (size_t)D / gqaw::kI4Group * 2;
+  if (a->num_pages) {
+    if ((s = check_tensor("key_pages", a->key_pages)) != GQAW_OK || (s = check_tensor("value_pages", a->value_pages)) != GQAW_OK ||
+        (s = check_tensor("key_scales", x->key_scales, scale_row)) != GQAW_OK ||
+        (s = check_tensor("value_scales", x->value_scales, scale_row)) != GQAW_OK)
+      return s;
+  }
+  const Part part[4] = {part_of(a->key_pages, "key_pages", a, L.sp, L.sh, L.sr, D / 2, 1),
+                        part_of(a->value_pages, "value_pages", a, L.sp, L.sh, L.sr, D / 2, 1),
+                        part_of(x->key_scales, "key_scales", a, L.tp, L.th, L.tr, D / gqaw::kI4Group, 2),
+                        part_of(x->value_scales, "value_scales", a, L.tp, L.th, L.tr, D / gqaw::kI4Group, 2)};
+  if (append)
+    for (int i = 0; i < 4; ++i)
+      for (int k = i + 1; k < 4; ++k)
+        if (overlap(part[i].all, part[k].all) && !woven_parts(part[i], part[k]))
+          return fail(GQAW_EINVAL, "%s overlaps %s", part[i].all.name, part[k].all.name);
+  struct {
+    Range r;
+    bool written, cache;
+  } t[10];
+  int n = 0;
+  auto add = [&](const Range &r, bool written, bool cache = false) { t[n++] = {r, written, cache}; };
+  add(range_of(a->workspace, need, "workspace"), true);
+  for (const Part &p : part) add(p.all, append, true);
+  if (attend) {
+    if ((s = check_tensor("query", a->query)) != GQAW_OK || (s = check_tensor("output", a->output)) != GQAW_OK) return s;
+    add(range_of(a->output, rows_bytes(N, L.os, a->num_heads * D, L.es), "output"), true);
+    add(range_of(a->query, rows_bytes(N, L.qs, a->num_heads * D, L.es), "query"), false);
+  }
+  if (append) {
+    if ((s = check_tensor("key", a->key)) != GQAW_OK || (s = check_tensor("value", a->value)) != GQAW_OK) return s;
+    add(range_of(a->key, rows_bytes(N, L.ks, a->kv_num_heads * D, L.es), "key"), false);
+    add(range_of(a->value, rows_bytes(N, L.vs, a->kv_num_heads * D, L.es), "value"), false);
+  }
+  const int outs = n;
+  if (read) {
+    if (!x->key_out && !x->value_out) return fail(GQAW_EINVAL, "key_out and value_out are NULL");
+    for (const void *p : {x->key_out, x->value_out})
+      if (p && !aligned(p, 16)) return fail(GQAW_EINVAL, "key_out / value_out are not 16-byte aligned");
+    if (x->key_out) add(range_of(x->key_out, rows_bytes(N, L.kos, a->kv_num_heads * D, L.es), "key_out"), true);
+    if (x->value_out) add(range_of(x->value_out, rows_bytes(N, L.vos, a->kv_num_heads * D, L.es), "value_out"), true);
+  }
+  for (int i = 0; i < n; ++i)
+    for (int k = i + 1; k < n; ++k) {
+      if (!(t[i].written || t[k].written) || (t[i].cache && t[k].cache) || !overlap(t[i].r, t[k].r)) continue;
+      if (i >= outs && L.kos == L.vos) {  // both read into one tensor, a token's keys beside its values
+        const long long gap = std::llabs(t[i].r.lo - t[k].r.lo), row = a->kv_num_heads * D * L.es;
+        if (gap >= row && gap + row <= L.kos * L.es) continue;
+      }
+      return fail(GQAW_EINVAL, "%s overlaps %s", t[i].r.name, t[k].r.name);
+    }
+  if ((s = check_paged_index(a)) != GQAW_OK) return s;
+  if (L.rot_dim && append && (s = check_tables(a->cos_cache, a->sin_cache, a->position_ids, L.es)) != GQAW_OK) return s;
+  return GQAW_OK;
+}
+
+gqaw_status run_i4(const gqaw_paged_i4_args *x, void *stream, int what) {
+  I4Plan L{};
+  gqaw_status s = plan_i4(x, &L);
+  if (s != GQAW_OK) return s;
+  const gqaw_paged_args *a = &x->paged;
+  if (a->batch_size == 0 || a->total_new_tokens == 0 || a->max_new_tokens == 0) return GQAW_OK;  // no token, nothing to do
+  if ((s = check_i4_pointers(x, L, what)) != GQAW_OK) return s;
+  if ((s = check_device(a->workspace, "workspace")) != GQAW_OK) return s;
+  I4Params p;
+  std::memset(&p, 0, sizeof(p));
+  fill_paged(a, L, &p);
+  // without pages no row is read, but copies of no bytes still name a source: a valid address
+  p.kp = a->num_pages ? a->key_pages : a->workspace;
+  p.vp = a->num_pages ? a->value_pages : a->workspace;
+  p.kscale = static_cast<uint16_t *>(a->num_pages ? x->key_scales : a->workspace);
+  p.vscale = static_cast<uint16_t *>(a->num_pages ? x->value_scales : a->workspace);
+  p.sp = L.sp, p.sh = L.sh, p.sr = L.sr;
+  p.tp = L.tp, p.th = L.th, p.tr = L.tr;
+  p.ko = x->key_out, p.vo = x->value_out;
+  p.kos = L.kos, p.vos = L.vos;
+  const bool bf16 = a->dtype == GQAW_BF16;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (what & kRead) {
+    e = gqaw::launch_i4_rows(p, 0, x->key_out ? a->kv_num_heads : 0, x->value_out ? a->kv_num_heads : 0, true, bf16, st);
+    if (e != cudaSuccess) return cuda_fail(e, "read kernel launch");
+    gqaw::count_launch();
+    return GQAW_OK;
+  }
+  if (what & kAppend) {
+    const bool turn_q = (what & kAttend) && (L.rot_dim > 0 || a->query_weight);
+    p.qout = static_cast<char *>(a->workspace) + L.off_q;
+    p.qos = (long long)a->num_heads * a->head_size;
+    if (turn_q && bf16) p.qlo = static_cast<char *>(a->workspace) + L.off_qlo;
+    e = gqaw::launch_i4_rows(p, turn_q ? a->num_heads : 0, a->kv_num_heads, a->kv_num_heads, false, bf16, st);
+    if (e != cudaSuccess) return cuda_fail(e, "append kernel launch");
+    gqaw::count_launch();
+    if (turn_q) {
+      p.q = p.qout;
+      p.qs = p.qos;
+    }
+  }
+  if (what & kAttend) {
+    e = gqaw::launch_i4_attend(p, bf16, st);
+    if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
+    gqaw::count_launch();
+  }
+  return GQAW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gqaw_paged_i4_workspace_bytes(const gqaw_paged_i4_args *args) {
+  I4Plan L{};
+  return plan_i4(args, &L) == GQAW_OK ? L.ws_bytes : 0;
+}
+
+gqaw_status gqaw_paged_i4_append(const gqaw_paged_i4_args *args, void *stream) { return run_i4(args, stream, kAppend); }
+
+gqaw_status gqaw_paged_i4_attend(const gqaw_paged_i4_args *args, void *stream) { return run_i4(args, stream, kAttend); }
+
+gqaw_status gqaw_paged_i4_step(const gqaw_paged_i4_args *args, void *stream) { return run_i4(args, stream, kAppend | kAttend); }
+
+gqaw_status gqaw_paged_i4_read(const gqaw_paged_i4_args *args, void *stream) { return run_i4(args, stream, kRead); }
+
+size_t gqaw_paged_i4_args_size(void) { return sizeof(gqaw_paged_i4_args); }
+
+}  // extern "C"

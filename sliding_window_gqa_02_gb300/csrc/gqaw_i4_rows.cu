@@ -1,0 +1,391 @@
+// gqaw_i4_rows.cu -- the row-wise part of the operators on 4-bit caches: the append (norm, turn,
+// quantize), the queries of a whole step (norm, turn), and reading rows back.
+//
+// Append, for the D elements x of one head of one token:
+//     r = 1 / sqrt(mean(x^2) + eps), y = (x r) w; pairs (y1, y2) -> (y1 c - y2 s, y2 c + y1 s)
+//     a = max |y| over 32 elements, s = a / 7 rounded up to five significant bits
+//     c = 8 + round(y / s)
+// A code is a decision: an element next to the border between two codes falls to either side with the
+// last bit of y, and then it is off by a whole step.  So y does not depend on the order of a sum or
+// on which products are contracted: the sum of squares is kept in two numbers (48 bits, errors of
+// sums and products carried along), r is rounded once, and every other operation is one IEEE
+// operation.  The same for queries, so that a step's are those of any other implementation.
+//
+// Bound: HBM for many tokens, latency for few.  A lane has 8 consecutive elements of a head (16 or
+// 32 bytes in, 4 bytes out), D / 8 lanes a row; a group's maximum is two exchanges among four lanes.
+// Reading back is the inverse.
+#include "gqaw_i4.cuh"
+
+namespace gqaw {
+
+namespace i4r {
+
+constexpr int kThreads = 128;
+constexpr long long kManyWarps = 152 * 16;  // 16 warps a SM
+
+// Eight elements as stored.
+template <typename T> struct Oct;
+template <> struct Oct<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const float *s) {
+    a = reinterpret_cast<const uint4 *>(s)[0];
+    b = reinterpret_cast<const uint4 *>(s)[1];
+  }
+  __device__ __forceinline__ void store(float *d) const {
+    reinterpret_cast<uint4 *>(d)[0] = a;
+    reinterpret_cast<uint4 *>(d)[1] = b;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    Elem<float>::unpack(a, f);
+    Elem<float>::unpack(b, f + 4);
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+  }
+  __device__ __forceinline__ void ones() { a = b = make_uint4(0x3f800000u, 0x3f800000u, 0x3f800000u, 0x3f800000u); }
+};
+template <> struct Oct<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *s) { a = *reinterpret_cast<const uint4 *>(s); }
+  __device__ __forceinline__ void store(__nv_bfloat16 *d) const { *reinterpret_cast<uint4 *>(d) = a; }
+  __device__ __forceinline__ void get(float (&f)[8]) const { Elem<__nv_bfloat16>::unpack(a, f); }
+  __device__ __forceinline__ static uint32_t pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    a = make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
+  }
+  __device__ __forceinline__ void ones() { a = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u); }
+};
+
+// What one launch does with a token's heads: nq query heads (to qout), nk key and nv value heads (to
+// the pages); cq, ck, cv warps a token for each.
+struct Job {
+  int nq, nk, nv, cq, ck, cv;
+  long long warps;
+  int checks;  // warps behind those, which flag malformed sequences, 32 each
+};
+
+// s + e += x, the error of the sum kept (Knuth's two-sum).
+__device__ __forceinline__ void add_two(float &s, float &e, float x) {
+  const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
+  e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
+  s = t;
+}
+
+// 1 / sqrt(mean of the row's squares + eps), rounded once to fp32 but for ties within 2^-20 of a
+// step.  All lanes of the warp call it; LPR lanes hold a row.
+template <int LPR>
+__device__ __forceinline__ float row_factor(const float (&x)[8], float eps) {
+  float s = 0.f, e = 0.f;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    const float sq = __fmul_rn(x[m], x[m]);
+    e = __fadd_rn(e, fmaf(x[m], x[m], -sq));
+    add_two(s, e, sq);
+  }
+#pragma unroll
+  for (int k = LPR / 2; k > 0; k >>= 1) {
+    const float s2 = __shfl_xor_sync(~0u, s, k), e2 = __shfl_xor_sync(~0u, e, k);
+    // both partners take the sums in the same order, so that they stay alike
+    const bool low = (threadIdx.x & k) == 0;
+    float a = low ? s : s2;
+    e = __fadd_rn(e, e2);
+    add_two(a, e, low ? s2 : s);
+    s = a;
+  }
+  s *= 1.f / (LPR * 8);
+  e *= 1.f / (LPR * 8);
+  add_two(s, e, eps);
+  const float hi = __fadd_rn(s, e), lo = __fadd_rn(__fsub_rn(s, hi), e);
+  const float r0 = rsqrtf(hi);
+  // Newton's step: r = r0 + r0 (1 - (hi + lo) r0^2) / 2
+  const float ph = __fmul_rn(r0, r0), pl = fmaf(r0, r0, -ph);
+  float t = fmaf(-hi, ph, 1.f);
+  t = fmaf(-hi, pl, t);
+  t = fmaf(-lo, ph, t);
+  float r = fmaf(0.5f * r0, t, r0);
+  // squares outside the range of fp32, zeros, and what is not finite: in 64 bits
+  const bool plain = hi > 1e-30f && hi < 1e30f;
+  if (__any_sync(~0u, !plain)) {
+    double d = 0.0;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) d += (double)x[m] * (double)x[m];
+#pragma unroll
+    for (int k = LPR / 2; k > 0; k >>= 1) d += __shfl_xor_sync(~0u, d, k);
+    if (!plain) r = (float)(1.0 / sqrt(d / (LPR * 8) + (double)eps));
+  }
+  return r;
+}
+
+// Codes of a lane's 8 elements, and the scale of the 32 that it shares with three other lanes.
+__device__ __forceinline__ uint32_t quantize(const float (&y)[8], uint32_t &scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) top = max(top, __float_as_uint(y[m]) & 0x7fffffffu);  // orders like |y|, NaN on top
+  top = max(top, __shfl_xor_sync(~0u, top, 1));
+  top = max(top, __shfl_xor_sync(~0u, top, 2));
+  // up to four stored bits of the mantissa: the other 19 of the 23, rounded up
+  scale = top >= 0x7f800000u ? 0x7fc00000u : (__float_as_uint(__fdiv_rn(__uint_as_float(top), 7.f)) + 0x7ffffu) & ~0x7ffffu;
+  const float s = __uint_as_float(scale);
+  uint32_t word = 0;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    const float q = fminf(fmaxf(rintf(__fdiv_rn(y[m], s)), -7.f), 7.f);
+    const uint32_t c = s > 0.f ? (uint32_t)((int)q + 8) : 8u;
+    word |= c << (4 * m);
+  }
+  return word;
+}
+
+// The other element of each pair that turns, for a lane's elements e, e + 1, ... of a row.
+template <int LPR>
+__device__ __forceinline__ void partners(const float (&y)[8], float (&z)[8], int e, int rot_dim, bool inter) {
+  const int lane = threadIdx.x & 31, first = lane - lane % LPR, half = rot_dim / 2;
+  if (inter) {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) z[m] = y[m ^ 1];
+  } else if (half % 8 == 0) {
+    const int src = first + (e >= rot_dim ? e : e < half ? e + half : e - half) / 8;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) z[m] = __shfl_sync(~0u, y[m], src);
+  } else {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const int el = e + m, at = el < half ? el + half : el < rot_dim ? el - half : el;
+      z[m] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float t = __shfl_sync(~0u, y[k], first + at / 8);
+        if (at % 8 == k) z[m] = t;
+      }
+    }
+  }
+}
+
+}  // namespace i4r
+
+// A warp has BATCH groups of 32 / LPR heads of one tensor of one token.
+template <typename T, int LPR, int BATCH>
+__global__ void __launch_bounds__(i4r::kThreads) i4_append_kernel(const I4Params p, const i4r::Job j) {
+  using namespace i4r;
+  constexpr int RPW = 32 / LPR, D = LPR * 8;
+  const int lane = threadIdx.x & 31, lr = lane % LPR, sub = lane / LPR, e = lr * 8;
+  const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  pdl_wait();
+  if (w < j.warps) {
+    const int chunks = j.cq + j.ck + j.cv, n = (int)(w / chunks);
+    int c = (int)(w - (long long)n * chunks);
+    const int kind = c < j.cq ? 0 : c < j.cq + j.ck ? 1 : 2;  // queries, keys, values
+    c -= kind == 0 ? 0 : kind == 1 ? j.cq : j.cq + j.ck;
+    const int nh = kind == 0 ? j.nq : kind == 1 ? j.nk : j.nv, h = c * (BATCH * RPW) + sub;
+    // the rows themselves, ahead of the dependent look-ups; lanes past the heads run along on ones
+    Oct<T> x[BATCH];
+    const T *in = (kind == 0   ? static_cast<const T *>(p.q) + n * p.qs
+                   : kind == 1 ? static_cast<const T *>(p.k) + n * p.ks
+                               : static_cast<const T *>(p.v) + n * p.vs) + (long long)h * D + e;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (h + i * RPW < nh)
+        x[i].load(in + i * RPW * D);
+      else
+        x[i].ones();
+    }
+    const int b = find_sequence(batch_of(p), n);
+    if (b >= 0) {  // else nobody's, or a malformed sequence's
+      long long pos = (long long)p.seqlens[b] + 1 - (p.qstart[b + 1] - n);
+      I4Place at{0, 0};
+      if (kind > 0) {
+        at = i4_place(p, b, pos);
+        if (at.page < 0 && lane == 0) pflag(p, GQAW_DEV_BAD_PAGE);
+      }
+      const T *wt = static_cast<const T *>(kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr);
+      const int half = p.rot_dim / 2;
+      bool turn = p.rot_dim > 0 && kind < 2;
+      if (turn) {
+        if (p.pos_ids) pos = p.pos_ids[n];
+        if (pos < 0 || pos >= p.rot_len) {
+          turn = false;
+          if (lane == 0) pflag(p, GQAW_DEV_BAD_POSITION);
+        }
+      }
+      float cs[8], sn[8], wo[8];
+#pragma unroll
+      for (int m = 0; m < 8; ++m) cs[m] = 1.f, sn[m] = 0.f;
+      if (turn) {
+        const T *tc = static_cast<const T *>(p.rcos) + pos * half, *ts = static_cast<const T *>(p.rsin) + pos * half;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          const int i = e + m, col = p.rot_inter ? i / 2 : i < half ? i : i - half;
+          if (i < p.rot_dim) {
+            cs[m] = Elem<T>::load(tc[col]);
+            sn[m] = Elem<T>::load(ts[col]);
+          }
+        }
+      }
+      if (wt) {
+        Oct<T> u;
+        u.load(wt + e);
+        u.get(wo);
+      }
+      if (at.page >= 0) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          if (c * (BATCH * RPW) + i * RPW >= nh) break;  // uniform over the warp
+          float y[8];
+          x[i].get(y);
+          if (wt) {
+            const float r = row_factor<LPR>(y, p.eps);
+#pragma unroll
+            for (int m = 0; m < 8; ++m) y[m] = __fmul_rn(__fmul_rn(y[m], r), wo[m]);
+          }
+          if (turn) {
+            float z[8];
+            partners<LPR>(y, z, e, p.rot_dim, p.rot_inter != 0);
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+              const int el = e + m;
+              const bool first = p.rot_inter ? el % 2 == 0 : el < half;
+              const float a = __fmul_rn(y[m], cs[m]), t = __fmul_rn(z[m], sn[m]);
+              if (el < p.rot_dim) y[m] = first ? __fsub_rn(a, t) : __fadd_rn(a, t);
+            }
+          }
+          const int head = h + i * RPW;
+          if (kind == 0) {
+            Oct<T> o;
+            o.set(y);
+            T *dst = static_cast<T *>(p.qout) + n * p.qos + (long long)head * D + e;
+            if (head < nh) o.store(dst);
+            if (p.qlo) {  // bf16: what the rounding leaves
+              float z[8];
+              o.get(z);
+#pragma unroll
+              for (int m = 0; m < 8; ++m) z[m] = fabsf(z[m]) < INFINITY ? __fsub_rn(y[m], z[m]) : 0.f;
+              o.set(z);
+              if (head < nh) o.store(dst + (static_cast<const T *>(p.qlo) - static_cast<const T *>(p.qout)));
+            }
+          } else {
+            uint32_t scale;
+            const uint32_t word = quantize(y, scale);
+            if (head < nh) {
+              unsigned char *codes = static_cast<unsigned char *>(kind == 1 ? p.kp : p.vp) + at.page * p.sp + head * p.sh + at.row * p.sr;
+              *reinterpret_cast<uint32_t *>(codes + lr * 4) = word;
+              if (lr % 4 == 0)
+                (kind == 1 ? p.kscale : p.vscale)[at.page * p.tp + head * p.th + at.row * p.tr + lr / 4] = (uint16_t)(scale >> 16);
+            }
+          }
+        }
+      }
+    }
+  } else if (w < j.warps + j.checks) {
+    const int b = (int)(w - j.warps) * 32 + lane;
+    if (b < p.B && malformed(batch_of(p), p.qstart[b], p.qstart[b + 1], p.seqlens[b])) pflag(p, GQAW_DEV_BAD_SEQLEN);
+  }
+  pdl_launch_dependents();
+}
+
+template <typename T, int LPR, int BATCH>
+__global__ void __launch_bounds__(i4r::kThreads) i4_read_kernel(const I4Params p, const i4r::Job j) {
+  using namespace i4r;
+  constexpr int RPW = 32 / LPR, D = LPR * 8;
+  const int lane = threadIdx.x & 31, lr = lane % LPR, sub = lane / LPR;
+  const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  pdl_wait();
+  if (w < j.warps) {
+    const int chunks = j.ck + j.cv, n = (int)(w / chunks);
+    int c = (int)(w - (long long)n * chunks);
+    const bool value = c >= j.ck;
+    c -= value ? j.ck : 0;
+    const int nh = value ? j.nv : j.nk, h = c * (BATCH * RPW) + sub;
+    const int b = find_sequence(batch_of(p), n);
+    if (b >= 0) {
+      const I4Place at = i4_place(p, b, (long long)p.seqlens[b] + 1 - (p.qstart[b + 1] - n));
+      if (at.page >= 0) {
+        const unsigned char *codes = static_cast<const unsigned char *>(value ? p.vp : p.kp) + at.page * p.sp + at.row * p.sr + lr * 4;
+        const uint16_t *scales = (value ? p.vscale : p.kscale) + at.page * p.tp + at.row * p.tr + lr / 4;
+        T *out = value ? static_cast<T *>(p.vo) + n * p.vos : static_cast<T *>(p.ko) + n * p.kos;
+        uint32_t word[BATCH];
+        float s[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int head = h + i * RPW;
+          word[i] = head < nh ? *reinterpret_cast<const uint32_t *>(codes + head * p.sh) : 0u;
+          s[i] = __uint_as_float(head < nh ? (uint32_t)scales[head * p.th] << 16 : 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int head = h + i * RPW;
+          float y[8];
+#pragma unroll
+          for (int m = 0; m < 8; ++m) y[m] = (float)((int)((word[i] >> (4 * m)) & 15u) - 8) * s[i];
+          Oct<T> o;
+          o.set(y);
+          if (head < nh) o.store(out + (long long)head * D + lr * 8);
+        }
+      } else if (lane == 0) {
+        pflag(p, GQAW_DEV_BAD_PAGE);
+      }
+    }
+  } else if (w < j.warps + j.checks) {
+    const int b = (int)(w - j.warps) * 32 + lane;
+    if (b < p.B && malformed(batch_of(p), p.qstart[b], p.qstart[b + 1], p.seqlens[b])) pflag(p, GQAW_DEV_BAD_SEQLEN);
+  }
+  pdl_launch_dependents();
+}
+
+namespace i4r {
+
+template <bool READ, typename T, int LPR>
+cudaError_t launch(const I4Params &p, const Job &j, int batch, const cudaLaunchConfig_t &cfg) {
+  if constexpr (READ)
+    return batch == 4 ? cudaLaunchKernelEx(&cfg, i4_read_kernel<T, LPR, 4>, p, j) : cudaLaunchKernelEx(&cfg, i4_read_kernel<T, LPR, 2>, p, j);
+  else
+    return batch == 4 ? cudaLaunchKernelEx(&cfg, i4_append_kernel<T, LPR, 4>, p, j) : cudaLaunchKernelEx(&cfg, i4_append_kernel<T, LPR, 2>, p, j);
+}
+
+template <bool READ, typename T>
+cudaError_t launch_d(const I4Params &p, const Job &j, int batch, const cudaLaunchConfig_t &cfg) {
+  switch (p.D) {
+    case 32: return launch<READ, T, 4>(p, j, batch, cfg);
+    case 64: return launch<READ, T, 8>(p, j, batch, cfg);
+    case 128: return launch<READ, T, 16>(p, j, batch, cfg);
+    default: return launch<READ, T, 32>(p, j, batch, cfg);
+  }
+}
+
+}  // namespace i4r
+
+// nq: query heads to norm and turn (0: none); nk, nv: key and value heads to append, or to read.
+cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read, bool bf16, cudaStream_t stream) {
+  using namespace i4r;
+  Job j;
+  j.nq = nq;
+  j.nk = nk;
+  j.nv = nv;
+  const int rpw = 32 / (p.D / 8);
+  auto chunks = [&](int heads, int batch) { return (heads + batch * rpw - 1) / (batch * rpw); };
+  const bool many = (long long)p.N * (chunks(nq, 4) + chunks(nk, 4) + chunks(nv, 4)) >= kManyWarps;
+  const int batch = many ? 4 : 2;
+  j.cq = chunks(nq, batch);
+  j.ck = chunks(nk, batch);
+  j.cv = chunks(nv, batch);
+  j.warps = (long long)p.N * (j.cq + j.ck + j.cv);
+  j.checks = (p.B + 31) / 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((j.warps + j.checks + kThreads / 32 - 1) / (kThreads / 32)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait()
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = read ? (bf16 ? launch_d<true, __nv_bfloat16>(p, j, batch, cfg) : launch_d<true, float>(p, j, batch, cfg))
+                             : (bf16 ? launch_d<false, __nv_bfloat16>(p, j, batch, cfg) : launch_d<false, float>(p, j, batch, cfg));
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace gqaw

@@ -38,7 +38,11 @@ EXPORTED = ["gqaw_resident_len", "gqaw_rollback_exact", "gqaw_workspace_bytes", 
             "gqa_windowed_step", "gqaw_attend", "gqaw_update_cache", "gqaw_device_status",
             "gqaw_last_error", "gqaw_launch_count", "gqaw_step_args_size", "gqa_windowed_step_noalloc",
             "gqaw_qk_norm_rotary", "gqaw_paged_workspace_bytes", "gqaw_paged_append", "gqaw_paged_attend",
-            "gqaw_paged_step", "gqaw_qk_args_size", "gqaw_paged_args_size"]
+            "gqaw_paged_step", "gqaw_qk_args_size", "gqaw_paged_args_size",
+            "gqaw_paged_i4_workspace_bytes", "gqaw_paged_i4_append", "gqaw_paged_i4_attend", "gqaw_paged_i4_step",
+            "gqaw_paged_i4_read", "gqaw_paged_i4_args_size"]
+
+GQAW_I4_GROUP = 32
 
 GQAW_NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024
 
@@ -173,6 +177,23 @@ class gqaw_paged_args(ctypes.Structure):
     ]
 
 
+class gqaw_paged_i4_args(ctypes.Structure):
+    """Mirror of ``gqaw_paged_i4_args`` in include/gqaw.h."""
+
+    _fields_ = [
+        ("paged", gqaw_paged_args),
+        ("key_scales", ctypes.c_void_p),
+        ("value_scales", ctypes.c_void_p),
+        ("scale_page_stride", ctypes.c_int64),
+        ("scale_head_stride", ctypes.c_int64),
+        ("scale_row_stride", ctypes.c_int64),
+        ("key_out", ctypes.c_void_p),
+        ("value_out", ctypes.c_void_p),
+        ("key_out_stride", ctypes.c_int64),
+        ("value_out_stride", ctypes.c_int64),
+    ]
+
+
 class GqawError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__("%s: %s" % (STATUS_NAMES.get(status, status), message))
@@ -219,8 +240,15 @@ def load(path: str = LIB_PATH):
         f = getattr(lib, name)
         f.restype = ctypes.c_int
         f.argtypes = [PP, ctypes.c_void_p]
+    PI = ctypes.POINTER(gqaw_paged_i4_args)
+    lib.gqaw_paged_i4_workspace_bytes.restype = ctypes.c_size_t
+    lib.gqaw_paged_i4_workspace_bytes.argtypes = [PI]
+    for name in ("gqaw_paged_i4_append", "gqaw_paged_i4_attend", "gqaw_paged_i4_step", "gqaw_paged_i4_read"):
+        f = getattr(lib, name)
+        f.restype = ctypes.c_int
+        f.argtypes = [PI, ctypes.c_void_p]
     for name, struct in (("gqaw_step_args", gqaw_step_args), ("gqaw_qk_args", gqaw_qk_args),
-                         ("gqaw_paged_args", gqaw_paged_args)):
+                         ("gqaw_paged_args", gqaw_paged_args), ("gqaw_paged_i4_args", gqaw_paged_i4_args)):
         size = getattr(lib, name + "_size")
         size.restype = ctypes.c_size_t
         size.argtypes = []
@@ -286,6 +314,26 @@ def gqaw_paged_attend(args: gqaw_paged_args, stream: int = 0) -> int:
 
 def gqaw_paged_step(args: gqaw_paged_args, stream: int = 0) -> int:
     return int(load().gqaw_paged_step(ctypes.byref(args), stream))
+
+
+def gqaw_paged_i4_workspace_bytes(args: gqaw_paged_i4_args) -> int:
+    return int(load().gqaw_paged_i4_workspace_bytes(ctypes.byref(args)))
+
+
+def gqaw_paged_i4_append(args: gqaw_paged_i4_args, stream: int = 0) -> int:
+    return int(load().gqaw_paged_i4_append(ctypes.byref(args), stream))
+
+
+def gqaw_paged_i4_attend(args: gqaw_paged_i4_args, stream: int = 0) -> int:
+    return int(load().gqaw_paged_i4_attend(ctypes.byref(args), stream))
+
+
+def gqaw_paged_i4_step(args: gqaw_paged_i4_args, stream: int = 0) -> int:
+    return int(load().gqaw_paged_i4_step(ctypes.byref(args), stream))
+
+
+def gqaw_paged_i4_read(args: gqaw_paged_i4_args, stream: int = 0) -> int:
+    return int(load().gqaw_paged_i4_read(ctypes.byref(args), stream))
 
 
 def gqaw_device_status(workspace: int, reset: bool = False, stream: int = 0):
@@ -413,9 +461,12 @@ def make_args(query, key, value, past_key, past_value, present_key, present_valu
 
 def new_workspace(args: gqaw_step_args, device, stream: int = 0):
     """Allocate (torch) and zero-initialise a workspace large enough for ``args``."""
+    return _new_workspace(gqaw_workspace_bytes(args), device, stream)
+
+
+def _new_workspace(n: int, device, stream: int):
     import torch
 
-    n = gqaw_workspace_bytes(args)
     if n == 0:
         check(GQAW_EINVAL)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
@@ -512,6 +563,31 @@ def make_qk_args(query, key, query_out, key_out, num_heads: int, kv_num_heads: i
     return a
 
 
+def _page_strides(pages, kv_num_heads: int, heads_inside_rows: bool):
+    """(page size, page stride, head stride, row stride) of a 4-dimensional tensor of pages, in its elements."""
+    n, d1, d2, D = (int(x) for x in pages.shape)
+    heads, page = (d2, d1) if heads_inside_rows else (d1, d2)
+    if heads != kv_num_heads:
+        raise ValueError("the pages hold %d kv heads, not %d" % (heads, kv_num_heads))
+    st = pages.stride()
+    # a dimension of one element may have any stride: one that cannot overlap is given instead
+    row, head = (int(st[1]), int(st[2])) if heads_inside_rows else (int(st[2]), int(st[1]))
+    if page == 1:
+        row = head * heads if heads > 1 else D
+    if heads == 1:
+        head = row * page
+    return page, int(st[0]) if n > 1 else max(row * page, head * heads), head, row
+
+
+def _equal_pages(names: str, k, v):
+    if k.dim() != 4 or tuple(k.shape) != tuple(v.shape) or k.dtype != v.dtype or k.device != v.device:
+        raise ValueError("%s: equal 4-dimensional tensors" % names)
+    if tuple(k.stride()) != tuple(v.stride()) or k.stride(-1) != 1:
+        raise ValueError("%s: equal strides, the last dimension contiguous" % names)
+    if any(n > 1 and st < k.shape[3] for n, st in zip(k.shape[:3], k.stride()[:3])):
+        raise ValueError("%s: rows must not overlap" % names)
+
+
 def make_paged_args(query, key, value, key_pages, value_pages, page_table, query_start, seqlens_k,
                     max_new_tokens: int, max_sequence_length: int, num_heads: int, kv_num_heads: int, output,
                     workspace=None, local_window_size: int = 0, scale: float = 0.0, softcap: float = 0.0,
@@ -529,44 +605,39 @@ def make_paged_args(query, key, value, key_pages, value_pages, page_table, query
     including its new tokens, less one.  ``workspace``: a uint8 tensor, or None when only the
     size is wanted.  The rest as in ``make_args``.
     """
-    if key_pages.dim() != 4 or tuple(key_pages.shape) != tuple(value_pages.shape) \
-            or key_pages.dtype != value_pages.dtype or key_pages.device != value_pages.device:
-        raise ValueError("key_pages and value_pages: equal 4-dimensional tensors")
-    if tuple(key_pages.stride()) != tuple(value_pages.stride()) or key_pages.stride(-1) != 1:
-        raise ValueError("key_pages and value_pages: equal strides, the last dimension contiguous")
-    if any(n > 1 and st < key_pages.shape[3] for n, st in zip(key_pages.shape[:3], key_pages.stride()[:3])):
-        raise ValueError("key_pages and value_pages: rows must not overlap")
-    pages, d1, d2, D = (int(x) for x in key_pages.shape)
-    heads, page = (d2, d1) if heads_inside_rows else (d1, d2)
-    if heads != kv_num_heads:
-        raise ValueError("the pages hold %d kv heads, not %d" % (heads, kv_num_heads))
-    like = key_pages
+    _equal_pages("key_pages and value_pages", key_pages, value_pages)
+    D = int(key_pages.shape[3])
     a = gqaw_paged_args()
+    a.page_size, a.page_stride, a.head_stride, a.row_stride = _page_strides(key_pages, kv_num_heads, heads_inside_rows)
+    _paged_common(a, key_pages, page_table, query_start, seqlens_k, max_new_tokens, max_sequence_length, num_heads,
+                  kv_num_heads, D, local_window_size, scale, softcap, head_sink, smooth_softmax, query_weight, key_weight,
+                  norm_eps, cos_cache, sin_cache, position_ids, rotary_interleaved, workspace,
+                  dict(query=query, key=key, value=value, output=output))
+    a.num_pages = int(key_pages.shape[0])
+    a.key_pages, a.value_pages = _ptr(key_pages), _ptr(value_pages)
+    return a
+
+
+def _paged_common(a, like, page_table, query_start, seqlens_k, max_new_tokens, max_sequence_length, num_heads,
+                  kv_num_heads, D, local_window_size, scale, softcap, head_sink, smooth_softmax, query_weight, key_weight,
+                  norm_eps, cos_cache, sin_cache, position_ids, rotary_interleaved, workspace, rows, more=()):
+    """The fields of ``gqaw_paged_args`` that do not depend on how the cache holds its rows.  ``like``:
+    the dtype and device of everything outside it; ``more``: further tensors of a row per token."""
     B, width = (int(x) for x in page_table.shape)
-    tokens = {int(t.shape[0]) for t in (query, key, value, output) if t is not None}
+    tokens = {int(t.shape[0]) for t in (*rows.values(), *more) if t is not None}
     if len(tokens) != 1:
         raise ValueError("query, key, value and output must have the same number of tokens")
     a.batch_size, a.total_new_tokens = B, tokens.pop()
     a.max_new_tokens, a.max_sequence_length = int(max_new_tokens), int(max_sequence_length)
     a.num_heads, a.kv_num_heads, a.head_size = int(num_heads), int(kv_num_heads), D
-    a.page_size, a.num_pages, a.page_table_width = page, pages, width
-    a.local_window_size, a.dtype = int(local_window_size), _dtype_code(key_pages)
+    a.page_table_width = width
+    a.local_window_size, a.dtype = int(local_window_size), _dtype_code(like)
     a.scale, a.softcap, a.norm_eps = float(scale), float(softcap), float(norm_eps)
     a.smooth_softmax = int(bool(smooth_softmax))
-    a.query, a.query_stride = _rows("query", query, num_heads, D, like)
-    a.key, a.key_stride = _rows("key", key, kv_num_heads, D, like)
-    a.value, a.value_stride = _rows("value", value, kv_num_heads, D, like)
-    a.output, a.output_stride = _rows("output", output, num_heads, D, like)
-    a.key_pages, a.value_pages = _ptr(key_pages), _ptr(value_pages)
-    st = key_pages.stride()
-    # a dimension of one element may have any stride: one that cannot overlap is given instead
-    row, head = (int(st[1]), int(st[2])) if heads_inside_rows else (int(st[2]), int(st[1]))
-    if page == 1:
-        row = head * heads if heads > 1 else D
-    if heads == 1:
-        head = row * page
-    a.page_stride = int(st[0]) if pages > 1 else max(row * page, head * heads)
-    a.head_stride, a.row_stride = head, row
+    for name, heads in (("query", num_heads), ("key", kv_num_heads), ("value", kv_num_heads), ("output", num_heads)):
+        ptr, stride = _rows(name, rows[name], heads, D, like)
+        setattr(a, name, ptr)
+        setattr(a, name + "_stride", stride)
     a.page_table = _index("page_table", page_table, "int32", (B, width), like)
     a.query_start = _index("query_start", query_start, "int32", (B + 1,), like)
     a.seqlens_k = _index("seqlens_k", seqlens_k, "int32", (B,), like)
@@ -576,16 +647,60 @@ def make_paged_args(query, key, value, key_pages, value_pages, page_table, query
     _tables(a, cos_cache, sin_cache, rotary_interleaved, like)
     a.position_ids = _index("position_ids", position_ids, "int64", (a.total_new_tokens,), like)
     _workspace(a, workspace, like)
-    return a
+
+
+def make_paged_i4_args(query, key, value, key_codes, value_codes, key_scales, value_scales, page_table, query_start,
+                       seqlens_k, max_new_tokens: int, max_sequence_length: int, num_heads: int, kv_num_heads: int, output,
+                       key_out=None, value_out=None, workspace=None, local_window_size: int = 0, scale: float = 0.0,
+                       softcap: float = 0.0, head_sink=None, smooth_softmax: bool = False, query_weight=None,
+                       key_weight=None, norm_eps: float = 1e-6, cos_cache=None, sin_cache=None, position_ids=None,
+                       rotary_interleaved: bool = False, heads_inside_rows: bool = False, dtype=None) -> gqaw_paged_i4_args:
+    """Fill a ``gqaw_paged_i4_args`` from CUDA tensors.
+
+    ``key_codes``/``value_codes``: uint8 (pages, kv heads, page size, D / 2) and
+    ``key_scales``/``value_scales``: bfloat16 (pages, kv heads, page size, D / 32), or with
+    ``heads_inside_rows`` (pages, page size, kv heads, ...); the last dimension contiguous, the
+    others strided alike for keys and values.  ``key_out``/``value_out``: where a read puts its rows,
+    (N, kv_num_heads * D) or (N, kv_num_heads, D).  ``dtype``: that of all rows outside the cache
+    (by default the first given row tensor's).  The rest as in ``make_paged_args``.
+    """
+    import torch
+    from types import SimpleNamespace
+
+    _equal_pages("key_codes and value_codes", key_codes, value_codes)
+    _equal_pages("key_scales and value_scales", key_scales, value_scales)
+    D = 2 * int(key_codes.shape[3])
+    if key_codes.dtype != torch.uint8 or key_scales.dtype != torch.bfloat16 or key_scales.device != key_codes.device \
+            or tuple(key_scales.shape) != (*key_codes.shape[:3], D // GQAW_I4_GROUP):
+        raise ValueError("codes: uint8 (..., D / 2) and scales: bfloat16 (..., D / 32) of the same pages and device")
+    rows = dict(query=query, key=key, value=value, output=output)
+    if dtype is None:
+        given = [t for t in (*rows.values(), key_out, value_out) if t is not None]
+        if not given:
+            raise ValueError("a row tensor or dtype is needed")
+        dtype = given[0].dtype
+    like = SimpleNamespace(dtype=dtype, device=key_codes.device)
+    x = gqaw_paged_i4_args()
+    a = x.paged
+    a.page_size, a.page_stride, a.head_stride, a.row_stride = _page_strides(key_codes, kv_num_heads, heads_inside_rows)
+    _, x.scale_page_stride, x.scale_head_stride, x.scale_row_stride = _page_strides(key_scales, kv_num_heads,
+                                                                                    heads_inside_rows)
+    _paged_common(a, like, page_table, query_start, seqlens_k, max_new_tokens, max_sequence_length, num_heads,
+                  kv_num_heads, D, local_window_size, scale, softcap, head_sink, smooth_softmax, query_weight, key_weight,
+                  norm_eps, cos_cache, sin_cache, position_ids, rotary_interleaved, workspace, rows, (key_out, value_out))
+    a.num_pages = int(key_codes.shape[0])
+    a.key_pages, a.value_pages = _ptr(key_codes), _ptr(value_codes)
+    x.key_scales, x.value_scales = _ptr(key_scales), _ptr(value_scales)
+    x.key_out, x.key_out_stride = _rows("key_out", key_out, kv_num_heads, D, like)
+    x.value_out, x.value_out_stride = _rows("value_out", value_out, kv_num_heads, D, like)
+    return x
+
+
+def new_paged_i4_workspace(args: gqaw_paged_i4_args, device, stream: int = 0):
+    """Allocate (torch) and zero-initialise a workspace large enough for ``args``."""
+    return _new_workspace(gqaw_paged_i4_workspace_bytes(args), device, stream)
 
 
 def new_paged_workspace(args: gqaw_paged_args, device, stream: int = 0):
     """Allocate (torch) and zero-initialise a workspace large enough for ``args``."""
-    import torch
-
-    n = gqaw_paged_workspace_bytes(args)
-    if n == 0:
-        check(GQAW_EINVAL)
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    check(gqaw_workspace_init(int(ws.data_ptr()), n, stream))
-    return ws
+    return _new_workspace(gqaw_paged_workspace_bytes(args), device, stream)
