@@ -5,7 +5,9 @@
 
 namespace gqaw {
 cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read, bool bf16, cudaStream_t stream);
-cudaError_t launch_i4_attend(const I4Params &p, bool bf16, cudaStream_t stream);
+cudaError_t launch_i4_attend_bf16(const I4Params &p, int nt, int sms, cudaStream_t stream);
+cudaError_t launch_i4_attend_split(const I4Params &p, int nt, int sms, cudaStream_t stream);
+cudaError_t launch_i4_attend_f32(const I4Params &p, int nt, int sms, cudaStream_t stream);
 }  // namespace gqaw
 
 namespace {
@@ -17,6 +19,9 @@ struct I4Plan : PagedSizes {
   long long sp, sh, sr;          // codes, bytes
   long long tp, th, tr;          // scales, elements
   long long kos, vos;
+  int nt;                        // operands of 8 query rows
+  int few;                       // sequences of at most this many tokens go to the kernel of 8 rows (0: none)
+  int gb, hblocks, tpt;
   size_t off_q, off_qlo, ws_bytes;
 };
 
@@ -60,7 +65,20 @@ gqaw_status plan_i4(const gqaw_paged_i4_args *x, I4Plan *L) {
       (s = row_stride("key_out_stride", x->key_out_stride, krow, L->es, a->total_new_tokens, &L->kos)) != GQAW_OK ||
       (s = row_stride("value_out_stride", x->value_out_stride, krow, L->es, a->total_new_tokens, &L->vos)) != GQAW_OK)
     return s;
-  L->ws_bytes = gqaw::kPagedPartialOffset;
+  // The kernel: 8 query rows of a kv head a product, and as many of them as the longest chunk fills, at
+  // most 4 (head size 256: 2), which is what registers hold.
+  const long long rows = (long long)std::max(1, a->max_new_tokens) * L->group;
+  L->nt = rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
+  L->gb = std::min(L->group, 8 * L->nt);
+  L->hblocks = (int)ceil_div(L->group, L->gb);
+  L->tpt = std::max(1, 8 * L->nt / L->gb);
+  // Single tokens among chunks would fill 8 of the rows: they have a launch of their own where there
+  // may be many (the others hold at most max_new_tokens, which bounds their number)
+  constexpr int kShort = 64;
+  const long long tok = L->nt > 1 && L->group <= 8 ? 8 / L->group : 0;
+  const long long spare = (long long)a->total_new_tokens - a->batch_size * tok;
+  if (tok && (a->batch_size - (spare > 0 ? ceil_div(spare, a->max_new_tokens) : 0)) * a->kv_num_heads >= kShort) L->few = (int)tok;
+  L->ws_bytes = gqaw::kPagedPartialOffset + align256((size_t)kSms * 2 * 8 * L->nt * (D + 4) * 4);
   L->off_q = L->ws_bytes;
   L->ws_bytes += align256((size_t)a->total_new_tokens * a->num_heads * D * L->es);
   L->off_qlo = L->ws_bytes;  // what bf16 leaves of turned queries
@@ -176,6 +194,43 @@ gqaw_status check_i4_pointers(const gqaw_paged_i4_args *x, const I4Plan &L, int 
   return GQAW_OK;
 }
 
+// The attention, a launch (or two) for every kPagedItems sequences.
+gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cudaStream_t st) {
+  if (gqaw::workspace_tickets_need_clear(a->workspace, gqaw::kPagedTicketOffset, gqaw::kPagedPartialOffset)) {
+    const cudaError_t e = cudaMemsetAsync(p.tickets, 0, gqaw::kPagedTickets * 4, st);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync (tickets)");
+  }
+  auto launch = [&](const I4Params &x, int nt) {
+    const cudaError_t e = a->dtype == GQAW_F32 ? gqaw::launch_i4_attend_f32(x, nt, kSms, st)
+                          : x.qlo              ? gqaw::launch_i4_attend_split(x, nt, kSms, st)
+                                               : gqaw::launch_i4_attend_bf16(x, nt, kSms, st);
+    if (e == cudaSuccess) gqaw::count_launch();
+    return e;
+  };
+  for (int b0 = 0; b0 < a->batch_size; b0 += gqaw::kPagedItems) {
+    p.B = std::min(gqaw::kPagedItems, a->batch_size - b0);
+    p.table = a->page_table + (long long)b0 * a->page_table_width;
+    p.qstart = a->query_start + b0;
+    p.seqlens = a->seqlens_k + b0;
+    p.s_lo = L.few + 1;
+    p.s_hi = a->max_new_tokens;
+    p.gb = L.gb;
+    p.hblocks = L.hblocks;
+    p.tpt = L.tpt;
+    cudaError_t e = launch(p, L.nt);
+    if (e == cudaSuccess && L.few) {
+      I4Params few = p;
+      few.s_lo = 1;
+      few.s_hi = few.tpt = L.few;
+      few.gb = L.group;
+      few.hblocks = 1;
+      e = launch(few, 1);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
+  }
+  return GQAW_OK;
+}
+
 gqaw_status run_i4(const gqaw_paged_i4_args *x, void *stream, int what) {
   I4Plan L{};
   gqaw_status s = plan_i4(x, &L);
@@ -218,12 +273,7 @@ gqaw_status run_i4(const gqaw_paged_i4_args *x, void *stream, int what) {
       p.qs = p.qos;
     }
   }
-  if (what & kAttend) {
-    e = gqaw::launch_i4_attend(p, bf16, st);
-    if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
-    gqaw::count_launch();
-  }
-  return GQAW_OK;
+  return what & kAttend ? run_attend(a, L, p, st) : GQAW_OK;
 }
 
 }  // namespace

@@ -140,15 +140,15 @@ class Batch:
         """Every output row against the definition over the cache as it is now.
 
         ``ref.attend``'s bound, with what these kernels round: a query element is taken in one (bf16) or
-        two parts of fp16 of the row's power of two (2^-23 relative to it, or 2^-23 of the row's largest
-        for the smallest ones), turned queries of bf16 in two parts (u^2), and each weight times its value
-        scale to fp16 (2^-12; fp32: two parts, 2^-22), or to bf16 with more than 32 rows.
+        two parts of fp16 after a power of two for its row (2^-23 relative to it, or 2^-39 of the row's
+        largest for the smallest ones), turned queries of bf16 in two parts (u^2), and each weight, or
+        weight times value scale, to fp16 (2^-12; fp32: two parts, 2^-23), or to bf16 with more than 32 rows.
 
         The types end: a weight of a key below fp32's smallest normal number, 2^-126 of the row's largest,
         may count as nothing, and a result below it is rounded to a multiple of bf16's smallest number, 2^-133.
-        A weight times its scale is held in fp16 as 2^6 of the largest scale's power of two: a product below
-        fp16's normal numbers is off by up to 2^-25 of that (fp32: 2^-36, in two parts), times a code of 8:
-        2^-31 2 8 / 7 < 2^-29 of the largest value, a key."""
+        In fp16 a weight of 1 times the largest scale s of its group (a weight of 1) is at least 2^12 (2^13),
+        and what is rounded to a subnormal is off by up to 2^-25: 2^-37 s, times a code of at most 8, where
+        the largest value is at least s or there is none: 2^-34 of it a key."""
         if turned:
             q32 = torch.from_numpy(i4.norm_turn(self.q.reshape(-1, self.Nq, self.D), self.qw, 1e-5, self.cos, self.sin,
                                                 self.table_pos(), self.interleaved)).to(self.q.device).double()
@@ -163,9 +163,8 @@ class Batch:
             rounded = (ref.u(self.dtype) ** 2 if turned and self.dtype == torch.bfloat16 else 0.0) + 2.0 ** -22
             want, bound = ref.attend(q, k, v, t - s, self.window, self.scale or 1 / math.sqrt(self.D), self.softcap, sink,
                                      self.dtype, rounded)
-            step = 2.0 ** (-29 if self.dtype == torch.bfloat16 else -40)
             top = torch.nan_to_num(v, nan=0.0, posinf=0.0, neginf=0.0).abs().amax()
-            bound = bound + (t + 1) * (2.0 ** -126 * (1 + top) + step * top)
+            bound = bound + (t + 1) * (2.0 ** -126 * (1 + top) + 2.0 ** -34 * top)
             got = self.out[self.rows(i)].reshape(s, self.Nq, self.D).double()
             bad = ~torch.isfinite(want)
             assert not (torch.isfinite(got) & bad).any(), "finite output where a visible value is not"
