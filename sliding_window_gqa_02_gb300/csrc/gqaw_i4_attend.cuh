@@ -9,31 +9,34 @@
 //   - codes go from shared memory to registers once and are matrix operands as they are: a nibble
 //     in the low bits of an fp16 is the subnormal number c 2^-24, one in the next four bits 16 c 2^-24,
 //     which the tensor cores take exactly; one AND makes two operands of two nibbles of a word, and the
-//     factor of 16 goes to the query (keys) or to the end (values).  Converting to bf16 through shared
-//     memory, as the 5th-generation tensor cores would need it, costs four bytes there for every
-//     byte of codes, written and read again: more than its 128 bytes a cycle.  Hence mma.sync with the
-//     keys (dimensions) as M, whose operands are registers, 8 query rows as N; its rate, a product of 16 x 8
-//     x 16 every 2 cycles of an SM, is 2.4 times what the memory feeds;
+//     factor of 16 goes to the query.  Converting to bf16 through shared memory, as the
+//     5th-generation tensor cores would need it, costs four bytes there for every byte of codes,
+//     written and read again: more than its 128 bytes a cycle.  Hence mma.sync with the keys (dimensions)
+//     as M, whose operands are registers, 8 query rows as N; its rate, a product of 16 x 8 x 16 every 2
+//     cycles of an SM, is 2.4 times what the memory feeds;
 //   - z = sum over groups g of s_g (sum_d c_d q_d - 8 sum_d q_d): the scale multiplies a group's sum in fp32,
 //     and the sum of the queries is where the accumulator starts;
-//   - o = sum_j (p_j s_j) (c_j - 8): with 8 rows the weights take the scales, one operand for each group,
-//     and the values are subnormal numbers less 8 2^-24 (kFold).  With more rows there are more weights
-//     than values: then the values are (c - 8) s in fp16, which holds them exactly.  (Here the 8 does not
-//     wait for the end as with the keys: 8 sum p s beside a small result would take its last bits.)
+//   - the values are (c - 8) s in fp16, which holds them exactly: 1024 + c by an OR, c - 8 by a sum, and
+//     a lane's dimensions (16 of 128) share a scale.  (The 8 does not wait for the end as with the keys: 8
+//     sum p s beside a small result would take its last bits.)
 //
 // Queries come as one or two parts of fp16 (QP; fp32, or turned bf16: two), after a power of two per
-// row that puts the largest element at 2^13; weights (times scales) as one part, or two for fp32 (PP).
-// A weight is at most 4, since the row's reference maximum moves when exceeded by more than that, and a
-// scale is taken relative to the largest power of two of its group so far: products stay below 2^15,
-// and whatever the scales' size none is lost beside 2^-25.  Sums and statistics are fp32.
+// row that puts the largest element at 2^13; weights as one part, or two for fp32 (PP).  A weight is at
+// most 2^15, since the row's reference moves when that is exceeded (and then puts the largest at 2^13); a
+// value scale is taken relative to the largest power of two of its group so far, which becomes 2^11: no
+// product leaves fp16, and whatever the scales' size none is lost beside 2^-36.  Sums and statistics are
+// fp32.
 //
-// Each warp works on its own, on tiles of 32 keys through a ring of its own (cp.async through the page
-// table, any page size and strides); no barrier of the CTA falls inside a unit.  Schedule, splits and
-// merges: gqaw_paged.cuh.
+// Each warp works on its own, on tiles of 32 keys through a ring of its own; no barrier of the CTA
+// falls inside a unit.  Tiles come by tensor TMA through the page table (codes, swizzled) and bulk copies
+// (scales), or row by row with cp.async where pages or strides do not allow that.  A unit's first tiles
+// are under way before the last unit's rows go out.  Schedule, splits and merges: gqaw_paged.cuh.
 //
-// Rows that nobody of a unit attends are not loaded and read as zeros.  A value scale that is not
-// finite counts as zero in the products, and the tokens that attend it are marked: their outputs of
-// that group are NaN, nobody else's.
+// Which of 8 rows is which: position x of 8 is key kappa(x) of a tile's, chosen so that the rows of
+// the even positions lie in different banks when four lanes read their dimensions of them.
+//
+// A value scale that is not finite counts as zero in the products, and the tokens that attend it are
+// marked: their outputs of that group are NaN, nobody else's.
 #pragma once
 
 #include <atomic>
@@ -47,7 +50,9 @@ namespace i4a {
 
 constexpr int kKeys = 32;      // a warp's tile
 constexpr int kUnitCost = 24;  // see gqaw_paged_sched.cuh
-constexpr float kLazy = 2.f;   // log2 units
+constexpr float kTopP = 13.f;  // log2 of the largest weight when the reference moves
+constexpr float kMaxP = 15.f;  // ... and of any
+constexpr int kTopV = 11;      // a scale's largest power of two becomes 2^kTopV
 
 template <int D, int NT, int QP>
 struct Lay {
@@ -56,32 +61,49 @@ struct Lay {
   static constexpr int kRow = D / 2;                     // bytes of a row's codes
   static constexpr int kCodes = kKeys * kRow;            // of a tile
   static constexpr int kScales = kKeys * G * 2;
-  static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V, their scales
+  static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V, their scales; a multiple of the swizzle's span
   static constexpr int W = D <= 128 && NT == 1 ? 12 : 8;
   static constexpr int S = D == 32 ? 8 : D == 64 ? 6 : D == 128 ? (W == 12 ? 3 : 4) : 2;
   static constexpr int kThreads = 32 * W;
-  static constexpr int PS = D + 4;                       // a row of a warp's state: D sums, maximum, sum of weights
-  static constexpr int kRing = S * kStage > R * PS * 4 ? S * kStage : R * PS * 4;  // the state takes the ring's place
+  static constexpr int PS = D + 4;                       // a row of a warp's state: D sums, reference, sum of weights
+  static constexpr bool kAhead = R * PS * 4 <= kStage;   // the state takes one stage's place, the next unit's tiles the others'
+  static constexpr int kRing = S * kStage > R * PS * 4 ? S * kStage : (R * PS * 4 + 1023) / 1024 * 1024;
   static constexpr int kNorm = W * kRing;                // per warp: scales as the products take them
-  static constexpr int kNormBytes = 2 * kKeys * G * 4;
+  static constexpr int kNormBytes = kKeys * G * 6;       // keys' in fp32, values' in fp16
   static constexpr int kQ = kNorm + W * kNormBytes;      // query operands [QP][NT][2 G][32 lanes] of 8 bytes
-  static constexpr int kQsum = kQ + QP * NT * 2 * G * 32 * 8;  // [R][G] fp32: where accumulators start
+  static constexpr int kQsum = kQ + QP * NT * 2 * G * 32 * 8;  // [G][R] fp32: where accumulators start
   static constexpr int kQexp = kQsum + R * G * 4;        // [R]: power of two of a row
-  static constexpr int kTotal = (kQexp + R * 4 + 15) / 16 * 16;
-  static_assert(kTotal + 12 * 1024 <= 232448, "shared memory");
+  static constexpr int kBars = (kQexp + R * 4 + 15) / 16 * 16;
+  static constexpr int kTotal = kBars + W * S * 8 + 1024;  // and room to align the base
+  static_assert(kTotal + 12 * 1024 + 512 <= 232448, "shared memory");
 };
 
-// Where 16-byte part `part` of row r's codes lies in a tile: parts are exchanged so that 8 rows of one
-// part, and the 4 even or 4 odd rows of 8, lie in different banks.
+// The key at position x of a tile.
+template <int D>
+__device__ __forceinline__ int kappa(int x) {
+  if (D == 128) return x ^ ((x >> 1) & 1);                                                  // 0 1 3 2 4 5 7 6
+  if (D == 64) return (x & ~3) | ((((x & 1) << 1) | ((x >> 1) & 1)) ^ ((x & 4) >> 1));      // 0 2 1 3 6 4 7 5
+  return x;
+}
+
+// Where 16-byte part `part` of row r's codes lies in a tile: as the TMA's swizzle exchanges the parts.
 template <int D>
 __device__ __forceinline__ int at_part(int r, int part) {
   const int x = D == 256 ? r & 7 : D == 128 ? (r >> 1) & 3 : D == 64 ? (r >> 2) & 1 : 0;
   return r * (D / 2) + ((part ^ x) << 4);
 }
 
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+// d = a b + c
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                    const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+// d += a b
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // An 8 x 8 matrix of 16-bit elements over the warp, transposed.
@@ -117,11 +139,7 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
   return r;
 }
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+using ptc::fast_exp2;
 // 2^e for any e, as what fp32 holds of it
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 // the same, and 0 where that is too small for fp32's normal numbers
@@ -132,23 +150,22 @@ __device__ __forceinline__ float times_pow2(float x, int e) {
   return x * pow2(a) * pow2(e - a);
 }
 
-// The scales of a key, as the products take them: N groups, four floats a load.
+// N consecutive 32-bit words of shared memory in wide loads.
 template <int N>
-__device__ __forceinline__ void lds_scales(const float *p, int key, float (&s)[N]) {
-  if constexpr (N >= 4) {
+__device__ __forceinline__ void lds_words(const void *p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(p + (i / 4) * (kKeys * 4) + key * 4);
-      s[i] = x.x, s[i + 1] = x.y, s[i + 2] = x.z, s[i + 3] = x.w;
+      const uint4 x = reinterpret_cast<const uint4 *>(p)[i / 4];
+      w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
     }
   } else if constexpr (N == 2) {
-    const float2 x = *reinterpret_cast<const float2 *>(p + key * 2);
-    s[0] = x.x, s[1] = x.y;
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    w[0] = x.x, w[1] = x.y;
   } else {
-    s[0] = p[key];
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
   }
 }
-
 __device__ __forceinline__ uint32_t lds32(const unsigned char *p) { return *reinterpret_cast<const uint32_t *>(p); }
 __device__ __forceinline__ uint32_t lds16(const unsigned char *p) { return *reinterpret_cast<const uint16_t *>(p); }
 
@@ -160,314 +177,445 @@ __device__ __forceinline__ void cp_async(void *dst, const void *src, bool ok) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N), "r"(n) : "memory");
 }
+// This thread's arrival on `bar` when its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A unit, as one thread prepares it for all warps.
+struct Unit {
+  int b, row0, ntok;           // sequence, first row of query / output, tokens
+  int kvh, h0, g, rows;        // kv head, first query head, query heads, rows
+  int t0, tiles;               // this CTA's key tiles
+  int in_lo, in_hi;            // tiles [in_lo, in_hi) have only keys that every row attends
+  uint32_t qpos, jlo, jhi;     // position of the first token; positions that some row attends
+  int cut, cf, cl;             // is the unit cut, and the first and last CTA with a part of it
+  int more;                    // is this a unit?
+  template <typename Walk>
+  __device__ inline void take(const I4Params &p, const PShape &shp, Walk &walk) {
+    PUnit u;
+    more = walk.next(shp, u);
+    if (!more) return;
+    b = u.b;
+    row0 = u.row0;
+    ntok = u.ntok;
+    kvh = u.hu / p.hblocks;
+    const int hb = u.hu - kvh * p.hblocks;
+    h0 = kvh * p.group + hb * p.gb;
+    g = min(p.gb, p.group - hb * p.gb);
+    rows = ntok * g;
+    t0 = u.kt + u.k0;
+    tiles = u.k1 - u.k0;
+    const long long lo = p.W > 0 && u.qpos - p.W + 1 > 0 ? u.qpos - p.W + 1 : 0, hi = u.qpos + u.ntok;
+    const long long all = p.W > 0 && hi - p.W > lo ? hi - p.W : lo;  // the last token's first key
+    qpos = (uint32_t)u.qpos;
+    jlo = (uint32_t)lo;
+    jhi = (uint32_t)hi;
+    in_lo = (int)((all + kKeys - 1) / kKeys);
+    in_hi = (int)((u.qpos + 1) / kKeys);
+    cut = u.k0 > 0 || u.k1 < u.nt;
+    cf = cut ? walk.owner(u.g0) : 0;
+    cl = cut ? walk.owner(u.g0 + u.nt - 1) : 0;
+  }
+};
 
 }  // namespace i4a
 
 // NT: operands of 8 query rows.  T: type of the rows outside the cache.
 template <typename T, int D, int NT, int QP>
-__global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1) i4_attend_kernel(const I4Params p) {
+__global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
+    i4_attend_kernel(const I4Params p, const __grid_constant__ I4Maps maps) {
   using namespace i4a;
   using L = Lay<D, NT, QP>;
   constexpr int W = L::W, S = L::S, G = L::G, R = L::R, PS = L::PS;
   constexpr int PP = sizeof(T) == 4 ? 2 : 1;         // parts of a weight
-  constexpr bool kFold = NT == 1;                    // the weights take the value scales
   constexpr bool kQreg = NT * QP * G <= 8;           // query operands in registers
   constexpr int SB = NT == 1 ? 2 : 1;                // blocks of 16 keys at once
-  constexpr int kTop = kFold ? 12 : 11;              // a scale's largest power of two becomes 2^kTop
+  constexpr int VW = D >= 64 ? D / 64 : 1;           // words of a lane's codes of a value row (D = 32: half of one)
+  constexpr int VT = D / 16;                         // operands of 16 dimensions
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PSched sched;
-  __shared__ int s_last;
+  __shared__ int s_last, s_state[W];  // ...; where each warp's state lies
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
   unsigned char *ring = smem + warp * L::kRing;
-  float *nk = reinterpret_cast<float *>(smem + L::kNorm + warp * L::kNormBytes);
-  float *nv = nk + kKeys * G;                        // kFold: [key][group] fp32, else [group][key] fp16
-  uint16_t *nvh = reinterpret_cast<uint16_t *>(nv);
+  float *nk = reinterpret_cast<float *>(smem + L::kNorm + warp * L::kNormBytes);  // [G / 4][position][4]
+  uint16_t *nv = reinterpret_cast<uint16_t *>(nk + kKeys * G);                    // [G][position]
   const uint2 *sq = reinterpret_cast<const uint2 *>(smem + L::kQ);
   float *sqsum = reinterpret_cast<float *>(smem + L::kQsum);
   int *sqexp = reinterpret_cast<int *>(smem + L::kQexp);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars) + warp * S;      // this warp's stages
+  const bool tma = p.box > 0;
+  const int box = tma ? min(p.box, kKeys) : 1, nbox = kKeys / box;
+  if (tid == 0 && tma) {
+    ptc::prefetch_map(&maps.k);
+    ptc::prefetch_map(&maps.v);
+  }
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(&full[i], tma ? 1 : 32);
+    mbar_fence_init();
+  }
+  __syncwarp();
   pdl_wait();
   const PShape shp = shape_of(p, kUnitCost);
   sched_build<kKeys>(p, shp, &sched);
-  PWalk<kKeys> walk(shp, &sched);
-  PUnit u;
-  while (walk.next(shp, u)) {
-    const int kvh = u.hu / p.hblocks, hb = u.hu - kvh * p.hblocks;
-    const int h0 = kvh * p.group + hb * p.gb, g = min(p.gb, p.group - hb * p.gb);
-    const int rows = u.ntok * g;
-    const long long jlo = p.W > 0 && u.qpos - p.W + 1 > 0 ? u.qpos - p.W + 1 : 0, jhi = u.qpos + u.ntok;
-    const int n = (u.k1 - u.k0 - warp + W - 1) / W;  // tiles of this warp: k0 + warp, k0 + warp + W, ...
-    auto key0 = [&](int i) { return (long long)(u.kt + u.k0 + warp + i * W) * kKeys; };
-    auto look_up = [&](int i) {  // this lane's page of the warp's tile i: -2 when not needed
-      const long long j = key0(i) + lane;
-      return i < n && j >= jlo && j < jhi ? p.table[(long long)u.b * p.width + (int)j / p.page] : -2;
-    };
-    auto load = [&](int i, int id) {
-      if (i < n) {  // uniform over the warp
-        constexpr int CPR = D / 32;  // 16-byte parts of a row
-        const int j = (int)key0(i) + lane, row = j - j / p.page * p.page;
-        long long off = -1, soff = 0;
-        if (id != -2) {
-          if ((unsigned)id < (unsigned)p.npages) {
-            off = id * p.sp + kvh * p.sh + row * p.sr;
-            soff = id * p.tp + kvh * p.th + row * p.tr;
-          } else {
-            pflag(p, GQAW_DEV_BAD_PAGE);
-          }
-        }
-        unsigned char *kb = ring + (i % S) * L::kStage, *sb = kb + 2 * L::kCodes;
-#pragma unroll
-        for (int c0 = 0; c0 < CPR; ++c0) {
-          const int c = c0 * 32 + lane, r = c / CPR, part = c % CPR;
-          const long long o = __shfl_sync(0xffffffffu, off, r);
-          const bool ok = o >= 0;
-          const unsigned char *k = static_cast<const unsigned char *>(p.kp) + (ok ? o : 0) + part * 16;
-          const unsigned char *v = static_cast<const unsigned char *>(p.vp) + (ok ? o : 0) + part * 16;
-          cp_async<16>(kb + at_part<D>(r, part), k, ok);
-          cp_async<16>(kb + L::kCodes + at_part<D>(r, part), v, ok);
-        }
-        if constexpr (G >= 2) {
-          cp_async<2 * G>(sb + lane * 2 * G, p.kscale + soff, off >= 0);
-          cp_async<2 * G>(sb + L::kScales + lane * 2 * G, p.vscale + soff, off >= 0);
-        } else {  // two bytes: too few for a copy
-          reinterpret_cast<uint16_t *>(sb)[lane] = off >= 0 ? p.kscale[soff] : (uint16_t)0;
-          reinterpret_cast<uint16_t *>(sb + L::kScales)[lane] = off >= 0 ? p.vscale[soff] : (uint16_t)0;
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    int id = look_up(0);
-    for (int i = 0; i < S - 1; ++i) {
-      const int next = look_up(i + 1);
-      load(i, id);
-      id = next;
-    }
+  __shared__ Unit units[3];  // the unit at hand, the next and the one behind it
+  const uint64_t pol = policy_evict_first();
+  const int my_group = gid * (D / 8) / kI4Group;  // of this lane's dimensions, gid D / 8 and on
+  bool fine = true;  // no wait of this warp has expired
 
-    // ---- queries: a warp has a row, a lane one element of every group
+  // lane b < nbox looks up box b of key tile t: -2 when no row attends any of its keys
+  auto look_up = [&](const Unit &x, int t, int end) {
+    const uint32_t j = (uint32_t)t * kKeys + lane * box;
+    return t < end && lane < nbox && j < x.jhi && j + box > x.jlo
+               ? p.table[(long long)x.b * p.width + (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift)] : -2;
+  };
+  // key tile t into stage st
+  auto load = [&](const Unit &x, int t, int end, int st, int id) {
+    if (t >= end) return;  // uniform over the warp
+    unsigned char *kb = ring + st * L::kStage, *sb = kb + 2 * L::kCodes;
+    const uint32_t j = (uint32_t)t * kKeys + lane * box;
+    const int row = (int)(j - (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift) * p.page);
+    const bool ok = id != -2 && (unsigned)id < (unsigned)p.npages;
+    if (id != -2 && !ok) pflag(p, GQAW_DEV_BAD_PAGE);
+    if (tma) {
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * box * (2 * L::kRow + 4 * G)));
+#pragma unroll 1
+      for (int b = 0; b < nbox; ++b) {
+        const int pid = __shfl_sync(0xffffffffu, id, b), r = __shfl_sync(0xffffffffu, row, b);
+        if (lane == 0 && ((mask >> b) & 1u)) {
+          ptc::tma_load_4d(kb + b * box * L::kRow, &maps.k, 0, r, x.kvh, pid, &full[st], pol);
+          ptc::tma_load_4d(kb + L::kCodes + b * box * L::kRow, &maps.v, 0, r, x.kvh, pid, &full[st], pol);
+          const long long soff = pid * p.tp + x.kvh * p.th + (long long)r * G;
+          bulk_g2s(sb + b * box * 2 * G, p.kscale + soff, (uint32_t)(box * 2 * G), &full[st], pol);
+          bulk_g2s(sb + L::kScales + b * box * 2 * G, p.vscale + soff, (uint32_t)(box * 2 * G), &full[st], pol);
+        }
+      }
+    } else {  // a lane has a key's row; those that are not needed become zeros
+      constexpr int CPR = D / 32;  // 16-byte parts of a row
+      const long long off = ok ? id * p.sp + x.kvh * p.sh + row * p.sr : -1;
+      const long long soff = ok ? id * p.tp + x.kvh * p.th + row * p.tr : 0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < CPR; ++c0) {
+        const int c = c0 * 32 + lane, r = c / CPR, part = c % CPR;
+        const long long o = __shfl_sync(0xffffffffu, off, r);
+        const unsigned char *k = static_cast<const unsigned char *>(p.kp) + (o >= 0 ? o : 0) + part * 16;
+        const unsigned char *v = static_cast<const unsigned char *>(p.vp) + (o >= 0 ? o : 0) + part * 16;
+        cp_async<16>(kb + at_part<D>(r, part), k, o >= 0);
+        cp_async<16>(kb + L::kCodes + at_part<D>(r, part), v, o >= 0);
+      }
+      if constexpr (G >= 2) {
+        cp_async<2 * G>(sb + lane * 2 * G, p.kscale + soff, ok);
+        cp_async<2 * G>(sb + L::kScales + lane * 2 * G, p.vscale + soff, ok);
+      } else {  // two bytes: too few for a copy
+        reinterpret_cast<uint16_t *>(sb)[lane] = ok ? p.kscale[soff] : (uint16_t)0;
+        reinterpret_cast<uint16_t *>(sb + L::kScales)[lane] = ok ? p.vscale[soff] : (uint16_t)0;
+      }
+      cp_async_arrive(&full[st]);
+    }
+  };
+  auto bump = [](int st) { return st + 1 == S ? 0 : st + 1; };
+  int id = -2;  // this lane's box of the next tile to load
+  auto load_first = [&](const Unit &x, int st) {  // from stage st on
+    const int t = x.t0 + warp, end = x.t0 + x.tiles;
+    int ids[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) ids[i] = look_up(x, t + i * W, end);
+    id = ids[0];
+#pragma unroll 1
+    for (int i = 0; i < S - 1; ++i) {
+      load(x, t + i * W, end, st, id);
+      st = bump(st);
+#pragma unroll
+      for (int k = 0; k < S - 1; ++k) id = k == i ? ids[k + 1] : id;
+    }
+  };
+  // one element of every group of row r
+  auto query_row = [&](const Unit &x, int r, float (&y)[G]) {
+    const int tok = r / x.g, hh = r - tok * x.g;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      y[i] = 0.f;
+      if (r < x.rows) {
+        const long long at = (x.row0 + tok) * p.qs + (long long)(x.h0 + hh) * D + i * 32 + lane;
+        y[i] = Elem<T>::load(static_cast<const T *>(p.q)[at]);
+        if (QP == 2 && sizeof(T) == 2) y[i] += Elem<T>::load(static_cast<const T *>(p.qlo)[at]);
+      }
+    }
+  };
+  // a warp's row as operands
+  auto put_query = [&](int r, const float (&x)[G]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < G; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int e = top ? min(140 - (int)(top >> 23), 126) : 0;  // x 2^e: the largest at 2^13
+    const int nib = lane & 7, step = (nib >> 1) & 1;
+    const float f = nib & 1 ? 0.0625f : 1.f, back = nib & 1 ? -8.f * 16.f / 16777216.f : -8.f / 16777216.f;  // a code of an odd nibble counts 16 times
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const float y = times_pow2(x[i], e) * f;
+      const __half h1 = __float2half_rn(y);
+      float sum = __half2float(h1);
+      const int slot = ((r / 8) * 2 * G + 2 * i + step) * 32 + (r & 7) * 4 + (lane >> 3);
+      __half *q = reinterpret_cast<__half *>(smem + L::kQ) + slot * 4 + (nib & 1) * 2 + (nib >> 2);
+      q[0] = h1;
+      if (QP == 2) {
+        const __half h2 = __float2half_rn(y - sum);
+        q[NT * 2 * G * 32 * 4] = h2;
+        sum += __half2float(h2);
+      }
+      sum *= back;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+      if (lane == 0) sqsum[i * R + r] = sum;
+    }
+    if (lane == 0) sqexp[r] = e;
+  };
+
+  // One thread walks the units, two ahead; its walker is kept out of everybody's registers
+  __shared__ __align__(16) unsigned char walker[sizeof(PWalk<kKeys>)];
+  PWalk<kKeys> *walk = reinterpret_cast<PWalk<kKeys> *>(walker);
+  if (tid == 0) {
+    *walk = PWalk<kKeys>(shp, &sched);
+    units[0].take(p, shp, *walk);
+    if (units[0].more) units[1].take(p, shp, *walk);
+  }
+  __syncthreads();
+  int st = 0, phase = 0;  // stage of the next tile, and how often the ring has gone round
+  if (units[0].more) {
+    load_first(units[0], 0);
     for (int r = warp; r < R; r += W) {
-      const int tok = r / g, hh = r - tok * g;
-      float x[G];
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        x[i] = 0.f;
-        if (r < rows) {
-          const long long at = (u.row0 + tok) * p.qs + (long long)(h0 + hh) * D + i * 32 + lane;
-          x[i] = Elem<T>::load(static_cast<const T *>(p.q)[at]);
-          if (QP == 2 && sizeof(T) == 2) x[i] += Elem<T>::load(static_cast<const T *>(p.qlo)[at]);
-        }
-        top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      const int e = top ? min(140 - (int)(top >> 23), 126) : 0;  // x 2^e: the largest at 2^13
-      const int nib = lane & 7, step = (nib >> 1) & 1;
-      const float f = nib & 1 ? 0.0625f : 1.f;                   // a code of an odd nibble counts 16 times
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const float y = times_pow2(x[i], e) * f;
-        const __half h1 = __float2half_rn(y);
-        float sum = __half2float(h1);
-        const int slot = ((r / 8) * 2 * G + 2 * i + step) * 32 + (r & 7) * 4 + (lane >> 3);
-        __half *q = reinterpret_cast<__half *>(smem + L::kQ) + slot * 4 + (nib & 1) * 2 + (nib >> 2);
-        q[0] = h1;
-        if (QP == 2) {
-          const __half h2 = __float2half_rn(y - sum);
-          q[NT * 2 * G * 32 * 4] = h2;
-          sum += __half2float(h2);
-        }
-        sum /= f;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        if (lane == 0) sqsum[r * G + i] = sum * (-8.f / 16777216.f);
-      }
-      if (lane == 0) sqexp[r] = e;
+      float q[G];
+      query_row(units[0], r, q);
+      put_query(r, q);
     }
     __syncthreads();
+  }
+  for (int un = 0; units[un].more;) {
+    const Unit &x = units[un];
+    const int rows = x.rows, end = x.t0 + x.tiles, in_lo = x.in_lo, in_hi = x.in_hi;
     uint2 qr[kQreg ? QP * NT * 2 * G : 1];
-    float qs[kQreg ? NT * G * 2 : 1];  // of this lane's two rows of each operand
+    float qs[kQreg ? NT * G : 1][4];  // where this lane's accumulators start
     if constexpr (kQreg) {
 #pragma unroll
       for (int i = 0; i < QP * NT * 2 * G; ++i) qr[i] = sq[i * 32 + lane];
 #pragma unroll
-      for (int i = 0; i < NT * G * 2; ++i) qs[i] = sqsum[((i / 2 / G) * 8 + 2 * t4 + (i & 1)) * G + i / 2 % G];
+      for (int i = 0; i < NT * G; ++i) {
+        const float2 y = *reinterpret_cast<const float2 *>(sqsum + (i % G) * R + i / G * 8 + 2 * t4);
+        qs[i][0] = qs[i][2] = y.x;
+        qs[i][1] = qs[i][3] = y.y;
+      }
     }
     // z = (sum s 2^se acc) 2^(24 - se - e) qscale, e the row's power of two; se is not 0 where queries are
     // so large (e < 0) that the keys' scales may be too small for fp32 beside acc < 1
     const int se = -min(0, __reduce_min_sync(0xffffffffu, lane < rows ? sqexp[min(lane, R - 1)] : 0));
     const float sfac = pow2(se);
-    float qf[NT][2], m[NT][2], l[NT][2];
+    float qf[NT][2], nb[NT][2], th[NT][2], l[NT][2];  // factor; minus the reference; what a logit less the reference may be
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         qf[nt][c] = p.qscale * pow2_or_0(24 - se - sqexp[nt * 8 + 2 * t4 + c]);
-        m[nt][c] = -INFINITY;
+        nb[nt][c] = 0.f;
+        th[nt][c] = -INFINITY;
         l[nt][c] = 0.f;
       }
-    float o[NT][2 * G][4];
+    float o[NT][VT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2 * G; ++i)
+      for (int i = 0; i < VT; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
     // of each group: the largest scale (bf16 bits) of the power of two seen so far, and the factor that
-    // takes that power to 2^kTop
+    // takes that power to 2^kTopV
     uint32_t thr[(G + 1) / 2];
-    float vf[G];
+    float vf[G], my_vf = pow2(127);
 #pragma unroll
     for (int i = 0; i < (G + 1) / 2; ++i) thr[i] = 0u;
 #pragma unroll
     for (int i = 0; i < G; ++i) vf[i] = pow2(127);
     uint32_t marked = 0;  // groups of row `lane` that attend a scale that is not finite
 
-    for (int i = 0; i < n; ++i) {
-      const int next = look_up(i + S);
-      load(i + S - 1, id);
-      id = next;
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-      __syncwarp();
-      const unsigned char *kb = ring + (i % S) * L::kStage, *vb = kb + L::kCodes, *sb = vb + L::kCodes;
-      const long long j0 = key0(i);
-      const bool inner = j0 >= jlo && j0 + kKeys - 1 <= u.qpos && (p.W == 0 || j0 >= jhi - p.W);
+    // lane-constant places in a tile: keys' codes of positions gid and gid + 8, 16, 24; values' of this lane's dimensions
+    int koff[G], voff[2];
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) koff[gr] = at_part<D>(kappa<D>(gid), gr) + t4 * 4;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) voff[c] = L::kCodes + at_part<D>(kappa<D>(2 * t4 + c), gid * (D / 16) / 16) + gid * (D / 16) % 16;
 
-      // ---- scales: a lane has a key
+    for (int t = x.t0 + warp; t < end; t += W) {
       {
+        const int next = look_up(x, t + S * W, end);
+        load(x, t + (S - 1) * W, end, st == 0 ? S - 1 : st - 1, id);
+        id = next;
+      }
+      if (!__all_sync(0xffffffffu, fine && mbar_wait(&full[st], phase & 1))) fine = false;
+      const unsigned char *kb = ring + st * L::kStage, *sb = kb + 2 * L::kCodes;
+      const bool inner = t >= in_lo && t < in_hi;
+
+      // ---- scales: a lane has a position
+      {
+        const int key = (lane & ~7) | kappa<D>(lane & 7);
         uint32_t kw[(G + 1) / 2], vw[(G + 1) / 2];
         if constexpr (G == 1) {
-          kw[0] = reinterpret_cast<const uint16_t *>(sb)[lane];
-          vw[0] = reinterpret_cast<const uint16_t *>(sb + L::kScales)[lane];
+          kw[0] = reinterpret_cast<const uint16_t *>(sb)[key];
+          vw[0] = reinterpret_cast<const uint16_t *>(sb + L::kScales)[key];
         } else {
+          lds_words(sb + key * 2 * G, kw);
+          lds_words(sb + L::kScales + key * 2 * G, vw);
+        }
+        if (!inner && ((uint32_t)t * kKeys + key < x.jlo || (uint32_t)t * kKeys + key >= x.jhi)) {  // a row of nobody in the unit, whatever it holds
 #pragma unroll
-          for (int x = 0; x < G / 2; ++x) {
-            kw[x] = reinterpret_cast<const uint32_t *>(sb)[lane * (G / 2) + x];
-            vw[x] = reinterpret_cast<const uint32_t *>(sb + L::kScales)[lane * (G / 2) + x];
-          }
+          for (int y = 0; y < (G + 1) / 2; ++y) vw[y] = 0u;
         }
         bool above = false, odd = false;
 #pragma unroll
-        for (int x = 0; x < (G + 1) / 2; ++x) {
-          const uint32_t a = vw[x] & 0x7fff7fffu;
-          above |= __vmaxu2(a, thr[x]) != thr[x];
-        }
+        for (int y = 0; y < (G + 1) / 2; ++y) above |= __vmaxu2(vw[y] & 0x7fff7fffu, thr[y]) != thr[y];
         if (__any_sync(0xffffffffu, above)) {
+          uint32_t bad = 0;
 #pragma unroll
-          for (int x = 0; x < (G + 1) / 2; ++x) {
+          for (int y = 0; y < (G + 1) / 2; ++y) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const uint32_t half = 0xffffu << (16 * hf), inf = 0x7f800000u >> (16 - 16 * hf);
-              if (2 * x + hf < G && (vw[x] & 0x7fff7fffu & half) >= inf) {
+              if (2 * y + hf < G && (vw[y] & 0x7fff7fffu & half) >= inf) {
                 odd = true;
-                vw[x] &= ~half;
+                bad |= 1u << (2 * y + hf);
+                vw[y] &= ~half;
               }
             }
-            uint32_t mx = vw[x] & 0x7fff7fffu;
+            uint32_t mx = vw[y] & 0x7fff7fffu;
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            mx = __vmaxu2(mx | 0x007f007fu, thr[x]);
-            thr[x] = mx;
+            mx = __vmaxu2(mx | 0x007f007fu, thr[y]);
+            thr[y] = mx;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              constexpr int kG = G;
-              const int gr = 2 * x + hf;
-              if (gr < kG) {
-                const float f = pow2(kTop + 127 - (int)((mx >> (16 * hf + 7)) & 0xffu));
-                const float down = f / vf[gr];
-                vf[gr] = f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) {
-                    o[nt][2 * gr][c] *= down;
-                    o[nt][2 * gr + 1][c] *= down;
-                  }
-              }
-            }
+            for (int hf = 0; hf < 2; ++hf)
+              if (2 * y + hf < G) vf[2 * y + hf] = pow2(kTopV + 127 - (int)((mx >> (16 * hf + 7)) & 0xffu));
           }
+          float f = vf[0];
+#pragma unroll
+          for (int gr = 1; gr < G; ++gr) f = my_group == gr ? vf[gr] : f;
+          const float down = f / my_vf;
+          my_vf = f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[nt][v][c] *= down;
           uint32_t who = __ballot_sync(0xffffffffu, odd);
           while (who) {  // a key with scales that are not finite: mark the rows that attend it
-            const int k = __ffs((int)who) - 1;
+            const int src = __ffs((int)who) - 1;
             who &= who - 1u;
-            const long long j = j0 + k, at = u.qpos + lane / g;
-            const bool sees = lane < rows && j <= at && j >= jlo && (p.W == 0 || j > at - p.W);
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-              const uint32_t bits = reinterpret_cast<const uint16_t *>(sb + L::kScales)[k * G + gr] & 0x7f80u;
-              if (sees && bits == 0x7f80u) marked |= 1u << gr;
-            }
+            const long long j = (long long)t * kKeys + __shfl_sync(0xffffffffu, key, src), at = (long long)x.qpos + lane / x.g;
+            const uint32_t groups = __shfl_sync(0xffffffffu, bad, src);
+            if (lane < rows && j <= at && (p.W == 0 || j > at - p.W)) marked |= groups;
           }
         }
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
           const uint32_t ka = gr & 1 ? kw[gr / 2] & 0xffff0000u : kw[gr / 2] << 16;
           const uint32_t va = gr & 1 ? vw[gr / 2] & 0xffff0000u : vw[gr / 2] << 16;
-          const float ks = __uint_as_float(ka) * sfac, vs = __uint_as_float(va) * vf[gr];
-          const int at = (gr / 4) * (kKeys * 4) + lane * (G < 4 ? G : 4) + gr % 4;
-          nk[at] = ks;
-          if (kFold)
-            nv[at] = vs;
-          else
-            nvh[gr * kKeys + lane] = __half_as_ushort(__float2half_rn(vs));
+          nk[(gr / 4) * (kKeys * 4) + lane * (G < 4 ? G : 4) + gr % 4] = __uint_as_float(ka) * sfac;
+          nv[gr * kKeys + lane] = __half_as_ushort(__float2half_rn(__uint_as_float(va) * vf[gr]));
         }
       }
       __syncwarp();
 
 #pragma unroll
       for (int b0 = 0; b0 < 2; b0 += SB) {
-        // ---- logits of SB blocks of 16 keys: this lane has keys gid and gid + 8, rows 2 t4 and 2 t4 + 1
+        // ---- logits of SB blocks of 16 keys: this lane has positions gid and gid + 8, rows 2 t4 and 2 t4 + 1
         float z[SB][NT][4];
 #pragma unroll
         for (int b = 0; b < SB; ++b) {
-          const int k0 = (b0 + b) * 16 + gid;
-          float s0[G], s1[G];
-          lds_scales<G>(nk, k0, s0);
-          lds_scales<G>(nk, k0 + 8, s1);
+          constexpr int GV = G < 4 ? G : 4;
 #pragma unroll
-          for (int gr = 0; gr < G; ++gr) {
-            const uint32_t w0 = lds32(kb + at_part<D>(k0, gr) + t4 * 4), w1 = lds32(kb + at_part<D>(k0 + 8, gr) + t4 * 4);
-            const uint32_t x0 = w0 >> 8, x1 = w1 >> 8;
+          for (int g0 = 0; g0 < G; g0 += GV) {
+            uint32_t s0[GV], s1[GV];
+            const float *ns = nk + (g0 / 4) * (kKeys * 4) + ((b0 + b) * 16 + gid) * GV;
+            lds_words(ns, s0);
+            lds_words(ns + 8 * GV, s1);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float c[4];
-              if constexpr (kQreg) {
-                c[0] = c[2] = qs[(nt * G + gr) * 2];
-                c[1] = c[3] = qs[(nt * G + gr) * 2 + 1];
-              } else {
-                c[0] = c[2] = sqsum[(nt * 8 + 2 * t4) * G + gr];
-                c[1] = c[3] = sqsum[(nt * 8 + 2 * t4 + 1) * G + gr];
+            for (int gg = 0; gg < GV; ++gg) {
+              const int gr = g0 + gg;
+              const unsigned char *kc = kb + koff[gr] + (b0 + b) * 16 * L::kRow;
+              const uint32_t w0 = lds32(kc), w1 = lds32(kc + 8 * L::kRow), x0 = w0 >> 8, x1 = w1 >> 8;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float c[4];
+                if constexpr (!kQreg) {
+                  const float2 y = *reinterpret_cast<const float2 *>(sqsum + gr * R + nt * 8 + 2 * t4);
+                  c[0] = c[2] = y.x;
+                  c[1] = c[3] = y.y;
+                }
+#pragma unroll
+                for (int q = 0; q < QP; ++q) {
+                  const int at = (q * NT + nt) * 2 * G + 2 * gr;
+                  const uint2 qa = kQreg ? qr[kQreg ? at : 0] : sq[at * 32 + lane], qb = kQreg ? qr[kQreg ? at + 1 : 0] : sq[(at + 1) * 32 + lane];
+                  if (kQreg && q == 0)
+                    mma(c, w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qa.x, qa.y, qs[kQreg ? nt * G + gr : 0]);
+                  else
+                    mma(c, w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qa.x, qa.y);
+                  mma(c, x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, qb.x, qb.y);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float s = __uint_as_float(e < 2 ? s0[gg] : s1[gg]);
+                  z[b][nt][e] = gr ? fmaf(s, c[e], z[b][nt][e]) : s * c[e];
+                }
               }
-#pragma unroll
-              for (int q = 0; q < QP; ++q) {
-                const int at = (q * NT + nt) * 2 * G + 2 * gr;
-                const uint2 qa = kQreg ? qr[kQreg ? at : 0] : sq[at * 32 + lane], qb = kQreg ? qr[kQreg ? at + 1 : 0] : sq[(at + 1) * 32 + lane];
-                mma(c, w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qa.x, qa.y);
-                mma(c, x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, qb.x, qb.y);
-              }
-              z[b][nt][0] = gr ? fmaf(s0[gr], c[0], z[b][nt][0]) : s0[gr] * c[0];
-              z[b][nt][1] = gr ? fmaf(s0[gr], c[1], z[b][nt][1]) : s0[gr] * c[1];
-              z[b][nt][2] = gr ? fmaf(s1[gr], c[2], z[b][nt][2]) : s1[gr] * c[2];
-              z[b][nt][3] = gr ? fmaf(s1[gr], c[3], z[b][nt][3]) : s1[gr] * c[3];
             }
           }
         }
-        // ---- softmax
+        // ---- softmax: logits less the reference
+        if (p.capmul != 0.f) {
+#pragma unroll
+          for (int b = 0; b < SB; ++b)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float y = z[b][nt][c] * qf[nt][c & 1];
+                z[b][nt][c] = (sizeof(T) == 4 ? cap_logit(p, y) : p.capmul * ptc::fast_tanh(y)) + nb[nt][c & 1];
+              }
+        } else {
+#pragma unroll
+          for (int b = 0; b < SB; ++b)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) z[b][nt][c] = fmaf(z[b][nt][c], qf[nt][c & 1], nb[nt][c & 1]);
+        }
+        if (!inner) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int r = nt * 8 + 2 * t4 + c;
+              // this row's keys, relative to the position of this lane's first one
+              const long long at = (long long)x.qpos + r / x.g, j = (long long)t * kKeys + b0 * 16 + kappa<D>(gid);
+              const int hi = r < rows ? (int)min(max(at - j, -1ll), 63ll) : -1;
+              const long long low = p.W > 0 ? max((long long)x.jlo, at - p.W + 1) : (long long)x.jlo;
+              const int lo = (int)min(max(low - j, 0ll), 64ll);
+#pragma unroll
+              for (int b = 0; b < SB; ++b)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                  if (b * 16 + hf * 8 > hi || b * 16 + hf * 8 < lo) z[b][nt][2 * hf + c] = -INFINITY;
+            }
+        }
         bool up = false;
 #pragma unroll
         for (int b = 0; b < SB; ++b)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float x = z[b][nt][c] * qf[nt][c & 1];
-              if (p.capmul != 0.f) x = sizeof(T) == 4 ? cap_logit(p, x) : p.capmul * ptc::fast_tanh(x);
-              if (!inner) {
-                const int r = nt * 8 + 2 * t4 + (c & 1);
-                const long long j = j0 + (b0 + b) * 16 + gid + (c & 2 ? 8 : 0), at = u.qpos + r / g;
-                if (r >= rows || j > at || j < jlo || (p.W > 0 && j <= at - p.W)) x = -INFINITY;
-              }
-              z[b][nt][c] = x;
-              up |= x > m[nt][c & 1] + kLazy;
-            }
+            for (int c = 0; c < 4; ++c) up |= z[b][nt][c] > th[nt][c & 1];
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -477,133 +625,150 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1) i4_attend_ke
               if (SB == 2) mx = fmaxf(mx, fmaxf(z[SB - 1][nt][c], z[SB - 1][nt][c + 2]));
 #pragma unroll
               for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-              if (mx > m[nt][c] + kLazy) {
-                const float f = fast_exp2(m[nt][c] - mx);  // 0 while nothing was seen
-                m[nt][c] = mx;
+              if (mx > th[nt][c]) {  // the same in the eight lanes of a row
+                const float by = mx - kTopP, f = th[nt][c] == -INFINITY ? 0.f : fast_exp2(-by);
+                nb[nt][c] -= by;
+                th[nt][c] = kMaxP;
                 l[nt][c] *= f;
 #pragma unroll
-                for (int x = 0; x < 2 * G; ++x) o[nt][x][c] *= f, o[nt][x][c + 2] *= f;
+                for (int v = 0; v < VT; ++v) o[nt][v][c] *= f, o[nt][v][c + 2] *= f;
+#pragma unroll
+                for (int b = 0; b < SB; ++b) z[b][nt][c] -= by, z[b][nt][c + 2] -= by;
               }
             }
         }
 #pragma unroll
         for (int b = 0; b < SB; ++b) {
-          // ---- weights
-          const int kc = (b0 + b) * 16;
-          uint32_t pb[NT][PP][kFold ? G : 1][2];
+          // ---- weights: rows of positions become rows of queries
+          uint32_t pb[NT][PP][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float pr[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float base = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
-              pr[c] = fast_exp2(z[b][nt][c] - base);
-              l[nt][c & 1] += pr[c];
-            }
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              float s[kFold ? G : 1] = {8192.f};
-              if constexpr (kFold) lds_scales<G>(nv, kc + gid + 8 * hf, s);
-#pragma unroll
-              for (int gr = 0; gr < (kFold ? G : 1); ++gr) {
-                const float w0 = pr[2 * hf] * s[gr], w1 = pr[2 * hf + 1] * s[gr];
-                const uint32_t h = half2_of(w0, w1);
-                pb[nt][0][gr][hf] = transpose(h);
-                if (PP == 2) {
-                  const float2 back = floats_of(h);
-                  pb[nt][PP - 1][gr][hf] = transpose(half2_of(w0 - back.x, w1 - back.y));
-                }
+              const float w0 = fast_exp2(z[b][nt][2 * hf]), w1 = fast_exp2(z[b][nt][2 * hf + 1]);
+              l[nt][0] += w0;
+              l[nt][1] += w1;
+              const uint32_t h = half2_of(w0, w1);
+              pb[nt][0][hf] = transpose(h);
+              if (PP == 2) {
+                const float2 back = floats_of(h);
+                pb[nt][PP - 1][hf] = transpose(half2_of(w0 - back.x, w1 - back.y));
               }
             }
+          // ---- values: this lane's D / 8 dimensions of positions 2 t4, + 1, + 8, + 9
+          const int pos = (b0 + b) * 16 + 2 * t4;
+          const uint32_t sa = *reinterpret_cast<const uint32_t *>(nv + my_group * kKeys + pos);
+          const uint32_t sc = *reinterpret_cast<const uint32_t *>(nv + my_group * kKeys + pos + 8);
+          uint32_t w[4][VW];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const unsigned char *vr = kb + voff[c & 1] + ((b0 + b) * 16 + (c & 2) * 4) * L::kRow;
+            if constexpr (D == 32)
+              w[c][0] = lds16(vr);
+            else
+              lds_words(vr, w[c]);
           }
-          // ---- values: this lane has dimensions 4 gid .. 4 gid + 3 of every group, keys 2 t4, + 1, + 8, + 9
-          const unsigned char *r0 = vb + 2 * gid;
-          const int ka = kc + 2 * t4;
 #pragma unroll
-          for (int gr = 0; gr < G; ++gr) {
-            const uint32_t xa = __byte_perm(lds16(r0 + at_part<D>(ka, gr)), lds16(r0 + at_part<D>(ka + 1, gr)), 0x5410);
-            const uint32_t xb = __byte_perm(lds16(r0 + at_part<D>(ka + 8, gr)), lds16(r0 + at_part<D>(ka + 9, gr)), 0x5410);
-            const uint32_t ya = xa >> 8, yb = xb >> 8;
-            uint32_t v[2][4] = {{xa & kLow, xa & kHigh, xb & kLow, xb & kHigh}, {ya & kLow, ya & kHigh, yb & kLow, yb & kHigh}};
-            if constexpr (kFold) {  // c - 8 (16 times) in units of 2^-24
+          for (int y = 0; y < VW; ++y)
 #pragma unroll
-              for (int x = 0; x < 2; ++x)
+            for (int hf = 0; hf < (D == 32 ? 1 : 2); ++hf) {
+              // four dimensions of two positions, in one word each
+              const uint32_t xa = __byte_perm(w[0][y], w[1][y], hf ? 0x7632 : 0x5410), xb = __byte_perm(w[2][y], w[3][y], hf ? 0x7632 : 0x5410);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[x][c] = hadd2(v[x][c], c & 1 ? 0x80808080u : 0x80088008u);
-            } else {  // (1024 + c) - 1032 and (1024 + 16 c) / 16 - 72: c - 8, then times its scale
-              const uint32_t sa = *reinterpret_cast<const uint32_t *>(nvh + gr * kKeys + ka), sc = *reinterpret_cast<const uint32_t *>(nvh + gr * kKeys + ka + 8);
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t a = k ? xa >> 8 : xa, c = k ? xb >> 8 : xb;
+                // (1024 + c) - 1032 and (1024 + 16 c) / 16 - 72: c - 8, then times its scale
+                const uint32_t v0 = hmul2(hadd2(and_or(a, kLow, 0x64006400u), 0xe408e408u), sa);
+                const uint32_t v1 = hmul2(hfma2(and_or(a, kHigh, 0x64006400u), 0x2c002c00u, 0xd480d480u), sa);
+                const uint32_t v2 = hmul2(hadd2(and_or(c, kLow, 0x64006400u), 0xe408e408u), sc);
+                const uint32_t v3 = hmul2(hfma2(and_or(c, kHigh, 0x64006400u), 0x2c002c00u, 0xd480d480u), sc);
 #pragma unroll
-              for (int x = 0; x < 2; ++x)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  uint32_t y = v[x][c] | 0x64006400u;
-                  y = c & 1 ? hfma2(y, 0x2c002c00u, 0xd480d480u) : hadd2(y, 0xe408e408u);
-                  v[x][c] = hmul2(y, c & 2 ? sc : sa);
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int q = 0; q < PP; ++q) {
-                const uint32_t *w = pb[nt][q][kFold ? gr : 0];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) mma(o[nt][2 * gr + x], v[x][0], v[x][1], v[x][2], v[x][3], w[0], w[1]);
+                  for (int q = 0; q < PP; ++q) {
+                    float(&acc)[4] = o[nt][(y * 2 + hf) * 2 + k];
+                    mma(acc, v0, v1, v2, v3, pb[nt][q][0], pb[nt][q][1]);
+                  }
               }
-          }
+            }
         }
       }
       __syncwarp();  // the stage and the scales are free
+      st = bump(st);
+      phase += st == 0;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
 
-    // ---- the warp's state into its ring: [R][D + 4]
-    float *mine = reinterpret_cast<float *>(ring);
+    // ---- the next unit's tiles and queries are on their way while this one's rows go out
+    const Unit &nx = units[un == 2 ? 0 : un + 1];
+    const bool more = nx.more;
+    float q[G];
+    if (more) {
+      if constexpr (L::kAhead) load_first(nx, st);
+      query_row(nx, min(warp, R - 1), q);
+    }
+
+    // ---- the warp's state: [R][D + 4], in the stage that no tile is under way to
+    const int state = L::kAhead ? (st == 0 ? S - 1 : st - 1) * L::kStage : 0;
+    float *mine = reinterpret_cast<float *>(ring + state);
+    // vf is a power of two, and its reciprocal one
+    const int ve = 127 - (int)(__float_as_uint(my_vf) >> 23);
+    const float v1 = pow2(ve / 2), v2 = pow2(ve - ve / 2);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int r = nt * 8 + 2 * t4 + c;
-        float x = l[nt][c];
+        float sum = l[nt][c];
 #pragma unroll
-        for (int s = 4; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-        const uint32_t bad = __shfl_sync(0xffffffffu, marked, r);
+        for (int s = 4; s < 32; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        const bool bad = (__shfl_sync(0xffffffffu, marked, r) >> my_group) & 1u;
         if (gid == 0) {
-          mine[r * PS + D] = m[nt][c];
-          mine[r * PS + D + 1] = x;
+          mine[r * PS + D] = th[nt][c] == -INFINITY ? -INFINITY : -nb[nt][c];
+          mine[r * PS + D + 1] = sum;
         }
+        float *to = mine + r * PS + gid * (D / 8);
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          // vf is a power of two, and its reciprocal one
-          const int e = 127 - (int)(__float_as_uint(vf[gr]) >> 23) + (kFold ? 24 : -13);
+        for (int v = 0; v < VT; v += 2) {
           float y[4];
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const float a = o[nt][2 * gr + d / 2][c + 2 * (d & 1)];
-            y[d] = times_pow2(kFold && (d & 1) ? a * 0.0625f : a, e);
-            if ((bad >> gr) & 1u) y[d] = NAN;
-          }
-          *reinterpret_cast<float4 *>(mine + r * PS + gr * 32 + gid * 4) = make_float4(y[0], y[1], y[2], y[3]);
+          for (int e = 0; e < 4; ++e) y[e] = bad ? NAN : o[nt][v + e / 2][c + 2 * (e & 1)] * v1 * v2;
+          *reinterpret_cast<float4 *>(to + 2 * v) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
+    if (lane == 0) s_state[warp] = warp * L::kRing + state;
     __syncthreads();
+    if (tid == 0) {  // the unit behind the next one, in the place of the last
+      Unit &y = units[un == 0 ? 2 : un - 1];
+      y.more = 0;
+      if (more) y.take(p, shp, *walk);
+    }
+    if (more) {
+      put_query(min(warp, R - 1), q);
+      for (int r = warp + W; r < R; r += W) {
+        query_row(nx, r, q);
+        put_query(r, q);
+      }
+    }
     // ---- the warps' states joined
-    const bool cut = u.k0 > 0 || u.k1 < u.nt;
-    const int cta = blockIdx.x, cf = cut ? walk.owner(u.g0) : cta, cl = cut ? walk.owner(u.g0 + u.nt - 1) : cta;
+    const bool cut = x.cut;
+    const int cta = blockIdx.x, cf = x.cf, cl = x.cl, g = x.g, row0 = x.row0, h0 = x.h0;
     T *out = static_cast<T *>(p.out);
     float *part = p.partials + ((long long)cta * 2 + (cta == cf ? 1 : 0)) * R * PS;
     for (int e = tid; e < rows * D; e += L::kThreads) {
       const int r = e / D, d = e - r * D, tok = r / g, h = h0 + r - tok * g;
-      float M = -INFINITY, A = 0.f, Z = 0.f;
+      float M = -INFINITY, A = 0.f, Z = 0.f, m[W];
 #pragma unroll
-      for (int w = 0; w < W; ++w) M = fmaxf(M, reinterpret_cast<const float *>(smem + w * L::kRing)[r * PS + D]);
+      for (int w = 0; w < W; ++w) {
+        m[w] = reinterpret_cast<const float *>(smem + s_state[w])[r * PS + D];
+        M = fmaxf(M, m[w]);
+      }
       const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float *x = reinterpret_cast<const float *>(smem + w * L::kRing) + r * PS;
-        const float f = exp2f(x[D] - ref);
-        Z = fmaf(f, x[D + 1], Z);
-        A = fmaf(f, x[d], A);
+        const float *y = reinterpret_cast<const float *>(smem + s_state[w]) + r * PS;
+        const float f = fast_exp2(m[w] - ref);
+        Z = fmaf(f, y[D + 1], Z);
+        A = fmaf(f, y[d], A);
       }
       if (cut) {
         part[r * PS + d] = A;
@@ -612,7 +777,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1) i4_attend_ke
           part[r * PS + D + 1] = Z;
         }
       } else {
-        out[(u.row0 + tok) * p.os + (long long)h * D + d] = Elem<T>::store(A * sink_reciprocal(Z, M, paged_sink_log2(p, h)));
+        out[(row0 + tok) * p.os + (long long)h * D + d] = Elem<T>::store(A * sink_reciprocal(Z, M, paged_sink_log2(p, h)));
       }
     }
     if (cut) {
@@ -628,18 +793,30 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1) i4_attend_ke
           const int r = e / D, d = e - r * D, tok = r / g, h = h0 + r - tok * g;
           float M, Z, A[1];
           merge_row<D, 1>(cf, cl, d, [&](int c) { return p.partials + ((long long)c * 2 + (c == cf)) * R * PS + r * PS; }, M, Z, A);
-          out[(u.row0 + tok) * p.os + (long long)h * D + d] = Elem<T>::store(A[0] * sink_reciprocal(Z, M, paged_sink_log2(p, h)));
+          out[(row0 + tok) * p.os + (long long)h * D + d] = Elem<T>::store(A[0] * sink_reciprocal(Z, M, paged_sink_log2(p, h)));
         }
         if (tid == 0) p.tickets[cf] = 0u;
       }
     }
-    __syncthreads();  // queries and rings are reused by the next unit
+    // the states were written by ordinary stores where the next tiles may land by TMA
+    tc::fence_proxy_async_smem();
+    __syncthreads();
+    if (!L::kAhead && more) load_first(nx, st);
+    un = un == 2 ? 0 : un + 1;
+  }
+  // every load that was issued has been waited for, unless a wait expired
+  if (!fine) {
+    if (lane == 0) {
+      pflag(p, GQAW_DEV_TIMEOUT);
+      const int n = phase * S + st;  // tiles in all
+      for (int i = n > S ? n - S : 0; i < n; ++i) mbar_wait(&full[i % S], (i / S) & 1);
+    }
   }
   pdl_launch_dependents();
 }
 
 template <typename T, int D, int NT, int QP>
-cudaError_t launch_i4_attend_one(const I4Params &p, int sms, cudaStream_t stream) {
+cudaError_t launch_i4_attend_one(const I4Params &p, const I4Maps &maps, int sms, cudaStream_t stream) {
   using L = i4a::Lay<D, NT, QP>;
   constexpr int kMaxDevices = 64;
   static std::atomic<bool> ready[kMaxDevices];
@@ -661,17 +838,17 @@ cudaError_t launch_i4_attend_one(const I4Params &p, int sms, cudaStream_t stream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, i4_attend_kernel<T, D, NT, QP>, p);
+  e = cudaLaunchKernelEx(&cfg, i4_attend_kernel<T, D, NT, QP>, p, maps);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // nt: 1, 2 or 4 (head size 256: 1 or 2) operands of 8 rows.
 template <typename T, int QP>
-cudaError_t launch_i4_attend_t(const I4Params &p, int nt, int sms, cudaStream_t stream) {
+cudaError_t launch_i4_attend_t(const I4Params &p, const I4Maps &maps, int nt, int sms, cudaStream_t stream) {
 #define GQAW_I4_D(D)                                                                      \
-  return nt == 1   ? launch_i4_attend_one<T, D, 1, QP>(p, sms, stream)                    \
-         : nt == 2 ? launch_i4_attend_one<T, D, 2, QP>(p, sms, stream)                    \
-                   : launch_i4_attend_one<T, D, D == 256 ? 2 : 4, QP>(p, sms, stream)
+  return nt == 1   ? launch_i4_attend_one<T, D, 1, QP>(p, maps, sms, stream)              \
+         : nt == 2 ? launch_i4_attend_one<T, D, 2, QP>(p, maps, sms, stream)              \
+                   : launch_i4_attend_one<T, D, D == 256 ? 2 : 4, QP>(p, maps, sms, stream)
   switch (p.D) {
     case 32: GQAW_I4_D(32);
     case 64: GQAW_I4_D(64);
