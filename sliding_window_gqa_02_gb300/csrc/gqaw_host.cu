@@ -526,15 +526,14 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// A tensor map, of bf16 and with 128-byte swizzle by default; dims/box innermost first, strides in bytes.
+// A bf16 tensor map with 128-byte swizzle; dims/box innermost first, strides in bytes.
 bool encode_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                const cuuint32_t *box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                const cuuint32_t *box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -653,14 +652,6 @@ bool encode_tensor_map(CUtensorMap *m, const void *base, int rank, const cuuint6
                        const cuuint32_t *box, bool bf16) {
   return encode_map(m, base, rank, dims, strides, box,
                     bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
-}
-// Rows of bytes (16, 32, 64 or 128), whose 16-byte parts are exchanged over as many bytes as a row has.
-bool encode_byte_map(CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
-  return encode_map(m, base, 4, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                    box[0] == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                    : box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                    : box[0] == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
-                                   : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 bool workspace_tickets_need_clear(const void *ws, size_t t0, size_t t1) { return tickets_need_clear(ws, t0, t1); }
 

@@ -6,7 +6,6 @@
 #pragma once
 
 #include "gqaw_paged.cuh"
-#include "gqaw_tc.cuh"
 
 namespace gqaw {
 
@@ -17,14 +16,11 @@ struct I4Params : PagedParams {
   long long tp, th, tr;         // elements between pages, heads, rows of scales
   void *ko, *vo;                // read: rows out, either may be NULL
   long long kos, vos;
-  int box;                      // attention: rows of a TMA box, 0: rows one by one
-  uint32_t div_mul;             // j / page = j div_mul >> div_shift, for j < 2^31
+  // attention: rows of the cache by 16 bytes of codes and one row's scales
+  uint32_t sp16, sr16, tpg, trg;  // strides of pages and rows, in 16 bytes and in rows of scales
+  int share;                      // a power of two: of the copies of a tile so many in a row have one page
+  uint32_t div_mul;               // j / page = j div_mul >> div_shift, for j < 2^31
   int div_shift;
-};
-
-struct I4Maps {
-  CUtensorMap k;  // key codes (pages, kv heads, rows, D / 2 bytes): box (D / 2, box rows, 1, 1)
-  CUtensorMap v;  // value codes
 };
 
 // Where position j of sequence b lies: page and row in it; page -1 when its entry is bad.

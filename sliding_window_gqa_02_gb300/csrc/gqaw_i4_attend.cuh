@@ -16,21 +16,23 @@
 //     cycles of an SM, is 2.4 times what the memory feeds;
 //   - z = sum over groups g of s_g (sum_d c_d q_d - 8 sum_d q_d): the scale multiplies a group's sum in fp32,
 //     and the sum of the queries is where the accumulator starts;
-//   - the values are (c - 8) s in fp16, which holds them exactly: 1024 + c by an OR, c - 8 by a sum, and
-//     a lane's dimensions (16 of 128) share a scale.  (The 8 does not wait for the end as with the keys: 8
-//     sum p s beside a small result would take its last bits.)
+//   - the values are (c - 8) s in fp16: a nibble in the upper bits of the mantissa of 16 is 16 + c, and
+//     (16 + c) s - 24 s one multiply-add, exact since 24 s is a number of fp16 (1032 s, of a nibble in the
+//     lower bits, is not); a lane's dimensions (16 of 128) share a scale.  (The 8 does not wait for the
+//     end as with the keys: 8 sum p s beside a small result would take its last bits.)
 //
 // Queries come as one or two parts of fp16 (QP; fp32, or turned bf16: two), after a power of two per
 // row that puts the largest element at 2^13; weights as one part, or two for fp32 (PP).  A weight is at
 // most 2^15, since the row's reference moves when that is exceeded (and then puts the largest at 2^13); a
-// value scale is taken relative to the largest power of two of its group so far, which becomes 2^11: no
-// product leaves fp16, and whatever the scales' size none is lost beside 2^-36.  Sums and statistics are
+// value scale is taken relative to the largest power of two of its group so far, which becomes 2^10: no
+// product leaves fp16, and whatever the scales' size none is lost beside 2^-35.  Sums and statistics are
 // fp32.
 //
 // Each warp works on its own, on tiles of 32 keys through a ring of its own; no barrier of the CTA
-// falls inside a unit.  Tiles come by tensor TMA through the page table (codes, swizzled) and bulk copies
-// (scales), or row by row with cp.async where pages or strides do not allow that.  A unit's first tiles
-// are under way before the last unit's rows go out.  Schedule, splits and merges: gqaw_paged.cuh.
+// falls inside a unit.  Tiles come by cp.async through the page table, any page size and strides: with
+// pages of 16 rows a tile by tensor TMA and bulk copies is eight copies, whose operands cost 300
+// instructions, and their own loads in place of these 80.  A unit's first tiles are under way before the
+// last unit's rows go out.  Schedule, splits and merges: gqaw_paged.cuh.
 //
 // Which of 8 rows is which: position x of 8 is key kappa(x) of a tile's, chosen so that the rows of
 // the even positions lie in different banks when four lanes read their dimensions of them.
@@ -40,6 +42,12 @@
 #pragma once
 
 #include <atomic>
+#ifndef GQAW_W
+#define GQAW_W 12
+#endif
+#ifndef GQAW_SB
+#define GQAW_SB 2
+#endif
 
 #include "gqaw_i4.cuh"
 #include "gqaw_paged_tc.cuh"
@@ -49,10 +57,10 @@ namespace gqaw {
 namespace i4a {
 
 constexpr int kKeys = 32;      // a warp's tile
-constexpr int kUnitCost = 24;  // see gqaw_paged_sched.cuh
+constexpr int kUnitCost = 32, kMergeCost = 32, kMinTiles = 12;  // see gqaw_paged_sched.cuh
 constexpr float kTopP = 13.f;  // log2 of the largest weight when the reference moves
 constexpr float kMaxP = 15.f;  // ... and of any
-constexpr int kTopV = 11;      // a scale's largest power of two becomes 2^kTopV
+constexpr int kTopV = 10;      // a scale's largest power of two becomes 2^kTopV: 24 s < 2^16
 
 template <int D, int NT, int QP>
 struct Lay {
@@ -62,14 +70,15 @@ struct Lay {
   static constexpr int kCodes = kKeys * kRow;            // of a tile
   static constexpr int kScales = kKeys * G * 2;
   static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V, their scales; a multiple of the swizzle's span
-  static constexpr int W = D <= 128 && NT == 1 ? 12 : 8;
-  static constexpr int S = D == 32 ? 8 : D == 64 ? 6 : D == 128 ? (W == 12 ? 3 : 4) : 2;
+  static constexpr int W = NT > 1 || D == 256 ? 8 : GQAW_W;
+  static constexpr int kFit = 170 * 1024 / (W * kStage), S = kFit > 8 ? 8 : kFit;  // stages
+  static_assert(S >= 2, "a tile under way beside the one at hand");
   static constexpr int kThreads = 32 * W;
   static constexpr int PS = D + 4;                       // a row of a warp's state: D sums, reference, sum of weights
   static constexpr bool kAhead = R * PS * 4 <= kStage;   // the state takes one stage's place, the next unit's tiles the others'
   static constexpr int kRing = S * kStage > R * PS * 4 ? S * kStage : (R * PS * 4 + 1023) / 1024 * 1024;
   static constexpr int kNorm = W * kRing;                // per warp: scales as the products take them
-  static constexpr int kNormBytes = kKeys * G * 6;       // keys' in fp32, values' in fp16
+  static constexpr int kNormBytes = (kKeys * G * 6 + G * 8 + 15) / 16 * 16;  // keys' in fp32, values' in fp16; their factors, powers of two seen
   static constexpr int kQ = kNorm + W * kNormBytes;      // query operands [QP][NT][2 G][32 lanes] of 8 bytes
   static constexpr int kQsum = kQ + QP * NT * 2 * G * 32 * 8;  // [G][R] fp32: where accumulators start
   static constexpr int kQexp = kQsum + R * G * 4;        // [R]: power of two of a row
@@ -86,7 +95,7 @@ __device__ __forceinline__ int kappa(int x) {
   return x;
 }
 
-// Where 16-byte part `part` of row r's codes lies in a tile: as the TMA's swizzle exchanges the parts.
+// Where 16-byte part `part` of row r's codes lies in a tile: parts are exchanged so that neighbours in the use lie in different banks.
 template <int D>
 __device__ __forceinline__ int at_part(int r, int part) {
   const int x = D == 256 ? r & 7 : D == 128 ? (r >> 1) & 3 : D == 64 ? (r >> 2) & 1 : 0;
@@ -177,11 +186,6 @@ __device__ __forceinline__ void cp_async(void *dst, const void *src, bool ok) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N), "r"(n) : "memory");
 }
-// This thread's arrival on `bar` when its copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // A unit, as one thread prepares it for all warps.
 struct Unit {
   int b, row0, ntok;           // sequence, first row of query / output, tokens
@@ -191,6 +195,9 @@ struct Unit {
   uint32_t qpos, jlo, jhi;     // position of the first token; positions that some row attends
   int cut, cf, cl;             // is the unit cut, and the first and last CTA with a part of it
   int more;                    // is this a unit?
+  const unsigned char *codes;  // the kv head's key codes; values' lie `values` bytes on
+  const uint16_t *scales;      // the same of scales
+  long long values, value_scales;
   template <typename Walk>
   __device__ inline void take(const I4Params &p, const PShape &shp, Walk &walk) {
     PUnit u;
@@ -204,6 +211,10 @@ struct Unit {
     h0 = kvh * p.group + hb * p.gb;
     g = min(p.gb, p.group - hb * p.gb);
     rows = ntok * g;
+    codes = static_cast<const unsigned char *>(p.kp) + kvh * p.sh;
+    values = static_cast<const unsigned char *>(p.vp) - static_cast<const unsigned char *>(p.kp);
+    scales = p.kscale + kvh * p.th;
+    value_scales = p.vscale - p.kscale;
     t0 = u.kt + u.k0;
     tiles = u.k1 - u.k0;
     const long long lo = p.W > 0 && u.qpos - p.W + 1 > 0 ? u.qpos - p.W + 1 : 0, hi = u.qpos + u.ntok;
@@ -224,16 +235,16 @@ struct Unit {
 // NT: operands of 8 query rows.  T: type of the rows outside the cache.
 template <typename T, int D, int NT, int QP>
 __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
-    i4_attend_kernel(const I4Params p, const __grid_constant__ I4Maps maps) {
+    i4_attend_kernel(const __grid_constant__ I4Params p) {
   using namespace i4a;
   using L = Lay<D, NT, QP>;
   constexpr int W = L::W, S = L::S, G = L::G, R = L::R, PS = L::PS;
   constexpr int PP = sizeof(T) == 4 ? 2 : 1;         // parts of a weight
   constexpr bool kQreg = NT * QP * G <= 8;           // query operands in registers
-  constexpr int SB = NT == 1 ? 2 : 1;                // blocks of 16 keys at once
+  constexpr int SB = NT == 1 ? GQAW_SB : 1;                // blocks of 16 keys at once
   constexpr int VW = D >= 64 ? D / 64 : 1;           // words of a lane's codes of a value row (D = 32: half of one)
   constexpr int VT = D / 16;                         // operands of 16 dimensions
-  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kTop = 0x03c003c0u;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PSched sched;
@@ -242,94 +253,93 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   unsigned char *ring = smem + warp * L::kRing;
   float *nk = reinterpret_cast<float *>(smem + L::kNorm + warp * L::kNormBytes);  // [G / 4][position][4]
   uint16_t *nv = reinterpret_cast<uint16_t *>(nk + kKeys * G);                    // [G][position]
+  float *vf = reinterpret_cast<float *>(nv + kKeys * G);  // of each group: the factor that takes the largest scale's power of two to 2^kTopV
+  uint32_t *thr = reinterpret_cast<uint32_t *>(vf + G);   // ... the largest scale (bf16 bits) of that power of two, two groups a word
   const uint2 *sq = reinterpret_cast<const uint2 *>(smem + L::kQ);
   float *sqsum = reinterpret_cast<float *>(smem + L::kQsum);
   int *sqexp = reinterpret_cast<int *>(smem + L::kQexp);
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars) + warp * S;      // this warp's stages
-  const bool tma = p.box > 0;
-  const int box = tma ? min(p.box, kKeys) : 1, nbox = kKeys / box;
-  if (tid == 0 && tma) {
-    ptc::prefetch_map(&maps.k);
-    ptc::prefetch_map(&maps.v);
-  }
-  if (lane == 0) {
-    for (int i = 0; i < S; ++i) mbar_init(&full[i], tma ? 1 : 32);
-    mbar_fence_init();
-  }
-  __syncwarp();
   pdl_wait();
-  const PShape shp = shape_of(p, kUnitCost);
+  PShape shp = shape_of(p, kUnitCost);
+  shp.merge_tiles = kMergeCost;
+  shp.min_tiles = kMinTiles;
   sched_build<kKeys>(p, shp, &sched);
   __shared__ Unit units[3];  // the unit at hand, the next and the one behind it
-  const uint64_t pol = policy_evict_first();
   const int my_group = gid * (D / 8) / kI4Group;  // of this lane's dimensions, gid D / 8 and on
-  bool fine = true;  // no wait of this warp has expired
 
-  // lane b < nbox looks up box b of key tile t: -2 when no row attends any of its keys
-  auto look_up = [&](const Unit &x, int t, int end) {
-    const uint32_t j = (uint32_t)t * kKeys + lane * box;
-    return t < end && lane < nbox && j < x.jhi && j + box > x.jlo
-               ? p.table[(long long)x.b * p.width + (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift)] : -2;
+  // A copy of the warp has 16 bytes of codes a lane: CPR lanes a row, RPC rows, CPR copies a tile.
+  constexpr int CPR = D / 32, RPC = 32 / CPR;
+  const int crow = lane / CPR, cpart = lane % CPR, share = p.share;
+  const uint32_t box = p.page % RPC == 0 ? share * RPC : 1, box_row = box == 1 ? crow : 0;  // rows with one page
+  auto page_of = [&](uint32_t j) { return (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift); };
+  // the pages of the rows that this lane copies of key tile t, and that of key `lane` for its scales: -2
+  // where no row attends them
+  struct Ids {
+    int row[CPR], key;
   };
-  // key tile t into stage st
-  auto load = [&](const Unit &x, int t, int end, int st, int id) {
-    if (t >= end) return;  // uniform over the warp
-    unsigned char *kb = ring + st * L::kStage, *sb = kb + 2 * L::kCodes;
-    const uint32_t j = (uint32_t)t * kKeys + lane * box;
-    const int row = (int)(j - (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift) * p.page);
-    const bool ok = id != -2 && (unsigned)id < (unsigned)p.npages;
-    if (id != -2 && !ok) pflag(p, GQAW_DEV_BAD_PAGE);
-    if (tma) {
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * box * (2 * L::kRow + 4 * G)));
-#pragma unroll 1
-      for (int b = 0; b < nbox; ++b) {
-        const int pid = __shfl_sync(0xffffffffu, id, b), r = __shfl_sync(0xffffffffu, row, b);
-        if (lane == 0 && ((mask >> b) & 1u)) {
-          ptc::tma_load_4d(kb + b * box * L::kRow, &maps.k, 0, r, x.kvh, pid, &full[st], pol);
-          ptc::tma_load_4d(kb + L::kCodes + b * box * L::kRow, &maps.v, 0, r, x.kvh, pid, &full[st], pol);
-          const long long soff = pid * p.tp + x.kvh * p.th + (long long)r * G;
-          bulk_g2s(sb + b * box * 2 * G, p.kscale + soff, (uint32_t)(box * 2 * G), &full[st], pol);
-          bulk_g2s(sb + L::kScales + b * box * 2 * G, p.vscale + soff, (uint32_t)(box * 2 * G), &full[st], pol);
-        }
+  auto look_up = [&](const Unit &x, int t, int end, Ids &ids) {
+    const int32_t *table = p.table + (long long)x.b * p.width;
+    const uint32_t j0 = (uint32_t)t * kKeys;
+#pragma unroll
+    for (int c = 0; c < CPR; ++c) {
+      if ((c & (share - 1)) == 0) {
+        const uint32_t j = j0 + c * RPC + box_row;
+        ids.row[c] = t < end && j < x.jhi && j + box > x.jlo ? table[page_of(j)] : -2;
       }
-    } else {  // a lane has a key's row; those that are not needed become zeros
-      constexpr int CPR = D / 32;  // 16-byte parts of a row
-      const long long off = ok ? id * p.sp + x.kvh * p.sh + row * p.sr : -1;
-      const long long soff = ok ? id * p.tp + x.kvh * p.th + row * p.tr : 0;
-#pragma unroll 1
-      for (int c0 = 0; c0 < CPR; ++c0) {
-        const int c = c0 * 32 + lane, r = c / CPR, part = c % CPR;
-        const long long o = __shfl_sync(0xffffffffu, off, r);
-        const unsigned char *k = static_cast<const unsigned char *>(p.kp) + (o >= 0 ? o : 0) + part * 16;
-        const unsigned char *v = static_cast<const unsigned char *>(p.vp) + (o >= 0 ? o : 0) + part * 16;
-        cp_async<16>(kb + at_part<D>(r, part), k, o >= 0);
-        cp_async<16>(kb + L::kCodes + at_part<D>(r, part), v, o >= 0);
-      }
-      if constexpr (G >= 2) {
-        cp_async<2 * G>(sb + lane * 2 * G, p.kscale + soff, ok);
-        cp_async<2 * G>(sb + L::kScales + lane * 2 * G, p.vscale + soff, ok);
-      } else {  // two bytes: too few for a copy
-        reinterpret_cast<uint16_t *>(sb)[lane] = ok ? p.kscale[soff] : (uint16_t)0;
-        reinterpret_cast<uint16_t *>(sb + L::kScales)[lane] = ok ? p.vscale[soff] : (uint16_t)0;
-      }
-      cp_async_arrive(&full[st]);
     }
+    ids.key = t < end && j0 + lane < x.jhi && j0 + lane >= x.jlo ? table[page_of(j0 + lane)] : -2;
+  };
+  // key tile t into stage st; rows that nobody needs become zeros
+  auto load = [&](const Unit &x, int t, int end, int st, const Ids &ids) {
+    if (t < end) {  // uniform over the warp
+      unsigned char *kb = ring + st * L::kStage, *sb = kb + 2 * L::kCodes;
+      const uint32_t j0 = (uint32_t)t * kKeys;
+      const bool whole = j0 >= x.jlo && j0 + kKeys <= x.jhi;
+      const unsigned char *at = nullptr;
+      bool ok = false;
+      unsigned char *dst = kb + at_part<D>(crow, cpart);
+#pragma unroll
+      for (int c = 0; c < CPR; ++c) {
+        const uint32_t j = j0 + c * RPC + crow;
+        if ((c & (share - 1)) == 0) {
+          const int id = ids.row[c];
+          ok = (unsigned)id < (unsigned)p.npages;
+          if (!ok && id != -2) pflag(p, GQAW_DEV_BAD_PAGE);
+          const uint32_t row = j - page_of(j) * p.page;
+          at = x.codes + (((uint64_t)(uint32_t)(ok ? id : 0) * p.sp16 + (uint64_t)row * p.sr16 + cpart) << 4);
+        } else {
+          at += (uint64_t)p.sr16 * (16 * RPC);
+        }
+        const bool need = ok && (whole || (j >= x.jlo && j < x.jhi));
+        unsigned char *to = D == 256 ? kb + at_part<D>(c * RPC + crow, cpart) : dst + c * RPC * L::kRow;
+        cp_async<16>(to, at, need);
+        cp_async<16>(to + L::kCodes, at + x.values, need);
+      }
+      const bool key_ok = (unsigned)ids.key < (unsigned)p.npages;
+      if (!key_ok && ids.key != -2) pflag(p, GQAW_DEV_BAD_PAGE);
+      const uint32_t j = j0 + lane, row = j - page_of(j) * p.page;
+      const uint16_t *ks = x.scales + ((uint64_t)(uint32_t)(key_ok ? ids.key : 0) * p.tpg + (uint64_t)row * p.trg) * G;
+      if constexpr (G >= 2) {
+        cp_async<2 * G>(sb + lane * 2 * G, ks, key_ok);
+        cp_async<2 * G>(sb + L::kScales + lane * 2 * G, ks + x.value_scales, key_ok);
+      } else {  // two bytes: too few for a copy
+        reinterpret_cast<uint16_t *>(sb)[lane] = key_ok ? *ks : (uint16_t)0;
+        reinterpret_cast<uint16_t *>(sb + L::kScales)[lane] = key_ok ? ks[x.value_scales] : (uint16_t)0;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto bump = [](int st) { return st + 1 == S ? 0 : st + 1; };
-  int id = -2;  // this lane's box of the next tile to load
+  Ids ids;  // of the next tile to load
   auto load_first = [&](const Unit &x, int st) {  // from stage st on
     const int t = x.t0 + warp, end = x.t0 + x.tiles;
-    int ids[S];
-#pragma unroll
-    for (int i = 0; i < S; ++i) ids[i] = look_up(x, t + i * W, end);
-    id = ids[0];
+    look_up(x, t, end, ids);
 #pragma unroll 1
     for (int i = 0; i < S - 1; ++i) {
-      load(x, t + i * W, end, st, id);
+      Ids next;
+      look_up(x, t + (i + 1) * W, end, next);
+      load(x, t + i * W, end, st, ids);
+      ids = next;
       st = bump(st);
-#pragma unroll
-      for (int k = 0; k < S - 1; ++k) id = k == i ? ids[k + 1] : id;
     }
   };
   // one element of every group of row r
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
     if (units[0].more) units[1].take(p, shp, *walk);
   }
   __syncthreads();
-  int st = 0, phase = 0;  // stage of the next tile, and how often the ring has gone round
+  int st = 0;  // stage of the next tile
   if (units[0].more) {
     load_first(units[0], 0);
     for (int r = warp; r < R; r += W) {
@@ -430,14 +440,10 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
       for (int i = 0; i < VT; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
-    // of each group: the largest scale (bf16 bits) of the power of two seen so far, and the factor that
-    // takes that power to 2^kTopV
-    uint32_t thr[(G + 1) / 2];
-    float vf[G], my_vf = pow2(127);
-#pragma unroll
-    for (int i = 0; i < (G + 1) / 2; ++i) thr[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < G; ++i) vf[i] = pow2(127);
+    float my_vf = pow2(127);  // this lane's group's factor
+    if (lane < G) vf[lane] = pow2(127);
+    if (lane < (G + 1) / 2) thr[lane] = 0u;
+    __syncwarp();
     uint32_t marked = 0;  // groups of row `lane` that attend a scale that is not finite
 
     // lane-constant places in a tile: keys' codes of positions gid and gid + 8, 16, 24; values' of this lane's dimensions
@@ -449,11 +455,13 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
 
     for (int t = x.t0 + warp; t < end; t += W) {
       {
-        const int next = look_up(x, t + S * W, end);
-        load(x, t + (S - 1) * W, end, st == 0 ? S - 1 : st - 1, id);
-        id = next;
+        Ids next;
+        look_up(x, t + S * W, end, next);
+        load(x, t + (S - 1) * W, end, st == 0 ? S - 1 : st - 1, ids);
+        ids = next;
       }
-      if (!__all_sync(0xffffffffu, fine && mbar_wait(&full[st], phase & 1))) fine = false;
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+      __syncwarp();
       const unsigned char *kb = ring + st * L::kStage, *sb = kb + 2 * L::kCodes;
       const bool inner = t >= in_lo && t < in_hi;
 
@@ -473,8 +481,10 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
           for (int y = 0; y < (G + 1) / 2; ++y) vw[y] = 0u;
         }
         bool above = false, odd = false;
+        uint32_t seen[(G + 1) / 2], fac[G];
+        lds_words(thr, seen);
 #pragma unroll
-        for (int y = 0; y < (G + 1) / 2; ++y) above |= __vmaxu2(vw[y] & 0x7fff7fffu, thr[y]) != thr[y];
+        for (int y = 0; y < (G + 1) / 2; ++y) above |= __vmaxu2(vw[y] & 0x7fff7fffu, seen[y]) != seen[y];
         if (__any_sync(0xffffffffu, above)) {
           uint32_t bad = 0;
 #pragma unroll
@@ -491,15 +501,13 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
             uint32_t mx = vw[y] & 0x7fff7fffu;
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            mx = __vmaxu2(mx | 0x007f007fu, thr[y]);
-            thr[y] = mx;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-              if (2 * y + hf < G) vf[2 * y + hf] = pow2(kTopV + 127 - (int)((mx >> (16 * hf + 7)) & 0xffu));
+            mx = __vmaxu2(mx | 0x007f007fu, seen[y]);
+            __syncwarp();
+            if (lane == 0) thr[y] = mx;
+            if (lane < 2 && 2 * y + lane < G) vf[2 * y + lane] = pow2(kTopV + 127 - (int)((mx >> (16 * lane + 7)) & 0xffu));
           }
-          float f = vf[0];
-#pragma unroll
-          for (int gr = 1; gr < G; ++gr) f = my_group == gr ? vf[gr] : f;
+          __syncwarp();
+          const float f = vf[my_group];
           const float down = f / my_vf;
           my_vf = f;
 #pragma unroll
@@ -517,12 +525,13 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
             if (lane < rows && j <= at && (p.W == 0 || j > at - p.W)) marked |= groups;
           }
         }
+        lds_words(vf, fac);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
           const uint32_t ka = gr & 1 ? kw[gr / 2] & 0xffff0000u : kw[gr / 2] << 16;
           const uint32_t va = gr & 1 ? vw[gr / 2] & 0xffff0000u : vw[gr / 2] << 16;
           nk[(gr / 4) * (kKeys * 4) + lane * (G < 4 ? G : 4) + gr % 4] = __uint_as_float(ka) * sfac;
-          nv[gr * kKeys + lane] = __half_as_ushort(__float2half_rn(__uint_as_float(va) * vf[gr]));
+          nv[gr * kKeys + lane] = __half_as_ushort(__float2half_rn(__uint_as_float(va) * __uint_as_float(fac[gr])));
         }
       }
       __syncwarp();
@@ -659,6 +668,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
           const int pos = (b0 + b) * 16 + 2 * t4;
           const uint32_t sa = *reinterpret_cast<const uint32_t *>(nv + my_group * kKeys + pos);
           const uint32_t sc = *reinterpret_cast<const uint32_t *>(nv + my_group * kKeys + pos + 8);
+          const uint32_t na = hmul2(sa, 0xce00ce00u), nc = hmul2(sc, 0xce00ce00u);  // -24 s
           uint32_t w[4][VW];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -676,12 +686,11 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
               const uint32_t xa = __byte_perm(w[0][y], w[1][y], hf ? 0x7632 : 0x5410), xb = __byte_perm(w[2][y], w[3][y], hf ? 0x7632 : 0x5410);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint32_t a = k ? xa >> 8 : xa, c = k ? xb >> 8 : xb;
-                // (1024 + c) - 1032 and (1024 + 16 c) / 16 - 72: c - 8, then times its scale
-                const uint32_t v0 = hmul2(hadd2(and_or(a, kLow, 0x64006400u), 0xe408e408u), sa);
-                const uint32_t v1 = hmul2(hfma2(and_or(a, kHigh, 0x64006400u), 0x2c002c00u, 0xd480d480u), sa);
-                const uint32_t v2 = hmul2(hadd2(and_or(c, kLow, 0x64006400u), 0xe408e408u), sc);
-                const uint32_t v3 = hmul2(hfma2(and_or(c, kHigh, 0x64006400u), 0x2c002c00u, 0xd480d480u), sc);
+                // a nibble in the upper bits of the mantissa of 16: 16 + c, times the scale, less 24 of it
+                const uint32_t v0 = hfma2(and_or(k ? xa >> 2 : xa << 6, kTop, 0x4c004c00u), sa, na);
+                const uint32_t v1 = hfma2(and_or(k ? xa >> 6 : xa << 2, kTop, 0x4c004c00u), sa, na);
+                const uint32_t v2 = hfma2(and_or(k ? xb >> 2 : xb << 6, kTop, 0x4c004c00u), sc, nc);
+                const uint32_t v3 = hfma2(and_or(k ? xb >> 6 : xb << 2, kTop, 0x4c004c00u), sc, nc);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -695,7 +704,6 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
       }
       __syncwarp();  // the stage and the scales are free
       st = bump(st);
-      phase += st == 0;
     }
 
     // ---- the next unit's tiles and queries are on their way while this one's rows go out
@@ -798,25 +806,15 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
         if (tid == 0) p.tickets[cf] = 0u;
       }
     }
-    // the states were written by ordinary stores where the next tiles may land by TMA
-    tc::fence_proxy_async_smem();
     __syncthreads();
     if (!L::kAhead && more) load_first(nx, st);
     un = un == 2 ? 0 : un + 1;
-  }
-  // every load that was issued has been waited for, unless a wait expired
-  if (!fine) {
-    if (lane == 0) {
-      pflag(p, GQAW_DEV_TIMEOUT);
-      const int n = phase * S + st;  // tiles in all
-      for (int i = n > S ? n - S : 0; i < n; ++i) mbar_wait(&full[i % S], (i / S) & 1);
-    }
   }
   pdl_launch_dependents();
 }
 
 template <typename T, int D, int NT, int QP>
-cudaError_t launch_i4_attend_one(const I4Params &p, const I4Maps &maps, int sms, cudaStream_t stream) {
+cudaError_t launch_i4_attend_one(const I4Params &p, int sms, cudaStream_t stream) {
   using L = i4a::Lay<D, NT, QP>;
   constexpr int kMaxDevices = 64;
   static std::atomic<bool> ready[kMaxDevices];
@@ -838,17 +836,17 @@ cudaError_t launch_i4_attend_one(const I4Params &p, const I4Maps &maps, int sms,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, i4_attend_kernel<T, D, NT, QP>, p, maps);
+  e = cudaLaunchKernelEx(&cfg, i4_attend_kernel<T, D, NT, QP>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // nt: 1, 2 or 4 (head size 256: 1 or 2) operands of 8 rows.
 template <typename T, int QP>
-cudaError_t launch_i4_attend_t(const I4Params &p, const I4Maps &maps, int nt, int sms, cudaStream_t stream) {
+cudaError_t launch_i4_attend_t(const I4Params &p, int nt, int sms, cudaStream_t stream) {
 #define GQAW_I4_D(D)                                                                      \
-  return nt == 1   ? launch_i4_attend_one<T, D, 1, QP>(p, maps, sms, stream)              \
-         : nt == 2 ? launch_i4_attend_one<T, D, 2, QP>(p, maps, sms, stream)              \
-                   : launch_i4_attend_one<T, D, D == 256 ? 2 : 4, QP>(p, maps, sms, stream)
+  return nt == 1   ? launch_i4_attend_one<T, D, 1, QP>(p, sms, stream)              \
+         : nt == 2 ? launch_i4_attend_one<T, D, 2, QP>(p, sms, stream)              \
+                   : launch_i4_attend_one<T, D, D == 256 ? 2 : 4, QP>(p, sms, stream)
   switch (p.D) {
     case 32: GQAW_I4_D(32);
     case 64: GQAW_I4_D(64);

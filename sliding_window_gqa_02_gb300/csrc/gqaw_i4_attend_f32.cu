@@ -3,8 +3,8 @@
 
 namespace gqaw {
 
-cudaError_t launch_i4_attend_f32(const I4Params &p, const I4Maps &maps, int nt, int sms, cudaStream_t stream) {
-  return launch_i4_attend_t<float, 2>(p, maps, nt, sms, stream);
+cudaError_t launch_i4_attend_f32(const I4Params &p, int nt, int sms, cudaStream_t stream) {
+  return launch_i4_attend_t<float, 2>(p, nt, sms, stream);
 }
 
 }  // namespace gqaw

@@ -3,8 +3,8 @@
 
 namespace gqaw {
 
-cudaError_t launch_i4_attend_split(const I4Params &p, const I4Maps &maps, int nt, int sms, cudaStream_t stream) {
-  return launch_i4_attend_t<__nv_bfloat16, 2>(p, maps, nt, sms, stream);
+cudaError_t launch_i4_attend_split(const I4Params &p, int nt, int sms, cudaStream_t stream) {
+  return launch_i4_attend_t<__nv_bfloat16, 2>(p, nt, sms, stream);
 }
 
 }  // namespace gqaw

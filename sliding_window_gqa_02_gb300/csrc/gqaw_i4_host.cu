@@ -5,10 +5,9 @@
 
 namespace gqaw {
 cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read, bool bf16, cudaStream_t stream);
-bool encode_byte_map(CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box);
-cudaError_t launch_i4_attend_bf16(const I4Params &p, const I4Maps &maps, int nt, int sms, cudaStream_t stream);
-cudaError_t launch_i4_attend_split(const I4Params &p, const I4Maps &maps, int nt, int sms, cudaStream_t stream);
-cudaError_t launch_i4_attend_f32(const I4Params &p, const I4Maps &maps, int nt, int sms, cudaStream_t stream);
+cudaError_t launch_i4_attend_bf16(const I4Params &p, int nt, int sms, cudaStream_t stream);
+cudaError_t launch_i4_attend_split(const I4Params &p, int nt, int sms, cudaStream_t stream);
+cudaError_t launch_i4_attend_f32(const I4Params &p, int nt, int sms, cudaStream_t stream);
 }  // namespace gqaw
 
 namespace {
@@ -39,7 +38,7 @@ gqaw_status page_strides(const char *what, int64_t page, int64_t head, int64_t r
     *sr = rows;
     for (long long x : {*sp, *sh, *sr}) {
       if (x < row) return fail(GQAW_EINVAL, "the page, head and row strides of the %s: all 0, or each at least %lld", what, row);
-      if (x > kMaxStride) return fail(GQAW_EUNSUPPORTED, "a stride of the %s of %lld is too large", what, x);
+      if (x / unit >= 1ll << 32) return fail(GQAW_EUNSUPPORTED, "a stride of the %s of %lld is too large", what, x);
       if (x % unit != 0) return fail(GQAW_EINVAL, "a stride of the %s of %lld is not a multiple of %lld", what, x, unit);
     }
     // no two rows share a byte: heads within rows, or rows within heads, inside a page
@@ -48,6 +47,7 @@ gqaw_status page_strides(const char *what, int64_t page, int64_t head, int64_t r
     const bool heads_inside = *sr >= of_row && *sp >= reach(r, *sr, of_row);
     if (!rows_inside && !heads_inside) return fail(GQAW_EINVAL, "the strides make rows of the %s overlap", what);
   }
+  if (*sp / unit >= 1ll << 32) return fail(GQAW_EUNSUPPORTED, "a page of the %s of %lld is too large", what, *sp);
   if (reach(a->num_pages, *sp, reach(a->kv_num_heads, *sh, reach(a->page_size, *sr, row))) == kMaxElements)
     return fail(GQAW_EUNSUPPORTED, "the %s reach over 2^48 elements or more", what);
   return GQAW_OK;
@@ -201,32 +201,23 @@ gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cu
     const cudaError_t e = cudaMemsetAsync(p.tickets, 0, gqaw::kPagedTickets * 4, st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync (tickets)");
   }
-  // Codes by tensor TMA and scales by bulk copies where pages tile 32 keys in boxes of at least 8 rows,
-  // a row's scales follow the last one's, and everything starts on 16 bytes.
-  gqaw::I4Maps maps;
-  std::memset(&maps, 0, sizeof(maps));
   const long long D = a->head_size;
-  const bool tiled = a->num_pages > 0 && a->page_size % 8 == 0 && (32 % a->page_size == 0 || a->page_size % 32 == 0) &&
-                     std::max(L.sp, std::max(L.sh, L.sr)) < (1ll << 40) && L.tr == D / gqaw::kI4Group && L.th % 8 == 0 &&
-                     L.tp % 8 == 0 && aligned(p.kscale, 16) && aligned(p.vscale, 16);
-  p.box = 0;
+  p.sp16 = (uint32_t)(L.sp / 16);
+  p.sr16 = (uint32_t)(L.sr / 16);
+  p.tpg = (uint32_t)(L.tp / (D / gqaw::kI4Group));
+  p.trg = (uint32_t)(L.tr / (D / gqaw::kI4Group));
+  // a copy of the whole warp has 1024 / D rows, a tile of 32 keys D / 32 copies
+  p.share = 1;
+  while (p.share < D / 32 && a->page_size % (1024 / D * p.share * 2) == 0) p.share *= 2;
   // ceil(2^(31 + l) / page) with 2^l >= page: its excess over the quotient, below 1, times j stays below 2^31 (Granlund, Montgomery)
   int l = 0;
   while ((1ll << l) < a->page_size) ++l;
   p.div_shift = 31 + l;
   p.div_mul = (uint32_t)(((unsigned __int128)1 << (31 + l)) / a->page_size + (((unsigned __int128)1 << (31 + l)) % a->page_size != 0));
-  if (tiled) {
-    p.box = std::min(a->page_size, 32);
-    const cuuint64_t dims[4] = {(cuuint64_t)D / 2, (cuuint64_t)a->page_size, (cuuint64_t)a->kv_num_heads, (cuuint64_t)a->num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)L.sr, (cuuint64_t)L.sh, (cuuint64_t)L.sp};
-    const cuuint32_t box[4] = {(cuuint32_t)D / 2, (cuuint32_t)p.box, 1, 1};
-    if (!gqaw::encode_byte_map(&maps.k, p.kp, dims, strides, box) || !gqaw::encode_byte_map(&maps.v, p.vp, dims, strides, box))
-      return fail(GQAW_ECUDA, "cuTensorMapEncodeTiled failed for the attention over a 4-bit cache");
-  }
   auto launch = [&](const I4Params &x, int nt) {
-    const cudaError_t e = a->dtype == GQAW_F32 ? gqaw::launch_i4_attend_f32(x, maps, nt, kSms, st)
-                          : x.qlo              ? gqaw::launch_i4_attend_split(x, maps, nt, kSms, st)
-                                               : gqaw::launch_i4_attend_bf16(x, maps, nt, kSms, st);
+    const cudaError_t e = a->dtype == GQAW_F32 ? gqaw::launch_i4_attend_f32(x, nt, kSms, st)
+                          : x.qlo              ? gqaw::launch_i4_attend_split(x, nt, kSms, st)
+                                               : gqaw::launch_i4_attend_bf16(x, nt, kSms, st);
     if (e == cudaSuccess) gqaw::count_launch();
     return e;
   };

@@ -16,7 +16,7 @@
 //     boundary cuts is finished by the last of its contributors, through partial results and a
 //     ticket; or
 //   - whole: CTA c takes unit c alone, when the units fit in the grid and the longest costs no
-//     more than an equal share plus kMergeTiles, what a cut costs (a merge is a chain of
+//     more than an equal share plus `merge_tiles`, what a cut costs (a merge is a chain of
 //     dependent memory round trips).
 // The ticket of a cut unit is indexed by the CTA it starts in (at most one unit leaves a CTA
 // at its end), so the tickets have a fixed place whatever the shapes.
@@ -101,8 +101,12 @@ GQAW_HD int find_sequence(const PBatch &p, int n) {
 
 // What the schedule needs to know of a call.
 struct PShape {
-  int tpt, W, heads;  // tokens per query tile; window (0: none); kv heads x head blocks
-  int unit_cost;      // key tiles that a unit costs beside its own
+  int tpt, W, heads;    // tokens per query tile; window (0: none); kv heads x head blocks
+  int unit_cost;        // key tiles that a unit costs beside its own
+  int merge_tiles = 7;  // ... and what a cut costs
+  // At least so many tiles a CTA: a cut costs more than it saves below that (one sequence of 1000
+  // keys and 8 kv heads: 11.9 us; at least four a CTA 15.9, one 11.8, but 2000 keys 12.2, 14.3, 13.4)
+  int min_tiles = 2;
 };
 
 // A sequence with new tokens, as the schedule keeps it in shared memory.
@@ -183,8 +187,6 @@ struct PTiles {
   }
 };
 
-constexpr int kMergeTiles = 7;
-
 // The last i in [0, n) with le(i), for le that holds at 0 and, once false, stays false: 32 places
 // at a time, for le may be a chain of divisions.  On the device a whole warp calls it.
 template <typename F>
@@ -205,11 +207,9 @@ GQAW_HD PStart sched_start(const PShape &p, const PSched *s, int cta, int grid) 
   PStart w;
   const long long V = s->V;
   const int heads = p.heads;
-  // at least two tiles a CTA: a cut costs more than it saves below that (one sequence of 1000
-  // keys and 8 kv heads: 11.9 us; at least four a CTA 15.9, one 11.8, but 2000 keys 12.2, 14.3, 13.4)
-  const long long want = s->U > (V + 1) / 2 ? s->U : (V + 1) / 2;
+  const long long most = (V + p.min_tiles - 1) / p.min_tiles, want = s->U > most ? s->U : most;
   w.G = (int)(want < 1 ? 1 : want < grid ? want : grid);
-  w.whole = s->U <= grid && s->longest <= (V + w.G - 1) / w.G + kMergeTiles;
+  w.whole = s->U <= grid && s->longest <= (V + w.G - 1) / w.G + p.merge_tiles;
   w.it = w.hu = w.r = 0;
   w.pos = 0;
   if (w.whole) {

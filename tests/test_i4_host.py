@@ -52,7 +52,9 @@ CALLS = ("gqaw_paged_i4_append", "gqaw_paged_i4_attend", "gqaw_paged_i4_step", "
     (dict(page_stride=2048, head_stride=512, row_stride=40), 1, "multiple of 16"),
     (dict(page_stride=1024, head_stride=496, row_stride=32), 1, "overlap"),
     (dict(page_stride=1 << 41, head_stride=512, row_stride=32), 2, "too large"),
-    (dict(page_stride=1 << 40, head_stride=512, row_stride=32, num_pages=1 << 20), 2, "2^48"),
+    (dict(page_stride=1 << 35, head_stride=512, row_stride=32, num_pages=1 << 20), 2, "2^48"),
+    (dict(page_stride=1 << 36, head_stride=512, row_stride=32), 2, "too large"),
+    (dict(scale_page_stride=1 << 33, scale_head_stride=32, scale_row_stride=2), 2, "too large"),
     (dict(scale_page_stride=64), 1, "scales"),
     (dict(scale_page_stride=64, scale_head_stride=31, scale_row_stride=2), 1, "multiple of 2"),
     (dict(scale_page_stride=64, scale_head_stride=30, scale_row_stride=2), 1, "overlap"),
