@@ -2,9 +2,13 @@
 // argument checks, the choice of kernel, launches.  No allocation and no synchronisation.
 #include "gqaw_i4.cuh"
 #include "gqaw_paged_check.cuh"
+#include "gqaw_paged_tc.cuh"
 
 namespace gqaw {
 cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read, bool bf16, cudaStream_t stream);
+cudaError_t launch_i4_prefill(const I4Params &p, const PagedMaps &maps, int grid, cudaStream_t stream);
+bool encode_tensor_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                       const cuuint32_t *box, bool bf16);
 cudaError_t launch_i4_attend_bf16(const I4Params &p, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_i4_attend_split(const I4Params &p, int nt, int sms, cudaStream_t stream);
 cudaError_t launch_i4_attend_f32(const I4Params &p, int nt, int sms, cudaStream_t stream);
@@ -19,6 +23,7 @@ struct I4Plan : PagedSizes {
   long long sp, sh, sr;          // codes, bytes
   long long tp, th, tr;          // scales, elements
   long long kos, vos;
+  bool prefill;                  // more rows than the kernel of nt takes at once: the prompt kernel
   int nt;                        // operands of 8 query rows
   int few;                       // sequences of at most this many tokens go to the kernel of 8 rows (0: none)
   int gb, hblocks, tpt;
@@ -70,16 +75,20 @@ gqaw_status plan_i4(const gqaw_paged_i4_args *x, I4Plan *L) {
   // most 4 (head size 256: 2), which is what registers hold.
   const long long rows = (long long)std::max(1, a->max_new_tokens) * L->group;
   L->nt = rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
-  L->gb = std::min(L->group, 8 * L->nt);
+  // Beyond that, in bf16 at head sizes 64 and 128, two query tiles of 128 rows on the 5th-generation tensor cores
+  L->prefill = rows > 32 && a->dtype == GQAW_BF16 && (D == 64 || D == 128) && L->group <= 128 &&
+               std::max<long long>(L->qs, a->num_heads * D) * L->es < (1ll << 40);
+  const int tile = L->prefill ? 256 : 8 * L->nt;
+  L->gb = L->prefill ? L->group : std::min(L->group, tile);
   L->hblocks = (int)ceil_div(L->group, L->gb);
-  L->tpt = std::max(1, 8 * L->nt / L->gb);
+  L->tpt = L->prefill ? 2 * (128 / L->group) : std::max(1, tile / L->gb);
   // Single tokens among chunks would fill 8 of the rows: they have a launch of their own where there
   // may be many (the others hold at most max_new_tokens, which bounds their number)
   constexpr int kShort = 64;
   const long long tok = L->nt > 1 && L->group <= 8 ? 8 / L->group : 0;
   const long long spare = (long long)a->total_new_tokens - a->batch_size * tok;
   if (tok && (a->batch_size - (spare > 0 ? ceil_div(spare, a->max_new_tokens) : 0)) * a->kv_num_heads >= kShort) L->few = (int)tok;
-  L->ws_bytes = gqaw::kPagedPartialOffset + align256((size_t)kSms * 2 * 8 * L->nt * (D + 4) * 4);
+  L->ws_bytes = gqaw::kPagedPartialOffset + align256((size_t)kSms * 2 * tile * (D + 4) * 4);
   L->off_q = L->ws_bytes;
   L->ws_bytes += align256((size_t)a->total_new_tokens * a->num_heads * D * L->es);
   L->off_qlo = L->ws_bytes;  // what bf16 leaves of turned queries
@@ -214,6 +223,17 @@ gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cu
   while ((1ll << l) < a->page_size) ++l;
   p.div_shift = 31 + l;
   p.div_mul = (uint32_t)(((unsigned __int128)1 << (31 + l)) / a->page_size + (((unsigned __int128)1 << (31 + l)) % a->page_size != 0));
+  gqaw::PagedMaps maps;
+  if (L.prefill) {  // only the queries come by TMA
+    std::memset(&maps, 0, sizeof(maps));
+    const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a->num_heads, (cuuint64_t)a->total_new_tokens};
+    const cuuint64_t qst[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.qs * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)L.group, (cuuint32_t)(L.tpt / 2)};
+    bool ok = gqaw::encode_tensor_map(&maps.q, p.q, 3, qd, qst, qb, true);
+    maps.ql = maps.q;
+    if (p.qlo) ok = ok && gqaw::encode_tensor_map(&maps.ql, p.qlo, 3, qd, qst, qb, true);
+    if (!ok) return fail(GQAW_ECUDA, "cuTensorMapEncodeTiled failed for the attention over a 4-bit cache");
+  }
   auto launch = [&](const I4Params &x, int nt) {
     const cudaError_t e = a->dtype == GQAW_F32 ? gqaw::launch_i4_attend_f32(x, nt, kSms, st)
                           : x.qlo              ? gqaw::launch_i4_attend_split(x, nt, kSms, st)
@@ -231,7 +251,8 @@ gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cu
     p.gb = L.gb;
     p.hblocks = L.hblocks;
     p.tpt = L.tpt;
-    cudaError_t e = launch(p, L.nt);
+    cudaError_t e = L.prefill ? gqaw::launch_i4_prefill(p, maps, kSms, st) : launch(p, L.nt);
+    if (e == cudaSuccess && L.prefill) gqaw::count_launch();
     if (e == cudaSuccess && L.few) {
       I4Params few = p;
       few.s_lo = 1;

@@ -24,7 +24,7 @@ class Batch:
         g = torch.Generator().manual_seed(seed)
         self.lens, self.Nq, self.Nkv, self.D, self.page, self.dtype = lens, Nq, Nkv, D, page, dtype
         self.window, self.softcap, self.interleaved, self.hir = window, softcap, interleaved, heads_inside_rows
-        self.scale, self.smooth = scale, smooth
+        self.scale, self.smooth, self.odd_scales = scale, smooth, odd_scales
         need = [(t + page - 1) // page for _, t in lens]
         pages = sum(need) + spare_pages
         perm = torch.randperm(pages, generator=g)
@@ -148,7 +148,11 @@ class Batch:
         may count as nothing, and a result below it is rounded to a multiple of bf16's smallest number, 2^-133.
         In fp16 a weight of 1 times the largest scale s of its group (a weight of 1) is at least 2^12 (2^13),
         and what is rounded to a subnormal is off by up to 2^-25: 2^-37 s, times a code of at most 8, where
-        the largest value is at least s or there is none: 2^-34 of it a key."""
+        the largest value is at least s or there is none: 2^-34 of it a key.
+
+        Scales that the append did not write: with more than 32 rows in bf16 every key and value element is
+        rounded once to bf16 (u), the keys' share in a logit like a query's, the values' beside the weights'."""
+        rounds = self.odd_scales and self.dtype == torch.bfloat16 and self.max_new * (self.Nq // self.Nkv) > 32
         if turned:
             q32 = torch.from_numpy(i4.norm_turn(self.q.reshape(-1, self.Nq, self.D), self.qw, 1e-5, self.cos, self.sin,
                                                 self.table_pos(), self.interleaved)).to(self.q.device).double()
@@ -161,10 +165,14 @@ class Batch:
             k, v = (ref.gather(x, self.table[i], t, True) for x in (k_all, v_all))
             q = (q32 if turned else self.q.reshape(-1, self.Nq, self.D).double())[self.rows(i)]
             rounded = (ref.u(self.dtype) ** 2 if turned and self.dtype == torch.bfloat16 else 0.0) + 2.0 ** -22
+            rounded += ref.u(self.dtype) if rounds else 0.0
             want, bound = ref.attend(q, k, v, t - s, self.window, self.scale or 1 / math.sqrt(self.D), self.softcap, sink,
                                      self.dtype, rounded)
             top = torch.nan_to_num(v, nan=0.0, posinf=0.0, neginf=0.0).abs().amax()
             bound = bound + (t + 1) * (2.0 ** -126 * (1 + top) + 2.0 ** -34 * top)
+            if rounds:
+                bound = bound + ref.u(self.dtype) * ref.attend(q, k, v.abs(), t - s, self.window, self.scale or 1 / math.sqrt(self.D),
+                                                               self.softcap, sink, self.dtype)[0]
             got = self.out[self.rows(i)].reshape(s, self.Nq, self.D).double()
             bad = ~torch.isfinite(want)
             assert not (torch.isfinite(got) & bad).any(), "finite output where a visible value is not"
