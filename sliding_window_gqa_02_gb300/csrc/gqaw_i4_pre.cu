@@ -8,7 +8,7 @@ namespace gqaw {
 cudaError_t launch_i4_prefill(const I4Params &p, const PagedMaps &maps, int grid, cudaStream_t stream) {
   static std::atomic<bool> ready[4][kPrefillDevices];
   auto two = [&](auto d, auto split, int i) {
-    return launch_prefill(paged_prefill2_kernel<d.value, split.value, I4Params>, ready[i], ppre::kThreads2,
+    return launch_prefill(paged_prefill2_kernel<d.value, split.value, I4Params>, ready[i], ppre::threads2<I4Params>,
                           ppre::Lay2<d.value, split.value>::kAlloc, p, maps, grid, stream);
   };
   constexpr std::integral_constant<int, 64> d64{};

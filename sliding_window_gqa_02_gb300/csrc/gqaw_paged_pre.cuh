@@ -63,6 +63,8 @@ constexpr int kThreads = kSoft + 96;
 // two query tiles at once
 constexpr int kSoft2 = 256, kThreads2 = kSoft2 + 128;
 constexpr int kMmaWarp2 = 8, kKWarp2 = 9, kVWarp2 = 10;
+template <typename P>
+constexpr int threads2 = std::is_same<P, I4Params>::value ? kSoft2 + 256 : kThreads2;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kUnitCost = 3;   // see gqaw_paged_sched.cuh
 constexpr float kRescaleLog2 = 8.0f;  // log2 units
@@ -760,7 +762,8 @@ struct Lay2 {
   static constexpr int kOdd = kSched + (int)((sizeof(PSched) + 15) / 16 * 16);  // uint32 [buffer][kind][8]
   static constexpr int kMisc = kOdd + kOddBufs * 16 * 4;
   static constexpr int kBars = kMisc + 16;
-  static constexpr int kAlloc = kBars + 40 * 8 + 1024;  // and room to align the base
+  static constexpr int kWalk = kBars + 40 * 8;  // of a cache in 4 bits: the walkers of the warps that write its tiles
+  static constexpr int kAlloc = kWalk + (i4t::kWarps + 1) * (int)sizeof(i4t::Walker) + 1024;  // and room to align the base
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
@@ -788,10 +791,10 @@ __device__ __forceinline__ Halves halves_of(const PagedParams &p, const PUnit &u
 // 384 threads launched with 168 registers; the two softmax warpgroups take 208 and the third gives
 // back to 88: 256 x 208 + 128 x 88 = 384 x 168.
 //
-// P: PagedParams, or I4Params for a cache in 4 bits: then warps 9 to 11 write the tiles (gqaw_i4_tiles.cuh),
-// and warp 9 loads Q.
+// P: PagedParams, or I4Params for a cache in 4 bits: then warps 9 to 15 write the tiles (gqaw_i4_tiles.cuh), and
+// warp 9 loads Q; 512 threads with 128 registers, 2 x 128 x (200 + 56).
 template <int D, bool SPLIT, typename P = PagedParams>
-__global__ void __launch_bounds__(ppre::kThreads2, 1)
+__global__ void __launch_bounds__(ppre::threads2<P>, 1)
     paged_prefill2_kernel(const P p, const __grid_constant__ PagedMaps maps) {
   using namespace ppre;
   using L = Lay2<D, SPLIT>;
@@ -825,9 +828,9 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
       mbar_init(&pv_done[x], 1);
     }
     for (int i = 0; i < L::kSt; ++i) {
-      mbar_init(&k_full[i], kI4 ? i4t::kBatches : 1);
+      mbar_init(&k_full[i], kI4 ? i4t::kBatches<D> : 1);
       mbar_init(&k_free[i], 1);
-      mbar_init(&v_full[i], kI4 ? i4t::kBatches : 1);
+      mbar_init(&v_full[i], kI4 ? i4t::kBatches<D> : 1);
       mbar_init(&v_free[i], 1);
     }
     mbar_fence_init();
@@ -835,7 +838,7 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
     for (int i = 0; i < kOddBufs * 16; ++i) odd[i] = 0u;
   }
   // query rows past a half's tokens stay zero
-  for (int e = tid; e < 2 * QP * L::kTile / 16; e += kThreads2) reinterpret_cast<uint4 *>(smem + L::kQ)[e] = make_uint4(0, 0, 0, 0);
+  for (int e = tid; e < 2 * QP * L::kTile / 16; e += threads2<P>) reinterpret_cast<uint4 *>(smem + L::kQ)[e] = make_uint4(0, 0, 0, 0);
   if (warp == 0) tc::tmem_alloc(tmem_slot, kTmemCols);
   tc::fence_proxy_async_smem();
   pdl_wait();
@@ -848,19 +851,23 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
   const int g = p.group, t1 = p.tpt / 2;
 
   if (warp >= kMmaWarp2) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (kI4)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (kI4 ? warp != kMmaWarp2 : warp == kKWarp2 || warp == kVWarp2) {
       if constexpr (kI4) {
         // ---------------------------------------------------------- tiles out of codes
-        const uint64_t qpol = policy_evict_first();
-        PWalk<kKeys> w(shp, sched);
-        PUnit u;
+        i4t::Walker *const walkers = reinterpret_cast<i4t::Walker *>(smem + L::kWalk);
+        i4t::Walker *const qw = walkers + i4t::kWarps;  // of the queries, lane 0 of warp 9 alone
+        if (warp == kKWarp2 && lane == 0) qw->walk = PWalk<kKeys>(shp, sched);
         int qi = 0;
         // the queries of the next unit, once the last S product with the previous ones is done
         auto queries = [&]() -> bool {
-          if (!w.next(shp, u)) return true;  // cannot happen: the batches follow the same walk
           if (!__all_sync(0xffffffffu, qi == 0 || mbar_wait(q_free, (qi - 1) & 1))) return false;
-          if (lane == 0) {
+          if (lane == 0 && qw->walk.next(shp, qw->u)) {
+            const PUnit &u = qw->u;
+            const uint64_t qpol = policy_evict_first();
             const int parts = u.ntok > t1 ? 2 : 1;
             mbar_arrive_expect_tx(q_full, (uint32_t)(parts * QP * L::HALVES * g * t1 * 128));
             for (int x = 0; x < parts; ++x)
@@ -873,7 +880,8 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
           return true;
         };
         const i4t::Rings rings{smem + L::kK, smem + L::kV, k_full, k_free, v_full, v_free};
-        const bool fine = i4t::convert<D, L::kSt, kHalf>(p, shp, sched, rings, abort_flag, warp - kKWarp2, lane, queries);
+        const bool fine = i4t::convert<D, L::kSt, kHalf>(p, shp, sched, walkers + (warp - kKWarp2), rings, abort_flag, warp - kKWarp2,
+                                                               lane, queries);
         if (lane == 0) {
           if (!fine) {
             pflag(p, GQAW_DEV_TIMEOUT);
@@ -1031,7 +1039,10 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (kI4)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax (warps 0-7)
     const int wq = warp & 3, x = warp >> 2;  // TMEM lane quarter, half
     const int r = wq * 32 + lane;            // row of the half = TMEM lane
@@ -1216,6 +1227,13 @@ __global__ void __launch_bounds__(ppre::kThreads2, 1)
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) v[c] = 0.f;
+          }
+          if constexpr (kI4) {  // the columns as the value tiles hold the dimensions
+            float y[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) y[i4t::value_column(c)] = v[c];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = y[c];
           }
           if (c32 == D / 32 - 1 && a < b) {  // O has left tensor memory: the next unit may overwrite it
             tc::fence_before_sync();
