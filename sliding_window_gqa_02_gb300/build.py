@@ -25,7 +25,7 @@ SOURCES = ["gqaw_host.cu", "gqaw_finish.cu", "gqaw_attend_f32.cu", "gqaw_attend_
            "gqaw_mmad_q8.cu", "gqaw_paged_host.cu", "gqaw_paged_rows.cu", "gqaw_paged_attend_f32.cu",
            "gqaw_paged_attend_bf16.cu", "gqaw_paged_dec.cu", "gqaw_paged_pre.cu", "gqaw_paged_f32.cu",
            "gqaw_i4_host.cu", "gqaw_i4_rows.cu", "gqaw_i4_attend_bf16.cu", "gqaw_i4_attend_split.cu",
-           "gqaw_i4_attend_f32.cu", "gqaw_i4_pre.cu"]
+           "gqaw_i4_attend_f32.cu", "gqaw_i4_pre.cu", "gqaw_i4_expand.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v", "-I", INCLUDE, "-I", CSRC]
 

@@ -7,6 +7,8 @@
 namespace gqaw {
 cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read, bool bf16, cudaStream_t stream);
 cudaError_t launch_i4_prefill(const I4Params &p, const PagedMaps &maps, int grid, cudaStream_t stream);
+cudaError_t launch_i4_expand(const I4Params &p, void *k, void *v, int32_t *table, int width, int pages, int sms, cudaStream_t stream);
+cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, int halves, int grid, cudaStream_t stream);
 bool encode_tensor_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                        const cuuint32_t *box, bool bf16);
 cudaError_t launch_i4_attend_bf16(const I4Params &p, int nt, int sms, cudaStream_t stream);
@@ -19,15 +21,21 @@ namespace {
 using gqaw::I4Params;
 using namespace gqaw::pcheck;
 
+// The attention's kernels: up to 8 nt query rows of a kv head at once; the bf16 prompt kernel with tiles written
+// from codes; the same over bf16 pages that a pass before it expands.
+enum I4Path { kRows = 0, kTiles = 1, kExpand = 2 };
+
 struct I4Plan : PagedSizes {
   long long sp, sh, sr;          // codes, bytes
   long long tp, th, tr;          // scales, elements
   long long kos, vos;
-  bool prefill;                  // more rows than the kernel of nt takes at once: the prompt kernel
+  int path;
+  int halves;                    // kExpand, kTiles: query tiles of 128 rows at once
+  int pages, width;              // kExpand: pages of 128 rows in the workspace, and entries of a row of their table
   int nt;                        // operands of 8 query rows
   int few;                       // sequences of at most this many tokens go to the kernel of 8 rows (0: none)
   int gb, hblocks, tpt;
-  size_t off_q, off_qlo, ws_bytes;
+  size_t off_q, off_qlo, off_k, off_v, off_table, ws_bytes;
 };
 
 // Strides of one part of the cache: rows of `row` units.  `unit`: what a stride is a multiple of.
@@ -75,24 +83,49 @@ gqaw_status plan_i4(const gqaw_paged_i4_args *x, I4Plan *L) {
   // most 4 (head size 256: 2), which is what registers hold.
   const long long rows = (long long)std::max(1, a->max_new_tokens) * L->group;
   L->nt = rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
-  // Beyond that, in bf16 at head sizes 64 and 128, two query tiles of 128 rows on the 5th-generation tensor cores
-  L->prefill = rows > 32 && a->dtype == GQAW_BF16 && (D == 64 || D == 128) && L->group <= 128 &&
-               std::max<long long>(L->qs, a->num_heads * D) * L->es < (1ll << 40);
-  const int tile = L->prefill ? 256 : 8 * L->nt;
-  L->gb = L->prefill ? L->group : std::min(L->group, tile);
-  L->hblocks = (int)ceil_div(L->group, L->gb);
-  L->tpt = L->prefill ? 2 * (128 / L->group) : std::max(1, tile / L->gb);
+  L->path = kRows;
   // Single tokens among chunks would fill 8 of the rows: they have a launch of their own where there
   // may be many (the others hold at most max_new_tokens, which bounds their number)
   constexpr int kShort = 64;
+  const int seqs = std::min(gqaw::kPagedItems, a->batch_size);
   const long long tok = L->nt > 1 && L->group <= 8 ? 8 / L->group : 0;
   const long long spare = (long long)a->total_new_tokens - a->batch_size * tok;
   if (tok && (a->batch_size - (spare > 0 ? ceil_div(spare, a->max_new_tokens) : 0)) * a->kv_num_heads >= kShort) L->few = (int)tok;
+  // More rows in bf16: the 5th-generation tensor cores.
+  if (rows > 8 * L->nt && a->dtype == GQAW_BF16 && D >= 64 && L->group <= 128 &&
+      std::max<long long>(L->qs, a->num_heads * D) * L->es < (1ll << 40)) {
+    // Expanded where a sequence may have more than one query tile and the workspace does not grow beyond kMost:
+    // for every sequence what its tokens attend (row ranges that repeat rows may make chunks of all)
+    constexpr unsigned long long kMost = 2ull << 30;
+    L->halves = D <= 128 ? 2 : 1;
+    L->tpt = L->halves * (128 / L->group);
+    const long long span = a->local_window_size > 0 ? std::min<long long>(a->max_sequence_length, (long long)a->local_window_size + a->max_new_tokens)
+                                                     : a->max_sequence_length;
+    const long long pages = seqs * (ceil_div(span, 128) + 1);
+    const unsigned long long bytes = (unsigned long long)pages * 128 * a->kv_num_heads * D * 4;
+    if (D == 256 ? bytes <= kMost : a->max_new_tokens > L->tpt && bytes <= kMost)
+      L->path = kExpand;
+    else if (D <= 128)
+      L->path = kTiles;
+    L->pages = (int)pages;
+    L->width = (int)ceil_div(a->max_sequence_length, 128);
+  }
+  const int tile = L->path != kRows ? 128 * L->halves : 8 * L->nt;
+  L->gb = L->path != kRows ? L->group : std::min(L->group, tile);
+  L->hblocks = (int)ceil_div(L->group, L->gb);
+  if (L->path == kRows) L->tpt = std::max(1, tile / L->gb);
   L->ws_bytes = gqaw::kPagedPartialOffset + align256((size_t)kSms * 2 * tile * (D + 4) * 4);
   L->off_q = L->ws_bytes;
   L->ws_bytes += align256((size_t)a->total_new_tokens * a->num_heads * D * L->es);
   L->off_qlo = L->ws_bytes;  // what bf16 leaves of turned queries
   if (a->dtype == GQAW_BF16) L->ws_bytes += align256((size_t)a->total_new_tokens * a->num_heads * D * L->es);
+  if (L->path == kExpand) {
+    const size_t half = align256((size_t)L->pages * 128 * a->kv_num_heads * D * 2);
+    L->off_k = L->ws_bytes;
+    L->off_v = L->off_k + half;
+    L->off_table = L->off_v + half;
+    L->ws_bytes = L->off_table + align256((size_t)seqs * L->width * 4);
+  }
   return GQAW_OK;
 }
 
@@ -224,14 +257,33 @@ gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cu
   p.div_shift = 31 + l;
   p.div_mul = (uint32_t)(((unsigned __int128)1 << (31 + l)) / a->page_size + (((unsigned __int128)1 << (31 + l)) % a->page_size != 0));
   gqaw::PagedMaps maps;
-  if (L.prefill) {  // only the queries come by TMA
+  gqaw::PagedParams wide;  // kExpand: the attention over the expanded pages
+  if (L.path != kRows) {
     std::memset(&maps, 0, sizeof(maps));
     const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a->num_heads, (cuuint64_t)a->total_new_tokens};
     const cuuint64_t qst[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.qs * 2};
-    const cuuint32_t qb[3] = {64, (cuuint32_t)L.group, (cuuint32_t)(L.tpt / 2)};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)L.group, (cuuint32_t)(L.tpt / L.halves)};
     bool ok = gqaw::encode_tensor_map(&maps.q, p.q, 3, qd, qst, qb, true);
     maps.ql = maps.q;
     if (p.qlo) ok = ok && gqaw::encode_tensor_map(&maps.ql, p.qlo, 3, qd, qst, qb, true);
+    if (L.path == kExpand) {
+      char *ws = static_cast<char *>(a->workspace);
+      wide = p;
+      wide.kp = ws + L.off_k;
+      wide.vp = ws + L.off_v;
+      wide.sr = D;
+      wide.sh = 128 * D;
+      wide.sp = wide.sh * a->kv_num_heads;
+      wide.table = reinterpret_cast<const int32_t *>(ws + L.off_table);
+      wide.page = 128;
+      wide.npages = L.pages;
+      wide.width = L.width;
+      const cuuint64_t cd[4] = {(cuuint64_t)D, 128, (cuuint64_t)a->kv_num_heads, (cuuint64_t)L.pages};
+      const cuuint64_t cst[3] = {(cuuint64_t)wide.sr * 2, (cuuint64_t)wide.sh * 2, (cuuint64_t)wide.sp * 2};
+      const cuuint32_t cb[4] = {64, 128, 1, 1};
+      ok = ok && gqaw::encode_tensor_map(&maps.k, wide.kp, 4, cd, cst, cb, true) &&
+           gqaw::encode_tensor_map(&maps.v, wide.vp, 4, cd, cst, cb, true);
+    }
     if (!ok) return fail(GQAW_ECUDA, "cuTensorMapEncodeTiled failed for the attention over a 4-bit cache");
   }
   auto launch = [&](const I4Params &x, int nt) {
@@ -251,8 +303,29 @@ gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cu
     p.gb = L.gb;
     p.hblocks = L.hblocks;
     p.tpt = L.tpt;
-    cudaError_t e = L.prefill ? gqaw::launch_i4_prefill(p, maps, kSms, st) : launch(p, L.nt);
-    if (e == cudaSuccess && L.prefill) gqaw::count_launch();
+    cudaError_t e;
+    switch (L.path) {
+      case kExpand:
+        e = gqaw::launch_i4_expand(p, wide.kp, wide.vp, const_cast<int32_t *>(wide.table), L.width, L.pages, kSms, st);
+        if (e != cudaSuccess) break;
+        gqaw::count_launch();
+        wide.B = p.B;
+        wide.qstart = p.qstart;
+        wide.seqlens = p.seqlens;
+        wide.s_lo = p.s_lo;
+        wide.s_hi = p.s_hi;
+        wide.gb = p.gb;
+        wide.hblocks = p.hblocks;
+        wide.tpt = p.tpt;
+        e = gqaw::launch_paged_prefill(wide, maps, L.halves, kSms, st);
+        if (e == cudaSuccess) gqaw::count_launch();
+        break;
+      case kTiles:
+        e = gqaw::launch_i4_prefill(p, maps, kSms, st);
+        if (e == cudaSuccess) gqaw::count_launch();
+        break;
+      default: e = launch(p, L.nt);
+    }
     if (e == cudaSuccess && L.few) {
       I4Params few = p;
       few.s_lo = 1;

@@ -19,7 +19,7 @@ class Batch:
 
     def __init__(self, lens, Nq, Nkv, D, page, dtype, seed=0, heads_inside_rows=False, extra_rows=0, lead_rows=0,
                  window=0, softcap=0.0, sink=False, scale=0.0, norm=False, rotary=0, interleaved=False, smooth=False,
-                 position_ids=False, fused=False, spare_pages=2, woven=False, odd_scales=False, filled=True):
+                 position_ids=False, fused=False, spare_pages=2, woven=False, odd_scales=False, filled=True, max_len=0):
         dev = torch.device("cuda:0")
         g = torch.Generator().manual_seed(seed)
         self.lens, self.Nq, self.Nkv, self.D, self.page, self.dtype = lens, Nq, Nkv, D, page, dtype
@@ -28,7 +28,7 @@ class Batch:
         need = [(t + page - 1) // page for _, t in lens]
         pages = sum(need) + spare_pages
         perm = torch.randperm(pages, generator=g)
-        width = max([1] + need)
+        width = max([1, -(-max_len // page)] + need)
         table = torch.full((len(lens), width), -1, dtype=torch.int32)
         at = 0
         for i, k in enumerate(need):
@@ -91,10 +91,10 @@ class Batch:
         self.qw = (1 + 0.2 * torch.randn(D, generator=g)).to(dtype).to(dev) if norm else None
         self.kw = (1 + 0.2 * torch.randn(D, generator=g)).to(dtype).to(dev) if norm else None
         self.max_new = max([0] + [s for s, _ in lens])
-        self.max_len = max([0] + [t for _, t in lens])
+        self.max_len = max([max_len] + [t for _, t in lens])
         self.cos = self.sin = self.ids = None
         if rotary:
-            rows = self.max_len + 50
+            rows = max([0] + [t for _, t in lens]) + 50
             ang = torch.arange(rows, dtype=torch.float64)[:, None] * 100.0 ** (
                 -torch.arange(0, rotary, 2, dtype=torch.float64) / rotary)
             self.cos, self.sin = (f(ang).to(dtype).to(dev).contiguous() for f in (torch.cos, torch.sin))

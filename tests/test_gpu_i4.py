@@ -168,6 +168,29 @@ def test_attend_chunks(dtype, D, Nq, Nkv, page, opt):
     t.check_output()
 
 
+LONG = 1 << 20  # a length for which the expanded pages of a few sequences would be too large
+
+
+@pytest.mark.parametrize("D,Nq,Nkv,page", SHAPES)
+@pytest.mark.parametrize("opt", [dict(), dict(window=LONG - 1, sink=True), dict(softcap=5.0, scale=0.3)])
+def test_attend_chunks_of_batches_that_may_be_long(D, Nq, Nkv, page, opt):
+    """The prompt kernel that takes codes, whose choice goes by the longest length that the call allows."""
+    t = Batch([(33, 33), (1, 300), (70, 200), (0, 5), (129, 401), (8, 8)], Nq, Nkv, D, page, BF16, seed=page, max_len=LONG, **opt)
+    t.call(gqaw.gqaw_paged_i4_attend)
+    t.check_output()
+
+
+@pytest.mark.parametrize("max_len", [0, LONG])
+@pytest.mark.parametrize("kw", [dict(odd_scales=True), dict(norm=True, rotary=64), dict(window=70, sink=True), dict(heads_inside_rows=True)])
+def test_chunks_either_way(max_len, kw):
+    """Chunks of several query tiles, with their keys expanded beforehand and as codes."""
+    for D, Nq, Nkv, page in ((128, 8, 2, 16), (64, 16, 1, 24)):
+        t = Batch([(200, 300), (1, 90), (300, 300), (2, 2)], Nq, Nkv, D, page, BF16, seed=3, max_len=max_len, lead_rows=1, extra_rows=2, **kw)
+        t.call(gqaw.gqaw_paged_i4_step)
+        t.check_output(turned=True)
+        assert (t.out[t.untouched()] == 7.0).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("opt", [dict(window=1), dict(window=100, softcap=30.0), dict(sink=True), dict(smooth=True, softcap=2.0),
                                  dict(scale=2.0), dict(odd_scales=True), dict(odd_scales=True, window=33)])
@@ -221,11 +244,12 @@ def test_attend_queries_of_any_size(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("S", [1, 6, 40])
-def test_attend_scales_that_are_not_finite(dtype, S):
+@pytest.mark.parametrize("S,max_len", [(1, 0), (6, 0), (40, 0), (70, 0), (70, LONG)])
+def test_attend_scales_that_are_not_finite(dtype, S, max_len):
     """A value scale that is NaN or infinite reaches the 32 elements of its group in the outputs of tokens that
     attend it, and nothing else."""
-    t = Batch([(S, 180), (S, 75)], 4, 2, 128, 16, dtype, seed=8, window=60)
+    t = Batch([(S, 180), (S, 75)], 4 if S < 70 else 8, 2, 128, 16, dtype, seed=8, window=60, max_len=max_len)
+    half = t.Nq // 2
     pos = {0: 180 - S // 2 - 1, 1: 75 - S}
     for i, j in pos.items():
         pg = int(t.table[i, j // 16])
@@ -233,12 +257,12 @@ def test_attend_scales_that_are_not_finite(dtype, S):
     t.call(gqaw.gqaw_paged_i4_attend)
     t.check_output()
     for i, j in pos.items():
-        rows = t.out[t.rows(i)].reshape(S, 4, 4, 32)
+        rows = t.out[t.rows(i)].reshape(S, t.Nq, 4, 32)
         first = t.lens[i][1] - S
         for s in range(S):
             sees = first + s >= j and j > first + s - 60
-            assert rows[s, 2:, 2].isfinite().any() != sees or not sees
-            assert rows[s, :2].isfinite().all() and rows[s, 2:, :2].isfinite().all() and rows[s, 2:, 3].isfinite().all()
+            assert rows[s, half:, 2].isfinite().any() != sees
+            assert rows[s, :half].isfinite().all() and rows[s, half:, :2].isfinite().all() and rows[s, half:, 3].isfinite().all()
             if not sees:
                 assert rows[s].isfinite().all()
 
