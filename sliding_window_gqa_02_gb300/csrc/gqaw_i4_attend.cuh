@@ -29,10 +29,10 @@
 // fp32.
 //
 // Each warp works on its own, on tiles of 32 keys through a ring of its own; no barrier of the CTA
-// falls inside a unit.  Tiles come by cp.async through the page table, any page size and strides: with
-// pages of 16 rows a tile by tensor TMA and bulk copies is eight copies, whose operands cost 300
-// instructions, and their own loads in place of these 80.  A unit's first tiles are under way before the
-// last unit's rows go out.  Schedule, splits and merges: gqaw_paged.cuh.
+// falls inside a unit.  Tiles come by cp.async through the page table, any page size and strides; with
+// pages of 16 rows a tile by tensor TMA and bulk copies is eight copies, whose operands took 300
+// instructions, and every lane's own look-ups 200.  A unit's first tiles are under way before the last
+// unit's rows go out.  Schedule, splits and merges: gqaw_paged.cuh.
 //
 // Which of 8 rows is which: position x of 8 is key kappa(x) of a tile's, chosen so that the rows of
 // the even positions lie in different banks when four lanes read their dimensions of them.
@@ -44,6 +44,9 @@
 #include <atomic>
 #ifndef GQAW_W
 #define GQAW_W 12
+#endif
+#ifndef GQAW_W2
+#define GQAW_W2 8
 #endif
 #ifndef GQAW_SB
 #define GQAW_SB 2
@@ -70,7 +73,7 @@ struct Lay {
   static constexpr int kCodes = kKeys * kRow;            // of a tile
   static constexpr int kScales = kKeys * G * 2;
   static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V, their scales; a multiple of the swizzle's span
-  static constexpr int W = NT > 1 || D == 256 ? 8 : GQAW_W;
+  static constexpr int W = NT > 2 || D == 256 ? 8 : NT == 2 ? GQAW_W2 : GQAW_W;
   static constexpr int kFit = 170 * 1024 / (W * kStage), S = kFit > 8 ? 8 : kFit;  // stages
   static_assert(S >= 2, "a tile under way beside the one at hand");
   static constexpr int kThreads = 32 * W;
@@ -266,58 +269,79 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   __shared__ Unit units[3];  // the unit at hand, the next and the one behind it
   const int my_group = gid * (D / 8) / kI4Group;  // of this lane's dimensions, gid D / 8 and on
 
-  // A copy of the warp has 16 bytes of codes a lane: CPR lanes a row, RPC rows, CPR copies a tile.
-  constexpr int CPR = D / 32, RPC = 32 / CPR;
-  const int crow = lane / CPR, cpart = lane % CPR, share = p.share;
-  const uint32_t box = p.page % RPC == 0 ? share * RPC : 1, box_row = box == 1 ? crow : 0;  // rows with one page
+  // A copy of the warp has 16 bytes of codes a lane: CPR lanes a row, a block of RPC rows, CPR copies a tile.
+  // Where blocks lie in one page each, a lane finds one block's addresses: those of TPB tiles at once, a
+  // hundredth of what every lane for its own rows takes, and hands them out by shuffles.
+  constexpr int CPR = D / 32, RPC = 32 / CPR, TPB = 32 / CPR;
+  const int crow = lane / CPR, cpart = lane % CPR;
   auto page_of = [&](uint32_t j) { return (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift); };
-  // the pages of the rows that this lane copies of key tile t, and that of key `lane` for its scales: -2
-  // where no row attends them
-  struct Ids {
-    int row[CPR], key;
+  const unsigned char *bcodes = nullptr;  // this lane's block of the batch of tiles at hand: codes (nullptr: not needed)
+  const uint16_t *bscales = nullptr;      // ... and scales, of keys
+  int bid = -2, bn = 0;                   // the page of its block of the next batch; tiles of this batch loaded
+  // its place in the batch that begins with tile t
+  auto block_at = [&](int t) { return (uint32_t)(t + lane / CPR * W) * kKeys + lane % CPR * RPC; };
+  auto look_up = [&](const Unit &x, int t, int end) {
+    const uint32_t j = block_at(t);
+    bid = t + lane / CPR * W < end && j < x.jhi && j + RPC > x.jlo ? p.table[(long long)x.b * p.width + page_of(j)] : -2;
   };
-  auto look_up = [&](const Unit &x, int t, int end, Ids &ids) {
-    const int32_t *table = p.table + (long long)x.b * p.width;
-    const uint32_t j0 = (uint32_t)t * kKeys;
-#pragma unroll
-    for (int c = 0; c < CPR; ++c) {
-      if ((c & (share - 1)) == 0) {
-        const uint32_t j = j0 + c * RPC + box_row;
-        ids.row[c] = t < end && j < x.jhi && j + box > x.jlo ? table[page_of(j)] : -2;
-      }
-    }
-    ids.key = t < end && j0 + lane < x.jhi && j0 + lane >= x.jlo ? table[page_of(j0 + lane)] : -2;
+  auto resolve = [&](const Unit &x, int t) {
+    const uint32_t j = block_at(t), row = j - page_of(j) * p.page;
+    const bool ok = (unsigned)bid < (unsigned)p.npages;
+    if (!ok && bid != -2) pflag(p, GQAW_DEV_BAD_PAGE);
+    bcodes = ok ? x.codes + (((uint64_t)(uint32_t)bid * p.sp16 + (uint64_t)row * p.sr16) << 4) : nullptr;
+    bscales = x.scales + ((uint64_t)(uint32_t)(ok ? bid : 0) * p.tpg + (uint64_t)row * p.trg) * G;
   };
+  const uint32_t code_off = (crow * p.sr16 + cpart) << 4, scale_off = lane % RPC * p.trg * G;
   // key tile t into stage st; rows that nobody needs become zeros
-  auto load = [&](const Unit &x, int t, int end, int st, const Ids &ids) {
+  auto load = [&](const Unit &x, int t, int end, int st) {
     if (t < end) {  // uniform over the warp
       unsigned char *kb = ring + st * L::kStage, *sb = kb + 2 * L::kCodes;
       const uint32_t j0 = (uint32_t)t * kKeys;
       const bool whole = j0 >= x.jlo && j0 + kKeys <= x.jhi;
-      const unsigned char *at = nullptr;
-      bool ok = false;
       unsigned char *dst = kb + at_part<D>(crow, cpart);
+      const uint16_t *ks = x.scales;
+      bool key_ok = false;
+      if (p.blocks) {
 #pragma unroll
-      for (int c = 0; c < CPR; ++c) {
-        const uint32_t j = j0 + c * RPC + crow;
-        if ((c & (share - 1)) == 0) {
-          const int id = ids.row[c];
-          ok = (unsigned)id < (unsigned)p.npages;
-          if (!ok && id != -2) pflag(p, GQAW_DEV_BAD_PAGE);
-          const uint32_t row = j - page_of(j) * p.page;
-          at = x.codes + (((uint64_t)(uint32_t)(ok ? id : 0) * p.sp16 + (uint64_t)row * p.sr16 + cpart) << 4);
-        } else {
-          at += (uint64_t)p.sr16 * (16 * RPC);
+        for (int c = 0; c < CPR; ++c) {
+          const uint32_t j = j0 + c * RPC + crow;
+          const uint64_t b = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(bcodes), bn * CPR + c);
+          const unsigned char *at = b ? reinterpret_cast<const unsigned char *>(b) + code_off : x.codes;
+          const bool need = b && (whole || (j >= x.jlo && j < x.jhi));
+          unsigned char *to = D == 256 ? kb + at_part<D>(c * RPC + crow, cpart) : dst + c * RPC * L::kRow;
+          cp_async<16>(to, at, need);
+          cp_async<16>(to + L::kCodes, at + x.values, need);
         }
-        const bool need = ok && (whole || (j >= x.jlo && j < x.jhi));
-        unsigned char *to = D == 256 ? kb + at_part<D>(c * RPC + crow, cpart) : dst + c * RPC * L::kRow;
-        cp_async<16>(to, at, need);
-        cp_async<16>(to + L::kCodes, at + x.values, need);
+        const int src = bn * CPR + lane / RPC;
+        const uint64_t b = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(bscales), src);
+        key_ok = __shfl_sync(0xffffffffu, bcodes != nullptr, src) && (whole || (j0 + lane >= x.jlo && j0 + lane < x.jhi));
+        ks = key_ok ? reinterpret_cast<const uint16_t *>(b) + scale_off : x.scales;
+        if (++bn == TPB) {  // the next batch
+          resolve(x, t + W);
+          look_up(x, t + (TPB + 1) * W, end);
+          bn = 0;
+        }
+      } else {  // pages of any size: every lane for its own rows
+        const int32_t *table = p.table + (long long)x.b * p.width;
+        auto page_at = [&](uint32_t j) {
+          const int id = j >= x.jlo && j < x.jhi ? table[page_of(j)] : -2;
+          if (id != -2 && (unsigned)id >= (unsigned)p.npages) pflag(p, GQAW_DEV_BAD_PAGE);
+          return (unsigned)id < (unsigned)p.npages ? id : -1;
+        };
+#pragma unroll 1
+        for (int c = 0; c < CPR; ++c) {
+          const uint32_t j = j0 + c * RPC + crow, row = j - page_of(j) * p.page;
+          const int id = page_at(j);
+          const unsigned char *at = x.codes + (((uint64_t)(uint32_t)max(id, 0) * p.sp16 + (uint64_t)row * p.sr16 + cpart) << 4);
+          unsigned char *to = kb + at_part<D>(c * RPC + crow, cpart);
+          cp_async<16>(to, at, id >= 0);
+          cp_async<16>(to + L::kCodes, at + x.values, id >= 0);
+        }
+        const uint32_t j = j0 + lane, row = j - page_of(j) * p.page;
+        const int id = page_at(j);
+        key_ok = id >= 0;
+        ks += ((uint64_t)(uint32_t)max(id, 0) * p.tpg + (uint64_t)row * p.trg) * G;
       }
-      const bool key_ok = (unsigned)ids.key < (unsigned)p.npages;
-      if (!key_ok && ids.key != -2) pflag(p, GQAW_DEV_BAD_PAGE);
-      const uint32_t j = j0 + lane, row = j - page_of(j) * p.page;
-      const uint16_t *ks = x.scales + ((uint64_t)(uint32_t)(key_ok ? ids.key : 0) * p.tpg + (uint64_t)row * p.trg) * G;
       if constexpr (G >= 2) {
         cp_async<2 * G>(sb + lane * 2 * G, ks, key_ok);
         cp_async<2 * G>(sb + L::kScales + lane * 2 * G, ks + x.value_scales, key_ok);
@@ -329,18 +353,25 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto bump = [](int st) { return st + 1 == S ? 0 : st + 1; };
-  Ids ids;  // of the next tile to load
   auto load_first = [&](const Unit &x, int st) {  // from stage st on
     const int t = x.t0 + warp, end = x.t0 + x.tiles;
-    look_up(x, t, end, ids);
+    if (p.blocks) {
+      look_up(x, t, end);
+      resolve(x, t);
+      look_up(x, t + TPB * W, end);
+      bn = 0;
+    }
 #pragma unroll 1
     for (int i = 0; i < S - 1; ++i) {
-      Ids next;
-      look_up(x, t + (i + 1) * W, end, next);
-      load(x, t + i * W, end, st, ids);
-      ids = next;
+      load(x, t + i * W, end, st);
       st = bump(st);
     }
+  };
+  // the table's entries that load_first() will want, on their way to the SM
+  auto prefetch_first = [&](const Unit &x) {
+    const uint32_t j = block_at(x.t0 + warp);
+    if (x.more && j < x.jhi && p.blocks)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.table + (long long)x.b * p.width + page_of(j)) : "memory");
   };
   // one element of every group of row r
   auto query_row = [&](const Unit &x, int r, float (&y)[G]) {
@@ -385,20 +416,24 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
     if (lane == 0) sqexp[r] = e;
   };
 
-  // One thread walks the units, two ahead; its walker is kept out of everybody's registers
+  // One thread walks the units, two ahead, of the warp that has least to do beside it; its walker is kept
+  // out of everybody's registers
+  constexpr int kWalkThread = L::kThreads - 32;
   __shared__ __align__(16) unsigned char walker[sizeof(PWalk<kKeys>)];
   PWalk<kKeys> *walk = reinterpret_cast<PWalk<kKeys> *>(walker);
   if (tid == 0) {
     *walk = PWalk<kKeys>(shp, &sched);
     units[0].take(p, shp, *walk);
-    if (units[0].more) units[1].take(p, shp, *walk);
   }
   __syncthreads();
   int st = 0;  // stage of the next tile
   if (units[0].more) {
+    float q[G];
+    query_row(units[0], min(warp, R - 1), q);
     load_first(units[0], 0);
-    for (int r = warp; r < R; r += W) {
-      float q[G];
+    if (tid == kWalkThread) units[1].take(p, shp, *walk);
+    put_query(min(warp, R - 1), q);
+    for (int r = warp + W; r < R; r += W) {
       query_row(units[0], r, q);
       put_query(r, q);
     }
@@ -453,13 +488,9 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
 #pragma unroll
     for (int c = 0; c < 2; ++c) voff[c] = L::kCodes + at_part<D>(kappa<D>(2 * t4 + c), gid * (D / 16) / 16) + gid * (D / 16) % 16;
 
+    prefetch_first(units[un == 2 ? 0 : un + 1]);
     for (int t = x.t0 + warp; t < end; t += W) {
-      {
-        Ids next;
-        look_up(x, t + S * W, end, next);
-        load(x, t + (S - 1) * W, end, st == 0 ? S - 1 : st - 1, ids);
-        ids = next;
-      }
+      load(x, t + (S - 1) * W, end, st == 0 ? S - 1 : st - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
       __syncwarp();
       const unsigned char *kb = ring + st * L::kStage, *sb = kb + 2 * L::kCodes;
@@ -745,7 +776,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
       }
     if (lane == 0) s_state[warp] = warp * L::kRing + state;
     __syncthreads();
-    if (tid == 0) {  // the unit behind the next one, in the place of the last
+    if (tid == kWalkThread) {  // the unit behind the next one, in the place of the last
       Unit &y = units[un == 0 ? 2 : un - 1];
       y.more = 0;
       if (more) y.take(p, shp, *walk);
@@ -762,9 +793,9 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
     const int cta = blockIdx.x, cf = x.cf, cl = x.cl, g = x.g, row0 = x.row0, h0 = x.h0;
     T *out = static_cast<T *>(p.out);
     float *part = p.partials + ((long long)cta * 2 + (cta == cf ? 1 : 0)) * R * PS;
-    for (int e = tid; e < rows * D; e += L::kThreads) {
-      const int r = e / D, d = e - r * D, tok = r / g, h = h0 + r - tok * g;
-      float M = -INFINITY, A = 0.f, Z = 0.f, m[W];
+    for (int e = tid; e < rows * (D / 4); e += L::kThreads) {  // four dimensions of a row
+      const int r = e / (D / 4), d = (e - r * (D / 4)) * 4, tok = r / g, h = h0 + r - tok * g;
+      float M = -INFINITY, Z = 0.f, m[W], A[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         m[w] = reinterpret_cast<const float *>(smem + s_state[w])[r * PS + D];
@@ -775,17 +806,23 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
       for (int w = 0; w < W; ++w) {
         const float *y = reinterpret_cast<const float *>(smem + s_state[w]) + r * PS;
         const float f = fast_exp2(m[w] - ref);
+        const float4 a = *reinterpret_cast<const float4 *>(y + d);
         Z = fmaf(f, y[D + 1], Z);
-        A = fmaf(f, y[d], A);
+        A[0] = fmaf(f, a.x, A[0]);
+        A[1] = fmaf(f, a.y, A[1]);
+        A[2] = fmaf(f, a.z, A[2]);
+        A[3] = fmaf(f, a.w, A[3]);
       }
       if (cut) {
-        part[r * PS + d] = A;
-        if (d == 0) {
-          part[r * PS + D] = M;
-          part[r * PS + D + 1] = Z;
-        }
+        *reinterpret_cast<float4 *>(part + r * PS + d) = make_float4(A[0], A[1], A[2], A[3]);
+        if (d == 0) *reinterpret_cast<float2 *>(part + r * PS + D) = make_float2(M, Z);
       } else {
-        out[(row0 + tok) * p.os + (long long)h * D + d] = Elem<T>::store(A * sink_reciprocal(Z, M, paged_sink_log2(p, h)));
+        const float inv = sink_reciprocal(Z, M, paged_sink_log2(p, h));
+        T *to = out + (row0 + tok) * p.os + (long long)h * D + d;
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4 *>(to) = make_float4(A[0] * inv, A[1] * inv, A[2] * inv, A[3] * inv);
+        else
+          *reinterpret_cast<uint2 *>(to) = make_uint2(tc::pack_bf16x2(A[0] * inv, A[1] * inv), tc::pack_bf16x2(A[2] * inv, A[3] * inv));
       }
     }
     if (cut) {

@@ -82,7 +82,7 @@ gqaw_status plan_i4(const gqaw_paged_i4_args *x, I4Plan *L) {
   // The kernel: 8 query rows of a kv head a product, and as many of them as the longest chunk fills, at
   // most 4 (head size 256: 2), which is what registers hold.
   const long long rows = (long long)std::max(1, a->max_new_tokens) * L->group;
-  L->nt = rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
+  L->nt = rows <= 8 ? 1 : 2;
   L->path = kRows;
   // Single tokens among chunks would fill 8 of the rows: they have a launch of their own where there
   // may be many (the others hold at most max_new_tokens, which bounds their number)
@@ -92,7 +92,7 @@ gqaw_status plan_i4(const gqaw_paged_i4_args *x, I4Plan *L) {
   const long long spare = (long long)a->total_new_tokens - a->batch_size * tok;
   if (tok && (a->batch_size - (spare > 0 ? ceil_div(spare, a->max_new_tokens) : 0)) * a->kv_num_heads >= kShort) L->few = (int)tok;
   // More rows in bf16: the 5th-generation tensor cores.
-  if (rows > 8 * L->nt && a->dtype == GQAW_BF16 && D >= 64 && L->group <= 128 &&
+  if (rows > 32 && a->dtype == GQAW_BF16 && D >= 64 && L->group <= 128 &&
       std::max<long long>(L->qs, a->num_heads * D) * L->es < (1ll << 40)) {
     // Expanded where a sequence may have more than one query tile and the workspace does not grow beyond kMost:
     // for every sequence what its tokens attend (row ranges that repeat rows may make chunks of all)
@@ -248,9 +248,7 @@ gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cu
   p.sr16 = (uint32_t)(L.sr / 16);
   p.tpg = (uint32_t)(L.tp / (D / gqaw::kI4Group));
   p.trg = (uint32_t)(L.tr / (D / gqaw::kI4Group));
-  // a copy of the whole warp has 1024 / D rows, a tile of 32 keys D / 32 copies
-  p.share = 1;
-  while (p.share < D / 32 && a->page_size % (1024 / D * p.share * 2) == 0) p.share *= 2;
+  p.blocks = a->page_size % (1024 / D) == 0;
   // ceil(2^(31 + l) / page) with 2^l >= page: its excess over the quotient, below 1, times j stays below 2^31 (Granlund, Montgomery)
   int l = 0;
   while ((1ll << l) < a->page_size) ++l;
