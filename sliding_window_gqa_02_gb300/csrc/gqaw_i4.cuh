@@ -18,6 +18,7 @@ struct I4Params : PagedParams {
   long long kos, vos;
   // attention: rows of the cache by 16 bytes of codes and one row's scales
   uint32_t sp16, sr16, tpg, trg;  // strides of pages and rows, in 16 bytes and in rows of scales
+  long long to_values, to_value_scales;  // bytes from key codes to value codes, and from key scales to value scales
   bool blocks;                    // the 1024 / D rows of a copy lie in one page
   uint32_t div_mul;               // j / page = j div_mul >> div_shift, for j < 2^31
   int div_shift;

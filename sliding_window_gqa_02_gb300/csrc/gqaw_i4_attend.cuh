@@ -182,6 +182,13 @@ __device__ __forceinline__ uint32_t lds32(const unsigned char *p) { return *rein
 __device__ __forceinline__ uint32_t lds16(const unsigned char *p) { return *reinterpret_cast<const uint16_t *>(p); }
 
 template <int N>
+__device__ __forceinline__ void cp_async(void *dst, const void *src) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(N) : "memory");
+}
+template <int N>
 __device__ __forceinline__ void cp_async(void *dst, const void *src, bool ok) {
   const int n = ok ? N : 0;  // 0: zeros
   if constexpr (N == 16)
@@ -198,9 +205,8 @@ struct Unit {
   uint32_t qpos, jlo, jhi;     // position of the first token; positions that some row attends
   int cut, cf, cl;             // is the unit cut, and the first and last CTA with a part of it
   int more;                    // is this a unit?
-  const unsigned char *codes;  // the kv head's key codes; values' lie `values` bytes on
-  const uint16_t *scales;      // the same of scales
-  long long values, value_scales;
+  const unsigned char *codes;  // the kv head's key codes and scales
+  const uint16_t *scales;
   template <typename Walk>
   __device__ inline void take(const I4Params &p, const PShape &shp, Walk &walk) {
     PUnit u;
@@ -215,9 +221,7 @@ struct Unit {
     g = min(p.gb, p.group - hb * p.gb);
     rows = ntok * g;
     codes = static_cast<const unsigned char *>(p.kp) + kvh * p.sh;
-    values = static_cast<const unsigned char *>(p.vp) - static_cast<const unsigned char *>(p.kp);
     scales = p.kscale + kvh * p.th;
-    value_scales = p.vscale - p.kscale;
     t0 = u.kt + u.k0;
     tiles = u.k1 - u.k0;
     const long long lo = p.W > 0 && u.qpos - p.W + 1 > 0 ? u.qpos - p.W + 1 : 0, hi = u.qpos + u.ntok;
@@ -275,8 +279,9 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   constexpr int CPR = D / 32, RPC = 32 / CPR, TPB = 32 / CPR;
   const int crow = lane / CPR, cpart = lane % CPR;
   auto page_of = [&](uint32_t j) { return (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift); };
-  const unsigned char *bcodes = nullptr;  // this lane's block of the batch of tiles at hand: codes (nullptr: not needed)
+  const unsigned char *bcodes = nullptr;  // this lane's block of the batch of tiles at hand: codes
   const uint16_t *bscales = nullptr;      // ... and scales, of keys
+  uint32_t bok = 0;                       // the lanes whose block is needed and has a page
   int bid = -2, bn = 0;                   // the page of its block of the next batch; tiles of this batch loaded
   // its place in the batch that begins with tile t
   auto block_at = [&](int t) { return (uint32_t)(t + lane / CPR * W) * kKeys + lane % CPR * RPC; };
@@ -288,8 +293,9 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
     const uint32_t j = block_at(t), row = j - page_of(j) * p.page;
     const bool ok = (unsigned)bid < (unsigned)p.npages;
     if (!ok && bid != -2) pflag(p, GQAW_DEV_BAD_PAGE);
-    bcodes = ok ? x.codes + (((uint64_t)(uint32_t)bid * p.sp16 + (uint64_t)row * p.sr16) << 4) : nullptr;
-    bscales = x.scales + ((uint64_t)(uint32_t)(ok ? bid : 0) * p.tpg + (uint64_t)row * p.trg) * G;
+    bok = __ballot_sync(0xffffffffu, ok);
+    bcodes = x.codes + (ok ? ((uint64_t)(uint32_t)bid * p.sp16 + (uint64_t)row * p.sr16) << 4 : 0ull);
+    bscales = x.scales + (ok ? ((uint64_t)(uint32_t)bid * p.tpg + (uint64_t)row * p.trg) * G : 0ull);
   };
   const uint32_t code_off = (crow * p.sr16 + cpart) << 4, scale_off = lane % RPC * p.trg * G;
   // key tile t into stage st; rows that nobody needs become zeros
@@ -300,22 +306,31 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
       const bool whole = j0 >= x.jlo && j0 + kKeys <= x.jhi;
       unsigned char *dst = kb + at_part<D>(crow, cpart);
       const uint16_t *ks = x.scales;
-      bool key_ok = false;
+      bool key_ok = false, plain = false;
       if (p.blocks) {
+        constexpr uint32_t kAll = CPR == 32 ? ~0u : (1u << CPR) - 1u;
+        const uint32_t ok = bok >> (bn * CPR);
+        plain = whole && (ok & kAll) == kAll;
 #pragma unroll
         for (int c = 0; c < CPR; ++c) {
-          const uint32_t j = j0 + c * RPC + crow;
-          const uint64_t b = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(bcodes), bn * CPR + c);
-          const unsigned char *at = b ? reinterpret_cast<const unsigned char *>(b) + code_off : x.codes;
-          const bool need = b && (whole || (j >= x.jlo && j < x.jhi));
+          const unsigned char *at =
+              reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(bcodes), bn * CPR + c)) + code_off;
           unsigned char *to = D == 256 ? kb + at_part<D>(c * RPC + crow, cpart) : dst + c * RPC * L::kRow;
-          cp_async<16>(to, at, need);
-          cp_async<16>(to + L::kCodes, at + x.values, need);
+          if (plain) {
+            cp_async<16>(to, at);
+            cp_async<16>(to + L::kCodes, at + p.to_values);
+          } else {
+            const uint32_t j = j0 + c * RPC + crow;
+            const bool need = ((ok >> c) & 1u) && (whole || (j >= x.jlo && j < x.jhi));
+            at = need ? at : x.codes;
+            cp_async<16>(to, at, need);
+            cp_async<16>(to + L::kCodes, at + p.to_values, need);
+          }
         }
         const int src = bn * CPR + lane / RPC;
-        const uint64_t b = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(bscales), src);
-        key_ok = __shfl_sync(0xffffffffu, bcodes != nullptr, src) && (whole || (j0 + lane >= x.jlo && j0 + lane < x.jhi));
-        ks = key_ok ? reinterpret_cast<const uint16_t *>(b) + scale_off : x.scales;
+        ks = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(bscales), src)) + scale_off;
+        key_ok = plain || (((bok >> src) & 1u) && (whole || (j0 + lane >= x.jlo && j0 + lane < x.jhi)));
+        if (!key_ok) ks = x.scales;
         if (++bn == TPB) {  // the next batch
           resolve(x, t + W);
           look_up(x, t + (TPB + 1) * W, end);
@@ -335,19 +350,25 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
           const unsigned char *at = x.codes + (((uint64_t)(uint32_t)max(id, 0) * p.sp16 + (uint64_t)row * p.sr16 + cpart) << 4);
           unsigned char *to = kb + at_part<D>(c * RPC + crow, cpart);
           cp_async<16>(to, at, id >= 0);
-          cp_async<16>(to + L::kCodes, at + x.values, id >= 0);
+          cp_async<16>(to + L::kCodes, at + p.to_values, id >= 0);
         }
         const uint32_t j = j0 + lane, row = j - page_of(j) * p.page;
         const int id = page_at(j);
         key_ok = id >= 0;
         ks += ((uint64_t)(uint32_t)max(id, 0) * p.tpg + (uint64_t)row * p.trg) * G;
       }
+      const void *vs = reinterpret_cast<const unsigned char *>(ks) + p.to_value_scales;
       if constexpr (G >= 2) {
-        cp_async<2 * G>(sb + lane * 2 * G, ks, key_ok);
-        cp_async<2 * G>(sb + L::kScales + lane * 2 * G, ks + x.value_scales, key_ok);
+        if (plain) {
+          cp_async<2 * G>(sb + lane * 2 * G, ks);
+          cp_async<2 * G>(sb + L::kScales + lane * 2 * G, vs);
+        } else {
+          cp_async<2 * G>(sb + lane * 2 * G, ks, key_ok);
+          cp_async<2 * G>(sb + L::kScales + lane * 2 * G, vs, key_ok);
+        }
       } else {  // two bytes: too few for a copy
         reinterpret_cast<uint16_t *>(sb)[lane] = key_ok ? *ks : (uint16_t)0;
-        reinterpret_cast<uint16_t *>(sb + L::kScales)[lane] = key_ok ? ks[x.value_scales] : (uint16_t)0;
+        reinterpret_cast<uint16_t *>(sb + L::kScales)[lane] = key_ok ? *static_cast<const uint16_t *>(vs) : (uint16_t)0;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");

@@ -249,6 +249,8 @@ gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cu
   p.tpg = (uint32_t)(L.tp / (D / gqaw::kI4Group));
   p.trg = (uint32_t)(L.tr / (D / gqaw::kI4Group));
   p.blocks = a->page_size % (1024 / D) == 0;
+  p.to_values = static_cast<const char *>(p.vp) - static_cast<const char *>(p.kp);
+  p.to_value_scales = reinterpret_cast<const char *>(p.vscale) - reinterpret_cast<const char *>(p.kscale);
   // ceil(2^(31 + l) / page) with 2^l >= page: its excess over the quotient, below 1, times j stays below 2^31 (Granlund, Montgomery)
   int l = 0;
   while ((1ll << l) < a->page_size) ++l;
