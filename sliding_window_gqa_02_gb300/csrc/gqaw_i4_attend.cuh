@@ -237,6 +237,35 @@ struct Unit {
   }
 };
 
+// Pages of any size: every lane copies its own rows' codes of the tile that begins at position j0 to kb.  Returns
+// whether the row of key `lane` is needed and has a page, and where its scales are.  Out of line, for
+// the tiles' usual way is short of instruction cache.
+template <int D>
+__device__ __noinline__ bool load_rows(const I4Params &p, const Unit &x, unsigned char *kb, uint32_t j0, int lane, const uint16_t *&scales) {
+  constexpr int CPR = D / 32, RPC = 32 / CPR;
+  const int crow = lane / CPR, cpart = lane % CPR;
+  const int32_t *table = p.table + (long long)x.b * p.width;
+  auto page_of = [&](uint32_t j) { return (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift); };
+  auto page_at = [&](uint32_t j) {
+    const int id = j >= x.jlo && j < x.jhi ? table[page_of(j)] : -2;
+    if (id != -2 && (unsigned)id >= (unsigned)p.npages) pflag(p, GQAW_DEV_BAD_PAGE);
+    return (unsigned)id < (unsigned)p.npages ? id : -1;
+  };
+#pragma unroll 1
+  for (int c = 0; c < CPR; ++c) {
+    const uint32_t j = j0 + c * RPC + crow, row = j - page_of(j) * p.page;
+    const int id = page_at(j);
+    const unsigned char *at = id >= 0 ? x.codes + (((uint64_t)(uint32_t)id * p.sp16 + (uint64_t)row * p.sr16 + cpart) << 4) : x.codes;
+    unsigned char *to = kb + at_part<D>(c * RPC + crow, cpart);
+    cp_async<16>(to, at, id >= 0);
+    cp_async<16>(to + kKeys * (D / 2), at + p.to_values, id >= 0);
+  }
+  const uint32_t j = j0 + lane, row = j - page_of(j) * p.page;
+  const int id = page_at(j);
+  scales = id >= 0 ? x.scales + ((uint64_t)(uint32_t)id * p.tpg + (uint64_t)row * p.trg) * (D / kI4Group) : x.scales;
+  return id >= 0;
+}
+
 }  // namespace i4a
 
 // NT: operands of 8 query rows.  T: type of the rows outside the cache.
@@ -287,7 +316,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   auto block_at = [&](int t) { return (uint32_t)(t + lane / CPR * W) * kKeys + lane % CPR * RPC; };
   auto look_up = [&](const Unit &x, int t, int end) {
     const uint32_t j = block_at(t);
-    bid = t + lane / CPR * W < end && j < x.jhi && j + RPC > x.jlo ? p.table[(long long)x.b * p.width + page_of(j)] : -2;
+    return t + lane / CPR * W < end && j < x.jhi && j + RPC > x.jlo ? p.table[(long long)x.b * p.width + page_of(j)] : -2;
   };
   auto resolve = [&](const Unit &x, int t) {
     const uint32_t j = block_at(t), row = j - page_of(j) * p.page;
@@ -333,29 +362,11 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
         if (!key_ok) ks = x.scales;
         if (++bn == TPB) {  // the next batch
           resolve(x, t + W);
-          look_up(x, t + (TPB + 1) * W, end);
+          bid = look_up(x, t + (TPB + 1) * W, end);
           bn = 0;
         }
-      } else {  // pages of any size: every lane for its own rows
-        const int32_t *table = p.table + (long long)x.b * p.width;
-        auto page_at = [&](uint32_t j) {
-          const int id = j >= x.jlo && j < x.jhi ? table[page_of(j)] : -2;
-          if (id != -2 && (unsigned)id >= (unsigned)p.npages) pflag(p, GQAW_DEV_BAD_PAGE);
-          return (unsigned)id < (unsigned)p.npages ? id : -1;
-        };
-#pragma unroll 1
-        for (int c = 0; c < CPR; ++c) {
-          const uint32_t j = j0 + c * RPC + crow, row = j - page_of(j) * p.page;
-          const int id = page_at(j);
-          const unsigned char *at = x.codes + (((uint64_t)(uint32_t)max(id, 0) * p.sp16 + (uint64_t)row * p.sr16 + cpart) << 4);
-          unsigned char *to = kb + at_part<D>(c * RPC + crow, cpart);
-          cp_async<16>(to, at, id >= 0);
-          cp_async<16>(to + L::kCodes, at + p.to_values, id >= 0);
-        }
-        const uint32_t j = j0 + lane, row = j - page_of(j) * p.page;
-        const int id = page_at(j);
-        key_ok = id >= 0;
-        ks += ((uint64_t)(uint32_t)max(id, 0) * p.tpg + (uint64_t)row * p.trg) * G;
+      } else {
+        key_ok = load_rows<D>(p, x, kb, j0, lane, ks);
       }
       const void *vs = reinterpret_cast<const unsigned char *>(ks) + p.to_value_scales;
       if constexpr (G >= 2) {
@@ -374,12 +385,14 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto bump = [](int st) { return st + 1 == S ? 0 : st + 1; };
-  auto load_first = [&](const Unit &x, int st) {  // from stage st on
+  // a unit's first tiles, from stage st on; id: first_page() of it
+  auto first_page = [&](const Unit &x) { return p.blocks && x.more ? look_up(x, x.t0 + warp, x.t0 + x.tiles) : -2; };
+  auto load_first = [&](const Unit &x, int st, int id) {
     const int t = x.t0 + warp, end = x.t0 + x.tiles;
     if (p.blocks) {
-      look_up(x, t, end);
+      bid = id;
       resolve(x, t);
-      look_up(x, t + TPB * W, end);
+      bid = look_up(x, t + TPB * W, end);
       bn = 0;
     }
 #pragma unroll 1
@@ -387,12 +400,6 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
       load(x, t + i * W, end, st);
       st = bump(st);
     }
-  };
-  // the table's entries that load_first() will want, on their way to the SM
-  auto prefetch_first = [&](const Unit &x) {
-    const uint32_t j = block_at(x.t0 + warp);
-    if (x.more && j < x.jhi && p.blocks)
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.table + (long long)x.b * p.width + page_of(j)) : "memory");
   };
   // one element of every group of row r
   auto query_row = [&](const Unit &x, int r, float (&y)[G]) {
@@ -451,7 +458,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   if (units[0].more) {
     float q[G];
     query_row(units[0], min(warp, R - 1), q);
-    load_first(units[0], 0);
+    load_first(units[0], 0, first_page(units[0]));
     if (tid == kWalkThread) units[1].take(p, shp, *walk);
     put_query(min(warp, R - 1), q);
     for (int r = warp + W; r < R; r += W) {
@@ -509,7 +516,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
 #pragma unroll
     for (int c = 0; c < 2; ++c) voff[c] = L::kCodes + at_part<D>(kappa<D>(2 * t4 + c), gid * (D / 16) / 16) + gid * (D / 16) % 16;
 
-    prefetch_first(units[un == 2 ? 0 : un + 1]);
+    const int nid = first_page(units[un == 2 ? 0 : un + 1]);  // long before it is wanted
     for (int t = x.t0 + warp; t < end; t += W) {
       load(x, t + (S - 1) * W, end, st == 0 ? S - 1 : st - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
@@ -763,8 +770,8 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
     const bool more = nx.more;
     float q[G];
     if (more) {
-      if constexpr (L::kAhead) load_first(nx, st);
       query_row(nx, min(warp, R - 1), q);
+      if constexpr (L::kAhead) load_first(nx, st, nid);
     }
 
     // ---- the warp's state: [R][D + 4], in the stage that no tile is under way to
@@ -865,7 +872,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
       }
     }
     __syncthreads();
-    if (!L::kAhead && more) load_first(nx, st);
+    if (!L::kAhead && more) load_first(nx, st, nid);
     un = un == 2 ? 0 : un + 1;
   }
   pdl_launch_dependents();
