@@ -65,9 +65,34 @@ template <> struct Oct<__nv_bfloat16> {
 // the pages); cq, ck, cv warps a token for each.
 struct Job {
   int nq, nk, nv, cq, ck, cv;
+  bool vec;    // the tables' rows split into whole vectors for a lane
   long long warps;
   int checks;  // warps behind those, which flag malformed sequences, 32 each
 };
+
+// Packed pairs of fp32: one instruction computes both lanes, each operation rounded by itself.
+__device__ __forceinline__ uint64_t pk(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpk(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
 
 // s + e += x, the error of the sum kept (Knuth's two-sum).
 __device__ __forceinline__ void add_two(float &s, float &e, float x) {
@@ -75,26 +100,39 @@ __device__ __forceinline__ void add_two(float &s, float &e, float x) {
   e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
   s = t;
 }
+__device__ __forceinline__ void add_two2(uint64_t &s, uint64_t &e, uint64_t x) {
+  const uint64_t t = add2(s, x), z = add2(t, neg2(s));
+  e = add2(e, add2(add2(s, neg2(add2(t, neg2(z)))), add2(x, neg2(z))));
+  s = t;
+}
 
 // 1 / sqrt(mean of the row's squares + eps), rounded once to fp32 but for ties within 2^-20 of a
-// step.  All lanes of the warp call it; LPR lanes hold a row.
-template <int LPR>
+// step.  All lanes of the warp call it; LPR lanes hold a row.  EXACT: squares are fp32 numbers (bf16).
+template <int LPR, bool EXACT>
 __device__ __forceinline__ float row_factor(const float (&x)[8], float eps) {
-  float s = 0.f, e = 0.f;
+  // (products that a sum follows are scalar: the packed ones may be contracted with it)
+  auto square = [&](int m) { return pk(__fmul_rn(x[m], x[m]), __fmul_rn(x[m + 1], x[m + 1])); };
+  uint64_t v = pk(x[0], x[1]), s2 = square(0), e2 = EXACT ? 0ull : fma2(v, v, neg2(s2));
 #pragma unroll
-  for (int m = 0; m < 8; ++m) {
-    const float sq = __fmul_rn(x[m], x[m]);
-    e = __fadd_rn(e, fmaf(x[m], x[m], -sq));
-    add_two(s, e, sq);
+  for (int m = 2; m < 8; m += 2) {
+    v = pk(x[m], x[m + 1]);
+    const uint64_t sq = square(m);
+    if (!EXACT) e2 = add2(e2, fma2(v, v, neg2(sq)));
+    add_two2(s2, e2, sq);
   }
+  float s, e, sb, eb;
+  unpk(s2, s, sb);
+  unpk(e2, e, eb);
+  e = __fadd_rn(e, eb);
+  add_two(s, e, sb);
 #pragma unroll
   for (int k = LPR / 2; k > 0; k >>= 1) {
-    const float s2 = __shfl_xor_sync(~0u, s, k), e2 = __shfl_xor_sync(~0u, e, k);
+    const float so = __shfl_xor_sync(~0u, s, k), eo = __shfl_xor_sync(~0u, e, k);
     // both partners take the sums in the same order, so that they stay alike
     const bool low = (threadIdx.x & k) == 0;
-    float a = low ? s : s2;
-    e = __fadd_rn(e, e2);
-    add_two(a, e, low ? s2 : s);
+    float a = low ? s : so;
+    e = __fadd_rn(e, eo);
+    add_two(a, e, low ? so : s);
     s = a;
   }
   s *= 1.f / (LPR * 8);
@@ -121,22 +159,48 @@ __device__ __forceinline__ float row_factor(const float (&x)[8], float eps) {
   return r;
 }
 
+// The larger magnitude; a NaN stays.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
 // Codes of a lane's 8 elements, and the scale of the 32 that it shares with three other lanes.
+//
+// The quotient y / s is rounded correctly by Markstein's theorem (1990): with r = 1 / s rounded
+// correctly and q = y r rounded, q + (y - q s) r is the rounded quotient, the residue exact in one multiply-add.
+// Adding 1.5 2^23 + 8 rounds it to an integer, halves to even, whose last four bits are the code.
 __device__ __forceinline__ uint32_t quantize(const float (&y)[8], uint32_t &scale) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int m = 0; m < 8; ++m) top = max(top, __float_as_uint(y[m]) & 0x7fffffffu);  // orders like |y|, NaN on top
-  top = max(top, __shfl_xor_sync(~0u, top, 1));
-  top = max(top, __shfl_xor_sync(~0u, top, 2));
+  float top = max_abs(max_abs(max_abs(y[0], y[1]), max_abs(y[2], y[3])), max_abs(max_abs(y[4], y[5]), max_abs(y[6], y[7])));
+  top = max_abs(top, __shfl_xor_sync(~0u, top, 1));
+  top = max_abs(top, __shfl_xor_sync(~0u, top, 2));
   // up to four stored bits of the mantissa: the other 19 of the 23, rounded up
-  scale = top >= 0x7f800000u ? 0x7fc00000u : (__float_as_uint(__fdiv_rn(__uint_as_float(top), 7.f)) + 0x7ffffu) & ~0x7ffffu;
+  const uint32_t bits = __float_as_uint(top);
+  scale = bits >= 0x7f800000u ? 0x7fc00000u : (__float_as_uint(__fdiv_rn(top, 7.f)) + 0x7ffffu) & ~0x7ffffu;
   const float s = __uint_as_float(scale);
+  const bool plain = s > 1e-30f && s < 1e30f;  // 1 / s and the residues are normal numbers
   uint32_t word = 0;
+  const float r = __frcp_rn(plain ? s : 1.f);
+  const uint64_t r2 = pk(r, r), ns2 = pk(-s, -s), c2 = pk(12582920.f, 12582920.f);
 #pragma unroll
-  for (int m = 0; m < 8; ++m) {
-    const float q = fminf(fmaxf(rintf(__fdiv_rn(y[m], s)), -7.f), 7.f);
-    const uint32_t c = s > 0.f ? (uint32_t)((int)q + 8) : 8u;
-    word |= c << (4 * m);
+  for (int m = 0; m < 8; m += 2) {
+    const uint64_t v = pk(y[m], y[m + 1]), q = mul2(v, r2), t = add2(fma2(fma2(q, ns2, v), r2, q), c2);
+    float a, b;
+    unpk(t, a, b);
+    // what stands above the last four bits is the same for all: taken off below
+    word += __float_as_uint(a) * (1u << (4 * m)) + __float_as_uint(b) * (16u << (4 * m));
+  }
+  word -= 0x4b400000u * 0x11111111u;
+  if (__any_sync(~0u, !plain)) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const float q = fminf(fmaxf(rintf(__fdiv_rn(y[m], s)), -7.f), 7.f);
+      const uint32_t c = s > 0.f ? (uint32_t)((int)q + 8) : 8u;
+      w |= c << (4 * m);
+    }
+    if (!plain) word = w;
   }
   return word;
 }
@@ -215,16 +279,30 @@ __global__ void __launch_bounds__(i4r::kThreads) i4_append_kernel(const I4Params
       float cs[8], sn[8], wo[8];
 #pragma unroll
       for (int m = 0; m < 8; ++m) cs[m] = 1.f, sn[m] = 0.f;
-      if (turn) {
+      if (turn) {  // the second factor with the sign that the product has
         const T *tc = static_cast<const T *>(p.rcos) + pos * half, *ts = static_cast<const T *>(p.rsin) + pos * half;
+        if (j.vec) {
+          if (e < p.rot_dim) {
+            const int col = e < half ? e : e - half;
+            Oct<T> u;
+            u.load(tc + col);
+            u.get(cs);
+            u.load(ts + col);
+            u.get(sn);
+          }
+        } else {
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          const int i = e + m, col = p.rot_inter ? i / 2 : i < half ? i : i - half;
-          if (i < p.rot_dim) {
-            cs[m] = Elem<T>::load(tc[col]);
-            sn[m] = Elem<T>::load(ts[col]);
+          for (int m = 0; m < 8; ++m) {
+            const int i = e + m, col = p.rot_inter ? i / 2 : i < half ? i : i - half;
+            if (i < p.rot_dim) {
+              cs[m] = Elem<T>::load(tc[col]);
+              sn[m] = Elem<T>::load(ts[col]);
+            }
           }
         }
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          if (p.rot_inter ? m % 2 == 0 : e + m < half) sn[m] = -sn[m];
       }
       if (wt) {
         Oct<T> u;
@@ -238,19 +316,18 @@ __global__ void __launch_bounds__(i4r::kThreads) i4_append_kernel(const I4Params
           float y[8];
           x[i].get(y);
           if (wt) {
-            const float r = row_factor<LPR>(y, p.eps);
+            const float r = row_factor<LPR, sizeof(T) == 2>(y, p.eps);
+            const uint64_t r2 = pk(r, r);
 #pragma unroll
-            for (int m = 0; m < 8; ++m) y[m] = __fmul_rn(__fmul_rn(y[m], r), wo[m]);
+            for (int m = 0; m < 8; m += 2) unpk(mul2(mul2(pk(y[m], y[m + 1]), r2), pk(wo[m], wo[m + 1])), y[m], y[m + 1]);
           }
           if (turn) {
             float z[8];
             partners<LPR>(y, z, e, p.rot_dim, p.rot_inter != 0);
 #pragma unroll
-            for (int m = 0; m < 8; ++m) {
-              const int el = e + m;
-              const bool first = p.rot_inter ? el % 2 == 0 : el < half;
-              const float a = __fmul_rn(y[m], cs[m]), t = __fmul_rn(z[m], sn[m]);
-              if (el < p.rot_dim) y[m] = first ? __fsub_rn(a, t) : __fadd_rn(a, t);
+            for (int m = 0; m < 8; ++m) {  // scalar: packed products may be contracted with the sum
+              const float a = __fadd_rn(__fmul_rn(y[m], cs[m]), __fmul_rn(z[m], sn[m]));
+              if (e + m < p.rot_dim) y[m] = a;
             }
           }
           const int head = h + i * RPW;
@@ -365,6 +442,8 @@ cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read,
   j.nq = nq;
   j.nk = nk;
   j.nv = nv;
+  const int half = p.rot_dim / 2;
+  j.vec = !p.rot_inter && half % 8 == 0 && reinterpret_cast<uintptr_t>(p.rcos) % 16 == 0 && reinterpret_cast<uintptr_t>(p.rsin) % 16 == 0;
   const int rpw = 32 / (p.D / 8);
   auto chunks = [&](int heads, int batch) { return (heads + batch * rpw - 1) / (batch * rpw); };
   const bool many = (long long)p.N * (chunks(nq, 4) + chunks(nk, 4) + chunks(nv, 4)) >= kManyWarps;

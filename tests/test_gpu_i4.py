@@ -89,6 +89,37 @@ def test_append_values_at_the_edges():
     assert torch.equal(back[6], v[6]) and (back[0] == 0).all() and back[3, :32].isnan().all() and (back[3, 32:64] != 7).any()
 
 
+def test_append_turn_rounds_each_operation():
+    """Elements that lie on the border of two codes when every product and sum of the turn is rounded, and
+    below it when a product is contracted with the sum: a c - b with b = fl(a c) - 3.5 scale."""
+    rng = np.random.default_rng(1)
+    t = Batch([(64, 64)], 1, 1, 32, 16, F32, rotary=2, position_ids=True, filled=False)
+    rows = t.cos.shape[0]
+    a, c = np.zeros(rows, np.float32), np.zeros(rows, np.float32)
+    i = 0
+    while i < rows:
+        x, y = (rng.random(2) * 0.5 + 1.0).astype(np.float32)
+        p = x * y
+        if np.float64(x) * np.float64(y) < np.float64(p):  # the rounded product lies above
+            a[i], c[i] = x, y
+            i += 1
+    s = np.float32(1.25)
+    b = a * c - np.float32(3.5) * s
+    assert (a * c - b == np.float32(3.5) * s).all()
+    ids = np.arange(64) % rows
+    x = np.zeros((64, 32), np.float32)
+    x[:, 0], x[:, 1], x[:, 2] = a[ids], b[ids], 7 * s
+    t.cos.copy_(torch.from_numpy(c)[:, None])
+    t.sin.fill_(1.0)
+    t.ids = torch.from_numpy(ids).to(t.k.device)
+    t.k.copy_(torch.from_numpy(x))
+    before = t.snapshot()
+    t.call(gqaw.gqaw_paged_i4_append)
+    t.check_pages(before)
+    t.call(gqaw.gqaw_paged_i4_read)
+    assert (t.ko[:, 0] == 4 * float(s)).all()
+
+
 def test_append_norm_far_rows():
     """Rows whose squares leave fp32 on either side are normed in 64 bits; so is a row of zeros."""
     t = Batch([(8, 8)], 1, 1, 64, 16, F32, norm=True, filled=False)
