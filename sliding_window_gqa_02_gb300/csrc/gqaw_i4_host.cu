@@ -251,11 +251,6 @@ gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cu
   p.blocks = a->page_size % (1024 / D) == 0;
   p.to_values = static_cast<const char *>(p.vp) - static_cast<const char *>(p.kp);
   p.to_value_scales = reinterpret_cast<const char *>(p.vscale) - reinterpret_cast<const char *>(p.kscale);
-  // ceil(2^(31 + l) / page) with 2^l >= page: its excess over the quotient, below 1, times j stays below 2^31 (Granlund, Montgomery)
-  int l = 0;
-  while ((1ll << l) < a->page_size) ++l;
-  p.div_shift = 31 + l;
-  p.div_mul = (uint32_t)(((unsigned __int128)1 << (31 + l)) / a->page_size + (((unsigned __int128)1 << (31 + l)) % a->page_size != 0));
   gqaw::PagedMaps maps;
   gqaw::PagedParams wide;  // kExpand: the attention over the expanded pages
   if (L.path != kRows) {
@@ -357,6 +352,11 @@ gqaw_status run_i4(const gqaw_paged_i4_args *x, void *stream, int what) {
   p.vscale = static_cast<uint16_t *>(a->num_pages ? x->value_scales : a->workspace);
   p.sp = L.sp, p.sh = L.sh, p.sr = L.sr;
   p.tp = L.tp, p.th = L.th, p.tr = L.tr;
+  // ceil(2^(31 + l) / page) with 2^l >= page: its excess over the quotient, below 1, times j stays below 2^31 (Granlund, Montgomery)
+  int l = 0;
+  while ((1ll << l) < a->page_size) ++l;
+  p.div_shift = 31 + l;
+  p.div_mul = (uint32_t)(((unsigned __int128)1 << (31 + l)) / a->page_size + (((unsigned __int128)1 << (31 + l)) % a->page_size != 0));
   p.ko = x->key_out, p.vo = x->value_out;
   p.kos = L.kos, p.vos = L.vos;
   const bool bf16 = a->dtype == GQAW_BF16;

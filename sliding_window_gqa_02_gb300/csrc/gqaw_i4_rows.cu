@@ -66,6 +66,7 @@ template <> struct Oct<__nv_bfloat16> {
 struct Job {
   int nq, nk, nv, cq, ck, cv;
   bool vec;    // the tables' rows split into whole vectors for a lane
+  int batch;   // groups of a warp
   long long warps;
   int checks;  // warps behind those, which flag malformed sequences, 32 each
 };
@@ -92,7 +93,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) { return fma2(b, 0xbf800000bf800000ull, a); }
 
 // s + e += x, the error of the sum kept (Knuth's two-sum).
 __device__ __forceinline__ void add_two(float &s, float &e, float x) {
@@ -101,8 +102,8 @@ __device__ __forceinline__ void add_two(float &s, float &e, float x) {
   s = t;
 }
 __device__ __forceinline__ void add_two2(uint64_t &s, uint64_t &e, uint64_t x) {
-  const uint64_t t = add2(s, x), z = add2(t, neg2(s));
-  e = add2(e, add2(add2(s, neg2(add2(t, neg2(z)))), add2(x, neg2(z))));
+  const uint64_t t = add2(s, x), z = sub2(t, s);
+  e = add2(e, add2(sub2(s, sub2(t, z)), sub2(x, z)));
   s = t;
 }
 
@@ -112,12 +113,12 @@ template <int LPR, bool EXACT>
 __device__ __forceinline__ float row_factor(const float (&x)[8], float eps) {
   // (products that a sum follows are scalar: the packed ones may be contracted with it)
   auto square = [&](int m) { return pk(__fmul_rn(x[m], x[m]), __fmul_rn(x[m + 1], x[m + 1])); };
-  uint64_t v = pk(x[0], x[1]), s2 = square(0), e2 = EXACT ? 0ull : fma2(v, v, neg2(s2));
+  uint64_t v = pk(x[0], x[1]), s2 = square(0), e2 = EXACT ? 0ull : fma2(v, v, sub2(0ull, s2));
 #pragma unroll
   for (int m = 2; m < 8; m += 2) {
     v = pk(x[m], x[m + 1]);
     const uint64_t sq = square(m);
-    if (!EXACT) e2 = add2(e2, fma2(v, v, neg2(sq)));
+    if (!EXACT) e2 = add2(e2, fma2(v, v, sub2(0ull, sq)));
     add_two2(s2, e2, sq);
   }
   float s, e, sb, eb;
@@ -177,9 +178,12 @@ __device__ __forceinline__ uint32_t quantize(const float (&y)[8], uint32_t &scal
   top = max_abs(top, __shfl_xor_sync(~0u, top, 2));
   // up to four stored bits of the mantissa: the other 19 of the 23, rounded up
   const uint32_t bits = __float_as_uint(top);
-  scale = bits >= 0x7f800000u ? 0x7fc00000u : (__float_as_uint(__fdiv_rn(top, 7.f)) + 0x7ffffu) & ~0x7ffffu;
+  constexpr float kSeventh = 1.f / 7.f;
+  const float seventh = __fmul_rn(top, kSeventh);
+  scale = (__float_as_uint(fmaf(fmaf(-seventh, 7.f, top), kSeventh, seventh)) + 0x7ffffu) & ~0x7ffffu;
+  const bool plain = top > 1e-29f && top < 1e30f;  // 1 / s and the residues are normal numbers
+  if (!plain) scale = bits >= 0x7f800000u ? 0x7fc00000u : (__float_as_uint(__fdiv_rn(top, 7.f)) + 0x7ffffu) & ~0x7ffffu;
   const float s = __uint_as_float(scale);
-  const bool plain = s > 1e-30f && s < 1e30f;  // 1 / s and the residues are normal numbers
   uint32_t word = 0;
   const float r = __frcp_rn(plain ? s : 1.f);
   const uint64_t r2 = pk(r, r), ns2 = pk(-s, -s), c2 = pk(12582920.f, 12582920.f);
@@ -232,32 +236,32 @@ __device__ __forceinline__ void partners(const float (&y)[8], float (&z)[8], int
 
 }  // namespace i4r
 
-// A warp has BATCH groups of 32 / LPR heads of one tensor of one token.
-template <typename T, int LPR, int BATCH>
-__global__ void __launch_bounds__(i4r::kThreads) i4_append_kernel(const I4Params p, const i4r::Job j) {
+// A warp has `batch` groups of 32 / LPR heads of one tensor of one token, one after the other (unrolled four times
+// the loop ran out of the instruction cache), the next one's elements on their way.
+#ifndef MINB
+#define MINB 5
+#endif
+template <typename T, int LPR>
+__global__ void __launch_bounds__(i4r::kThreads, MINB) i4_append_kernel(const I4Params p, const i4r::Job j) {
   using namespace i4r;
   constexpr int RPW = 32 / LPR, D = LPR * 8;
   const int lane = threadIdx.x & 31, lr = lane % LPR, sub = lane / LPR, e = lr * 8;
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   pdl_wait();
   if (w < j.warps) {
-    const int chunks = j.cq + j.ck + j.cv, n = (int)(w / chunks);
-    int c = (int)(w - (long long)n * chunks);
+    const int chunks = j.cq + j.ck + j.cv, n = (int)((uint32_t)w / (uint32_t)chunks);  // fewer than 2^31 rows
+    int c = (int)w - n * chunks;
     const int kind = c < j.cq ? 0 : c < j.cq + j.ck ? 1 : 2;  // queries, keys, values
     c -= kind == 0 ? 0 : kind == 1 ? j.cq : j.cq + j.ck;
-    const int nh = kind == 0 ? j.nq : kind == 1 ? j.nk : j.nv, h = c * (BATCH * RPW) + sub;
+    const int nh = kind == 0 ? j.nq : kind == 1 ? j.nk : j.nv, first = c * (j.batch * RPW), h = first + sub;
+    const int groups = min(j.batch, (nh - first + RPW - 1) / RPW);
     // the rows themselves, ahead of the dependent look-ups; lanes past the heads run along on ones
-    Oct<T> x[BATCH];
+    Oct<T> x;
+    x.ones();
     const T *in = (kind == 0   ? static_cast<const T *>(p.q) + n * p.qs
                    : kind == 1 ? static_cast<const T *>(p.k) + n * p.ks
                                : static_cast<const T *>(p.v) + n * p.vs) + (long long)h * D + e;
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      if (h + i * RPW < nh)
-        x[i].load(in + i * RPW * D);
-      else
-        x[i].ones();
-    }
+    if (h < nh) x.load(in);
     const int b = find_sequence(batch_of(p), n);
     if (b >= 0) {  // else nobody's, or a malformed sequence's
       long long pos = (long long)p.seqlens[b] + 1 - (p.qstart[b + 1] - n);
@@ -310,11 +314,12 @@ __global__ void __launch_bounds__(i4r::kThreads) i4_append_kernel(const I4Params
         u.get(wo);
       }
       if (at.page >= 0) {
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          if (c * (BATCH * RPW) + i * RPW >= nh) break;  // uniform over the warp
+#pragma unroll 1
+        for (int i = 0; i < groups; ++i) {
           float y[8];
-          x[i].get(y);
+          x.get(y);
+          x.ones();
+          if (i + 1 < groups && h + (i + 1) * RPW < nh) x.load(in + (i + 1) * RPW * D);
           if (wt) {
             const float r = row_factor<LPR, sizeof(T) == 2>(y, p.eps);
             const uint64_t r2 = pk(r, r);
@@ -372,8 +377,8 @@ __global__ void __launch_bounds__(i4r::kThreads) i4_read_kernel(const I4Params p
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   pdl_wait();
   if (w < j.warps) {
-    const int chunks = j.ck + j.cv, n = (int)(w / chunks);
-    int c = (int)(w - (long long)n * chunks);
+    const int chunks = j.ck + j.cv, n = (int)((uint32_t)w / (uint32_t)chunks);
+    int c = (int)w - n * chunks;
     const bool value = c >= j.ck;
     c -= value ? j.ck : 0;
     const int nh = value ? j.nv : j.nk, h = c * (BATCH * RPW) + sub;
@@ -416,20 +421,20 @@ __global__ void __launch_bounds__(i4r::kThreads) i4_read_kernel(const I4Params p
 namespace i4r {
 
 template <bool READ, typename T, int LPR>
-cudaError_t launch(const I4Params &p, const Job &j, int batch, const cudaLaunchConfig_t &cfg) {
+cudaError_t launch(const I4Params &p, const Job &j, const cudaLaunchConfig_t &cfg) {
   if constexpr (READ)
-    return batch == 4 ? cudaLaunchKernelEx(&cfg, i4_read_kernel<T, LPR, 4>, p, j) : cudaLaunchKernelEx(&cfg, i4_read_kernel<T, LPR, 2>, p, j);
+    return j.batch == 4 ? cudaLaunchKernelEx(&cfg, i4_read_kernel<T, LPR, 4>, p, j) : cudaLaunchKernelEx(&cfg, i4_read_kernel<T, LPR, 2>, p, j);
   else
-    return batch == 4 ? cudaLaunchKernelEx(&cfg, i4_append_kernel<T, LPR, 4>, p, j) : cudaLaunchKernelEx(&cfg, i4_append_kernel<T, LPR, 2>, p, j);
+    return cudaLaunchKernelEx(&cfg, i4_append_kernel<T, LPR>, p, j);
 }
 
 template <bool READ, typename T>
-cudaError_t launch_d(const I4Params &p, const Job &j, int batch, const cudaLaunchConfig_t &cfg) {
+cudaError_t launch_d(const I4Params &p, const Job &j, const cudaLaunchConfig_t &cfg) {
   switch (p.D) {
-    case 32: return launch<READ, T, 4>(p, j, batch, cfg);
-    case 64: return launch<READ, T, 8>(p, j, batch, cfg);
-    case 128: return launch<READ, T, 16>(p, j, batch, cfg);
-    default: return launch<READ, T, 32>(p, j, batch, cfg);
+    case 32: return launch<READ, T, 4>(p, j, cfg);
+    case 64: return launch<READ, T, 8>(p, j, cfg);
+    case 128: return launch<READ, T, 16>(p, j, cfg);
+    default: return launch<READ, T, 32>(p, j, cfg);
   }
 }
 
@@ -446,11 +451,14 @@ cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read,
   j.vec = !p.rot_inter && half % 8 == 0 && reinterpret_cast<uintptr_t>(p.rcos) % 16 == 0 && reinterpret_cast<uintptr_t>(p.rsin) % 16 == 0;
   const int rpw = 32 / (p.D / 8);
   auto chunks = [&](int heads, int batch) { return (heads + batch * rpw - 1) / (batch * rpw); };
-  const bool many = (long long)p.N * (chunks(nq, 4) + chunks(nk, 4) + chunks(nv, 4)) >= kManyWarps;
-  const int batch = many ? 4 : 2;
-  j.cq = chunks(nq, batch);
-  j.ck = chunks(nk, batch);
-  j.cv = chunks(nv, batch);
+#ifndef BBIG
+#define BBIG 4
+#endif
+  auto warps = [&](int batch) { return (long long)p.N * (chunks(nq, batch) + chunks(nk, batch) + chunks(nv, batch)); };
+  j.batch = read ? (warps(4) >= kManyWarps ? 4 : 2) : warps(BBIG) >= kManyWarps ? BBIG : warps(2) >= kManyWarps ? 2 : 1;
+  j.cq = chunks(nq, j.batch);
+  j.ck = chunks(nk, j.batch);
+  j.cv = chunks(nv, j.batch);
   j.warps = (long long)p.N * (j.cq + j.ck + j.cv);
   j.checks = (p.B + 31) / 32;
   cudaLaunchConfig_t cfg = {};
@@ -462,8 +470,8 @@ cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = read ? (bf16 ? launch_d<true, __nv_bfloat16>(p, j, batch, cfg) : launch_d<true, float>(p, j, batch, cfg))
-                             : (bf16 ? launch_d<false, __nv_bfloat16>(p, j, batch, cfg) : launch_d<false, float>(p, j, batch, cfg));
+  const cudaError_t e = read ? (bf16 ? launch_d<true, __nv_bfloat16>(p, j, cfg) : launch_d<true, float>(p, j, cfg))
+                             : (bf16 ? launch_d<false, __nv_bfloat16>(p, j, cfg) : launch_d<false, float>(p, j, cfg));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
