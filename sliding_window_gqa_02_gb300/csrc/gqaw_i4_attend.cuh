@@ -1,5 +1,5 @@
-// gqaw_i4_attend.cuh -- attention over a paged cache held in 4 bits, up to 32 query rows of a kv
-// head at once.
+// gqaw_i4_attend.cuh -- attention over a paged cache held in 4 bits, 8 query rows of a kv head at once
+// (fp32: 16).
 //
 //     o_i = sum_j softmax_j(cap(scale q_i k_j)) v_j,  j <= i (and j > i - W), with sinks,
 // k = (c - 8) s and v likewise, c the code of an element and s the scale of its 32 elements.
@@ -42,15 +42,7 @@
 #pragma once
 
 #include <atomic>
-#ifndef GQAW_W
-#define GQAW_W 12
-#endif
-#ifndef GQAW_W2
-#define GQAW_W2 8
-#endif
-#ifndef GQAW_SB
-#define GQAW_SB 2
-#endif
+#include <type_traits>
 
 #include "gqaw_i4.cuh"
 #include "gqaw_paged_tc.cuh"
@@ -60,7 +52,9 @@ namespace gqaw {
 namespace i4a {
 
 constexpr int kKeys = 32;      // a warp's tile
-constexpr int kUnitCost = 32, kMergeCost = 32, kMinTiles = 12;  // see gqaw_paged_sched.cuh
+// See gqaw_paged_sched.cuh.  20 to 48 tiles a unit, and 32 or 60 a cut, differ by 2%, but for 16 contexts of 8192
+// keys and 8 heads, whose units are better whole (58 us with 32, 52 with 60).
+constexpr int kUnitCost = 32, kMergeCost = 60, kMinTiles = 12;
 constexpr float kTopP = 13.f;  // log2 of the largest weight when the reference moves
 constexpr float kMaxP = 15.f;  // ... and of any
 constexpr int kTopV = 10;      // a scale's largest power of two becomes 2^kTopV: 24 s < 2^16
@@ -73,7 +67,7 @@ struct Lay {
   static constexpr int kCodes = kKeys * kRow;            // of a tile
   static constexpr int kScales = kKeys * G * 2;
   static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V, their scales; a multiple of the swizzle's span
-  static constexpr int W = NT > 2 || D == 256 ? 8 : NT == 2 ? GQAW_W2 : GQAW_W;
+  static constexpr int W = NT > 1 || D == 256 ? 8 : 12;
   static constexpr int kFit = 170 * 1024 / (W * kStage), S = kFit > 8 ? 8 : kFit;  // stages
   static_assert(S >= 2, "a tile under way beside the one at hand");
   static constexpr int kThreads = 32 * W;
@@ -138,11 +132,6 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 // (x & mask) | bits
@@ -277,7 +266,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   constexpr int W = L::W, S = L::S, G = L::G, R = L::R, PS = L::PS;
   constexpr int PP = sizeof(T) == 4 ? 2 : 1;         // parts of a weight
   constexpr bool kQreg = NT * QP * G <= 8;           // query operands in registers
-  constexpr int SB = NT == 1 ? GQAW_SB : 1;                // blocks of 16 keys at once
+  constexpr int SB = NT == 1 ? 2 : 1;                  // blocks of 16 keys at once
   constexpr int VW = D >= 64 ? D / 64 : 1;           // words of a lane's codes of a value row (D = 32: half of one)
   constexpr int VT = D / 16;                         // operands of 16 dimensions
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kTop = 0x03c003c0u;
@@ -905,20 +894,21 @@ cudaError_t launch_i4_attend_one(const I4Params &p, int sms, cudaStream_t stream
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// nt: 1, 2 or 4 (head size 256: 1 or 2) operands of 8 rows.
+// nt: operands of 8 query rows, 1 or (fp32 at head sizes up to 128) 2.
 template <typename T, int QP>
 cudaError_t launch_i4_attend_t(const I4Params &p, int nt, int sms, cudaStream_t stream) {
-#define GQAW_I4_D(D)                                                                      \
-  return nt == 1   ? launch_i4_attend_one<T, D, 1, QP>(p, sms, stream)              \
-         : nt == 2 ? launch_i4_attend_one<T, D, 2, QP>(p, sms, stream)              \
-                   : launch_i4_attend_one<T, D, D == 256 ? 2 : 4, QP>(p, sms, stream)
+  auto pick = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if constexpr (sizeof(T) == 4 && D <= 128)
+      if (nt == 2) return launch_i4_attend_one<T, D, 2, QP>(p, sms, stream);
+    return launch_i4_attend_one<T, D, 1, QP>(p, sms, stream);
+  };
   switch (p.D) {
-    case 32: GQAW_I4_D(32);
-    case 64: GQAW_I4_D(64);
-    case 128: GQAW_I4_D(128);
-    default: GQAW_I4_D(256);
+    case 32: return pick(std::integral_constant<int, 32>());
+    case 64: return pick(std::integral_constant<int, 64>());
+    case 128: return pick(std::integral_constant<int, 128>());
+    default: return pick(std::integral_constant<int, 256>());
   }
-#undef GQAW_I4_D
 }
 
 }  // namespace gqaw

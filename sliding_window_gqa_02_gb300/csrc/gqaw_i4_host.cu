@@ -79,16 +79,19 @@ gqaw_status plan_i4(const gqaw_paged_i4_args *x, I4Plan *L) {
       (s = row_stride("key_out_stride", x->key_out_stride, krow, L->es, a->total_new_tokens, &L->kos)) != GQAW_OK ||
       (s = row_stride("value_out_stride", x->value_out_stride, krow, L->es, a->total_new_tokens, &L->vos)) != GQAW_OK)
     return s;
-  // The kernel: 8 query rows of a kv head a product, and as many of them as the longest chunk fills, at
-  // most 4 (head size 256: 2), which is what registers hold.
+  // The kernel: 8 query rows of a kv head a product, more by query tiles that read the keys again (from L2): 16
+  // rows at once, whose registers leave 8 warps a SM, take as long (16 x 8 tokens at 6000 keys, window 4096,
+  // 109 us both ways) or longer (head size 64 56 -> 67, 256 91 -> 136), and 32 longer still (156).  In fp32, where
+  // every product is two, 16 are faster (a prompt of 1024 259 -> 214 us, 8 x 8 tokens 72 -> 60).
   const long long rows = (long long)std::max(1, a->max_new_tokens) * L->group;
-  L->nt = rows <= 8 ? 1 : 2;
+  L->nt = rows > 8 && a->dtype == GQAW_F32 && D <= 128 ? 2 : 1;
   L->path = kRows;
   // Single tokens among chunks would fill 8 of the rows: they have a launch of their own where there
   // may be many (the others hold at most max_new_tokens, which bounds their number)
   constexpr int kShort = 64;
   const int seqs = std::min(gqaw::kPagedItems, a->batch_size);
-  const long long tok = L->nt > 1 && L->group <= 8 ? 8 / L->group : 0;
+  const bool wide = L->nt > 1 || (rows > 32 && a->dtype == GQAW_BF16 && D >= 64);
+  const long long tok = wide && L->group <= 8 ? 8 / L->group : 0;
   const long long spare = (long long)a->total_new_tokens - a->batch_size * tok;
   if (tok && (a->batch_size - (spare > 0 ? ceil_div(spare, a->max_new_tokens) : 0)) * a->kv_num_heads >= kShort) L->few = (int)tok;
   // More rows in bf16: the 5th-generation tensor cores.

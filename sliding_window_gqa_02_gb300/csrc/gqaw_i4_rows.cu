@@ -11,7 +11,8 @@
 // sums and products carried along), r is rounded once, and every other operation is one IEEE
 // operation.  The same for queries, so that a step's are those of any other implementation.
 //
-// Bound: HBM for many tokens, latency for few.  A lane has 8 consecutive elements of a head (16 or
+// Bound: the append by its instructions for many tokens (some 360 for 256 elements; 2313 tokens of 1 to 8
+// heads at 16 bits 14 us, 70% of the issue slots), by latency for few (64 tokens 5.6 us).  A lane has 8 consecutive elements of a head (16 or
 // 32 bytes in, 4 bytes out), D / 8 lanes a row; a group's maximum is two exchanges among four lanes.
 // Reading back is the inverse.
 #include "gqaw_i4.cuh"
@@ -238,11 +239,8 @@ __device__ __forceinline__ void partners(const float (&y)[8], float (&z)[8], int
 
 // A warp has `batch` groups of 32 / LPR heads of one tensor of one token, one after the other (unrolled four times
 // the loop ran out of the instruction cache), the next one's elements on their way.
-#ifndef MINB
-#define MINB 5
-#endif
 template <typename T, int LPR>
-__global__ void __launch_bounds__(i4r::kThreads, MINB) i4_append_kernel(const I4Params p, const i4r::Job j) {
+__global__ void __launch_bounds__(i4r::kThreads, 5) i4_append_kernel(const I4Params p, const i4r::Job j) {
   using namespace i4r;
   constexpr int RPW = 32 / LPR, D = LPR * 8;
   const int lane = threadIdx.x & 31, lr = lane % LPR, sub = lane / LPR, e = lr * 8;
@@ -451,11 +449,8 @@ cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read,
   j.vec = !p.rot_inter && half % 8 == 0 && reinterpret_cast<uintptr_t>(p.rcos) % 16 == 0 && reinterpret_cast<uintptr_t>(p.rsin) % 16 == 0;
   const int rpw = 32 / (p.D / 8);
   auto chunks = [&](int heads, int batch) { return (heads + batch * rpw - 1) / (batch * rpw); };
-#ifndef BBIG
-#define BBIG 4
-#endif
   auto warps = [&](int batch) { return (long long)p.N * (chunks(nq, batch) + chunks(nk, batch) + chunks(nv, batch)); };
-  j.batch = read ? (warps(4) >= kManyWarps ? 4 : 2) : warps(BBIG) >= kManyWarps ? BBIG : warps(2) >= kManyWarps ? 2 : 1;
+  j.batch = read ? (warps(4) >= kManyWarps ? 4 : 2) : warps(4) >= kManyWarps ? 4 : warps(2) >= kManyWarps ? 2 : 1;
   j.cq = chunks(nq, j.batch);
   j.ck = chunks(nk, j.batch);
   j.cv = chunks(nv, j.batch);
