@@ -461,7 +461,7 @@ size_t gqaw_paged_args_size(void);
  * value a bf16 number: reading a row back as bf16 or fp32 loses nothing, and the tensor cores
  * see the values that the cache holds.  Other writers may use any bf16 scale and any code; a
  * product of more than eight bits is then rounded to bf16 where it is needed as bf16 (reading
- * back as bf16, attention of more than 32 query rows per kv head in bf16).
+ * back as bf16, the attention of prompt chunks in bf16).
  * ------------------------------------------------------------------------------- */
 
 #define GQAW_I4_GROUP 32
@@ -491,8 +491,9 @@ typedef struct gqaw_paged_i4_args {
   int64_t value_out_stride;
 } gqaw_paged_i4_args;
 
-/* Workspace bytes of any of the four calls below, as gqaw_paged_workspace_bytes(); an append and a
- * read need 256 bytes alone, for the device status word.  A workspace serves paged calls on 4-bit and
+/* Workspace bytes of any of the four calls below, as gqaw_paged_workspace_bytes(); with prompt chunks it
+ * holds the rows that they attend as bf16 too, where those are 2 GiB at most for the longest sequences
+ * that the call allows.  An append and a read need 256 bytes alone, for the device status word.  A workspace serves paged calls on 4-bit and
  * on other caches alike, in stream order, if it is large enough for each. */
 size_t gqaw_paged_i4_workspace_bytes(const gqaw_paged_i4_args *args);
 
@@ -503,10 +504,10 @@ size_t gqaw_paged_i4_workspace_bytes(const gqaw_paged_i4_args *args);
 gqaw_status gqaw_paged_i4_append(const gqaw_paged_i4_args *args, void *stream);
 
 /* Attention over the cache as gqaw_paged_attend; logits and outputs are those of the values that
- * the codes stand for.  Sums and statistics are fp32.  Up to 32 query rows per kv head in a
- * sequence (and fp32 rows at any number) are multiplied as they are, in two parts of fp16 for
- * fp32; the softmax weights, times the value scales, are rounded to fp16 (2^-12 relative), or
- * two parts of it for fp32.  More rows in bf16: softmax weights are rounded to bf16. */
+ * the codes stand for.  Sums and statistics are fp32.  Queries are multiplied as they are, fp32
+ * ones in two parts of fp16; the softmax weights, times the value scales, are rounded to fp16
+ * (2^-12 relative), or two parts of it for fp32.  Prompt chunks in bf16 (more than 40 query rows per kv
+ * head in a sequence, 64 with head size 256, and more than a little work): weights are rounded to bf16. */
 gqaw_status gqaw_paged_i4_attend(const gqaw_paged_i4_args *args, void *stream);
 
 /* The whole step as gqaw_paged_step: append, and attention of the normed and turned queries. */

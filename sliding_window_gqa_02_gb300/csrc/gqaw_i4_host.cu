@@ -86,24 +86,31 @@ gqaw_status plan_i4(const gqaw_paged_i4_args *x, I4Plan *L) {
   const long long rows = (long long)std::max(1, a->max_new_tokens) * L->group;
   L->nt = rows > 8 && a->dtype == GQAW_F32 && D <= 128 ? 2 : 1;
   L->path = kRows;
+  // Many rows in bf16: the 5th-generation tensor cores, whose tiles of keys cost as much for 1 row as for 128.  16
+  // chunks at 6000 keys (window 4096, 8 heads) cross at 36 rows with head size 64, 50 with 128, 62 with 256.
+  // With little work in all (rows times keys) their fixed part decides, a CTA that joins a unit's many cuts: one
+  // chunk at 6000 keys and head size 128, 128 rows 67 us and 44 by rows, 256 72 and 76; at 1000 keys 256 rows
+  // 40 and 38 (head size 256 43 and 62, 128 rows 43 and 27); 4 chunks of 48 rows at 6000 70 and 64, of 128 66
+  // and 134; one of 128 at 32000 105 and 154.
+  const long long span = a->local_window_size > 0 ? std::min<long long>(a->max_sequence_length, (long long)a->local_window_size + a->max_new_tokens)
+                                                   : a->max_sequence_length;
+  constexpr double kLittle = 1e7;
+  const bool little = rows <= (D == 256 ? 128 : 256) && (double)a->total_new_tokens * a->num_heads * span <= kLittle;
+  const bool many = a->dtype == GQAW_BF16 && D >= 64 && L->group <= 128 && rows > (D == 256 ? 64 : 40) && !little &&
+                    std::max<long long>(L->qs, a->num_heads * D) * L->es < (1ll << 40);
   // Single tokens among chunks would fill 8 of the rows: they have a launch of their own where there
   // may be many (the others hold at most max_new_tokens, which bounds their number)
   constexpr int kShort = 64;
   const int seqs = std::min(gqaw::kPagedItems, a->batch_size);
-  const bool wide = L->nt > 1 || (rows > 32 && a->dtype == GQAW_BF16 && D >= 64);
-  const long long tok = wide && L->group <= 8 ? 8 / L->group : 0;
+  const long long tok = (L->nt > 1 || many) && L->group <= 8 ? 8 / L->group : 0;
   const long long spare = (long long)a->total_new_tokens - a->batch_size * tok;
   if (tok && (a->batch_size - (spare > 0 ? ceil_div(spare, a->max_new_tokens) : 0)) * a->kv_num_heads >= kShort) L->few = (int)tok;
-  // More rows in bf16: the 5th-generation tensor cores.
-  if (rows > 32 && a->dtype == GQAW_BF16 && D >= 64 && L->group <= 128 &&
-      std::max<long long>(L->qs, a->num_heads * D) * L->es < (1ll << 40)) {
+  if (many) {
     // Expanded where a sequence may have more than one query tile and the workspace does not grow beyond kMost:
     // for every sequence what its tokens attend (row ranges that repeat rows may make chunks of all)
     constexpr unsigned long long kMost = 2ull << 30;
     L->halves = D <= 128 ? 2 : 1;
     L->tpt = L->halves * (128 / L->group);
-    const long long span = a->local_window_size > 0 ? std::min<long long>(a->max_sequence_length, (long long)a->local_window_size + a->max_new_tokens)
-                                                     : a->max_sequence_length;
     const long long pages = seqs * (ceil_div(span, 128) + 1);
     const unsigned long long bytes = (unsigned long long)pages * 128 * a->kv_num_heads * D * 4;
     if (D == 256 ? bytes <= kMost : a->max_new_tokens > L->tpt && bytes <= kMost)

@@ -142,7 +142,7 @@ class Batch:
         ``ref.attend``'s bound, with what these kernels round: a query element is taken in one (bf16) or
         two parts of fp16 after a power of two for its row (2^-23 relative to it, or 2^-39 of the row's
         largest for the smallest ones), turned queries of bf16 in two parts (u^2), and each weight, or
-        weight times value scale, to fp16 (2^-12; fp32: two parts, 2^-23), or to bf16 with more than 32 rows.
+        weight times value scale, to fp16 (2^-12; fp32: two parts, 2^-23), or to bf16 with many rows.
 
         The types end: a weight of a key below fp32's smallest normal number, 2^-126 of the row's largest,
         may count as nothing, and a result below it is rounded to a multiple of bf16's smallest number, 2^-133.
@@ -150,7 +150,7 @@ class Batch:
         and what is rounded to a subnormal is off by up to 2^-25: 2^-37 s, times a code of at most 8, where
         the largest value is at least s or there is none: 2^-34 of it a key.
 
-        Scales that the append did not write: with more than 32 rows in bf16 every key and value element is
+        Scales that the append did not write: with many rows in bf16 every key and value element is
         rounded once to bf16 (u), the keys' share in a logit like a query's, the values' beside the weights'."""
         rounds = self.odd_scales and self.dtype == torch.bfloat16 and self.max_new * (self.Nq // self.Nkv) > 32
         if turned:

@@ -222,6 +222,17 @@ def test_chunks_either_way(max_len, kw):
         assert (t.out[t.untouched()] == 7.0).all()
 
 
+@pytest.mark.parametrize("max_len", [0, 8192, LONG])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_chunks_by_the_work_that_a_call_may_be(D, max_len):
+    """The same chunks by rows, with expanded keys (head size 256) and as codes: a call chooses by the longest
+    sequences that it allows."""
+    t = Batch([(32, 300), (1, 90), (20, 1000), (2, 2)], 8, 2, D, 16, BF16, seed=3, max_len=max_len, lead_rows=1, extra_rows=2)
+    t.call(gqaw.gqaw_paged_i4_attend)
+    t.check_output()
+    assert (t.out[t.untouched()] == 7.0).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("opt", [dict(window=1), dict(window=100, softcap=30.0), dict(sink=True), dict(smooth=True, softcap=2.0),
                                  dict(scale=2.0), dict(odd_scales=True), dict(odd_scales=True, window=33)])
