@@ -34,6 +34,11 @@
 // instructions, and every lane's own look-ups 200.  A unit's first tiles are under way before the last
 // unit's rows go out.  Schedule, splits and merges: gqaw_paged.cuh.
 //
+// Measured: 64 contexts of 4 k to 33 k keys (8 kv heads of 128, 4 query heads each) 257 us, 4.05 TB/s or 60% of
+// the copy rate: issue slots are 44 to 52% busy with some 337 instructions for 16 keys of a warp (148 of them keys
+// and softmax, 128 values, 37 scales, 24 loads), 12 warps a SM hide no more of each other's latencies, and registers
+// (168) allow no more.  A unit's start and end are 4 to 6 us, the schedule 2, a cut 3.5.
+//
 // Which of 8 rows is which: position x of 8 is key kappa(x) of a tile's, chosen so that the rows of
 // the even positions lie in different banks when four lanes read their dimensions of them.
 //
