@@ -3,6 +3,13 @@
 
 namespace gqaw {
 
+// What the models on the host take from this file: the schedule's cost of a unit, and the buffers of odd bits.
+namespace model {
+constexpr int kUnitCost = 3;
+constexpr int kOddBufs = 3;
+static_assert(kUnitCost == ppre::kUnitCost && kOddBufs == ppre::kOddBufs, "the kernels'");
+}  // namespace model
+
 // halves: query tiles of 128 rows per unit, 1 or 2 (2: head sizes 64 and 128).  The queries come
 // in two parts where p.qlo is set.
 cudaError_t launch_paged_prefill(const PagedParams &p, const PagedMaps &maps, int halves, int grid, cudaStream_t stream) {
