@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
 #pragma unroll
     for (int i = 0; i < G; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
     top = __reduce_max_sync(0xffffffffu, top);
-    const int e = top ? min(140 - (int)(top >> 23), 126) : 0;  // x 2^e: the largest at 2^13
+    // x 2^e: the largest at 2^13; a row that is not finite stays so and takes no part in what rows share
+    const int e = top && top < 0x7f800000u ? min(140 - (int)(top >> 23), 126) : 0;
     const int nib = lane & 7, step = (nib >> 1) & 1;
     const float f = nib & 1 ? 0.0625f : 1.f, back = nib & 1 ? -8.f * 16.f / 16777216.f : -8.f / 16777216.f;  // a code of an odd nibble counts 16 times
 #pragma unroll
@@ -477,8 +478,9 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
       }
     }
     // z = (sum s 2^se acc) 2^(24 - se - e) qscale, e the row's power of two; se is not 0 where queries are
-    // so large (e < 0) that the keys' scales may be too small for fp32 beside acc < 1
-    const int se = -min(0, __reduce_min_sync(0xffffffffu, lane < rows ? sqexp[min(lane, R - 1)] : 0));
+    // so large (e < 0) that the keys' scales may be too small for fp32 beside acc < 1: the smallest, 2^-133, times
+    // what of acc counts, 2^-26 and more, is a normal number with 2^40, and other rows' scales up to 2^87 have room
+    const int se = min(40, -min(0, __reduce_min_sync(0xffffffffu, lane < rows ? sqexp[min(lane, R - 1)] : 0)));
     const float sfac = pow2(se);
     float qf[NT][2], nb[NT][2], th[NT][2], l[NT][2];  // factor; minus the reference; what a logit less the reference may be
 #pragma unroll

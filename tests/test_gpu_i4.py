@@ -286,6 +286,26 @@ def test_attend_queries_of_any_size(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 3e37, -1e30])
+def test_attend_one_query_row_does_not_reach_the_others(dtype, value):
+    """A head of one token that is not finite or very large, beside large keys: other rows keep their bits."""
+    for D in (64, 128):
+        t = Batch([(3, 90), (1, 40)], 4, 2, D, 16, dtype, seed=12, scale=2.0 ** -20)
+        t.ks.copy_((t.ks.float() * 2.0 ** 20).to(BF16))
+        t.call(gqaw.gqaw_paged_i4_attend)
+        t.check_output()
+        before = t.out.clone().reshape(-1, 4, D)
+        t.q[1, D + 5] = value  # token 1, head 1
+        t.call(gqaw.gqaw_paged_i4_attend)
+        after = t.out.reshape(-1, 4, D)
+        same = torch.ones(4, 4, dtype=torch.bool)
+        same[1, 1] = False
+        assert torch.equal(after[same], before[same])
+        if value != value or abs(value) == float("inf"):
+            assert after[1, 1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("S,max_len", [(1, 0), (6, 0), (40, 0), (70, 0), (70, LONG)])
 def test_attend_scales_that_are_not_finite(dtype, S, max_len):
     """A value scale that is NaN or infinite reaches the 32 elements of its group in the outputs of tokens that
