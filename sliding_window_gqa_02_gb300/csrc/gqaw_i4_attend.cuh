@@ -26,7 +26,10 @@
 // most 2^15, since the row's reference moves when that is exceeded (and then puts the largest at 2^13); a
 // value scale is taken relative to the largest power of two of its group so far, which becomes 2^10: no
 // product leaves fp16, and whatever the scales' size none is lost beside 2^-35.  Sums and statistics are
-// fp32.
+// fp32.  The tensor cores cut what a sum loses, which adds up over a long context: for fp32 rows (kExact) the codes of
+// the keys are signed, so that no large sum is taken back, a product's values are added outside, the smaller
+// parts come first, and exponents are taken near 0 (error against 64 bits at 500 to 12,000 keys 9.6e-7 -> 2e-7, the
+// time the same).  The reference moves by whole powers of two and is never rounded.
 //
 // Each warp works on its own, on tiles of 32 keys through a ring of its own; no barrier of the CTA
 // falls inside a unit.  Tiles come by cp.async through the page table, any page size and strides; with
@@ -132,6 +135,11 @@ __device__ __forceinline__ float2 floats_of(uint32_t h) { return __half22float2(
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -270,6 +278,9 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   using L = Lay<D, NT, QP>;
   constexpr int W = L::W, S = L::S, G = L::G, R = L::R, PS = L::PS;
   constexpr int PP = sizeof(T) == 4 ? 2 : 1;         // parts of a weight
+  constexpr bool kExact = sizeof(T) == 4;            // see above
+  // Exponents of fp32 rows are taken near 0, where they have most bits, and the power of two comes after
+  constexpr float kTopZ = kExact ? 0.f : kTopP, kMaxZ = kExact ? kMaxP - kTopP : kMaxP;
   constexpr bool kQreg = NT * QP * G <= 8;           // query operands in registers
   constexpr int SB = NT == 1 ? 2 : 1;                  // blocks of 16 keys at once
   constexpr int VW = D >= 64 ? D / 64 : 1;           // words of a lane's codes of a value row (D = 32: half of one)
@@ -431,10 +442,12 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
         q[NT * 2 * G * 32 * 4] = h2;
         sum += __half2float(h2);
       }
-      sum *= back;
+      if constexpr (!kExact) {
+        sum *= back;
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      if (lane == 0) sqsum[i * R + r] = sum;
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        if (lane == 0) sqsum[i * R + r] = sum;
+      }
     }
     if (lane == 0) sqexp[r] = e;
   };
@@ -481,7 +494,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
     // so large (e < 0) that the keys' scales may be too small for fp32 beside acc < 1: the smallest, 2^-133, times
     // what of acc counts, 2^-26 and more, is a normal number with 2^40, and other rows' scales up to 2^87 have room
     const int se = min(40, -min(0, __reduce_min_sync(0xffffffffu, lane < rows ? sqexp[min(lane, R - 1)] : 0)));
-    const float sfac = pow2(se);
+    const float sfac = pow2(se - (kExact ? 24 : 0));  // (signed codes are whole numbers, not multiples of 2^-24)
     float qf[NT][2], nb[NT][2], th[NT][2], l[NT][2];  // factor; minus the reference; what a logit less the reference may be
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -609,23 +622,35 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
               const int gr = g0 + gg;
               const unsigned char *kc = kb + koff[gr] + (b0 + b) * 16 * L::kRow;
               const uint32_t w0 = lds32(kc), w1 = lds32(kc + 8 * L::kRow), x0 = w0 >> 8, x1 = w1 >> 8;
+              uint32_t a[8];  // even and odd nibbles of the lower and upper bytes
+              if constexpr (kExact) {  // 1024 + c less 1032; 1024 + 16 c less 1152: 16 (c - 8)
+                auto even = [&](uint32_t w) { return hadd2(and_or(w, kLow, 0x64006400u), 0xe408e408u); };
+                auto odd = [&](uint32_t w) { return hadd2(and_or(w, kHigh, 0x64006400u), 0xe480e480u); };
+                a[0] = even(w0), a[1] = even(w1), a[2] = odd(w0), a[3] = odd(w1);
+                a[4] = even(x0), a[5] = even(x1), a[6] = odd(x0), a[7] = odd(x1);
+              } else {
+                a[0] = w0 & kLow, a[1] = w1 & kLow, a[2] = w0 & kHigh, a[3] = w1 & kHigh;
+                a[4] = x0 & kLow, a[5] = x1 & kLow, a[6] = x0 & kHigh, a[7] = x1 & kHigh;
+              }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 float c[4];
-                if constexpr (!kQreg) {
+                if constexpr (kExact) {
+                  c[0] = c[1] = c[2] = c[3] = 0.f;
+                } else if constexpr (!kQreg) {
                   const float2 y = *reinterpret_cast<const float2 *>(sqsum + gr * R + nt * 8 + 2 * t4);
                   c[0] = c[2] = y.x;
                   c[1] = c[3] = y.y;
                 }
 #pragma unroll
-                for (int q = 0; q < QP; ++q) {
+                for (int q = QP - 1; q >= 0; --q) {  // the smaller part first
                   const int at = (q * NT + nt) * 2 * G + 2 * gr;
                   const uint2 qa = kQreg ? qr[kQreg ? at : 0] : sq[at * 32 + lane], qb = kQreg ? qr[kQreg ? at + 1 : 0] : sq[(at + 1) * 32 + lane];
-                  if (kQreg && q == 0)
-                    mma(c, w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qa.x, qa.y, qs[kQreg ? nt * G + gr : 0]);
+                  if (kQreg && q == QP - 1 && !kExact)
+                    mma(c, a[0], a[1], a[2], a[3], qa.x, qa.y, qs[kQreg ? nt * G + gr : 0]);
                   else
-                    mma(c, w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh, qa.x, qa.y);
-                  mma(c, x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, qb.x, qb.y);
+                    mma(c, a[0], a[1], a[2], a[3], qa.x, qa.y);
+                  mma(c, a[4], a[5], a[6], a[7], qb.x, qb.y);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -690,9 +715,10 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
 #pragma unroll
               for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
               if (mx > th[nt][c]) {  // the same in the eight lanes of a row
-                const float by = mx - kTopP, f = th[nt][c] == -INFINITY ? 0.f : fast_exp2(-by);
+                // whole powers of two, so that neither the reference nor what was summed is rounded
+                const float by = rintf(mx - kTopZ), f = th[nt][c] == -INFINITY ? 0.f : fast_exp2(-by);
                 nb[nt][c] -= by;
-                th[nt][c] = kMaxP;
+                th[nt][c] = kMaxZ;
                 l[nt][c] *= f;
 #pragma unroll
                 for (int v = 0; v < VT; ++v) o[nt][v][c] *= f, o[nt][v][c + 2] *= f;
@@ -709,7 +735,8 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const float w0 = fast_exp2(z[b][nt][2 * hf]), w1 = fast_exp2(z[b][nt][2 * hf + 1]);
+              float w0 = fast_exp2(z[b][nt][2 * hf]), w1 = fast_exp2(z[b][nt][2 * hf + 1]);
+              if (kExact) w0 *= 8192.f, w1 *= 8192.f;  // 2^kTopP
               l[nt][0] += w0;
               l[nt][1] += w1;
               const uint32_t h = half2_of(w0, w1);
@@ -747,12 +774,19 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
                 const uint32_t v2 = hfma2(and_or(k ? xb >> 2 : xb << 6, kTop, 0x4c004c00u), sc, nc);
                 const uint32_t v3 = hfma2(and_or(k ? xb >> 6 : xb << 2, kTop, 0x4c004c00u), sc, nc);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                  float(&acc)[4] = o[nt][(y * 2 + hf) * 2 + k];
+                  if constexpr (kExact) {
+                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                    float part[4];
+                    mma(part, v0, v1, v2, v3, pb[nt][PP - 1][0], pb[nt][PP - 1][1], zero);
+                    mma(part, v0, v1, v2, v3, pb[nt][0][0], pb[nt][0][1]);
 #pragma unroll
-                  for (int q = 0; q < PP; ++q) {
-                    float(&acc)[4] = o[nt][(y * 2 + hf) * 2 + k];
-                    mma(acc, v0, v1, v2, v3, pb[nt][q][0], pb[nt][q][1]);
+                    for (int e = 0; e < 4; ++e) acc[e] += part[e];
+                  } else {
+                    mma(acc, v0, v1, v2, v3, pb[nt][0][0], pb[nt][0][1]);
                   }
+                }
               }
             }
         }
@@ -786,7 +820,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
         for (int s = 4; s < 32; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
         const bool bad = (__shfl_sync(0xffffffffu, marked, r) >> my_group) & 1u;
         if (gid == 0) {
-          mine[r * PS + D] = th[nt][c] == -INFINITY ? -INFINITY : -nb[nt][c];
+          mine[r * PS + D] = th[nt][c] == -INFINITY ? -INFINITY : -nb[nt][c] - (kExact ? kTopP : 0.f);
           mine[r * PS + D + 1] = sum;
         }
         float *to = mine + r * PS + gid * (D / 8);
