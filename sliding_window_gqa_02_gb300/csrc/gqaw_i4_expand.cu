@@ -4,7 +4,7 @@
 // Worth it where a sequence has more than one query tile: in the kernel that takes codes
 // (gqaw_i4_tiles.cuh) every query tile converts all its key tiles again, beside the softmax and on the same
 // issue slots, while here each is converted once (8 chunks of 512 tokens with a window of 4096: 479 us
-// there, 361 here, of which this pass is 43).
+// there, 365 here, of which this pass is 43).
 //
 // Bound: HBM, mostly the writes (3.6 times the bytes of the codes).  A task is 128 rows of one head, keys or
 // values; a warp has 32 of them, a lane 16 bytes of codes a row and 64 bytes of values, all loads ahead of the
