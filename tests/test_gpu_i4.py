@@ -422,6 +422,75 @@ def test_malformed_sequences_and_bad_pages():
     t.check_read()
 
 
+@pytest.mark.parametrize("D,max_len", [(128, 0), (64, LONG), (256, 0)])
+def test_malformed_chunks_and_bad_pages(D, max_len):
+    """The same where prompt kernels run, on expanded keys and on codes."""
+    lens = [(100, 300), (120, 200), (1, 20), (90, 333)]
+    t = Batch(lens, 8, 2, D, 16, BF16, seed=14, max_len=max_len, lead_rows=1, extra_rows=3)
+    t.seqlens[1] = 5  # shorter than its new tokens
+    t.call(gqaw.gqaw_paged_i4_attend, flags=gqaw.GQAW_DEV_BAD_SEQLEN)
+    t.check_output(skip=(1,))
+    assert (t.out[t.rows(1)] == 7.0).all() and (t.out[t.untouched()] == 7.0).all()
+    t = Batch(lens, 8, 2, D, 16, BF16, seed=14, max_len=max_len)
+    t.seqlens[3] = t.max_len  # longer than the call allows
+    t.table[0, 2], t.table[0, 3] = 1 << 20, -1
+    t.call(gqaw.gqaw_paged_i4_attend, flags=gqaw.GQAW_DEV_BAD_SEQLEN | gqaw.GQAW_DEV_BAD_PAGE)
+    t.check_output(skip=(0, 3))
+    assert (t.out[t.rows(3)] == 7.0).all()
+
+
+@pytest.mark.parametrize("max_len", [0, LONG])
+def test_chunks_of_more_sequences_than_one_launch_takes(max_len):
+    lens = [(70, 70 + i) if i % 60 == 7 else (i % 3, 20 + i) for i in range(300)]
+    t = Batch(lens, 4, 1, 64, 32, BF16, seed=19, max_len=max_len)
+    t.call(gqaw.gqaw_paged_i4_attend)
+    t.check_output()
+
+
+def test_graphs_of_all_paths_on_one_workspace():
+    """Captured steps by rows, on codes and on expanded keys, in turn on one workspace; and two streams with a
+    workspace each at once."""
+    shapes = [([(1, 900), (1, 40)], 0), ([(60, 300), (3, 3), (1, 50)], LONG), ([(90, 300), (70, 70)], 0)]
+    ts = [Batch(lens, 8, 2, 128, 16, BF16, seed=20 + i, norm=True, rotary=128, max_len=m) for i, (lens, m) in enumerate(shapes)]
+    for t in ts:
+        t.args()
+    ws = max((t.ws for t in ts), key=lambda w: w.numel())
+    own = [t.ws for t in ts]
+    side = torch.cuda.Stream()
+    graphs = []
+    with torch.cuda.stream(side):
+        for t in ts:
+            t.ws = ws
+            args = t.args()
+            gqaw.check(gqaw.gqaw_paged_i4_step(args, side.cuda_stream))
+            side.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                gqaw.check(gqaw.gqaw_paged_i4_step(args, torch.cuda.current_stream().cuda_stream))
+            graphs.append((g, args))
+        for _ in range(3):
+            for (g, _), t in zip(graphs, ts):
+                t.out.fill_(7.0)
+                g.replay()
+        side.synchronize()
+    for t in ts:
+        t.check_output(turned=True)
+    firsts = [t.out.clone() for t in ts]
+    streams = [torch.cuda.Stream() for _ in ts]
+    calls = []
+    for t, w in zip(ts, own):
+        t.ws = w
+        t.out.fill_(7.0)
+        calls.append(t.args())
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for a, st in zip(calls, streams):
+            gqaw.check(gqaw.gqaw_paged_i4_step(a, st.cuda_stream))
+    torch.cuda.synchronize()
+    for t, first in zip(ts, firsts):
+        assert torch.equal(t.out, first)
+
+
 def test_no_pages_and_no_tokens():
     t = Batch([(0, 0), (0, 0)], 4, 2, 64, 16, BF16, extra_rows=4, spare_pages=1)
     for fn in (gqaw.gqaw_paged_i4_append, gqaw.gqaw_paged_i4_attend, gqaw.gqaw_paged_i4_step, gqaw.gqaw_paged_i4_read):
