@@ -17,8 +17,9 @@
 // group's maximum is two exchanges among four lanes.  With 32 elements a lane the scale and the steps of the
 // sum are computed once and not by four lanes: the 2689 tokens take 12.7 us, but the 32 take 7.0, since a lane's
 // chain of operations is longer; the short one stands.
-// Reading back is the inverse: 32768 tokens, 38 MB in and 134 MB out, in 38 us (4.5 TB/s, issue slots 70% busy).
-#include "gqaw_i4.cuh"
+// Reading back is the inverse, a warp for keys and values of a token, whose look-ups were most of its
+// instructions: 32768 tokens, 38 MB in and 134 MB out, in 31 us (38 with a warp for each, 5.5 TB/s).
+#include "gqaw_i4_tiles.cuh"
 
 namespace gqaw {
 
@@ -370,6 +371,7 @@ __global__ void __launch_bounds__(i4r::kThreads, 5) i4_append_kernel(const I4Par
   pdl_launch_dependents();
 }
 
+// A warp has `BATCH` groups of 32 / LPR heads of one token, keys and values.
 template <typename T, int LPR, int BATCH>
 __global__ void __launch_bounds__(i4r::kThreads) i4_read_kernel(const I4Params p, const i4r::Job j) {
   using namespace i4r;
@@ -378,36 +380,39 @@ __global__ void __launch_bounds__(i4r::kThreads) i4_read_kernel(const I4Params p
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   pdl_wait();
   if (w < j.warps) {
-    const int chunks = j.ck + j.cv, n = (int)((uint32_t)w / (uint32_t)chunks);
-    int c = (int)w - n * chunks;
-    const bool value = c >= j.ck;
-    c -= value ? j.ck : 0;
-    const int nh = value ? j.nv : j.nk, h = c * (BATCH * RPW) + sub;
+    const int n = (int)((uint32_t)w / (uint32_t)j.ck), h = ((int)w - n * j.ck) * (BATCH * RPW) + sub;
     const int b = find_sequence(batch_of(p), n);
     if (b >= 0) {
       const I4Place at = i4_place(p, b, (long long)p.seqlens[b] + 1 - (p.qstart[b + 1] - n));
       if (at.page >= 0) {
-        const unsigned char *codes = static_cast<const unsigned char *>(value ? p.vp : p.kp) + at.page * p.sp + at.row * p.sr + lr * 4;
-        const uint16_t *scales = (value ? p.vscale : p.kscale) + at.page * p.tp + at.row * p.tr + lr / 4;
-        T *out = value ? static_cast<T *>(p.vo) + n * p.vos : static_cast<T *>(p.ko) + n * p.kos;
-        uint32_t word[BATCH];
-        float s[BATCH];
+        const long long code = at.page * p.sp + at.row * p.sr + lr * 4, scale = at.page * p.tp + at.row * p.tr + lr / 4;
+        uint32_t word[2][BATCH], s[2][BATCH];
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          const int head = h + i * RPW;
-          word[i] = head < nh ? *reinterpret_cast<const uint32_t *>(codes + head * p.sh) : 0u;
-          s[i] = __uint_as_float(head < nh ? (uint32_t)scales[head * p.th] << 16 : 0u);
-        }
+        for (int v = 0; v < 2; ++v)
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          const int head = h + i * RPW;
-          float y[8];
+          for (int i = 0; i < BATCH; ++i) {
+            const int head = h + i * RPW;
+            const bool have = head < (v ? j.nv : j.nk);
+            word[v][i] = have ? *reinterpret_cast<const uint32_t *>(static_cast<const unsigned char *>(v ? p.vp : p.kp) + code + head * p.sh) : 0u;
+            s[v][i] = have ? (v ? p.vscale : p.kscale)[scale + head * p.th] : 0u;
+          }
 #pragma unroll
-          for (int m = 0; m < 8; ++m) y[m] = (float)((int)((word[i] >> (4 * m)) & 15u) - 8) * s[i];
-          Oct<T> o;
-          o.set(y);
-          if (head < nh) o.store(out + (long long)head * D + lr * 8);
-        }
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int head = h + i * RPW;
+            Oct<T> o;
+            if constexpr (sizeof(T) == 2) {  // a product of two bf16 numbers, rounded once
+              o.a = i4t::values8<false>(word[v][i], s[v][i] * 0x10001u, 0u, true);
+            } else {
+              float y[8];
+#pragma unroll
+              for (int m = 0; m < 8; ++m)  // 2^23 + c less 2^23 + 8
+                y[m] = (__uint_as_float(((word[v][i] >> (4 * m)) & 15u) | 0x4b000000u) - 8388616.f) * __uint_as_float(s[v][i] << 16);
+              o.set(y);
+            }
+            if (head < (v ? j.nv : j.nk)) o.store((v ? static_cast<T *>(p.vo) + n * p.vos : static_cast<T *>(p.ko) + n * p.kos) + (long long)head * D + lr * 8);
+          }
       } else if (lane == 0) {
         pflag(p, GQAW_DEV_BAD_PAGE);
       }
@@ -452,12 +457,14 @@ cudaError_t launch_i4_rows(const I4Params &p, int nq, int nk, int nv, bool read,
   j.vec = !p.rot_inter && half % 8 == 0 && reinterpret_cast<uintptr_t>(p.rcos) % 16 == 0 && reinterpret_cast<uintptr_t>(p.rsin) % 16 == 0;
   const int rpw = 32 / (p.D / 8);
   auto chunks = [&](int heads, int batch) { return (heads + batch * rpw - 1) / (batch * rpw); };
-  auto warps = [&](int batch) { return (long long)p.N * (chunks(nq, batch) + chunks(nk, batch) + chunks(nv, batch)); };
+  auto warps = [&](int batch) {  // a warp that reads has a token's keys and values
+    return (long long)p.N * (read ? chunks(nk > nv ? nk : nv, batch) : chunks(nq, batch) + chunks(nk, batch) + chunks(nv, batch));
+  };
   j.batch = read ? (warps(4) >= kManyWarps ? 4 : 2) : warps(4) >= kManyWarps ? 4 : warps(2) >= kManyWarps ? 2 : 1;
   j.cq = chunks(nq, j.batch);
-  j.ck = chunks(nk, j.batch);
-  j.cv = chunks(nv, j.batch);
-  j.warps = (long long)p.N * (j.cq + j.ck + j.cv);
+  j.ck = chunks(read && nv > nk ? nv : nk, j.batch);
+  j.cv = read ? 0 : chunks(nv, j.batch);
+  j.warps = warps(j.batch);
   j.checks = (p.B + 31) / 32;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((j.warps + j.checks + kThreads / 32 - 1) / (kThreads / 32)));
