@@ -395,6 +395,27 @@ def test_a_run_of_prompt_decode_and_read():
     assert diff < 4 * 2.0 ** -8
 
 
+@pytest.mark.parametrize("dtype,S,max_len", [(BF16, 3, 0), (BF16, 70, 0), (BF16, 60, LONG), (F32, 20, 0)])
+def test_offsets_past_32_bits(dtype, S, max_len):
+    """Pages a gigabyte apart, codes and scales: every path finds its rows."""
+    t = Batch([(S, 90), (1, 40)], 8, 2, 64, 32, dtype, seed=21, max_len=max_len, norm=True, rotary=64)
+    far = []
+    for x, stride in ((t.kc, 1 << 30), (t.vc, 1 << 30), (t.ks, (1 << 30) + 64), (t.vs, (1 << 30) + 64)):
+        n = x.shape[0]
+        buf = torch.empty((n - 1) * stride + x[0].numel(), dtype=x.dtype, device=x.device)
+        y = buf.as_strided(x.shape, (stride, *x.stride()[1:]))
+        y.copy_(x)
+        far.append(y)
+    t.kc, t.vc, t.ks, t.vs = far
+    assert far[0].shape[0] > 5
+    before = t.snapshot()
+    t.call(gqaw.gqaw_paged_i4_step)
+    t.check_pages(before)
+    t.check_output(turned=True)
+    t.call(gqaw.gqaw_paged_i4_read)
+    t.check_read()
+
+
 # ------------------------------------------------------------------------------ malformed, graphs, streams
 
 
