@@ -5,6 +5,7 @@
 // sr their strides in bytes.
 #pragma once
 
+#include "gqaw_i4_rules.cuh"
 #include "gqaw_paged.cuh"
 
 namespace gqaw {
@@ -21,7 +22,7 @@ struct I4Params : PagedParams {
   // attention: rows of the cache by 16 bytes of codes and one row's scales
   uint32_t sp16, sr16, tpg, trg;  // strides of pages and rows, in 16 bytes and in rows of scales
   long long to_values, to_value_scales;  // bytes from key codes to value codes, and from key scales to value scales
-  bool blocks;                    // the 1024 / D rows of a copy lie in one page
+  bool blocks;                    // i4_blocks()
 };
 
 // Where position j of sequence b lies: page and row in it; page -1 when its entry is bad.

@@ -258,7 +258,7 @@ gqaw_status run_attend(const gqaw_paged_args *a, const I4Plan &L, I4Params p, cu
   p.sr16 = (uint32_t)(L.sr / 16);
   p.tpg = (uint32_t)(L.tp / (D / gqaw::kI4Group));
   p.trg = (uint32_t)(L.tr / (D / gqaw::kI4Group));
-  p.blocks = a->page_size % (1024 / D) == 0;
+  p.blocks = gqaw::i4_blocks(a->page_size, D, L.sr, L.tr);
   p.to_values = static_cast<const char *>(p.vp) - static_cast<const char *>(p.kp);
   p.to_value_scales = reinterpret_cast<const char *>(p.vscale) - reinterpret_cast<const char *>(p.kscale);
   gqaw::PagedMaps maps;

@@ -1,0 +1,39 @@
+"""Operators on 4-bit caches over layouts and tables that lie at the ends of what a call may give."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from i4_driver import Batch
+from sliding_window_gqa_02_gb300 import gqaw
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+LONG = 1 << 20  # a length for which the expanded pages of a few sequences would be too large
+
+
+@pytest.mark.parametrize("dtype,S", [(BF16, 1), (BF16, 3), (F32, 4)])
+@pytest.mark.parametrize("D,row", [(32, 160 << 20), (64, 300 << 20), (128, 640 << 20), (256, 1500 << 20)])
+def test_rows_far_apart(dtype, S, D, row):
+    """Rows of a page so far apart that their offsets in a block of one copy pass 32 bits: codes, then scales."""
+    page = 1024 // D
+    for codes, scales in ((row, 0), (0, min(row, (1 << 32) // page * (D // 32) - 16))):  # a page of scales has an end of its own
+        t = Batch([(S, page), (1, page - 1)], 4, 2, D, page, dtype, seed=41, norm=True, rotary=32, heads_inside_rows=True, spare_pages=0)
+        far = []
+        for x, stride in ((t.kc, codes), (t.vc, codes), (t.ks, scales), (t.vs, scales)):
+            if stride:
+                n, r = x.shape[:2]
+                buf = torch.empty((n * r - 1) * stride + x[0, 0].numel(), dtype=x.dtype, device=x.device)
+                y = buf.as_strided(x.shape, (r * stride, stride, *x.stride()[2:]))
+                y.copy_(x)
+                x = y
+            far.append(x)
+        t.kc, t.vc, t.ks, t.vs = far
+        before = t.snapshot()
+        t.call(gqaw.gqaw_paged_i4_step)
+        t.check_pages(before)
+        t.check_output(turned=True)
+        t.call(gqaw.gqaw_paged_i4_read)
+        t.check_read()
+        del t, far, x, y, buf
+        torch.cuda.empty_cache()
