@@ -25,8 +25,9 @@
 // row that puts the largest element at 2^13; weights as one part, or two for fp32 (PP).  A weight is at
 // most 2^15, since the row's reference moves when that is exceeded (and then puts the largest at 2^13); a
 // value scale is taken relative to the largest power of two of its group so far, which becomes 2^10: no
-// product leaves fp16, and whatever the scales' size none is lost beside 2^-35.  Sums and statistics are
-// fp32.  The tensor cores cut what a sum loses, which adds up over a long context: for fp32 rows (kExact) the codes of
+// product leaves fp16, and with scales up to 2^24 apart each is exact.  What a row does not attend must not change it,
+// however large, so scales farther off count as zero there, and the rows that attend them are computed again
+// in fp32 (wide_rows()).  Sums and statistics are fp32.  The tensor cores cut what a sum loses, which adds up over a long context: for fp32 rows (kExact) the codes of
 // the keys are signed, so that no large sum is taken back, a product's values are added outside, the smaller
 // parts come first, and exponents are taken near 0 (error against 64 bits at 500 to 12,000 keys 9.6e-7 -> 2e-7, the
 // time the same).  The reference moves by whole powers of two and is never rounded.
@@ -66,6 +67,11 @@ constexpr int kUnitCost = 32, kMergeCost = 60, kMinTiles = 12;
 constexpr float kTopP = 13.f;  // log2 of the largest weight when the reference moves
 constexpr float kMaxP = 15.f;  // ... and of any
 constexpr int kTopV = 10;      // a scale's largest power of two becomes 2^kTopV: 24 s < 2^16
+// How many powers of two the value scales of a group may lie above and below the largest of a warp's first tile.  In fp16
+// the smallest is then 2^-14 or more, and its values are exact; a weight that fp16 rounds to a multiple of 2^-38 of the
+// row's largest is off by 2^-14 of any other value.  Rows that attend other scales are computed by wide_rows().
+constexpr int kAbove = 10, kBelow = 14;
+constexpr uint32_t kWide = 1u << 16;
 
 template <int D, int NT, int QP>
 struct Lay {
@@ -83,7 +89,10 @@ struct Lay {
   static constexpr bool kAhead = R * PS * 4 <= kStage;   // the state takes one stage's place, the next unit's tiles the others'
   static constexpr int kRing = S * kStage > R * PS * 4 ? S * kStage : (R * PS * 4 + 1023) / 1024 * 1024;
   static constexpr int kNorm = W * kRing;                // per warp: scales as the products take them
-  static constexpr int kNormBytes = (kKeys * G * 6 + G * 8 + 15) / 16 * 16;  // keys' in fp32, values' in fp16; their factors, powers of two seen
+  // per warp: keys' scales in fp32, values' in fp16, their factors; in bf16 bits, two groups a word, the largest scale of the
+  // largest power of two seen, less the smallest that may come; that; and the largest that may come
+  static constexpr int kWords = (G + 1) / 2, kSeen = (kKeys * G * 6 + G * 4 + 15) / 16 * 16;
+  static constexpr int kNormBytes = (kSeen + 3 * kWords * 4 + 15) / 16 * 16;
   static constexpr int kQ = kNorm + W * kNormBytes;      // query operands [QP][NT][2 G][32 lanes] of 8 bytes
   static constexpr int kQsum = kQ + QP * NT * 2 * G * 32 * 8;  // [G][R] fp32: where accumulators start
   static constexpr int kQexp = kQsum + R * G * 4;        // [R]: power of two of a row
@@ -268,6 +277,168 @@ __device__ __noinline__ bool load_rows(const I4Params &p, const Unit &x, unsigne
   return id >= 0;
 }
 
+// The state of a warp's tiles of a unit in fp32 throughout, for the rows of `rows` alone, which attend value scales too
+// far apart for one power of two in fp16.  The large ones may be another row's, or under next to no weight, so every row
+// and lane has a power of two of its own: a sum holds 2^ro of what it stands for, ro going down for a product above 2^40
+// and up when a tile begins with less than 1.  At the end the reference moves so that the weights add up to 2^-13: no sum
+// of warps and CTAs leaves fp32 where the average does not.
+//
+// Out of line and written for few registers, since ordinary caches do not come here: a lane has a key for the logits and
+// D / 32 dimensions for the values.  The queries are the operands of the products (put_query()).  Bound by its own
+// instructions: 64 contexts of 4 k to 33 k keys that all have such scales take 5.9 ms, and 0.26 without.
+template <typename T, int D, int NT, int QP>
+__device__ __noinline__ void wide_rows(const I4Params &p, const Unit &x, const unsigned char *smem, float *mine, uint32_t rows, uint32_t marked,
+                                       int warp, int lane) {
+  using L = Lay<D, NT, QP>;
+  constexpr int G = L::G, R = L::R, PS = L::PS, DL = D / 32, kNone = 1 << 20;
+  const int my_group = lane * DL / kI4Group;
+  const uint2 *sq = reinterpret_cast<const uint2 *>(smem + L::kQ);
+  const int *sqexp = reinterpret_cast<const int *>(smem + L::kQexp);
+  const int se = min(40, -min(0, __reduce_min_sync(0xffffffffu, lane < x.rows ? sqexp[min(lane, R - 1)] : 0)));
+  const float sfac = pow2(se - 24);
+  float o[R][DL], l[R], m[R];  // the reference is a whole number
+  int ro[R];
+  __syncwarp();  // the other rows' state is written
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    l[r] = 0.f;
+    m[r] = -INFINITY;
+    ro[r] = kNone;
+#pragma unroll
+    for (int d = 0; d < DL; ++d) o[r][d] = 0.f;
+  }
+#pragma unroll 1
+  for (int t = x.t0 + warp; t < x.t0 + x.tiles; t += L::W) {
+    const uint32_t j = (uint32_t)t * kKeys + lane;
+    const bool in = j >= x.jlo && j < x.jhi;
+    const I4Place at = in ? i4_place(p, x.b, j) : I4Place{-1, 0};
+    const bool ok = at.page >= 0;  // else a row of zeros
+    const unsigned char *codes = x.codes + (ok ? at.page * p.sp + at.row * p.sr : 0ll);
+    const uint16_t *scales = x.scales + (ok ? at.page * p.tp + at.row * p.tr : 0ll);
+    float w[R];  // logits, then weights
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r] = 0.f;
+#pragma unroll 1
+    for (int gr = 0; gr < G; ++gr) {
+      const float s = ok ? __uint_as_float((uint32_t)scales[gr] << 16) * sfac : 0.f;
+      float acc[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r] = 0.f;
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {  // eight dimensions
+        const uint32_t word = ok ? *reinterpret_cast<const uint32_t *>(codes + gr * 16 + b * 4) : 0x88888888u;
+        float c[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {  // odd ones count 16 times, their queries a sixteenth
+          const float y = (float)((int)((word >> (4 * k)) & 15u) - 8);
+          c[k] = k & 1 ? 16.f * y : y;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (!((rows >> r) & 1u)) continue;
+#pragma unroll
+          for (int q = QP - 1; q >= 0; --q)
+#pragma unroll
+            for (int step = 0; step < 2; ++step) {
+              const uint2 y = sq[((q * NT + r / 8) * 2 * G + 2 * gr + step) * 32 + (r & 7) * 4 + b];
+              const float2 even = floats_of(y.x), odd = floats_of(y.y);
+              acc[r] = fmaf(c[2 * step], even.x, acc[r]);
+              acc[r] = fmaf(c[2 * step + 4], even.y, acc[r]);
+              acc[r] = fmaf(c[2 * step + 1], odd.x, acc[r]);
+              acc[r] = fmaf(c[2 * step + 5], odd.y, acc[r]);
+            }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) w[r] = fmaf(s, acc[r], w[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (!((rows >> r) & 1u)) continue;
+      float z = w[r] * (p.qscale * pow2_or_0(24 - se - sqexp[r]));
+      if (p.capmul != 0.f) z = sizeof(T) == 4 ? cap_logit(p, z) : p.capmul * ptc::fast_tanh(z);
+      const long long pos = (long long)x.qpos + r / x.g;
+      if (!(r < x.rows && in && j <= pos && (p.W == 0 || j > pos - p.W))) z = -INFINITY;
+      float mx = z;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+      float top = 0.f;
+      if (mx > m[r]) {
+        const float to = rintf(mx), f = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - to);
+        m[r] = to;
+        l[r] *= f;
+#pragma unroll
+        for (int d = 0; d < DL; ++d) o[r][d] *= f;
+      }
+      w[r] = fast_exp2(z - (m[r] == -INFINITY ? 0.f : m[r]));
+      l[r] += w[r];
+#pragma unroll
+      for (int d = 0; d < DL; ++d) top = fmaxf(top, fabsf(o[r][d]));
+      if (top == 0.f) {
+        ro[r] = kNone;
+      } else if (top < 1.f) {
+        const int up = 24 - ((int)(__float_as_uint(top) >> 23) - 127);
+        ro[r] += up;
+#pragma unroll
+        for (int d = 0; d < DL; ++d) o[r][d] = times_pow2(o[r][d], up);
+      }
+    }
+#pragma unroll 1
+    for (int key = 0; key < kKeys; ++key) {
+      const unsigned char *vc = reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), key)) + p.to_values;
+      const unsigned char *vs = reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(scales), key)) + p.to_value_scales;
+      const bool have = __shfl_sync(0xffffffffu, ok, key);
+      const uint32_t bits = have ? reinterpret_cast<const uint16_t *>(vs)[my_group] : 0u;
+      const bool some = (bits & 0x7fffu) != 0u && (bits & 0x7fffu) < 0x7f80u;  // one that is not finite: `marked`
+      uint32_t word = 0;
+      if (some) {
+        if constexpr (DL == 8) word = reinterpret_cast<const uint32_t *>(vc)[lane];
+        else if constexpr (DL == 4) word = reinterpret_cast<const uint16_t *>(vc)[lane];
+        else if constexpr (DL == 2) word = vc[lane];
+        else word = vc[lane / 2] >> (4 * (lane & 1));
+      }
+      const int es = max((int)(bits >> 7 & 0xffu), 1) - 127;
+      const float s = times_pow2(__uint_as_float(bits << 16), -es);  // its power of two taken off
+      float v[DL];
+#pragma unroll
+      for (int d = 0; d < DL; ++d) v[d] = s * (float)((int)((word >> (4 * d)) & 15u) - 8);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!((rows >> r) & 1u)) continue;
+        const float pr = __shfl_sync(0xffffffffu, w[r], key);
+        if (some && pr != 0.f) {
+          const int over = (int)(__float_as_uint(pr) >> 23 & 0xffu) - 127 + es + ro[r];  // the product's power of two
+          if (over > 40) {
+            const int down = over - 24;
+            ro[r] -= down;
+#pragma unroll
+            for (int d = 0; d < DL; ++d) o[r][d] *= pow2_or_0(-down);
+          }
+          const float u = times_pow2(pr, ro[r] + es);
+#pragma unroll
+          for (int d = 0; d < DL; ++d) o[r][d] = fmaf(u, v[d], o[r][d]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float sum = l[r];
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    int e = sum > 0.f && sum < INFINITY ? (int)(__float_as_uint(sum) >> 23) - 127 + 13 : 0;
+    if (!(m[r] + (float)e - m[r] == (float)e)) e = 0;  // a reference too large for that
+    const bool bad = (__shfl_sync(0xffffffffu, marked, r) >> my_group) & 1u;
+    if (!((rows >> r) & 1u)) continue;
+#pragma unroll
+    for (int d = 0; d < DL; ++d) mine[r * PS + lane * DL + d] = bad ? NAN : times_pow2(o[r][d], -ro[r] - e);
+    if (lane == 0) {
+      mine[r * PS + D] = m[r] + (float)e;
+      mine[r * PS + D + 1] = times_pow2(sum, -e);
+    }
+  }
+}
+
 }  // namespace i4a
 
 // NT: operands of 8 query rows.  T: type of the rows outside the cache.
@@ -295,7 +466,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   float *nk = reinterpret_cast<float *>(smem + L::kNorm + warp * L::kNormBytes);  // [G / 4][position][4]
   uint16_t *nv = reinterpret_cast<uint16_t *>(nk + kKeys * G);                    // [G][position]
   float *vf = reinterpret_cast<float *>(nv + kKeys * G);  // of each group: the factor that takes the largest scale's power of two to 2^kTopV
-  uint32_t *thr = reinterpret_cast<uint32_t *>(vf + G);   // ... the largest scale (bf16 bits) of that power of two, two groups a word
+  uint32_t *seen_at = reinterpret_cast<uint32_t *>(smem + L::kNorm + warp * L::kNormBytes + L::kSeen);
   const uint2 *sq = reinterpret_cast<const uint2 *>(smem + L::kQ);
   float *sqsum = reinterpret_cast<float *>(smem + L::kQsum);
   int *sqexp = reinterpret_cast<int *>(smem + L::kQexp);
@@ -513,10 +684,35 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
     float my_vf = pow2(127);  // this lane's group's factor
-    if (lane < G) vf[lane] = pow2(127);
-    if (lane < (G + 1) / 2) thr[lane] = 0u;
-    __syncwarp();
-    uint32_t marked = 0;  // groups of row `lane` that attend a scale that is not finite
+    if (x.t0 + warp < end) {  // what the first tile's scales say of the others
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+      __syncwarp();
+      const int key = (lane & ~7) | kappa<D>(lane & 7);
+      const long long j = (long long)(x.t0 + warp) * kKeys + key, last = (long long)x.qpos + x.ntok - 1;
+      // The largest of the keys that all rows attend, if one is not zero: what only some of them attend is not to say how
+      // the others are computed.  A group of zeros may have no other scale after that.
+      const bool some = j >= x.jlo && j < x.jhi, all = j <= (long long)x.qpos && j >= (long long)x.jlo && (p.W == 0 || j > last - p.W);
+      const uint16_t *vs = reinterpret_cast<const uint16_t *>(ring + st * L::kStage + 2 * L::kCodes + L::kScales) + key * G;
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        const uint32_t h = vs[gr] & 0x7fffu, fin = h < 0x7f80u ? h : 0u;
+        uint32_t mx = __reduce_max_sync(0xffffffffu, all ? fin : 0u);
+        if (mx == 0u) mx = __reduce_max_sync(0xffffffffu, some ? fin : 0u);
+        const int e = (int)(mx >> 7), low = mx ? max(e - kBelow, 0) << 7 : 0;
+        if (lane == 0) {
+          uint16_t *to = reinterpret_cast<uint16_t *>(seen_at) + gr;
+          to[0] = (uint16_t)(mx ? (mx | 0x7fu) - low : 0u);
+          to[2 * L::kWords] = (uint16_t)low;
+          to[4 * L::kWords] = (uint16_t)(mx ? min(e + kAbove, 254) << 7 | 0x7f : 0);
+          vf[gr] = pow2(kTopV + 127 - e);
+        }
+      }
+      if (G == 1 && lane == 0)  // the other half of the only word
+        reinterpret_cast<uint16_t *>(seen_at)[1] = reinterpret_cast<uint16_t *>(seen_at)[3] = reinterpret_cast<uint16_t *>(seen_at)[5] = 0;
+      __syncwarp();
+      my_vf = vf[my_group];
+    }
+    uint32_t marked = 0;  // groups of row `lane` that attend a scale that is not finite; kWide: it attends one too far off
 
     // lane-constant places in a tile: keys' codes of positions gid and gid + 8, 16, 24; values' of this lane's dimensions
     int koff[G], voff[2];
@@ -548,30 +744,34 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
 #pragma unroll
           for (int y = 0; y < (G + 1) / 2; ++y) vw[y] = 0u;
         }
-        bool above = false, odd = false;
-        uint32_t seen[(G + 1) / 2], fac[G];
-        lds_words(thr, seen);
+        uint32_t seen[2 * L::kWords], fac[G];
+        lds_words(seen_at, seen);
+        bool outside = false;  // above the largest so far, or below what may come (zeros among these)
 #pragma unroll
-        for (int y = 0; y < (G + 1) / 2; ++y) above |= __vmaxu2(vw[y] & 0x7fff7fffu, seen[y]) != seen[y];
-        if (__any_sync(0xffffffffu, above)) {
-          uint32_t bad = 0;
+        for (int y = 0; y < L::kWords; ++y) {
+          // of both halves at once: a lower one that takes from the upper is below its range, and found by itself
+          const uint32_t d = (vw[y] & 0x7fff7fffu) - seen[L::kWords + y];
+          outside |= __vmaxu2(d, seen[y]) != seen[y];
+        }
+        if (__any_sync(0xffffffffu, outside)) {
+          uint32_t bad = 0;  // of this lane's key: groups with a scale that is not finite; kWide: with one that lies too far off
 #pragma unroll
-          for (int y = 0; y < (G + 1) / 2; ++y) {
+          for (int y = 0; y < L::kWords; ++y) {
+            const uint32_t low = seen[L::kWords + y], roof = seen_at[2 * L::kWords + y], top = seen[y] + low;
+            uint32_t x2 = vw[y] & 0x7fff7fffu;
+            const uint32_t less = ((x2 | 0x80008000u) - 0x00010001u) ^ 0x80008000u;  // by one, zeros on top
+            const uint32_t off = (__vmaxu2(x2, roof) ^ roof) | (__vminu2(less, low) ^ low);
+            if (off) {
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint32_t half = 0xffffu << (16 * hf), inf = 0x7f800000u >> (16 - 16 * hf);
-              if (2 * y + hf < G && (vw[y] & 0x7fff7fffu & half) >= inf) {
-                odd = true;
-                bad |= 1u << (2 * y + hf);
-                vw[y] &= ~half;
-              }
+              for (int hf = 0; hf < 2; ++hf)
+                if (off >> (16 * hf) & 0xffffu) {
+                  bad |= (x2 >> (16 * hf) & 0xffffu) >= 0x7f80u ? 1u << (2 * y + hf) : kWide;
+                  vw[y] &= ~(0xffffu << (16 * hf));
+                }
+              x2 = vw[y] & 0x7fff7fffu;
             }
-            uint32_t mx = vw[y] & 0x7fff7fffu;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            mx = __vmaxu2(mx | 0x007f007fu, seen[y]);
-            __syncwarp();
-            if (lane == 0) thr[y] = mx;
+            const uint32_t mx = __vmaxu2(__reduce_max_sync(0xffffffffu, x2 & 0xffffu) | __reduce_max_sync(0xffffffffu, x2 >> 16) << 16 | 0x007f007fu, top);
+            if (lane == 0) seen_at[y] = mx - low;
             if (lane < 2 && 2 * y + lane < G) vf[2 * y + lane] = pow2(kTopV + 127 - (int)((mx >> (16 * lane + 7)) & 0xffu));
           }
           __syncwarp();
@@ -584,8 +784,8 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
             for (int v = 0; v < VT; ++v)
 #pragma unroll
               for (int c = 0; c < 4; ++c) o[nt][v][c] *= down;
-          uint32_t who = __ballot_sync(0xffffffffu, odd);
-          while (who) {  // a key with scales that are not finite: mark the rows that attend it
+          uint32_t who = __ballot_sync(0xffffffffu, bad != 0u);
+          while (who) {  // mark the rows that attend such a key
             const int src = __ffs((int)who) - 1;
             who &= who - 1u;
             const long long j = (long long)t * kKeys + __shfl_sync(0xffffffffu, key, src), at = (long long)x.qpos + lane / x.g;
@@ -832,6 +1032,8 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
           *reinterpret_cast<float4 *>(to + 2 * v) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
+    const uint32_t wide = __ballot_sync(0xffffffffu, (marked & kWide) != 0u);
+    if (wide) wide_rows<T, D, NT, QP>(p, x, smem, mine, wide, marked, warp, lane);
     if (lane == 0) s_state[warp] = warp * L::kRing + state;
     __syncthreads();
     if (tid == kWalkThread) {  // the unit behind the next one, in the place of the last
