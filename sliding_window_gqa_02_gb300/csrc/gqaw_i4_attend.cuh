@@ -69,8 +69,9 @@ constexpr float kMaxP = 15.f;  // ... and of any
 constexpr int kTopV = 10;      // a scale's largest power of two becomes 2^kTopV: 24 s < 2^16
 // How many powers of two the value scales of a group may lie above and below the largest of a warp's first tile.  In fp16
 // the smallest is then 2^-14 or more, and its values are exact; a weight that fp16 rounds to a multiple of 2^-38 of the
-// row's largest is off by 2^-14 of any other value.  Rows that attend other scales are computed by wide_rows().
-constexpr int kAbove = 10, kBelow = 14;
+// row's largest is off by 2^-14 of any other value.  Rows that attend other scales are computed by wide_rows(); so are those
+// of 2^(kEnd + 1) and more, since 2^31 weights of 2^15 times 8 of them would leave fp32.
+constexpr int kAbove = 10, kBelow = 14, kEnd = 63;
 constexpr uint32_t kWide = 1u << 16;
 
 template <int D, int NT, int QP>
@@ -279,8 +280,8 @@ __device__ __noinline__ bool load_rows(const I4Params &p, const Unit &x, unsigne
 
 // The state of a warp's tiles of a unit in fp32 throughout, for the rows of `rows` alone, which attend value scales too
 // far apart for one power of two in fp16.  The large ones may be another row's, or under next to no weight, so every row
-// and lane has a power of two of its own: a sum holds 2^ro of what it stands for, ro going down for a product above 2^40
-// and up when a tile begins with less than 1.  At the end the reference moves so that the weights add up to 2^-13: no sum
+// and lane has a power of two of its own: a sum holds 2^ro of what it stands for, ro going down for a product above 2^88
+// (2^31 of them stay in fp32, and beside them what is 2^-200 of the largest) and up when a tile begins with less than 1.  At the end the reference moves so that the weights add up to 2^-13: no sum
 // of warps and CTAs leaves fp32 where the average does not.
 //
 // Out of line and written for few registers, since ordinary caches do not come here: a lane has a key for the logits and
@@ -290,7 +291,7 @@ template <typename T, int D, int NT, int QP>
 __device__ __noinline__ void wide_rows(const I4Params &p, const Unit &x, const unsigned char *smem, float *mine, uint32_t rows, uint32_t marked,
                                        int warp, int lane) {
   using L = Lay<D, NT, QP>;
-  constexpr int G = L::G, R = L::R, PS = L::PS, DL = D / 32, kNone = 1 << 20;
+  constexpr int G = L::G, R = L::R, PS = L::PS, DL = D / 32, kNone = 1 << 20, kHigh = 80;
   const int my_group = lane * DL / kI4Group;
   const uint2 *sq = reinterpret_cast<const uint2 *>(smem + L::kQ);
   const int *sqexp = reinterpret_cast<const int *>(smem + L::kQexp);
@@ -377,7 +378,7 @@ __device__ __noinline__ void wide_rows(const I4Params &p, const Unit &x, const u
       if (top == 0.f) {
         ro[r] = kNone;
       } else if (top < 1.f) {
-        const int up = 24 - ((int)(__float_as_uint(top) >> 23) - 127);
+        const int up = kHigh - ((int)(__float_as_uint(top) >> 23) - 127);
         ro[r] += up;
 #pragma unroll
         for (int d = 0; d < DL; ++d) o[r][d] = times_pow2(o[r][d], up);
@@ -408,11 +409,11 @@ __device__ __noinline__ void wide_rows(const I4Params &p, const Unit &x, const u
         const float pr = __shfl_sync(0xffffffffu, w[r], key);
         if (some && pr != 0.f) {
           const int over = (int)(__float_as_uint(pr) >> 23 & 0xffu) - 127 + es + ro[r];  // the product's power of two
-          if (over > 40) {
-            const int down = over - 24;
+          if (over > kHigh + 8) {
+            const int down = over - kHigh;
             ro[r] -= down;
 #pragma unroll
-            for (int d = 0; d < DL; ++d) o[r][d] *= pow2_or_0(-down);
+            for (int d = 0; d < DL; ++d) o[r][d] = times_pow2(o[r][d], -down);
           }
           const float u = times_pow2(pr, ro[r] + es);
 #pragma unroll
@@ -698,13 +699,14 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
         const uint32_t h = vs[gr] & 0x7fffu, fin = h < 0x7f80u ? h : 0u;
         uint32_t mx = __reduce_max_sync(0xffffffffu, all ? fin : 0u);
         if (mx == 0u) mx = __reduce_max_sync(0xffffffffu, some ? fin : 0u);
-        const int e = (int)(mx >> 7), low = mx ? max(e - kBelow, 0) << 7 : 0;
+        const int e = (int)(mx >> 7), low = mx ? max(min(e, 127 + kEnd) - kBelow, 0) << 7 : 0;
+        const uint32_t roof = mx ? (uint32_t)(min(e + kAbove, 127 + kEnd) << 7 | 0x7f) : 0u;
         if (lane == 0) {
           uint16_t *to = reinterpret_cast<uint16_t *>(seen_at) + gr;
-          to[0] = (uint16_t)(mx ? (mx | 0x7fu) - low : 0u);
+          to[0] = (uint16_t)(mx ? min(mx | 0x7fu, roof) - low : 0u);
           to[2 * L::kWords] = (uint16_t)low;
-          to[4 * L::kWords] = (uint16_t)(mx ? min(e + kAbove, 254) << 7 | 0x7f : 0);
-          vf[gr] = pow2(kTopV + 127 - e);
+          to[4 * L::kWords] = (uint16_t)roof;
+          vf[gr] = pow2(kTopV + 127 - min(e, 127 + kEnd));
         }
       }
       if (G == 1 && lane == 0)  // the other half of the only word

@@ -187,3 +187,40 @@ def test_a_row_attends_the_same_whatever_others_attend():
     check_rows(full)
     diff = (t.out[0].double() - full.out[0].double()).abs()
     assert (diff <= 2.0 ** -8 * t.out[0].double().abs() + 2.0 ** -9 * t.out[0].double().abs().max()).all()
+
+
+# ------------------------------------------------------------------------------ values near the type's end
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kw", [dict(), dict(sink=True), dict(softcap=3.0), dict(window=100)])
+def test_values_near_the_end_of_the_type(dtype, kw):
+    """Elements up to 2e38 whose averages are finite, by rows: one CTA's units, cut ones, few and many keys."""
+    for D, lens in ((64, [(1, 300), (2, 9000), (8, 8)]), (128, [(1, 5000), (1, 1), (6, 40)]), (256, [(2, 700)]), (32, [(3, 90)])):
+        t = Batch(lens, 4, 2, D, 16, dtype, seed=37, **kw)
+        t.vs.copy_((t.vs.double() * 2.0 ** 125.5).to(BF16))
+        assert t.held()[1].nan_to_num(0.0).abs().max() < 3.3e38
+        t.call(gqaw.gqaw_paged_i4_attend)
+        check_rows(t)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_key_near_the_end_of_the_type(dtype):
+    """One value of 2^125 among small ones, under an ordinary weight."""
+    t = Batch([(1, 3000), (3, 70)], 4, 2, 128, 16, dtype, seed=38)
+    scale_values(t, 0, 1234, 125)
+    scale_values(t, 1, 5, 125)
+    t.call(gqaw.gqaw_paged_i4_attend)
+    check_rows(t)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_long_context_of_large_values(dtype):
+    """The same sign everywhere and weights alike: sums over 40,000 keys of what is near the type's end."""
+    t = Batch([(1, 40000)], 2, 1, 64, 64, dtype, seed=45)
+    t.q.fill_(0.0)
+    t.vc.fill_(0xFF)
+    for power in (62, 70, 100, 125):
+        t.vs.copy_(torch.where(t.vs.isnan(), t.vs, torch.full_like(t.vs, 2.0 ** power)))
+        t.call(gqaw.gqaw_paged_i4_attend)
+        check_rows(t)
