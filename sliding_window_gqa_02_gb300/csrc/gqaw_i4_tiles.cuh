@@ -36,8 +36,8 @@ __device__ __forceinline__ uint32_t bf_fma2(uint32_t a, uint32_t b, uint32_t c) 
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-// Nibble k of each half of w as a value.  EXACT: the scale has so few bits that 24 of it are a bf16 number: the
-// nibble in the upper bits of the mantissa of 16 is 16 + c, times the scale less 24 of it one multiply-add.  Else in
+// Nibble k of each half of w as a value.  EXACT: the scale has so few bits, and is so small, that 24 of it
+// are a bf16 number: the nibble in the upper bits of the mantissa of 16 is 16 + c, times the scale less 24 of it one multiply-add.  Else in
 // the lower bits of 128: less 136, then times the scale.
 template <bool EXACT, int K>
 __device__ __forceinline__ uint32_t nibble2(uint32_t w, uint32_t s, uint32_t s24) {
@@ -186,7 +186,8 @@ __device__ inline bool convert(const I4Params &p, const PShape &shp, const PSche
         *reinterpret_cast<uint4 *>(to + (el / 8) * HALF_BYTES + (((el & 7) ^ (r & 7)) << 4)) = values8<exact.value>(word, s2, s24, order);
       }
     };
-    if (__any_sync(0xffffffffu, (cur.scale & 3u) != 0u))  // more than six bits: not of this library's append
+    // more than six bits, not of this library's append; or from 2^123 on, where 24 of it leave bf16 (or not finite)
+    if (__any_sync(0xffffffffu, (cur.scale & 3u) != 0u || (cur.scale & 0x7fffu) >= (123u + 127u) << 7))
       put(std::false_type(), !value);
     else if (value)
       put(std::true_type(), false);

@@ -224,3 +224,34 @@ def test_a_long_context_of_large_values(dtype):
         t.vs.copy_(torch.where(t.vs.isnan(), t.vs, torch.full_like(t.vs, 2.0 ** power)))
         t.call(gqaw.gqaw_paged_i4_attend)
         check_rows(t)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("max_len", [0, LONG])
+def test_chunks_with_one_large_value(D, max_len):
+    """Prompt chunks, on expanded keys and on codes: a key with elements up to 1.4e38 (a scale that times 24 leaves the
+    type), which some tokens do not attend and the others attend with a weight of 2^-30."""
+    t = Batch([(200, 300), (100, 100), (70, 70), (90, 91)], 8, 2, D, 16, BF16, seed=39, max_len=max_len, scale=1.0)
+    t.q.fill_(1.0)
+    t.ks.copy_(torch.where(t.ks.isnan(), t.ks, t.ks * 2.0 ** -8))
+    for i, j in ((0, 180), (1, 60)):
+        pg, r = int(t.table[i, j // 16]), j % 16
+        t.kc[pg, :, r] = 0x77
+        t.ks[pg, :, r] = 30 * math.log(2) / D
+        t.vs[pg, :, r] = 1.1 * 2.0 ** 124
+        t.vs.view(torch.int16)[pg, :, r] &= ~7  # five significant bits, as the append writes them
+    t.call(gqaw.gqaw_paged_i4_attend)
+    check_rows(t, coarse=False)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("max_len", [0, LONG])
+def test_chunks_with_large_keys(D, max_len):
+    """Keys near the end of the type under queries near the other."""
+    t = Batch([(200, 300), (100, 100), (70, 70), (90, 91)], 8, 2, D, 16, BF16, seed=40, max_len=max_len, scale=1.0)
+    t.ks.copy_((t.ks.double() * 2.0 ** 125.5).to(BF16))
+    t.ks.view(torch.int16)[:] &= ~7
+    t.ks.copy_(t.ks.nan_to_num(0.25))
+    t.q.copy_((t.q.double() * 2.0 ** -124 / D).to(BF16))
+    t.call(gqaw.gqaw_paged_i4_attend)
+    check_rows(t)
