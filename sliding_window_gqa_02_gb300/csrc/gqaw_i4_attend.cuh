@@ -259,8 +259,8 @@ __device__ __noinline__ bool load_rows(const I4Params &p, const Unit &x, unsigne
   const int32_t *table = p.table + (long long)x.b * p.width;
   auto page_of = [&](uint32_t j) { return (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift); };
   auto page_at = [&](uint32_t j) {
-    const int id = j >= x.jlo && j < x.jhi ? table[page_of(j)] : -2;
-    if (id != -2 && (unsigned)id >= (unsigned)p.npages) pflag(p, GQAW_DEV_BAD_PAGE);
+    const int id = j >= x.jlo && j < x.jhi ? needed_page(table[page_of(j)]) : kNotNeeded;
+    if (id != kNotNeeded && (unsigned)id >= (unsigned)p.npages) pflag(p, GQAW_DEV_BAD_PAGE);
     return (unsigned)id < (unsigned)p.npages ? id : -1;
   };
 #pragma unroll 1
@@ -488,17 +488,17 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   const unsigned char *bcodes = nullptr;  // this lane's block of the batch of tiles at hand: codes
   const uint16_t *bscales = nullptr;      // ... and scales, of keys
   uint32_t bok = 0;                       // the lanes whose block is needed and has a page
-  int bid = -2, bn = 0;                   // the page of its block of the next batch; tiles of this batch loaded
+  int bid = kNotNeeded, bn = 0;                   // the page of its block of the next batch; tiles of this batch loaded
   // its place in the batch that begins with tile t
   auto block_at = [&](int t) { return (uint32_t)(t + lane / CPR * W) * kKeys + lane % CPR * RPC; };
   auto look_up = [&](const Unit &x, int t, int end) {
     const uint32_t j = block_at(t);
-    return t + lane / CPR * W < end && j < x.jhi && j + RPC > x.jlo ? p.table[(long long)x.b * p.width + page_of(j)] : -2;
+    return t + lane / CPR * W < end && j < x.jhi && j + RPC > x.jlo ? needed_page(p.table[(long long)x.b * p.width + page_of(j)]) : kNotNeeded;
   };
   auto resolve = [&](const Unit &x, int t) {
     const uint32_t j = block_at(t), row = j - page_of(j) * p.page;
     const bool ok = (unsigned)bid < (unsigned)p.npages;
-    if (!ok && bid != -2) pflag(p, GQAW_DEV_BAD_PAGE);
+    if (!ok && bid != kNotNeeded) pflag(p, GQAW_DEV_BAD_PAGE);
     bok = __ballot_sync(0xffffffffu, ok);
     bcodes = x.codes + (ok ? ((uint64_t)(uint32_t)bid * p.sp16 + (uint64_t)row * p.sr16) << 4 : 0ull);
     bscales = x.scales + (ok ? ((uint64_t)(uint32_t)bid * p.tpg + (uint64_t)row * p.trg) * G : 0ull);
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   };
   auto bump = [](int st) { return st + 1 == S ? 0 : st + 1; };
   // a unit's first tiles, from stage st on; id: first_page() of it
-  auto first_page = [&](const Unit &x) { return p.blocks && x.more ? look_up(x, x.t0 + warp, x.t0 + x.tiles) : -2; };
+  auto first_page = [&](const Unit &x) { return p.blocks && x.more ? look_up(x, x.t0 + warp, x.t0 + x.tiles) : kNotNeeded; };
   auto load_first = [&](const Unit &x, int st, int id) {
     const int t = x.t0 + warp, end = x.t0 + x.tiles;
     if (p.blocks) {

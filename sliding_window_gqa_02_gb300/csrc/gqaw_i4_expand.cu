@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) i4_expand_kernel(const I4Params p, c
 #pragma unroll
     for (int c = 0; c < CPR; ++c) {
       const uint32_t j = j0 + c * RPC;
-      id[c] = j >= from && j < to ? __ldg(table + (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift)) : -2;
+      id[c] = j >= from && j < to ? needed_page(__ldg(table + (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift))) : kNotNeeded;
     }
     uint4 codes[CPR];
     uint32_t scale[CPR];
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) i4_expand_kernel(const I4Params p, c
     for (int c = 0; c < CPR; ++c) {
       const uint32_t j = j0 + c * RPC, r = j - (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift) * p.page;
       const bool ok = (unsigned)id[c] < (unsigned)p.npages;
-      bad |= !ok && id[c] != -2;
+      bad |= !ok && id[c] != kNotNeeded;
       codes[c] = make_uint4(0u, 0u, 0u, 0u);
       scale[c] = 0u;
       if (ok) {

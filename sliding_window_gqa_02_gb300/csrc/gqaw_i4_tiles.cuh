@@ -122,17 +122,17 @@ __device__ inline bool convert(const I4Params &p, const PShape &shp, const PSche
     }
   };
   struct Ids {
-    int id;         // this lane's page: -2 when its row is not needed
+    int id;         // this lane's page, or kNotNeeded
     uint32_t row;   // its row in it
     int kvh;
     uint32_t at;    // i | gk << 6 | kFresh, or kNone
   };
   auto look_up = [&]() {
-    Ids x{-2, 0u, 0, kNone};
+    Ids x{kNotNeeded, 0u, 0, kNone};
     if (!have) return x;
     const uint32_t j = (uint32_t)(wk->u.kt + wk->u.k0 + tile) * 128 + (i & (NB - 1)) * RPC + row;
     const uint32_t page = (uint32_t)(((uint64_t)j * p.div_mul) >> p.div_shift);
-    if (j >= wk->lo && j < wk->hi) x.id = __ldg(p.table + (long long)wk->u.b * p.width + page);
+    if (j >= wk->lo && j < wk->hi) x.id = needed_page(__ldg(p.table + (long long)wk->u.b * p.width + page));
     x.row = j - page * p.page;
     x.kvh = wk->u.hu;
     x.at = (uint32_t)i | ((uint32_t)gk << 6 & ~kFresh) | (fresh ? kFresh : 0u);
@@ -153,7 +153,7 @@ __device__ inline bool convert(const I4Params &p, const PShape &shp, const PSche
       const uint16_t *sbase = (value ? p.vscale : p.kscale) + x.kvh * p.th + part;
       b.codes = __ldg(base + ((uint64_t)(uint32_t)x.id * p.sp16 + (uint64_t)x.row * p.sr16 + part));
       b.scale = __ldg(sbase + ((uint64_t)(uint32_t)x.id * p.tpg + (uint64_t)x.row * p.trg) * (D / kI4Group));
-    } else if (x.id != -2) {
+    } else if (x.id != kNotNeeded) {
       pflag(p, GQAW_DEV_BAD_PAGE);
     }
     return b;

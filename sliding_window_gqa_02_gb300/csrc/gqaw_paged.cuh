@@ -106,6 +106,11 @@ __device__ inline void sched_build(const PagedParams &p, const PShape &shp, PSch
   __syncthreads();
 }
 
+// A page table entry that is looked up ahead of its use, or that none is needed there: apart from any that a table may
+// hold, of which all below 0 are as bad as -1.
+constexpr int kNotNeeded = -2;
+__device__ __forceinline__ int needed_page(int entry) { return max(entry, -1); }
+
 // Row offset (elements) of position j of sequence b, kv head h; -1 when its table entry is bad.
 __device__ __forceinline__ long long cache_row(const PagedParams &p, int b, int h, int j) {
   const int pg = j / p.page;

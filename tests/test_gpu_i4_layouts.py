@@ -37,3 +37,20 @@ def test_rows_far_apart(dtype, S, D, row):
         t.check_read()
         del t, far, x, y, buf
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("entry", [-1, -2, -3, -(1 << 31), 1 << 20, (1 << 31) - 1])
+@pytest.mark.parametrize("dtype,S,D,page,max_len", [(BF16, 1, 64, 16, 0), (BF16, 4, 128, 24, 0), (BF16, 2, 32, 16, 0), (F32, 3, 64, 16, 0),
+                                                    (F32, 9, 128, 7, 0), (BF16, 100, 128, 16, 0), (BF16, 70, 64, 24, LONG),
+                                                    (BF16, 60, 128, 16, LONG), (BF16, 90, 256, 32, 0)])
+def test_every_bad_entry_is_flagged(entry, dtype, S, D, page, max_len):
+    """A table entry out of range sets the flag, whatever it is, in every kernel; other sequences are right, and
+    an entry that nobody needs is not looked at."""
+    t = Batch([(S, 310), (S, 200), (1, 33), (S, 128)], 8, 2, D, page, dtype, seed=51, max_len=max_len, window=150)
+    t.table[0, max(0, 310 - S - 150 + 1) // page + 2] = entry
+    t.call(gqaw.gqaw_paged_i4_attend, flags=gqaw.GQAW_DEV_BAD_PAGE)
+    t.check_output(skip=(0,))
+    u = Batch([(S, 310), (1, 40)], 8, 2, D, page, dtype, seed=52, max_len=max_len, window=20)
+    u.table[0, 0] = entry
+    u.call(gqaw.gqaw_paged_i4_attend)
+    u.check_output()
