@@ -125,14 +125,14 @@ __global__ void __launch_bounds__(prow::Lay<T, D, BM>::kThreads) paged_rows_atte
 
     // Tile k (relative to the unit) sits in stage k % kStages.  Its table entries are read by
     // the last warp, which seldom has rows where time matters, a tile before its loads go out.
-    auto look_up = [&](int k) {  // this thread's page of tile k: -2 when not needed
+    auto look_up = [&](int k) {  // this thread's page of tile k
       const long long j = (long long)(u.kt + k) * kKeys + (tid & 31);
-      return k < u.k1 && j >= jlo && j < jhi ? p.table[(long long)u.b * p.width + (int)j / p.page] : -2;
+      return k < u.k1 && j >= jlo && j < jhi ? needed_page(p.table[(long long)u.b * p.width + (int)j / p.page]) : kNotNeeded;
     };
     auto put_rows = [&](int k, int id) {
       const int j = (u.kt + k) * kKeys + (tid & 31);
       long long off = -1;
-      if (id != -2) {
+      if (id != kNotNeeded) {
         if ((unsigned)id < (unsigned)p.npages)
           off = id * p.sp + kvh * p.sh + (long long)(j - j / p.page * p.page) * p.sr;
         else
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(prow::Lay<T, D, BM>::kThreads) paged_rows_atte
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const bool finder = tid >= kThreads - 32;
-    int id = -2;
+    int id = kNotNeeded;
     if (finder)
       for (int k = 0; k < kStages; ++k) put_rows(u.k0 + k, look_up(u.k0 + k));
     // the query rows, scaled

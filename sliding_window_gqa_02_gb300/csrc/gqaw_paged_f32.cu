@@ -95,17 +95,17 @@ __global__ void __launch_bounds__(pf32::Lay<D>::kThreads, 1)
     const int n = (u.k1 - u.k0 - warp + W - 1) / W;  // tiles of this warp: k0 + warp, k0 + warp + W, ...
     const int first = used;                          // the number of the unit's first tile
     auto key0 = [&](int i) { return (long long)(u.kt + u.k0 + warp + i * W) * kKeys; };
-    // lane b < nbox looks up box b of the warp's tile i: -2 when no row attends any of its keys
+    // lane b < nbox looks up box b of the warp's tile i: kNotNeeded when no row attends any of its keys
     auto look_up = [&](int i) {
       const long long j = key0(i) + lane * box;
-      return i < n && lane < nbox && j < jhi && j + box > jlo ? p.table[(long long)u.b * p.width + (int)j / p.page] : -2;
+      return i < n && lane < nbox && j < jhi && j + box > jlo ? needed_page(p.table[(long long)u.b * p.width + (int)j / p.page]) : kNotNeeded;
     };
     auto load = [&](int i, int id) {
       if (i >= n) return;  // uniform over the warp
       const int st = (first + i) % S;
       const int j = (int)key0(i) + lane * box, row = j - j / p.page * p.page;
-      const bool ok = id != -2 && (unsigned)id < (unsigned)p.npages;
-      if (id != -2 && !ok) pflag(p, GQAW_DEV_BAD_PAGE);
+      const bool ok = (unsigned)id < (unsigned)p.npages;
+      if (id != kNotNeeded && !ok) pflag(p, GQAW_DEV_BAD_PAGE);
       const uint32_t mask = __ballot_sync(0xffffffffu, ok);
       if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(mask) * 2 * L::B * box * 128));
       for (int b = 0; b < nbox; ++b) {

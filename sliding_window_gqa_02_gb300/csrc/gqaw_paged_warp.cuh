@@ -67,16 +67,16 @@ __global__ void __launch_bounds__(pwarp::Lay<T, D>::kThreads, pwarp::Lay<T, D>::
     const int n = (u.k1 - u.k0 - warp + W - 1) / W;  // tiles of this warp: k0 + warp, k0 + warp + W, ...
 
     auto key0 = [&](int i) { return (long long)(u.kt + u.k0 + warp + i * W) * kKeys; };
-    auto look_up = [&](int i) {  // this lane's page of the warp's tile i: -2 when not needed
+    auto look_up = [&](int i) {  // this lane's page of the warp's tile i
       const long long j = key0(i) + lane;
-      return i < n && j >= jlo && j < jhi ? p.table[(long long)u.b * p.width + (int)j / p.page] : -2;
+      return i < n && j >= jlo && j < jhi ? needed_page(p.table[(long long)u.b * p.width + (int)j / p.page]) : kNotNeeded;
     };
     auto load = [&](int i, int id) {
       if (i < n) {  // uniform over the warp
         constexpr int CPR = D * (int)sizeof(T) / 16;  // 16-byte parts of a row
         const int j = (int)key0(i) + lane;
         long long off = -1;
-        if (id != -2) {
+        if (id != kNotNeeded) {
           if ((unsigned)id < (unsigned)p.npages)
             off = id * p.sp + kvh * p.sh + (long long)(j - j / p.page * p.page) * p.sr;
           else
