@@ -355,7 +355,8 @@ gqaw_status run_i4(const gqaw_paged_i4_args *x, void *stream, int what) {
   I4Params p;
   std::memset(&p, 0, sizeof(p));
   fill_paged(a, L, &p);
-  // without pages no row is read, but copies of no bytes still name a source: a valid address
+  // without pages no row is read, but copies of no bytes still name a source: a valid address, of every head
+  if (!a->num_pages) L.sp = L.sh = L.sr = L.tp = L.th = L.tr = 0;
   p.kp = a->num_pages ? a->key_pages : a->workspace;
   p.vp = a->num_pages ? a->value_pages : a->workspace;
   p.kscale = static_cast<uint16_t *>(a->num_pages ? x->key_scales : a->workspace);

@@ -54,3 +54,35 @@ def test_every_bad_entry_is_flagged(entry, dtype, S, D, page, max_len):
     u.table[0, 0] = entry
     u.call(gqaw.gqaw_paged_i4_attend)
     u.check_output()
+
+
+@pytest.mark.parametrize("dtype,S,D,max_len", [(BF16, 1, 64, 0), (BF16, 5, 32, 0), (F32, 3, 128, 0), (BF16, 1, 256, 0), (BF16, 100, 128, 0),
+                                               (BF16, 90, 256, 0), (BF16, 60, 128, LONG)])
+@pytest.mark.parametrize("page", [16, 1 << 22])
+def test_a_cache_without_pages(dtype, S, D, max_len, page):
+    """No page exists: every table entry is out of range, the tokens' outputs are unspecified, rows read back are left
+    as they were.  With pages so large that a head's place lies beyond any memory of the call."""
+    t = Batch([(S, 140), (0, 5), (1, 9), (S, 200)], 8, 2, D, 16, dtype, seed=53, norm=True, rotary=32, extra_rows=2, max_len=max_len)
+    t.page = page
+    t.kc, t.vc = (torch.empty(0, 2, page, D // 2, dtype=torch.uint8, device="cuda") for _ in "kv")
+    t.ks, t.vs = (torch.empty(0, 2, page, D // 32, dtype=BF16, device="cuda") for _ in "kv")
+    t.max_len = min(t.max_len, t.table.shape[1] * page)
+    assert t.args().paged.num_pages == 0
+    for call in (gqaw.gqaw_paged_i4_append, gqaw.gqaw_paged_i4_attend, gqaw.gqaw_paged_i4_step, gqaw.gqaw_paged_i4_read):
+        t.call(call, flags=gqaw.GQAW_DEV_BAD_PAGE)
+    assert (t.out[2 * S + 1:] == 7.0).all() and (t.ko == 7.0).all() and (t.vo == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype,max_new,D,max_len", [(BF16, 1, 64, 0), (BF16, 8, 128, 0), (F32, 20, 64, 0), (BF16, 300, 128, 0),
+                                                     (BF16, 300, 256, 0), (BF16, 60, 128, LONG), (BF16, 60, 64, 4 * LONG)])
+def test_a_batch_without_tokens(dtype, max_new, D, max_len):
+    """Every sequence idle, though the call allows new tokens: the kernels run and find nothing to do."""
+    t = Batch([(0, 90), (0, 0), (0, 400)], 8, 2, D, 16, dtype, seed=54, norm=True, rotary=32, extra_rows=max_new, max_len=max_len)
+    t.max_new, t.max_len = max_new, max(t.max_len, max_new)
+    before, launches = t.snapshot(), gqaw.gqaw_launch_count()
+    for call in (gqaw.gqaw_paged_i4_append, gqaw.gqaw_paged_i4_attend, gqaw.gqaw_paged_i4_step, gqaw.gqaw_paged_i4_read):
+        t.call(call)
+    assert gqaw.gqaw_launch_count() >= launches + 5
+    assert (t.out == 7.0).all() and (t.ko == 7.0).all() and (t.vo == 7.0).all()
+    for x, y in zip(t.snapshot(), before):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
