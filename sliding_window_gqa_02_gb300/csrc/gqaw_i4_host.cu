@@ -166,9 +166,9 @@ Part part_of(const void *p, const char *name, const gqaw_paged_args *a, long lon
   return x;
 }
 
-// Do two parts of the cache lie apart, though the bytes between their first and last overlap?  At a
-// level down to which their strides agree, what the inner dimensions of one reach over lies between two of
-// the other's.
+// Do two parts of the cache lie apart, though the bytes between their first and last overlap?  At a level down to
+// which their strides agree, what the inner dimensions of one reach over lies between two of the other's; and of the levels
+// outside it, each steps over what both reach over together.
 bool woven_parts(const Part &x, const Part &y) {
   const Part &f = x.all.lo < y.all.lo ? x : y, &g = x.all.lo < y.all.lo ? y : x;
   const long long gap = g.all.lo - f.all.lo;
@@ -177,8 +177,12 @@ bool woven_parts(const Part &x, const Part &y) {
     for (int i = from; i < p.n; ++i) b += (p.dim[i].count - 1) * p.dim[i].stride;
     return b;
   };
-  for (int k = 0; k < f.n && k < g.n && f.dim[k].stride == g.dim[k].stride && f.dim[k].count == g.dim[k].count; ++k)
-    if (gap >= inner(f, k + 1) && gap + inner(g, k + 1) <= f.dim[k].stride) return true;
+  for (int k = 0; k < f.n && k < g.n && f.dim[k].stride == g.dim[k].stride && f.dim[k].count == g.dim[k].count; ++k) {
+    long long both = gap + inner(g, k + 1);
+    bool apart = gap >= inner(f, k + 1) && both <= f.dim[k].stride;
+    for (int i = k; i > 0; --i) apart = apart && (both += (f.dim[i].count - 1) * f.dim[i].stride) <= f.dim[i - 1].stride;
+    if (apart) return true;
+  }
   return false;
 }
 
