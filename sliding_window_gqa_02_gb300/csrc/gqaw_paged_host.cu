@@ -225,7 +225,8 @@ unsigned long long pages_bytes(const gqaw_paged_args *a, const Plan &L) {
 // Do the rows of two caches of the same strides lie apart, though the bytes between their first and
 // last overlap?  With the strides ascending, a block of a level is what its inner dimensions reach
 // over, and the blocks lie a stride apart: two caches woven at that level have each other's blocks
-// between their own (a page's, a head's or a row's keys beside its values).
+// between their own (a page's, a head's or a row's keys beside its values), and the levels outside it
+// step over what both reach over together.
 bool woven_pages(const gqaw_paged_args *a, const Plan &L) {
   struct {
     long long stride, count;
@@ -233,10 +234,19 @@ bool woven_pages(const gqaw_paged_args *a, const Plan &L) {
   std::sort(dim, dim + 3, [](const auto &x, const auto &y) { return x.stride < y.stride; });
   const long long gap = std::llabs(static_cast<const char *>(a->key_pages) - static_cast<const char *>(a->value_pages)) / L.es;
   long long block = a->head_size;
-  for (const auto &d : dim) {
-    if (d.count < 2) continue;  // such a dimension may have any stride
-    if (gap >= block && gap + block <= d.stride) return true;
-    block += (d.count - 1) * d.stride;
+  for (int k = 0; k < 3; ++k) {
+    if (dim[k].count < 2) continue;  // such a dimension may have any stride
+    if (gap >= block) {
+      long long both = gap + block;
+      bool apart = true;
+      for (int i = k; i < 3; ++i)
+        if (dim[i].count > 1) {
+          apart = apart && both <= dim[i].stride;
+          both += (dim[i].count - 1) * dim[i].stride;
+        }
+      if (apart) return true;
+    }
+    block += (dim[k].count - 1) * dim[k].stride;
   }
   return false;
 }
