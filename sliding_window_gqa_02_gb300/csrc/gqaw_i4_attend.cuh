@@ -73,6 +73,7 @@ constexpr int kTopV = 10;      // a scale's largest power of two becomes 2^kTopV
 // of 2^(kEnd + 1) and more, since 2^31 weights of 2^15 times 8 of them would leave fp32.
 constexpr int kAbove = 10, kBelow = 14, kEnd = 63;
 constexpr uint32_t kWide = 1u << 16;
+constexpr int kLarge = -64;    // a row's power of two: queries of 2^77 and more
 
 template <int D, int NT, int QP>
 struct Lay {
@@ -93,7 +94,7 @@ struct Lay {
   // per warp: keys' scales in fp32, values' in fp16, their factors; in bf16 bits, two groups a word, the largest scale of the
   // largest power of two seen, less the smallest that may come; that; and the largest that may come
   static constexpr int kWords = (G + 1) / 2, kSeen = (kKeys * G * 6 + G * 4 + 15) / 16 * 16;
-  static constexpr int kNormBytes = (kSeen + 3 * kWords * 4 + 15) / 16 * 16;
+  static constexpr int kNormBytes = (kSeen + 3 * kWords * 4 + R * 4 + 15) / 16 * 16;
   static constexpr int kQ = kNorm + W * kNormBytes;      // query operands [QP][NT][2 G][32 lanes] of 8 bytes
   static constexpr int kQsum = kQ + QP * NT * 2 * G * 32 * 8;  // [G][R] fp32: where accumulators start
   static constexpr int kQexp = kQsum + R * G * 4;        // [R]: power of two of a row
@@ -278,14 +279,45 @@ __device__ __noinline__ bool load_rows(const I4Params &p, const Unit &x, unsigne
   return id >= 0;
 }
 
+// What the value scales of a warp's first tile of a unit say of the others.  Out of line, which leaves the loop over the
+// tiles its registers (64 long contexts 262 us, 264 to 267 otherwise).
+template <int D, int kWords>
+__device__ __noinline__ void first_scales(const I4Params &p, const Unit &x, const uint16_t *scales, uint32_t *seen_at, float *vf, int warp, int lane) {
+  constexpr int G = D / kI4Group;
+  const int key = (lane & ~7) | kappa<D>(lane & 7);
+  const long long j = (long long)(x.t0 + warp) * kKeys + key, last = (long long)x.qpos + x.ntok - 1;
+  // The largest of the keys that all rows attend, if one is not zero: what only some of them attend is not to say how
+  // the others are computed.  A group of zeros may have no other scale after that.
+  const bool some = j >= x.jlo && j < x.jhi, all = j <= (long long)x.qpos && j >= (long long)x.jlo && (p.W == 0 || j > last - p.W);
+  const uint16_t *vs = scales + key * G;
+#pragma unroll
+  for (int gr = 0; gr < G; ++gr) {
+    const uint32_t h = vs[gr] & 0x7fffu, fin = h < 0x7f80u ? h : 0u;
+    uint32_t mx = __reduce_max_sync(0xffffffffu, all ? fin : 0u);
+    if (mx == 0u) mx = __reduce_max_sync(0xffffffffu, some ? fin : 0u);
+    const int e = (int)(mx >> 7), low = mx ? max(min(e, 127 + kEnd) - kBelow, 0) << 7 : 0;
+    const uint32_t roof = mx ? (uint32_t)(min(e + kAbove, 127 + kEnd) << 7 | 0x7f) : 0u;
+    if (lane == 0) {
+      uint16_t *to = reinterpret_cast<uint16_t *>(seen_at) + gr;
+      to[0] = (uint16_t)(mx ? min(mx | 0x7fu, roof) - low : 0u);
+      to[2 * kWords] = (uint16_t)low;
+      to[4 * kWords] = (uint16_t)roof;
+      vf[gr] = pow2(kTopV + 127 - min(e, 127 + kEnd));
+    }
+  }
+  if (G == 1 && lane == 0)  // the other half of the only word
+    reinterpret_cast<uint16_t *>(seen_at)[1] = reinterpret_cast<uint16_t *>(seen_at)[3] = reinterpret_cast<uint16_t *>(seen_at)[5] = 0;
+  __syncwarp();
+}
+
 // The state of a warp's tiles of a unit in fp32 throughout, for the rows of `rows` alone, which attend value scales too
-// far apart for one power of two in fp16.  The large ones may be another row's, or under next to no weight, so every row
+// far apart for one power of two in fp16, or have queries of 2^77 and more.  The large scales may be another row's, or under next to no weight, so every row
 // and lane has a power of two of its own: a sum holds 2^ro of what it stands for, ro going down for a product above 2^88
 // (2^31 of them stay in fp32, and beside them what is 2^-200 of the largest) and up when a tile begins with less than 1.  At the end the reference moves so that the weights add up to 2^-13: no sum
 // of warps and CTAs leaves fp32 where the average does not.
 //
-// Out of line and written for few registers, since ordinary caches do not come here: a lane has a key for the logits and
-// D / 32 dimensions for the values.  The queries are the operands of the products (put_query()).  Bound by its own
+// Out of line and written for few registers, since ordinary caches do not come here: a lane has a key for the logits (its
+// scales relative to the largest's power of two) and D / 32 dimensions for the values.  The queries are the operands of the products (put_query()).  Bound by its own
 // instructions: 64 contexts of 4 k to 33 k keys that all have such scales take 5.9 ms, and 0.26 without.
 template <typename T, int D, int NT, int QP>
 __device__ __noinline__ void wide_rows(const I4Params &p, const Unit &x, const unsigned char *smem, float *mine, uint32_t rows, uint32_t marked,
@@ -295,8 +327,6 @@ __device__ __noinline__ void wide_rows(const I4Params &p, const Unit &x, const u
   const int my_group = lane * DL / kI4Group;
   const uint2 *sq = reinterpret_cast<const uint2 *>(smem + L::kQ);
   const int *sqexp = reinterpret_cast<const int *>(smem + L::kQexp);
-  const int se = min(40, -min(0, __reduce_min_sync(0xffffffffu, lane < x.rows ? sqexp[min(lane, R - 1)] : 0)));
-  const float sfac = pow2(se - 24);
   float o[R][DL], l[R], m[R];  // the reference is a whole number
   int ro[R];
   __syncwarp();  // the other rows' state is written
@@ -316,12 +346,15 @@ __device__ __noinline__ void wide_rows(const I4Params &p, const Unit &x, const u
     const bool ok = at.page >= 0;  // else a row of zeros
     const unsigned char *codes = x.codes + (ok ? at.page * p.sp + at.row * p.sr : 0ll);
     const uint16_t *scales = x.scales + (ok ? at.page * p.tp + at.row * p.tr : 0ll);
+    int ks = -126;  // the power of two of the key's largest scale
+#pragma unroll 1
+    for (int gr = 0; gr < G; ++gr) ks = max(ks, ok ? (int)(scales[gr] >> 7 & 0xffu) - 127 : -126);
     float w[R];  // logits, then weights
 #pragma unroll
     for (int r = 0; r < R; ++r) w[r] = 0.f;
 #pragma unroll 1
     for (int gr = 0; gr < G; ++gr) {
-      const float s = ok ? __uint_as_float((uint32_t)scales[gr] << 16) * sfac : 0.f;
+      const float s = ok ? times_pow2(__uint_as_float((uint32_t)scales[gr] << 16), -ks) : 0.f;
       float acc[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[r] = 0.f;
@@ -356,7 +389,7 @@ __device__ __noinline__ void wide_rows(const I4Params &p, const Unit &x, const u
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (!((rows >> r) & 1u)) continue;
-      float z = w[r] * (p.qscale * pow2_or_0(24 - se - sqexp[r]));
+      float z = times_pow2(w[r] * p.qscale, ks - sqexp[r]);
       if (p.capmul != 0.f) z = sizeof(T) == 4 ? cap_logit(p, z) : p.capmul * ptc::fast_tanh(z);
       const long long pos = (long long)x.qpos + r / x.g;
       if (!(r < x.rows && in && j <= pos && (p.W == 0 || j > pos - p.W))) z = -INFINITY;
@@ -468,6 +501,10 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
   uint16_t *nv = reinterpret_cast<uint16_t *>(nk + kKeys * G);                    // [G][position]
   float *vf = reinterpret_cast<float *>(nv + kKeys * G);  // of each group: the factor that takes the largest scale's power of two to 2^kTopV
   uint32_t *seen_at = reinterpret_cast<uint32_t *>(smem + L::kNorm + warp * L::kNormBytes + L::kSeen);
+  // of each row: groups in which it attends a scale that is not finite; kWide: it attends one too far off, or its queries are so
+  // large that the smallest scales, 2^-133, would leave fp32 beside acc < 1 (a factor for these would make the others' logits
+  // leave it)
+  uint32_t *marks = seen_at + 3 * L::kWords;
   const uint2 *sq = reinterpret_cast<const uint2 *>(smem + L::kQ);
   float *sqsum = reinterpret_cast<float *>(smem + L::kQsum);
   int *sqexp = reinterpret_cast<int *>(smem + L::kQexp);
@@ -662,17 +699,13 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
         qs[i][1] = qs[i][3] = y.y;
       }
     }
-    // z = (sum s 2^se acc) 2^(24 - se - e) qscale, e the row's power of two; se is not 0 where queries are
-    // so large (e < 0) that the keys' scales may be too small for fp32 beside acc < 1: the smallest, 2^-133, times
-    // what of acc counts, 2^-26 and more, is a normal number with 2^40, and other rows' scales up to 2^87 have room
-    const int se = min(40, -min(0, __reduce_min_sync(0xffffffffu, lane < rows ? sqexp[min(lane, R - 1)] : 0)));
-    const float sfac = pow2(se - (kExact ? 24 : 0));  // (signed codes are whole numbers, not multiples of 2^-24)
+    // z = (sum s acc) 2^(24 - e) qscale, e the row's power of two
     float qf[NT][2], nb[NT][2], th[NT][2], l[NT][2];  // factor; minus the reference; what a logit less the reference may be
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        qf[nt][c] = p.qscale * pow2_or_0(24 - se - sqexp[nt * 8 + 2 * t4 + c]);
+        qf[nt][c] = p.qscale * pow2_or_0(24 - sqexp[nt * 8 + 2 * t4 + c]);
         nb[nt][c] = 0.f;
         th[nt][c] = -INFINITY;
         l[nt][c] = 0.f;
@@ -684,37 +717,13 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
       for (int i = 0; i < VT; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
-    float my_vf = pow2(127);  // this lane's group's factor
-    if (x.t0 + warp < end) {  // what the first tile's scales say of the others
+    if (x.t0 + warp < end) {
       asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
       __syncwarp();
-      const int key = (lane & ~7) | kappa<D>(lane & 7);
-      const long long j = (long long)(x.t0 + warp) * kKeys + key, last = (long long)x.qpos + x.ntok - 1;
-      // The largest of the keys that all rows attend, if one is not zero: what only some of them attend is not to say how
-      // the others are computed.  A group of zeros may have no other scale after that.
-      const bool some = j >= x.jlo && j < x.jhi, all = j <= (long long)x.qpos && j >= (long long)x.jlo && (p.W == 0 || j > last - p.W);
-      const uint16_t *vs = reinterpret_cast<const uint16_t *>(ring + st * L::kStage + 2 * L::kCodes + L::kScales) + key * G;
-#pragma unroll
-      for (int gr = 0; gr < G; ++gr) {
-        const uint32_t h = vs[gr] & 0x7fffu, fin = h < 0x7f80u ? h : 0u;
-        uint32_t mx = __reduce_max_sync(0xffffffffu, all ? fin : 0u);
-        if (mx == 0u) mx = __reduce_max_sync(0xffffffffu, some ? fin : 0u);
-        const int e = (int)(mx >> 7), low = mx ? max(min(e, 127 + kEnd) - kBelow, 0) << 7 : 0;
-        const uint32_t roof = mx ? (uint32_t)(min(e + kAbove, 127 + kEnd) << 7 | 0x7f) : 0u;
-        if (lane == 0) {
-          uint16_t *to = reinterpret_cast<uint16_t *>(seen_at) + gr;
-          to[0] = (uint16_t)(mx ? min(mx | 0x7fu, roof) - low : 0u);
-          to[2 * L::kWords] = (uint16_t)low;
-          to[4 * L::kWords] = (uint16_t)roof;
-          vf[gr] = pow2(kTopV + 127 - min(e, 127 + kEnd));
-        }
-      }
-      if (G == 1 && lane == 0)  // the other half of the only word
-        reinterpret_cast<uint16_t *>(seen_at)[1] = reinterpret_cast<uint16_t *>(seen_at)[3] = reinterpret_cast<uint16_t *>(seen_at)[5] = 0;
-      __syncwarp();
-      my_vf = vf[my_group];
+      first_scales<D, L::kWords>(p, x, reinterpret_cast<const uint16_t *>(ring + st * L::kStage + 2 * L::kCodes + L::kScales), seen_at, vf, warp, lane);
     }
-    uint32_t marked = 0;  // groups of row `lane` that attend a scale that is not finite; kWide: it attends one too far off
+    if (lane < R) marks[lane] = lane < rows && sqexp[lane] < kLarge ? kWide : 0u;
+    __syncwarp();
 
     // lane-constant places in a tile: keys' codes of positions gid and gid + 8, 16, 24; values' of this lane's dimensions
     int koff[G], voff[2];
@@ -756,6 +765,8 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
           outside |= __vmaxu2(d, seen[y]) != seen[y];
         }
         if (__any_sync(0xffffffffu, outside)) {
+          const float before = vf[my_group];
+          __syncwarp();
           uint32_t bad = 0;  // of this lane's key: groups with a scale that is not finite; kWide: with one that lies too far off
 #pragma unroll
           for (int y = 0; y < L::kWords; ++y) {
@@ -777,9 +788,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
             if (lane < 2 && 2 * y + lane < G) vf[2 * y + lane] = pow2(kTopV + 127 - (int)((mx >> (16 * lane + 7)) & 0xffu));
           }
           __syncwarp();
-          const float f = vf[my_group];
-          const float down = f / my_vf;
-          my_vf = f;
+          const float down = vf[my_group] / before;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -792,7 +801,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
             who &= who - 1u;
             const long long j = (long long)t * kKeys + __shfl_sync(0xffffffffu, key, src), at = (long long)x.qpos + lane / x.g;
             const uint32_t groups = __shfl_sync(0xffffffffu, bad, src);
-            if (lane < rows && j <= at && (p.W == 0 || j > at - p.W)) marked |= groups;
+            if (lane < rows && j <= at && (p.W == 0 || j > at - p.W)) marks[lane] |= groups;
           }
         }
         lds_words(vf, fac);
@@ -800,7 +809,8 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
         for (int gr = 0; gr < G; ++gr) {
           const uint32_t ka = gr & 1 ? kw[gr / 2] & 0xffff0000u : kw[gr / 2] << 16;
           const uint32_t va = gr & 1 ? vw[gr / 2] & 0xffff0000u : vw[gr / 2] << 16;
-          nk[(gr / 4) * (kKeys * 4) + lane * (G < 4 ? G : 4) + gr % 4] = __uint_as_float(ka) * sfac;
+          // (signed codes are not multiples of 2^-24)
+          nk[(gr / 4) * (kKeys * 4) + lane * (G < 4 ? G : 4) + gr % 4] = kExact ? __uint_as_float(ka) * (1.f / 16777216.f) : __uint_as_float(ka);
           nv[gr * kKeys + lane] = __half_as_ushort(__float2half_rn(__uint_as_float(va) * __uint_as_float(fac[gr])));
         }
       }
@@ -1010,7 +1020,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
     const int state = L::kAhead ? (st == 0 ? S - 1 : st - 1) * L::kStage : 0;
     float *mine = reinterpret_cast<float *>(ring + state);
     // vf is a power of two, and its reciprocal one
-    const int ve = 127 - (int)(__float_as_uint(my_vf) >> 23);
+    const int ve = 127 - (int)(__float_as_uint(vf[my_group]) >> 23);
     const float v1 = pow2(ve / 2), v2 = pow2(ve - ve / 2);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -1020,7 +1030,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
         float sum = l[nt][c];
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        const bool bad = (__shfl_sync(0xffffffffu, marked, r) >> my_group) & 1u;
+        const bool bad = (marks[r] >> my_group) & 1u;
         if (gid == 0) {
           mine[r * PS + D] = th[nt][c] == -INFINITY ? -INFINITY : -nb[nt][c] - (kExact ? kTopP : 0.f);
           mine[r * PS + D + 1] = sum;
@@ -1034,7 +1044,7 @@ __global__ void __launch_bounds__(i4a::Lay<D, NT, QP>::kThreads, 1)
           *reinterpret_cast<float4 *>(to + 2 * v) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
-    const uint32_t wide = __ballot_sync(0xffffffffu, (marked & kWide) != 0u);
+    const uint32_t marked = marks[lane % R], wide = __ballot_sync(0xffffffffu, lane < R && (marked & kWide));
     if (wide) wide_rows<T, D, NT, QP>(p, x, smem, mine, wide, marked, warp, lane);
     if (lane == 0) s_state[warp] = warp * L::kRing + state;
     __syncthreads();

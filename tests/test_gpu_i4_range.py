@@ -255,3 +255,36 @@ def test_chunks_with_large_keys(D, max_len):
     t.q.copy_((t.q.double() * 2.0 ** -124 / D).to(BF16))
     t.call(gqaw.gqaw_paged_i4_attend)
     check_rows(t)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+def test_large_queries_beside_small_ones_over_large_keys(dtype, D):
+    """A very large row, whose own logits may leave fp32, and very small ones over very large keys: the small ones have
+    ordinary logits and keep their bits."""
+    t = Batch([(3, 90), (1, 700)], 4, 2, D, 16, dtype, seed=46, scale=1.0)
+    t.ks.copy_((t.ks.double() * 2.0 ** 110).to(BF16))
+    t.q.copy_((t.q.double() * 2.0 ** -112).to(dtype))
+    t.call(gqaw.gqaw_paged_i4_attend)
+    check_rows(t)
+    before = t.out.clone().reshape(-1, 4, D)
+    for value in (2.0 ** 20, 2.0 ** 70, 1e30, 3e38, float("inf")):
+        t.q[1, D + 5] = value  # token 1, head 1
+        t.call(gqaw.gqaw_paged_i4_attend)
+        after = t.out.reshape(-1, 4, D)
+        same = torch.ones(4, 4, dtype=torch.bool)
+        same[1, 1] = False
+        assert torch.equal(after[same], before[same])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("f", [1e-30, 1e-10, 1e5, 1e20, 1e25, 1e30, 1e36])
+def test_rows_of_queries_of_every_size(dtype, f):
+    """Queries of size f with keys to match, among rows a thousand times smaller."""
+    for D, S in ((64, 3), (128, 8), (256, 1)):
+        t = Batch([(S, 300), (1, 40)], 4, 2, D, 16, dtype, seed=47, scale=1.0)
+        t.q.copy_((t.q.double() * f).to(dtype))
+        t.q.view(-1, 4, D)[:, 1::2] /= 1000
+        t.ks.copy_((t.ks.double() / f / 8).to(BF16))
+        t.call(gqaw.gqaw_paged_i4_attend)
+        check_rows(t)
