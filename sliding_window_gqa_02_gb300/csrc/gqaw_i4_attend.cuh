@@ -11,9 +11,10 @@
 //     which the tensor cores take exactly; one AND makes two operands of two nibbles of a word, and the
 //     factor of 16 goes to the query.  Converting to bf16 through shared memory, as the
 //     5th-generation tensor cores would need it, costs four bytes there for every byte of codes,
-//     written and read again: more than its 128 bytes a cycle.  Hence mma.sync with the keys (dimensions)
-//     as M, whose operands are registers, 8 query rows as N; its rate, a product of 16 x 8 x 16 every 2
-//     cycles of an SM, is 2.4 times what the memory feeds;
+//     written and read again: more than its 128 bytes a cycle at the rate of HBM.  (Where several units
+//     share their keys through L2, as 32 rows a kv head do, that would not bind: at 0.75 TB/s a seventh of the time.)
+//     Hence mma.sync with the keys (dimensions) as M, whose operands are registers, 8 query rows as N; its
+//     rate, a product of 16 x 8 x 16 every 2 cycles of an SM, is 2.4 times what the memory feeds;
 //   - z = sum over groups g of s_g (sum_d c_d q_d - 8 sum_d q_d): the scale multiplies a group's sum in fp32,
 //     and the sum of the queries is where the accumulator starts;
 //   - the values are (c - 8) s in fp16: a nibble in the upper bits of the mantissa of 16 is 16 + c, and
@@ -25,12 +26,13 @@
 // row that puts the largest element at 2^13; weights as one part, or two for fp32 (PP).  A weight is at
 // most 2^15, since the row's reference moves when that is exceeded (and then puts the largest at 2^13); a
 // value scale is taken relative to the largest power of two of its group so far, which becomes 2^10: no
-// product leaves fp16, and with scales up to 2^24 apart each is exact.  What a row does not attend must not change it,
-// however large, so scales farther off count as zero there, and the rows that attend them are computed again
-// in fp32 (wide_rows()).  Sums and statistics are fp32.  The tensor cores cut what a sum loses, which adds up over a long context: for fp32 rows (kExact) the codes of
-// the keys are signed, so that no large sum is taken back, a product's values are added outside, the smaller
-// parts come first, and exponents are taken near 0 (error against 64 bits at 500 to 12,000 keys 9.6e-7 -> 2e-7, the
-// time the same).  The reference moves by whole powers of two and is never rounded.
+// product leaves fp16, and with scales up to 2^24 apart each is exact.  What a row does not attend must not
+// change it, however large, so scales farther off count as zero there, and the rows that attend them are
+// computed again in fp32 (wide_rows()).  Sums and statistics are fp32.  The tensor cores cut what a sum loses,
+// which adds up over a long context: for fp32 rows (kExact) the codes of the keys are signed, so that no large
+// sum is taken back, a product's values are added outside, the smaller parts come first, and exponents are
+// taken near 0 (error against 64 bits at 500 to 12,000 keys 9.6e-7 -> 2e-7, the time the same).  The reference
+// moves by whole powers of two and is never rounded.
 //
 // Each warp works on its own, on tiles of 32 keys through a ring of its own; no barrier of the CTA
 // falls inside a unit.  Tiles come by cp.async through the page table, any page size and strides; with
@@ -98,8 +100,7 @@ struct Lay {
   static constexpr int kQ = kNorm + W * kNormBytes;      // query operands [QP][NT][2 G][32 lanes] of 8 bytes
   static constexpr int kQsum = kQ + QP * NT * 2 * G * 32 * 8;  // [G][R] fp32: where accumulators start
   static constexpr int kQexp = kQsum + R * G * 4;        // [R]: power of two of a row
-  static constexpr int kBars = (kQexp + R * 4 + 15) / 16 * 16;
-  static constexpr int kTotal = kBars + W * S * 8 + 1024;  // and room to align the base
+  static constexpr int kTotal = kQexp + R * 4 + 1024;    // and room to align the base
   static_assert(kTotal + 12 * 1024 + 512 <= 232448, "shared memory");
 };
 

@@ -1,5 +1,5 @@
-// gqaw_i4_pre.cu -- instances of the prompt kernel for caches in 4 bits: more than 32 query rows of a kv
-// head, bf16, head sizes 64 and 128.
+// gqaw_i4_pre.cu -- instances of the prompt kernel for caches in 4 bits: bf16, head sizes 64 and 128, more
+// than 40 query rows of a kv head.
 #include "gqaw_paged_pre.cuh"
 
 namespace gqaw {
