@@ -40,8 +40,8 @@
 // instructions, and every lane's own look-ups 200.  A unit's first tiles are under way before the last
 // unit's rows go out.  Schedule, splits and merges: gqaw_paged.cuh.
 //
-// Measured: 64 contexts of 4 k to 33 k keys (8 kv heads of 128, 4 query heads each) 257 us, 4.05 TB/s or 60% of
-// the copy rate: issue slots are 44 to 52% busy with some 337 instructions for 16 keys of a warp (148 of them keys
+// Measured: 64 contexts of 4 k to 33 k keys (8 kv heads of 128, 4 query heads each) 262 us, 3.98 TB/s or 59% of
+// the copy rate: issue slots are 43 to 52% busy with some 337 instructions for 16 keys of a warp (148 of them keys
 // and softmax, 128 values, 37 scales, 24 loads), 12 warps a SM hide no more of each other's latencies, and registers
 // (168) allow no more.  A unit's start and end are 4 to 6 us, the schedule 2, a cut 3.5.
 //
@@ -73,7 +73,7 @@ constexpr int kTopV = 10;      // a scale's largest power of two becomes 2^kTopV
 // the smallest is then 2^-14 or more, and its values are exact; a weight that fp16 rounds to a multiple of 2^-38 of the
 // row's largest is off by 2^-14 of any other value.  Rows that attend other scales are computed by wide_rows(); so are those
 // of 2^(kEnd + 1) and more, since 2^31 weights of 2^15 times 8 of them would leave fp32.
-constexpr int kAbove = 10, kBelow = 14, kEnd = 63;
+constexpr int kAbove = 10, kBelow = 14, kEnd = 63, kUsual = -3;
 constexpr uint32_t kWide = 1u << 16;
 constexpr int kLarge = -64;    // a row's power of two: queries of 2^77 and more
 
@@ -288,7 +288,7 @@ __device__ __noinline__ void first_scales(const I4Params &p, const Unit &x, cons
   const int key = (lane & ~7) | kappa<D>(lane & 7);
   const long long j = (long long)(x.t0 + warp) * kKeys + key, last = (long long)x.qpos + x.ntok - 1;
   // The largest of the keys that all rows attend, if one is not zero: what only some of them attend is not to say how
-  // the others are computed.  A group of zeros may have no other scale after that.
+  // the others are computed.  A group of zeros, like those of padding, may have scales around 2^kUsual after that.
   const bool some = j >= x.jlo && j < x.jhi, all = j <= (long long)x.qpos && j >= (long long)x.jlo && (p.W == 0 || j > last - p.W);
   const uint16_t *vs = scales + key * G;
 #pragma unroll
@@ -296,14 +296,14 @@ __device__ __noinline__ void first_scales(const I4Params &p, const Unit &x, cons
     const uint32_t h = vs[gr] & 0x7fffu, fin = h < 0x7f80u ? h : 0u;
     uint32_t mx = __reduce_max_sync(0xffffffffu, all ? fin : 0u);
     if (mx == 0u) mx = __reduce_max_sync(0xffffffffu, some ? fin : 0u);
-    const int e = (int)(mx >> 7), low = mx ? max(min(e, 127 + kEnd) - kBelow, 0) << 7 : 0;
-    const uint32_t roof = mx ? (uint32_t)(min(e + kAbove, 127 + kEnd) << 7 | 0x7f) : 0u;
+    const int e = mx ? (int)(mx >> 7) : 127 + kUsual, low = max(min(e, 127 + kEnd) - kBelow, 0) << 7;
+    const uint32_t roof = (uint32_t)(min(e + kAbove, 127 + kEnd) << 7 | 0x7f);
     if (lane == 0) {
       uint16_t *to = reinterpret_cast<uint16_t *>(seen_at) + gr;
-      to[0] = (uint16_t)(mx ? min(mx | 0x7fu, roof) - low : 0u);
+      to[0] = (uint16_t)(mx ? min(mx | 0x7fu, roof) - low : 0u);  // (none: as if the smallest had been seen)
       to[2 * kWords] = (uint16_t)low;
       to[4 * kWords] = (uint16_t)roof;
-      vf[gr] = pow2(kTopV + 127 - min(e, 127 + kEnd));
+      vf[gr] = pow2(kTopV + 127 - (mx ? min(e, 127 + kEnd) : low >> 7));
     }
   }
   if (G == 1 && lane == 0)  // the other half of the only word
@@ -319,7 +319,7 @@ __device__ __noinline__ void first_scales(const I4Params &p, const Unit &x, cons
 //
 // Out of line and written for few registers, since ordinary caches do not come here: a lane has a key for the logits (its
 // scales relative to the largest's power of two) and D / 32 dimensions for the values.  The queries are the operands of the products (put_query()).  Bound by its own
-// instructions: 64 contexts of 4 k to 33 k keys that all have such scales take 5.9 ms, and 0.26 without.
+// instructions: 64 contexts of 4 k to 33 k keys that all have such scales take 6.8 ms, and 0.262 without.
 template <typename T, int D, int NT, int QP>
 __device__ __noinline__ void wide_rows(const I4Params &p, const Unit &x, const unsigned char *smem, float *mine, uint32_t rows, uint32_t marked,
                                        int warp, int lane) {
