@@ -458,8 +458,9 @@ size_t gqaw_paged_args_size(void);
  *     c = 8 + round(x / scale)       (in fp32, halves to even; so 1 <= c <= 15),
  * a scale and codes of 0 and 8 for a group of zeros, and a scale that is not a number for a
  * group with an element that is not finite.  Five bits times the three of c - 8 make every
- * value a bf16 number: reading a row back as bf16 or fp32 loses nothing, and the tensor cores
- * see the values that the cache holds.  Other writers may use any bf16 scale and any code; a
+ * value a bf16 number: reading a row back as bf16 or fp32 loses nothing of what the cache holds, and
+ * the tensor cores see the values that it holds.  A group whose largest element is within 1 / 17 of the
+ * type's largest number may hold, and read back, an infinite one: its scale is rounded up.  Other writers may use any bf16 scale and any code; a
  * product of more than eight bits is then rounded to bf16 where it is needed as bf16 (reading
  * back as bf16, the attention of prompt chunks in bf16).
  * ------------------------------------------------------------------------------- */
@@ -493,8 +494,9 @@ typedef struct gqaw_paged_i4_args {
 
 /* Workspace bytes of any of the four calls below, as gqaw_paged_workspace_bytes(); with prompt chunks it
  * holds the rows that they attend as bf16 too, where those are 2 GiB at most for the longest sequences
- * that the call allows.  An append and a read need 256 bytes alone, for the device status word.  A workspace serves paged calls on 4-bit and
- * on other caches alike, in stream order, if it is large enough for each. */
+ * that the call allows (chunks of longer ones run slower: with head size 256 seven times, else a fifth).  An append
+ * and a read need 256 bytes alone, zeroed by gqaw_workspace_init(), for the device status word.  A workspace
+ * serves paged calls on 4-bit and on other caches alike, in stream order, if it is large enough for each. */
 size_t gqaw_paged_i4_workspace_bytes(const gqaw_paged_i4_args *args);
 
 /* Append: key rows, normed with key_weight and turned by their positions (each if given) in
@@ -505,9 +507,14 @@ gqaw_status gqaw_paged_i4_append(const gqaw_paged_i4_args *args, void *stream);
 
 /* Attention over the cache as gqaw_paged_attend; logits and outputs are those of the values that
  * the codes stand for.  Sums and statistics are fp32.  Queries are multiplied as they are, fp32
- * ones in two parts of fp16; the softmax weights, times the value scales, are rounded to fp16
- * (2^-12 relative), or two parts of it for fp32.  Prompt chunks in bf16 (more than 40 query rows per kv
- * head in a sequence, 64 with head size 256, and more than a little work): weights are rounded to bf16. */
+ * ones in two parts of fp16; the softmax weights are rounded to fp16 (2^-12 relative, and those below 2^-27 of
+ * the row's largest to a multiple of 2^-38 of it), or two parts of it for fp32; values are not rounded.  Rows that
+ * attend value scales more than 2^10 above or 2^14 below others of their group, or of 2^64 and more, or whose
+ * queries reach 2^77, are computed without the tensor cores in fp32, some 25 times slower.  A value scale that is
+ * not finite makes the elements of its group not finite for the tokens that attend it, and nothing else.
+ * Prompt chunks in bf16 (more than 40 query rows per kv head in a sequence, 64 with head size 256, and more than a
+ * little work): weights are rounded to bf16 and reach 2^8, with a softcap of up to 44 2^64, before their sums are
+ * divided; so averages of values beyond 2^119 (2^63) over the number of keys may come out infinite there. */
 gqaw_status gqaw_paged_i4_attend(const gqaw_paged_i4_args *args, void *stream);
 
 /* The whole step as gqaw_paged_step: append, and attention of the normed and turned queries. */

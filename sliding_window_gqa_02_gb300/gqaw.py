@@ -697,7 +697,8 @@ def make_paged_i4_args(query, key, value, key_codes, value_codes, key_scales, va
 
 
 def new_paged_i4_workspace(args: gqaw_paged_i4_args, device, stream: int = 0):
-    """Allocate (torch) and zero-initialise a workspace large enough for ``args``."""
+    """Allocate (torch) and zero-initialise a workspace large enough for any call with ``args``; appends and reads
+    alone take one of 256 bytes that ``gqaw_workspace_init`` has zeroed."""
     return _new_workspace(gqaw_paged_i4_workspace_bytes(args), device, stream)
 
 
